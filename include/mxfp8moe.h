@@ -461,6 +461,143 @@ mxfp8_status mxfp8_swiglu_bwd_quantize(const uint16_t* h, const uint16_t* da, in
 size_t mxfp8_convert_sweep_bytes(int32_t mode);
 mxfp8_status mxfp8_convert_sweep(int32_t mode, void* out, size_t out_bytes, void* stream);
 
+/*
+ * Experts with any number of rows, in 16-bit floating point and in 8-bit
+ * integers, and the routing around them.  These calls share none of the
+ * multiples-of-128 contract above: every size from 1 up is taken, splits may
+ * be any numbers.  Element types:
+ */
+typedef enum mxfp8_type {
+  MXFP8_TYPE_F32 = 0,
+  MXFP8_TYPE_BF16 = 1,
+  MXFP8_TYPE_F16 = 2
+} mxfp8_type;
+
+/*
+ * mxfp8_ragged_gemm -- one product of an expert linear over ragged experts.
+ * Expert g owns m_splits[g] consecutive rows of the R rows of the product, in
+ * order; i(r) = row_index[r], or r where row_index is NULL (then S = R):
+ *   NT  C[r, n]    = sum_k X[i(r), k] W[g, n, k]       forward
+ *   NN  C[r, k]    = sum_n dY[r, n] W[g, n, k]         gradient of the input
+ *   TN  C[g, n, k] = sum over r of g of dY[r, n] X[i(r), k]   of the weight
+ * Sums are fp32, rounded once (nearest even) to the output's type.  Results are
+ * the same from run to run.
+ *   type    MXFP8_TYPE_BF16 or MXFP8_TYPE_F16: X, dY, W
+ *   a       NT: X [S, K]; NN, TN: dY [R, N].  Row stride lda >= the row length
+ *   b       NT, NN: W [G, N, K] contiguous (ldb ignored); TN: X [S, K], row
+ *           stride ldb
+ *   c       NT [R, N], NN [R, K], row stride ldc; TN [G, N, K] contiguous (ldc
+ *           ignored).  c_type: MXFP8_TYPE_F32 or `type`
+ *   m_splits  device int64 [G], 1 <= G <= 1024.  A negative split counts as 0.
+ *           Rows of C past the last expert's are not written, and rows past R
+ *           not read, whatever the splits sum to
+ *   row_index  NULL or device int32 [R] (NT, TN).  Entries outside [0, S) stand
+ *           for a row of zeros; entries past the last expert's row are not read
+ * TN writes zeros for an expert without rows.  Row values of experts that own
+ * other rows never reach a result (infinities and NaN included).
+ * Strides are in elements.  Faster where pointers, strides and the contraction
+ * length are multiples of 16 bytes; right for all.
+ * Errors: EINVAL for NULL pointers, sizes < 1 (R, S >= 0), strides shorter than
+ * a row, G out of range, host m_splits, row_index with NN, S != R without
+ * row_index, over 2^31 - 1 rows, columns or tiles; ENOTSUP for other types.
+ */
+mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int64_t lda,
+                               const void* b, int64_t ldb, void* c, int64_t ldc, int32_t c_type,
+                               int64_t R, int64_t S, int64_t N, int64_t K,
+                               const int64_t* m_splits, int32_t G, const int32_t* row_index,
+                               void* stream);
+
+/*
+ * mxfp8_quantize_int8 -- a tensor's rows as 8-bit integers with a scale each:
+ *   scale[t] = max|x[t]| / 127 in fp32 (nearest); q[t] = the integers nearest
+ *   to x[t] / scale[t], ties to even, in [-127, 127].
+ * A row of zeros: scale 0, codes 0.  A row with an infinity or NaN: scale NaN,
+ * codes 0, so that products with it are NaN.  For weights, rows are output
+ * channels.
+ *   x [T, K] bf16 / fp16 (type), row stride ldx; q int8 [T, K]; scale fp32 [T]
+ * Errors: EINVAL for NULL, K < 1, T < 0, ldx < K; ENOTSUP for other types.
+ */
+mxfp8_status mxfp8_quantize_int8(const void* x, int32_t type, int64_t T, int64_t K, int64_t ldx,
+                                 int8_t* q, float* scale, void* stream);
+
+/*
+ * mxfp8_ragged_gemm_int8 -- the forward product in 8-bit integers:
+ *   C[r, n] = (sum_k q[i(r), k] w[g, n, k]) * scale[i(r)] * w_scale[g, n]
+ * The integer sum is exact; it is then rounded to fp32, multiplied by the two
+ * scales in that order and rounded to the output's type.
+ *   q [S, K] int8, row stride ldq; scale [S]; w [G, N, K] int8; w_scale [G, N];
+ *   c [R, N], row stride ldc, c_type any mxfp8_type; the rest as
+ *   mxfp8_ragged_gemm (NT).
+ * Errors: as mxfp8_ragged_gemm; EINVAL for K > 131071 (sums past 32 bits).
+ */
+mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* scale,
+                                    const int8_t* w, const float* w_scale, void* c, int64_t ldc,
+                                    int32_t c_type, int64_t R, int64_t S, int64_t N, int64_t K,
+                                    const int64_t* m_splits, int32_t G, const int32_t* row_index,
+                                    void* stream);
+
+/*
+ * mxfp8_moe_route -- the top_k experts of each token, their weights, and the
+ * order of the rows that the products above take.
+ * Choice: the top_k largest logits, equal ones by lowest expert.  Logits of
+ * -inf or NaN are never chosen; a token whose mask is 0 chooses none and its
+ * logits are not looked at.  Logits must not be +inf.
+ * Weights: exp(logit) over its sum over the chosen experts (renormalize != 0)
+ * or over all experts.
+ *   logits [T, E] (type: any mxfp8_type), 1 <= E <= 1024, top_k <= min(E, 16)
+ *   token_mask  NULL or uint8 [T]
+ *   ids int32 [T, top_k]      by falling logit; -1 where there is none
+ *   weights fp32 [T, top_k]   0 where there is none
+ *   m_splits int64 [E]        rows of each expert
+ *   row_token int32 [T top_k] token of each row, rows ordered by expert, then
+ *                             token; -1 past the last row
+ *   row_pos int32 [T, top_k]  row of each choice, -1 where there is none
+ *   workspace   of mxfp8_moe_route_workspace_bytes(T, E) bytes; needs no
+ *               initialisation (NULL where that is 0)
+ * Errors: EINVAL for NULL, sizes out of range, T top_k >= 2^31, a small
+ * workspace; ENOTSUP for other types.  T = 0 writes m_splits only.
+ */
+size_t mxfp8_moe_route_workspace_bytes(int64_t T, int32_t E);
+mxfp8_status mxfp8_moe_route(const void* logits, int32_t type, int64_t T, int32_t E,
+                             int32_t top_k, int32_t renormalize, const uint8_t* token_mask,
+                             int32_t* ids, float* weights, int64_t* m_splits, int32_t* row_token,
+                             int32_t* row_pos, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * mxfp8_moe_route_bwd -- gradient of the logits from that of the weights:
+ * dlogits [T, E] of the logits' type, every value written (0 for masked tokens and,
+ * when renormalized, for experts that were not chosen).  ids and weights as
+ * mxfp8_moe_route gave them; dweights fp32 [T, top_k], ignored where ids is -1.
+ */
+mxfp8_status mxfp8_moe_route_bwd(const void* logits, int32_t type, int64_t T, int32_t E,
+                                 int32_t top_k, int32_t renormalize, const int32_t* ids,
+                                 const float* weights, const float* dweights, void* dlogits,
+                                 void* stream);
+
+/*
+ * mxfp8_moe_combine -- out[t] = sum_j weights[t, j] y[row_pos[t, j]], fp32 sums in
+ * the order of j, rounded once.  A row_pos outside [0, R) adds nothing.
+ *   y [R, H], out [T, H] bf16 / fp16 (type); row_pos int32 [T, top_k];
+ *   weights fp32 [T, top_k] or NULL (all 1: the gradient of the gather that
+ *   row_token does); 1 <= top_k <= 16
+ */
+mxfp8_status mxfp8_moe_combine(const void* y, int32_t type, int64_t T, int64_t R, int64_t H,
+                               int32_t top_k, const int32_t* row_pos, const float* weights,
+                               void* out, void* stream);
+
+/*
+ * mxfp8_moe_combine_bwd -- dy[row_pos[t, j]] = weights[t, j] dout[t] and
+ * dweights[t, j] = <y[row_pos[t, j]], dout[t]> (fp32; 0 where row_pos is
+ * outside [0, R)).  dy or dweights may be NULL (not wanted; y may be NULL
+ * without dweights).  No row is named twice; rows of dy that none names are
+ * not written.
+ */
+mxfp8_status mxfp8_moe_combine_bwd(const void* dout, const void* y, int32_t type, int64_t T,
+                                   int64_t R, int64_t H, int32_t top_k, const int32_t* row_pos,
+                                   const float* weights, void* dy, float* dweights,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -491,3 +491,303 @@ def convert_sweep(mode, stream=None):
     st = lib.mxfp8_convert_sweep(mode, _ptr(out), need, _stream(stream))
     _native.check(st, "mxfp8_convert_sweep")
     return out
+
+
+# ----------------------------------------------------------------------------
+# experts with any number of rows, and the routing around them
+# ----------------------------------------------------------------------------
+
+_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _rows_of(t, dtype, shape, name):
+    """A device matrix with contiguous rows; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return ld
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
+def _type_of(t, name, floats=(torch.bfloat16, torch.float16)):
+    if t.dtype not in floats:
+        raise NotImplementedError(f"{name} of {t.dtype} is not supported")
+    return _TYPE[t.dtype]
+
+
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _row_index(row_index, like):
+    if row_index is None:
+        return None
+    if not isinstance(row_index, torch.Tensor) or row_index.dim() != 1:
+        raise ValueError("row_index must be a 1-D tensor")
+    _need(row_index, torch.int32, tuple(row_index.shape), "row_index")
+    return row_index
+
+
+def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None, stream=None):
+    """One product of an expert linear whose experts have any number of rows.
+
+    layout "NT" (forward): a = X [S, K], b = W [G, N, K] -> [R, N]
+    layout "NN" (dgrad):   a = dY [R, N], b = W [G, N, K] -> [R, K]
+    layout "TN" (wgrad):   a = dY [R, N], b = X [S, K] -> [G, N, K]
+
+    bf16 or fp16 operands; m_splits device int64 [G], expert g owning that many
+    consecutive rows of R.  row_index (int32 [R], NT and TN): row r of the
+    product is row row_index[r] of X; without it S = R.  a, X and out may
+    have a row stride.  out_dtype: the operands' (default) or float32.  Rows
+    past the last expert's are not written (mxfp8_ragged_gemm).
+    """
+    lib = _lib()
+    lay = _LAYOUTS[layout]
+    ms = _splits(m_splits)
+    g = ms.numel()
+    ra, ca = _matrix(a, "a")
+    ty = _type_of(a, "a")
+    index = _row_index(row_index, a)
+    if lay == LAYOUT_TN:
+        s, k = _matrix(b, "b")
+        r, n = ra, ca
+    else:
+        if not isinstance(b, torch.Tensor) or b.dim() != 3:
+            raise ValueError("b must be [G, N, K]")
+        n, k = b.shape[1:]
+        s = ra
+        r = index.numel() if index is not None and lay == LAYOUT_NT else ra
+    if index is not None:
+        if lay == LAYOUT_NN:
+            raise ValueError("NN takes no row_index")
+        if index.numel() != r:
+            raise ValueError(f"row_index must have {r} entries, got {index.numel()}")
+    elif lay == LAYOUT_TN and s != r:
+        raise ValueError(f"b must have {r} rows without a row_index, got {s}")
+    lda = _rows_of(a, a.dtype, (ra, k if lay == LAYOUT_NT else n), "a")
+    if lay == LAYOUT_TN:
+        ldb = _rows_of(b, a.dtype, (s, k), "b")
+    else:
+        _need(b, a.dtype, (g, n, k), "b")
+        ldb = k
+    out_dtype = a.dtype if out_dtype is None else out_dtype
+    if out_dtype not in (a.dtype, torch.float32):
+        raise NotImplementedError(f"output dtype {out_dtype} is not supported")
+    if lay == LAYOUT_TN:
+        if out is None:
+            out = _empty((g, n, k), out_dtype, a)
+        _need(out, out_dtype, (g, n, k), "out")
+        ldc = k
+    else:
+        shape = (r, n if lay == LAYOUT_NT else k)
+        if out is None:
+            out = _empty(shape, out_dtype, a)
+        ldc = _rows_of(out, out_dtype, shape, "out")
+    _same_device(a, b=b, m_splits=ms, row_index=index, out=out)
+    st = lib.mxfp8_ragged_gemm(lay, ty, _ptr(a), lda, _ptr(b), ldb, _ptr(out), ldc,
+                               _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
+                               _stream(stream))
+    _native.check(st, "mxfp8_ragged_gemm")
+    return out
+
+
+def quantize_int8(x, out=None, stream=None):
+    """Rows of a bf16 / fp16 matrix as 8-bit integers: (q int8 [T, K], scale
+    fp32 [T]) with x ~ q * scale, scale = max|row| / 127.  out: optional (q,
+    scale) buffers.  For weights [G, N, K] pass the view [G * N, K]."""
+    lib = _lib()
+    t, k = _matrix(x, "x")
+    ty = _type_of(x, "x")
+    ldx = _rows_of(x, x.dtype, (t, k), "x")
+    q, scale = (None, None) if out is None else out
+    q = _empty((t, k), torch.int8, x) if q is None else q
+    scale = _empty((t,), torch.float32, x) if scale is None else scale
+    _need(q, torch.int8, (t, k), "q")
+    _need(scale, torch.float32, (t,), "scale")
+    _same_device(x, q=q, scale=scale)
+    st = lib.mxfp8_quantize_int8(_ptr(x), ty, t, k, ldx, _ptr(q), _ptr(scale), _stream(stream))
+    _native.check(st, "mxfp8_quantize_int8")
+    return q, scale
+
+
+def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=torch.bfloat16,
+                     out=None, stream=None):
+    """Forward product in 8-bit integers: q [S, K] int8 with scale [S] (as
+    quantize_int8 gives them), w [G, N, K] int8 with w_scale [G, N] -> [R, N],
+    (sum of q w) * scale * w_scale.  row_index and m_splits as ragged_gemm."""
+    lib = _lib()
+    ms = _splits(m_splits)
+    g = ms.numel()
+    s, k = _matrix(q, "q")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [G, N, K]")
+    n = w.shape[1]
+    index = _row_index(row_index, q)
+    r = s if index is None else index.numel()
+    ldq = _rows_of(q, torch.int8, (s, k), "q")
+    _need(scale, torch.float32, (s,), "scale")
+    _need(w, torch.int8, (g, n, k), "w")
+    _need(w_scale, torch.float32, (g, n), "w_scale")
+    if out_dtype not in _TYPE:
+        raise NotImplementedError(f"output dtype {out_dtype} is not supported")
+    if out is None:
+        out = _empty((r, n), out_dtype, q)
+    ldc = _rows_of(out, out_dtype, (r, n), "out")
+    _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out)
+    st = lib.mxfp8_ragged_gemm_int8(_ptr(q), ldq, _ptr(scale), _ptr(w), _ptr(w_scale), _ptr(out),
+                                    ldc, _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
+                                    _stream(stream))
+    _native.check(st, "mxfp8_ragged_gemm_int8")
+    return out
+
+
+@dataclass
+class Route:
+    """Where the tokens go (moe_route): ids, weights and row_pos [T, top_k],
+    m_splits [E], row_token [T * top_k]."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    m_splits: torch.Tensor
+    row_token: torch.Tensor
+    row_pos: torch.Tensor
+    renormalize: bool = True
+
+
+def moe_route_workspace_bytes(tokens, experts):
+    return int(_lib().mxfp8_moe_route_workspace_bytes(tokens, experts))
+
+
+def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, workspace=None,
+              stream=None):
+    """logits [T, E] (fp32, bf16, fp16) -> Route: each token's top_k experts
+    (equal logits by lowest expert) and softmax weights, over the chosen
+    experts (renormalize) or over all; the rows' order by expert.  token_mask:
+    bool or uint8 [T], tokens with 0 are not routed."""
+    lib = _lib()
+    t, e = _matrix(logits, "logits")
+    ty = _type_of(logits, "logits", tuple(_TYPE))
+    _need(logits, logits.dtype, (t, e), "logits")
+    if token_mask is not None:
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _need(token_mask, torch.uint8, (t,), "token_mask")
+    if out is None:
+        out = Route(_empty((t, top_k), torch.int32, logits),
+                    _empty((t, top_k), torch.float32, logits),
+                    _empty((e,), torch.int64, logits),
+                    _empty((t * top_k,), torch.int32, logits),
+                    _empty((t, top_k), torch.int32, logits))
+    out.renormalize = bool(renormalize)
+    _need(out.ids, torch.int32, (t, top_k), "ids")
+    _need(out.weights, torch.float32, (t, top_k), "weights")
+    _need(out.m_splits, torch.int64, (e,), "m_splits")
+    _need(out.row_token, torch.int32, (t * top_k,), "row_token")
+    _need(out.row_pos, torch.int32, (t, top_k), "row_pos")
+    need = lib.mxfp8_moe_route_workspace_bytes(t, e)
+    size = need
+    if workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+        if not workspace.is_cuda or size < need:
+            raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
+    elif need:
+        workspace = _empty((need,), torch.uint8, logits)
+    _same_device(logits, token_mask=token_mask, ids=out.ids, weights=out.weights,
+                 m_splits=out.m_splits, row_token=out.row_token, row_pos=out.row_pos,
+                 workspace=workspace)
+    st = lib.mxfp8_moe_route(_ptr(logits), ty, t, e, top_k, int(out.renormalize),
+                             _ptr(token_mask), _ptr(out.ids), _ptr(out.weights),
+                             _ptr(out.m_splits), _ptr(out.row_token), _ptr(out.row_pos),
+                             _ptr(workspace), size, _stream(stream))
+    _native.check(st, "mxfp8_moe_route")
+    return out
+
+
+def moe_route_bwd(logits, route, dweights, out=None, stream=None):
+    """Gradient of the logits [T, E] (their type) from that of route.weights."""
+    lib = _lib()
+    t, e = _matrix(logits, "logits")
+    ty = _type_of(logits, "logits", tuple(_TYPE))
+    k = _matrix(route.ids, "ids")[1]
+    _need(logits, logits.dtype, (t, e), "logits")
+    _need(route.ids, torch.int32, (t, k), "ids")
+    _need(route.weights, torch.float32, (t, k), "weights")
+    _need(dweights, torch.float32, (t, k), "dweights")
+    if out is None:
+        out = torch.empty_like(logits)
+    _need(out, logits.dtype, (t, e), "out")
+    _same_device(logits, ids=route.ids, weights=route.weights, dweights=dweights, out=out)
+    st = lib.mxfp8_moe_route_bwd(_ptr(logits), ty, t, e, k, int(route.renormalize),
+                                 _ptr(route.ids), _ptr(route.weights), _ptr(dweights), _ptr(out),
+                                 _stream(stream))
+    _native.check(st, "mxfp8_moe_route_bwd")
+    return out
+
+
+def moe_combine(y, row_pos, weights=None, out=None, stream=None):
+    """out [T, H] = sum over j of weights[:, j] * y[row_pos[:, j]] (y [R, H]
+    bf16 / fp16, fp32 sums).  Without weights the plain sum, which is the
+    gradient of the gather by row_token."""
+    lib = _lib()
+    r, h = _matrix(y, "y")
+    ty = _type_of(y, "y")
+    t, k = _matrix(row_pos, "row_pos")
+    _need(y, y.dtype, (r, h), "y")
+    _need(row_pos, torch.int32, (t, k), "row_pos")
+    if weights is not None:
+        _need(weights, torch.float32, (t, k), "weights")
+    if out is None:
+        out = _empty((t, h), y.dtype, y)
+    _need(out, y.dtype, (t, h), "out")
+    _same_device(y, row_pos=row_pos, weights=weights, out=out)
+    st = lib.mxfp8_moe_combine(_ptr(y), ty, t, r, h, k, _ptr(row_pos), _ptr(weights), _ptr(out),
+                               _stream(stream))
+    _native.check(st, "mxfp8_moe_combine")
+    return out
+
+
+def moe_combine_bwd(dout, y, row_pos, weights=None, want_dy=True, want_dweights=True, out=None,
+                    stream=None):
+    """Gradients of moe_combine: (dy [R, H], dweights [T, top_k] fp32), None
+    for one that is not wanted.  Rows of dy that no row_pos names are not
+    written.  out: optional (dy, dweights) buffers."""
+    lib = _lib()
+    t, h = _matrix(dout, "dout")
+    ty = _type_of(dout, "dout")
+    r = _matrix(y, "y")[0]
+    k = _matrix(row_pos, "row_pos")[1]
+    _need(dout, dout.dtype, (t, h), "dout")
+    _need(y, dout.dtype, (r, h), "y")
+    _need(row_pos, torch.int32, (t, k), "row_pos")
+    if weights is not None:
+        _need(weights, torch.float32, (t, k), "weights")
+    dy, dw = (None, None) if out is None else out
+    if want_dy:
+        dy = torch.empty_like(y) if dy is None else dy
+        _need(dy, dout.dtype, (r, h), "dy")
+    else:
+        dy = None
+    if want_dweights:
+        dw = _empty((t, k), torch.float32, dout) if dw is None else dw
+        _need(dw, torch.float32, (t, k), "dweights")
+    else:
+        dw = None
+    _same_device(dout, y=y, row_pos=row_pos, weights=weights, dy=dy, dweights=dw)
+    st = lib.mxfp8_moe_combine_bwd(_ptr(dout), _ptr(y), ty, t, r, h, k, _ptr(row_pos),
+                                   _ptr(weights), _ptr(dy), _ptr(dw), _stream(stream))
+    _native.check(st, "mxfp8_moe_combine_bwd")
+    return dy, dw

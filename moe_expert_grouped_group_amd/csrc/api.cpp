@@ -10,6 +10,7 @@
 #include <cstring>
 
 #include "kernels.h"
+#include "ragged_common.h"
 
 namespace {
 
@@ -460,6 +461,236 @@ mxfp8_status mxfp8_convert_sweep(int32_t mode, void* out, size_t out_bytes, void
   REQUIRE(out != nullptr && out_bytes >= need, "%s: mode %d needs a buffer of %zu bytes", fn,
           (int)mode, need);
   return hip_status(mx::launch_convert_sweep(mode, static_cast<uint8_t*>(out), as_stream(stream)),
+                    fn);
+}
+
+namespace {
+
+constexpr int64_t kI32Max = 0x7FFFFFFF;
+
+// What the ragged products check alike: sizes, splits, and the row index.
+mxfp8_status check_ragged(const char* fn, int layout, int64_t R, int64_t S, int64_t N, int64_t K,
+                          const int64_t* m_splits, int32_t G, const int32_t* row_index) {
+  REQUIRE(R >= 0 && S >= 0 && R <= kI32Max && S <= kI32Max,
+          "%s: R = %lld and S = %lld must be 0 to 2^31 - 1", fn, (long long)R, (long long)S);
+  REQUIRE(N >= 1 && K >= 1 && N <= kI32Max && K <= kI32Max,
+          "%s: N = %lld and K = %lld must be 1 to 2^31 - 1", fn, (long long)N, (long long)K);
+  REQUIRE(G >= 1 && G <= mx::kRaggedMaxGroups, "%s: G = %d must be 1 to %d", fn, (int)G,
+          mx::kRaggedMaxGroups);
+  REQUIRE(row_index == nullptr || layout != MXFP8_LAYOUT_NN, "%s: NN takes no row_index", fn);
+  REQUIRE(row_index != nullptr || S == R, "%s: S = %lld must be R = %lld without a row_index", fn,
+          (long long)S, (long long)R);
+  REQUIRE(mx::ragged_blocks(layout, R, N, K, G) <= kI32Max, "%s: over 2^31 - 1 output tiles", fn);
+  return check_device_splits(m_splits, G, fn);
+}
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+
+mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int64_t lda,
+                               const void* b, int64_t ldb, void* c, int64_t ldc, int32_t c_type,
+                               int64_t R, int64_t S, int64_t N, int64_t K,
+                               const int64_t* m_splits, int32_t G, const int32_t* row_index,
+                               void* stream) {
+  const char* fn = "mxfp8_ragged_gemm";
+  REQUIRE(layout == MXFP8_LAYOUT_NT || layout == MXFP8_LAYOUT_NN || layout == MXFP8_LAYOUT_TN,
+          "%s: unknown layout %d", fn, (int)layout);
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: operand type %d is not supported", fn, (int)type);
+  if (c_type != MXFP8_TYPE_F32 && c_type != type)
+    return fail(MXFP8_ENOTSUP, "%s: output type %d is not supported", fn, (int)c_type);
+  mxfp8_status st = check_ragged(fn, layout, R, S, N, K, m_splits, G, row_index);
+  if (st != MXFP8_OK) return st;
+  const bool tn = layout == MXFP8_LAYOUT_TN;
+  REQUIRE(lda >= (layout == MXFP8_LAYOUT_NT ? K : N), "%s: lda = %lld is shorter than a row", fn,
+          (long long)lda);
+  REQUIRE(!tn || ldb >= K, "%s: ldb = %lld is shorter than a row", fn, (long long)ldb);
+  REQUIRE(tn || ldc >= (layout == MXFP8_LAYOUT_NT ? N : K), "%s: ldc = %lld is shorter than a row",
+          fn, (long long)ldc);
+  if (R == 0 && !tn) return ok();
+  REQUIRE(c != nullptr, "%s: c is NULL", fn);
+  REQUIRE(tn ? (R == 0 || a) && (S == 0 || R == 0 || b) : b && (a || S == 0),
+          "%s: NULL operand", fn);
+  REQUIRE(aligned_to(a, 2) && aligned_to(b, 2) && aligned_to(c, c_type == 0 ? 4 : 2) &&
+              aligned_to(row_index, 4) && aligned_to(m_splits, 8),
+          "%s: a pointer is not aligned to its element", fn);
+  mx::RaggedArgs p{};
+  p.a = a;
+  p.b = b;
+  p.c = c;
+  p.lda = lda;
+  p.ldb = tn ? ldb : K;
+  p.ldc = tn ? K : ldc;
+  p.R = R;
+  p.S = S;
+  p.N = N;
+  p.K = K;
+  p.m_splits = m_splits;
+  p.row_index = row_index;
+  p.G = G;
+  return hip_status(
+      mx::launch_ragged_gemm(layout, type == MXFP8_TYPE_F16, c_type, p, as_stream(stream)), fn);
+}
+
+mxfp8_status mxfp8_quantize_int8(const void* x, int32_t type, int64_t T, int64_t K, int64_t ldx,
+                                 int8_t* q, float* scale, void* stream) {
+  const char* fn = "mxfp8_quantize_int8";
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: type %d is not supported", fn, (int)type);
+  REQUIRE(T >= 0 && T <= kI32Max && K >= 1 && K <= kI32Max,
+          "%s: T = %lld must be 0 to 2^31 - 1, K = %lld 1 to 2^31 - 1", fn, (long long)T,
+          (long long)K);
+  REQUIRE(ldx >= K, "%s: ldx = %lld is shorter than a row", fn, (long long)ldx);
+  if (T == 0) return ok();
+  REQUIRE(x && q && scale, "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(x, 2) && aligned_to(scale, 4), "%s: a pointer is not aligned to its element",
+          fn);
+  return hip_status(
+      mx::launch_quantize_int8(x, type == MXFP8_TYPE_F16, T, K, ldx, q, scale, as_stream(stream)),
+      fn);
+}
+
+mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* scale,
+                                    const int8_t* w, const float* w_scale, void* c, int64_t ldc,
+                                    int32_t c_type, int64_t R, int64_t S, int64_t N, int64_t K,
+                                    const int64_t* m_splits, int32_t G, const int32_t* row_index,
+                                    void* stream) {
+  const char* fn = "mxfp8_ragged_gemm_int8";
+  if (c_type != MXFP8_TYPE_F32 && c_type != MXFP8_TYPE_BF16 && c_type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: output type %d is not supported", fn, (int)c_type);
+  mxfp8_status st = check_ragged(fn, MXFP8_LAYOUT_NT, R, S, N, K, m_splits, G, row_index);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(K <= 131071, "%s: K = %lld: sums of over 131071 products can pass 32 bits", fn,
+          (long long)K);
+  REQUIRE(ldq >= K, "%s: ldq = %lld is shorter than a row", fn, (long long)ldq);
+  REQUIRE(ldc >= N, "%s: ldc = %lld is shorter than a row", fn, (long long)ldc);
+  if (R == 0) return ok();
+  REQUIRE(c && w && w_scale && (S == 0 || (q && scale)), "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(scale, 4) && aligned_to(w_scale, 4) && aligned_to(c, c_type == 0 ? 4 : 2) &&
+              aligned_to(row_index, 4) && aligned_to(m_splits, 8),
+          "%s: a pointer is not aligned to its element", fn);
+  mx::RaggedArgs p{};
+  p.a = q;
+  p.b = w;
+  p.c = c;
+  p.lda = ldq;
+  p.ldb = K;
+  p.ldc = ldc;
+  p.R = R;
+  p.S = S;
+  p.N = N;
+  p.K = K;
+  p.m_splits = m_splits;
+  p.row_index = row_index;
+  p.sa = scale;
+  p.sb = w_scale;
+  p.G = G;
+  return hip_status(mx::launch_ragged_gemm_int8(c_type, p, as_stream(stream)), fn);
+}
+
+namespace {
+
+mxfp8_status check_route(const char* fn, int32_t type, int64_t T, int32_t E, int32_t top_k) {
+  if (type != MXFP8_TYPE_F32 && type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: logits type %d is not supported", fn, (int)type);
+  REQUIRE(E >= 1 && E <= 1024, "%s: E = %d must be 1 to 1024", fn, (int)E);
+  REQUIRE(top_k >= 1 && top_k <= 16 && top_k <= E, "%s: top_k = %d must be 1 to min(E, 16)", fn,
+          (int)top_k);
+  REQUIRE(T >= 0 && T <= kI32Max / top_k, "%s: T = %lld: T * top_k must be below 2^31", fn,
+          (long long)T);
+  return MXFP8_OK;
+}
+
+mxfp8_status check_join(const char* fn, int32_t type, int64_t T, int64_t R, int64_t H,
+                        int32_t top_k) {
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: type %d is not supported", fn, (int)type);
+  REQUIRE(T >= 0 && R >= 0 && T <= kI32Max && R <= kI32Max,
+          "%s: T = %lld and R = %lld must be 0 to 2^31 - 1", fn, (long long)T, (long long)R);
+  REQUIRE(H >= 1 && H <= kI32Max, "%s: H = %lld must be 1 to 2^31 - 1", fn, (long long)H);
+  REQUIRE(T * ((H + 7) / 8) / 256 < kI32Max, "%s: T * H is too large", fn);
+  REQUIRE(top_k >= 1 && top_k <= 16, "%s: top_k = %d must be 1 to 16", fn, (int)top_k);
+  return MXFP8_OK;
+}
+
+}  // namespace
+
+size_t mxfp8_moe_route_workspace_bytes(int64_t T, int32_t E) {
+  return mx::route_workspace_bytes(T, E);
+}
+
+mxfp8_status mxfp8_moe_route(const void* logits, int32_t type, int64_t T, int32_t E,
+                             int32_t top_k, int32_t renormalize, const uint8_t* token_mask,
+                             int32_t* ids, float* weights, int64_t* m_splits, int32_t* row_token,
+                             int32_t* row_pos, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const char* fn = "mxfp8_moe_route";
+  mxfp8_status st = check_route(fn, type, T, E, top_k);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(m_splits != nullptr, "%s: m_splits is NULL", fn);
+  REQUIRE(T == 0 || (logits && ids && weights && row_token && row_pos), "%s: NULL pointer", fn);
+  const size_t need = mx::route_workspace_bytes(T, E);
+  REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need),
+          "%s: needs a workspace of %zu bytes", fn, need);
+  REQUIRE(aligned_to(logits, type == 0 ? 4 : 2) && aligned_to(ids, 4) && aligned_to(weights, 4) &&
+              aligned_to(m_splits, 8) && aligned_to(row_token, 4) && aligned_to(row_pos, 4) &&
+              (need == 0 || aligned_to(workspace, 2)),
+          "%s: a pointer is not aligned to its element", fn);
+  return hip_status(mx::launch_route(logits, type, T, E, top_k, renormalize != 0, token_mask, ids,
+                                     weights, m_splits, row_token, row_pos, workspace,
+                                     as_stream(stream)),
+                    fn);
+}
+
+mxfp8_status mxfp8_moe_route_bwd(const void* logits, int32_t type, int64_t T, int32_t E,
+                                 int32_t top_k, int32_t renormalize, const int32_t* ids,
+                                 const float* weights, const float* dweights, void* dlogits,
+                                 void* stream) {
+  const char* fn = "mxfp8_moe_route_bwd";
+  mxfp8_status st = check_route(fn, type, T, E, top_k);
+  if (st != MXFP8_OK) return st;
+  if (T == 0) return ok();
+  REQUIRE(logits && ids && weights && dweights && dlogits, "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(logits, type == 0 ? 4 : 2) && aligned_to(dlogits, type == 0 ? 4 : 2) &&
+              aligned_to(ids, 4) && aligned_to(weights, 4) && aligned_to(dweights, 4),
+          "%s: a pointer is not aligned to its element", fn);
+  return hip_status(mx::launch_route_bwd(logits, type, T, E, top_k, renormalize != 0, ids, weights,
+                                         dweights, dlogits, as_stream(stream)),
+                    fn);
+}
+
+mxfp8_status mxfp8_moe_combine(const void* y, int32_t type, int64_t T, int64_t R, int64_t H,
+                               int32_t top_k, const int32_t* row_pos, const float* weights,
+                               void* out, void* stream) {
+  const char* fn = "mxfp8_moe_combine";
+  mxfp8_status st = check_join(fn, type, T, R, H, top_k);
+  if (st != MXFP8_OK) return st;
+  if (T == 0) return ok();
+  REQUIRE(row_pos && out && (y || R == 0), "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(y, 2) && aligned_to(out, 2) && aligned_to(row_pos, 4) &&
+              aligned_to(weights, 4),
+          "%s: a pointer is not aligned to its element", fn);
+  return hip_status(mx::launch_join(y, type == MXFP8_TYPE_F16, T, R, H, top_k, row_pos, weights,
+                                    out, as_stream(stream)),
+                    fn);
+}
+
+mxfp8_status mxfp8_moe_combine_bwd(const void* dout, const void* y, int32_t type, int64_t T,
+                                   int64_t R, int64_t H, int32_t top_k, const int32_t* row_pos,
+                                   const float* weights, void* dy, float* dweights,
+                                   void* stream) {
+  const char* fn = "mxfp8_moe_combine_bwd";
+  mxfp8_status st = check_join(fn, type, T, R, H, top_k);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(dy != nullptr || dweights != nullptr || R == 0 || T == 0, "%s: no output asked for", fn);
+  if (T == 0 || (dy == nullptr && dweights == nullptr)) return ok();
+  REQUIRE(dout && row_pos && (dweights == nullptr || y || R == 0), "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(dout, 2) && aligned_to(y, 2) && aligned_to(dy, 2) && aligned_to(row_pos, 4) &&
+              aligned_to(weights, 4) && aligned_to(dweights, 4),
+          "%s: a pointer is not aligned to its element", fn);
+  return hip_status(mx::launch_join_bwd(dout, y, type == MXFP8_TYPE_F16, T, R, H, top_k, row_pos,
+                                        weights, dy, dweights, as_stream(stream)),
                     fn);
 }
 

@@ -59,4 +59,26 @@ hipError_t launch_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* sa, const
                                       uint8_t* q_row, uint8_t* s_row, uint8_t* q_col,
                                       uint8_t* s_col, hipStream_t st);
 
+// Products grouped by expert with ragged row counts (ragged.hip); layout and
+// out as in the C header's enums.
+struct RaggedArgs;
+hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st);
+int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G);
+hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,
+                                int8_t* q, float* scale, hipStream_t st);
+// Routing (routing.hip); type: 0 fp32, 1 bf16, 2 fp16.
+size_t route_workspace_bytes(int64_t T, int32_t E);
+hipError_t launch_route(const void* logits, int type, int64_t T, int32_t E, int32_t k, bool renorm,
+                        const uint8_t* mask, int32_t* ids, float* weights, int64_t* m_splits,
+                        int32_t* row_token, int32_t* row_pos, void* ws, hipStream_t st);
+hipError_t launch_route_bwd(const void* logits, int type, int64_t T, int32_t E, int32_t k,
+                            bool renorm, const int32_t* ids, const float* weights,
+                            const float* dweights, void* dlogits, hipStream_t st);
+hipError_t launch_join(const void* y, bool f16, int64_t T, int64_t R, int64_t H, int32_t k,
+                       const int32_t* pos, const float* weights, void* out, hipStream_t st);
+hipError_t launch_join_bwd(const void* dout, const void* y, bool f16, int64_t T, int64_t R,
+                           int64_t H, int32_t k, const int32_t* pos, const float* weights,
+                           void* dy, float* dweights, hipStream_t st);
+
 }  // namespace mx

@@ -1,0 +1,315 @@
+// Products grouped by expert with any number of rows per expert.
+//
+//   forward (NT): C[r, n]    = sum_k X[i(r), k] W[g, n, k]     r a row of expert g
+//   dgrad   (NN): C[r, k]    = sum_n dY[r, n]   W[g, n, k]
+//   wgrad   (TN): C[g, n, k] = sum over rows r of g of dY[r, n] X[i(r), k]
+//
+// i(r) is row_index[r] or r.  Experts own consecutive rows, m_splits[g] of
+// them, read on the device; rows after the last expert's are not touched.
+#include <algorithm>
+
+#include "ragged_common.h"
+
+namespace mx {
+
+// ---------------------------------------------------------------------------
+// Any size, stride and alignment.
+//
+// 128 x 128 output tile, 4 waves of 64 x 64, contraction in steps of 64 bytes.
+// Chunks go through registers: a 16-byte load at element alignment where the
+// whole chunk lies inside the operand, single elements at its edge, zeros
+// outside.  Both operands lie in LDS with the contraction contiguous; an operand whose
+// contraction runs over its rows (W in NN, both in TN) is transposed by the
+// store to LDS.
+// ---------------------------------------------------------------------------
+constexpr int kAnyT = 128;         // tile edge
+constexpr int kAnyBytes = 64;      // contraction bytes per step
+constexpr int kAnyPitch = 80;      // LDS row: 64 bytes + 16, so that 16-byte reads of
+                                   // consecutive rows start in different banks
+
+// Up to 16 bytes from p, the first n elements of them valid (n <= 0: none).
+template <typename E>
+__device__ __forceinline__ u32x4_t load_chunk(const E* p, int64_t n) {
+  constexpr int kN = 16 / sizeof(E);
+  u32x4_t v = {0, 0, 0, 0};
+  if (n >= kN) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (n > 0) {
+    E e[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) e[i] = i < n ? p[i] : (E)0;
+    __builtin_memcpy(&v, e, 16);
+  }
+  return v;
+}
+
+// The row tile `t` (of `tile` rows) among all experts: its expert, first row
+// and row count, from the splits, by the whole workgroup.  Returns false past
+// the last tile.  G <= 1024, 256 threads.
+struct RowTile {
+  int g;
+  int64_t row0;
+  int rows;
+};
+__device__ bool find_row_tile(const int64_t* m_splits, int G, int64_t R, int tile, int64_t t,
+                              RowTile* out, int64_t* lds /* 2 * 256 + 3 */) {
+  const int tid = threadIdx.x;
+  constexpr int per = kRaggedMaxGroups / 256;
+  int64_t rows[per], r_sum = 0, t_sum = 0;
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    const int g = tid * per + i;
+    rows[i] = g < G ? split_rows(m_splits, g, R) : 0;
+    r_sum += rows[i];
+    t_sum += (rows[i] + tile - 1) / tile;
+  }
+  int64_t* sr = lds;
+  int64_t* st = lds + 256;
+  int64_t* found = lds + 512;
+  sr[tid] = r_sum;
+  st[tid] = t_sum;
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int64_t r = tid >= d ? sr[tid - d] : 0, u = tid >= d ? st[tid - d] : 0;
+    __syncthreads();
+    sr[tid] += r;
+    st[tid] += u;
+    __syncthreads();
+  }
+  int64_t r0 = sr[tid] - r_sum, t0 = st[tid] - t_sum;
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    const int64_t nt = (rows[i] + tile - 1) / tile;
+    if (t >= t0 && t < t0 + nt) {
+      const int64_t lo = r0 + (t - t0) * tile;
+      const int64_t hi = r0 + rows[i] < R ? r0 + rows[i] : R;   // never past the rows there are
+      found[0] = tid * per + i;
+      found[1] = lo;
+      found[2] = hi - lo < tile ? hi - lo : tile;
+    }
+    r0 += rows[i];
+    t0 += nt;
+  }
+  __syncthreads();
+  out->g = (int)found[0];
+  out->row0 = found[1];
+  out->rows = (int)found[2];
+  return found[0] >= 0 && found[2] > 0;
+}
+
+// Rows [lo, lo + len) of expert g (TN), clipped to the R rows there are.
+__device__ void expert_rows(const int64_t* m_splits, int g, int64_t R, int64_t* lo, int64_t* len,
+                            int64_t* lds /* 256 */) {
+  const int tid = threadIdx.x;
+  int64_t s = 0;
+  for (int i = tid; i < g; i += 256) s += split_rows(m_splits, i, R);
+  lds[tid] = s;
+  __syncthreads();
+  for (int d = 128; d > 0; d >>= 1) {
+    if (tid < d) lds[tid] += lds[tid + d];
+    __syncthreads();
+  }
+  const int64_t at = lds[0] < R ? lds[0] : R;
+  const int64_t m = split_rows(m_splits, g, R);
+  *lo = at;
+  *len = m < R - at ? m : R - at;
+  __syncthreads();
+}
+
+template <typename T, typename O, int LAYOUT>
+__global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p) {
+  typedef typename T::elem E;
+  constexpr int kPer = 16 / sizeof(E);             // elements of a chunk
+  constexpr int kStep = kAnyBytes / sizeof(E);     // contraction elements per step
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kAnyT * kAnyPitch];
+  __shared__ int64_t scan[2 * 256 + 3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+
+  // the tile: rows [m0, m0 + rows) of A's output dimension, columns from n0
+  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
+  const int64_t nt = (cols + kAnyT - 1) / kAnyT;
+  const int64_t ct = (int64_t)blockIdx.x % nt, rt = (int64_t)blockIdx.x / nt;
+  const int64_t n0 = ct * kAnyT;
+  int g;
+  int64_t m0, rows, con, lo = 0;   // con: contraction length; lo: its first row (TN)
+  if (LAYOUT != 2) {
+    RowTile t;
+    if (!find_row_tile(p.m_splits, p.G, p.R, kAnyT, rt, &t, scan)) return;
+    g = t.g;
+    m0 = t.row0;
+    rows = t.rows;
+    con = LAYOUT == 0 ? p.K : p.N;
+  } else {
+    const int64_t mt = (p.N + kAnyT - 1) / kAnyT;
+    g = (int)(rt / mt);
+    m0 = (rt % mt) * kAnyT;
+    rows = p.N - m0 < kAnyT ? p.N - m0 : kAnyT;
+    expert_rows(p.m_splits, g, p.R, &lo, &con, scan);
+  }
+
+  // this thread's chunks: two of each operand.  Contraction contiguous: row
+  // (tid >> 2) + 64 i, chunk tid & 3.  Contraction over rows: contraction
+  // row (tid >> 4) + 16 i, 8 columns from 8 (tid & 15).
+  const E* a = (const E*)p.a;
+  const E* b = (const E*)p.b;
+  if (LAYOUT != 2) b += (int64_t)g * p.N * p.K;
+  u32x4_t ra[2], rb[2];
+  auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (LAYOUT != 2) {
+        const int r = (tid >> 2) + 64 * i;
+        const int64_t k = k0 + (tid & 3) * kPer;
+        int64_t n = r < rows ? con - k : 0;
+        int64_t row = m0 + r;
+        if (LAYOUT == 0 && p.row_index != nullptr) {
+          row = n > 0 ? p.row_index[row] : 0;
+          if (row < 0 || row >= p.S) n = 0, row = 0;
+        }
+        ra[i] = load_chunk<E>(a + row * p.lda + k, n);
+      } else {
+        const int64_t k = k0 + (tid >> 4) + 16 * i;
+        const int64_t c = (tid & 15) * 8;
+        ra[i] = load_chunk<E>(a + (lo + k) * p.lda + m0 + c, k < con ? p.N - m0 - c : 0);
+      }
+      if (LAYOUT == 0) {
+        const int64_t r = n0 + (tid >> 2) + 64 * i;
+        const int64_t k = k0 + (tid & 3) * kPer;
+        rb[i] = load_chunk<E>(b + r * p.K + k, r < p.N ? con - k : 0);
+      } else {
+        const int64_t k = k0 + (tid >> 4) + 16 * i;
+        const int64_t c = n0 + (tid & 15) * 8;
+        int64_t n = k < con ? p.K - c : 0;
+        int64_t row = lo + k;
+        if (LAYOUT == 2 && p.row_index != nullptr) {
+          row = n > 0 ? p.row_index[row] : 0;
+          if (row < 0 || row >= p.S) n = 0, row = 0;
+        }
+        rb[i] = load_chunk<E>(b + row * (LAYOUT == 2 ? p.ldb : p.K) + c, n);
+      }
+    }
+  };
+  uint8_t* la = smem;
+  uint8_t* lb = smem + kAnyT * kAnyPitch;
+  auto put = [&](uint8_t* at, u32x4_t v, int i, bool over_rows) {
+    if (!over_rows) {
+      *(u32x4_t*)(at + ((tid >> 2) + 64 * i) * kAnyPitch + (tid & 3) * 16) = v;
+    } else {
+      E e[kPer];
+      __builtin_memcpy(e, &v, 16);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        *(E*)(at + ((tid & 15) * 8 + j) * kAnyPitch + ((tid >> 4) + 16 * i) * sizeof(E)) = e[j];
+    }
+  };
+
+  typename T::acc acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i >> 1][i & 1][r] = 0;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const uint8_t* fa = la + (wm + (lane & 31)) * kAnyPitch + (lane >> 5) * 16;
+  const uint8_t* fb = lb + (wn + (lane & 31)) * kAnyPitch + (lane >> 5) * 16;
+
+  if (con > 0) fetch(0);
+  for (int64_t k0 = 0; k0 < con; k0 += kStep) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      put(la, ra[i], i, LAYOUT == 2);
+      put(lb, rb[i], i, LAYOUT != 0);
+    }
+    __syncthreads();
+    if (k0 + kStep < con) fetch(k0 + kStep);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4_t va[2], vb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        va[i] = *(const u32x4_t*)(fa + i * 32 * kAnyPitch + s * 32);
+        vb[i] = *(const u32x4_t*)(fb + i * 32 * kAnyPitch + s * 32);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = T::mma(va[i], vb[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+
+  // accumulator r of a 32 x 32 block in lane l: row 8 (r / 4) + 4 (l / 32) + r % 4,
+  // column l % 32
+  typename O::elem* c = (typename O::elem*)p.c;
+  const int64_t ldc = LAYOUT == 2 ? p.K : p.ldc;
+  c += LAYOUT == 2 ? ((int64_t)g * p.N + m0) * p.K : m0 * ldc;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = n0 + wn + 32 * j + (lane & 31);
+      float sb = 1.f;
+      if (sizeof(E) == 1 && n < cols) sb = p.sb[(int64_t)g * p.N + n];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int m = wm + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + (r & 3);
+        if (m < rows && n < cols) {
+          float v = (float)acc[i][j][r];
+          if (sizeof(E) == 1) {
+            int64_t row = m0 + m;
+            if (p.row_index != nullptr) row = p.row_index[row];
+            v = row >= 0 && row < p.S ? v * p.sa[row] * sb : 0.f;
+          }
+          c[m * ldc + n] = O::cvt(v);
+        }
+      }
+    }
+}
+
+namespace {
+
+template <typename T, typename O, int LAYOUT>
+hipError_t launch_any(const RaggedArgs& p, hipStream_t st) {
+  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
+  const int64_t nt = (cols + kAnyT - 1) / kAnyT;
+  // an expert's last tile may be partial: at most one more tile for each
+  // expert that has rows
+  const int64_t rt = LAYOUT == 2 ? p.G * ((p.N + kAnyT - 1) / kAnyT)
+                                 : p.R / kAnyT + std::min<int64_t>(p.G, p.R);
+  ragged_any_kernel<T, O, LAYOUT><<<dim3((uint32_t)(nt * rt)), dim3(256), 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t launch_layout(int layout, const RaggedArgs& p, hipStream_t st) {
+  if (layout == 0) return launch_any<T, O, 0>(p, st);
+  if (layout == 1) return launch_any<T, O, 1>(p, st);
+  return launch_any<T, O, 2>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p,
+                              hipStream_t st) {
+  if (f16) {
+    if (out == 0) return launch_layout<TypeF16, OutF32>(layout, p, st);
+    return launch_layout<TypeF16, OutF16>(layout, p, st);
+  }
+  if (out == 0) return launch_layout<TypeBf16, OutF32>(layout, p, st);
+  return launch_layout<TypeBf16, OutBf16>(layout, p, st);
+}
+
+hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st) {
+  if (out == 0) return launch_any<TypeI8, OutF32, 0>(p, st);
+  if (out == 1) return launch_any<TypeI8, OutBf16, 0>(p, st);
+  return launch_any<TypeI8, OutF16, 0>(p, st);
+}
+
+// Workgroups that any call may launch at most (the grid's limit).
+int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G) {
+  const int64_t cols = ((layout == 0 ? N : K) + kAnyT - 1) / kAnyT;
+  return cols * (layout == 2 ? (int64_t)G * ((N + kAnyT - 1) / kAnyT)
+                             : R / kAnyT + std::min<int64_t>(G, R));
+}
+
+}  // namespace mx

@@ -1,0 +1,664 @@
+// Routing around the experts' products: the k best experts of each token and
+// their weights, the order of the rows by expert, the weighted sum of the
+// experts' rows, and the gradients of both.
+//
+//   choice   the top_k largest logits of a token, equal ones by lowest index;
+//            -inf and NaN are never chosen, masked tokens choose nothing
+//   weights  w_j = exp(l_j - max) / Z, Z over the chosen experts (renormalize)
+//            or over all of them
+//   order    rows of expert 0, then expert 1, ...; by token within an expert
+//   gradient renormalize: dl_j = w_j (dw_j - sum_i w_i dw_i) at the chosen
+//            experts, 0 elsewhere; otherwise dl_e = p_e (d_e - sum_i w_i dw_i)
+//            with d_e = dw_j where e is choice j, else 0
+//   join     out[t] = sum_j w[t, j] y[pos[t, j]]; dy[pos[t, j]] = w[t, j] dout[t];
+//            dw[t, j] = <y[pos[t, j]], dout[t]>
+//
+// Nothing here depends on the order in which workgroups or atomics run: the
+// only atomics set bits.
+#include <algorithm>
+
+#include "ragged_common.h"
+
+namespace mx {
+
+constexpr int kRouteThreads = 1024;
+constexpr int kMaxTopK = 16;
+constexpr int kMaxChunk = 512;      // tokens of a workgroup at most
+
+// Element i of a 16- or 32-bit floating tensor as fp32.  type: 0 fp32, 1 bf16, 2 fp16.
+template <int TYPE>
+__device__ __forceinline__ float load_float(const void* p, int64_t i) {
+  if (TYPE == 0) return ((const float*)p)[i];
+  if (TYPE == 1) return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+  return (float)((const _Float16*)p)[i];
+}
+template <int TYPE>
+__device__ __forceinline__ void store_float(void* p, int64_t i, float v) {
+  if (TYPE == 0) ((float*)p)[i] = v;
+  else if (TYPE == 1) ((__bf16*)p)[i] = (__bf16)v;
+  else ((_Float16*)p)[i] = (_Float16)v;
+}
+
+// Reductions over the L consecutive lanes (L a power of two) that share a token.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ int lanes_min(int v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v = min(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+struct RouteArgs {
+  const void* logits;       // [T, E]
+  const uint8_t* mask;      // [T] or NULL; 0: the token is not routed
+  int64_t T;
+  int32_t E, k, renorm;
+  int32_t chunk;            // tokens of a workgroup, a multiple of 32
+  int32_t blocks;
+  int32_t* ids;             // [T, k]
+  float* weights;           // [T, k]
+  int64_t* m_splits;        // [E]
+  int32_t* row_token;       // [T k]
+  int32_t* row_pos;         // [T, k]
+  uint16_t* hist;           // workspace [blocks, E]: rows of each expert in a chunk
+};
+
+// A token's logits, E / L (rounded up) in each of its L lanes: lane s holds
+// experts s, s + L, ...  NaN and what lies past E become -inf.
+template <int TYPE, int L, int V>
+__device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int sub,
+                                            bool on, float* v) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = sub + i * L;
+    const float x = on && e < E ? load_float<TYPE>(logits, t * E + e) : -INFINITY;
+    v[i] = x == x ? x : -INFINITY;
+  }
+}
+
+// Choice and weights of one workgroup's tokens, and which tokens of the chunk
+// each expert got (bits[e * words + t / 32]).
+template <int TYPE, int L, int V>
+__device__ void choose(const RouteArgs& p, int64_t t0, int n, uint32_t* bits) {
+  constexpr int kTokens = kRouteThreads / L;   // tokens at a time
+  const int sub = threadIdx.x % L, words = p.chunk / 32;
+  for (int base = 0; base < n; base += kTokens) {
+    const int at = base + (int)threadIdx.x / L;
+    const int64_t t = t0 + at;
+    const bool on = at < n && (p.mask == nullptr || p.mask[t] != 0);
+    float v[V];
+    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on, v);
+    float top = -INFINITY, sum = 0.f, mine_w = 0.f;
+    int mine_id = -1;
+    float all = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+      float best = v[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = fmaxf(best, v[i]);
+      best = lanes_max<L>(best);
+      int id = INT32_MAX;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (v[i] == best) id = sub + i * L;
+      id = lanes_min<L>(id);
+      const bool live = best > -INFINITY;
+      if (j == 0) {
+        top = live ? best : 0.f;
+        if (!p.renorm) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) all += expf(v[i] - top);
+          all = lanes_sum<L>(all);
+        }
+      }
+      const float w = live ? expf(best - top) : 0.f;
+      sum += w;
+      // the chosen one leaves
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (live && id == sub + i * L) v[i] = -INFINITY;
+      if (live && sub == 0) atomicOr(&bits[id * words + at / 32], 1u << (at & 31));
+      // lane j % L keeps choice j (k <= 16 <= L)
+      if (sub == j) {
+        mine_w = w;
+        mine_id = live ? id : -1;
+      }
+    }
+    const float z = p.renorm ? sum : all;
+    if (at < n && sub < p.k) {
+      p.ids[t * p.k + sub] = mine_id;
+      p.weights[t * p.k + sub] = mine_id >= 0 ? mine_w / z : 0.f;
+    }
+  }
+}
+
+// Exclusive prefix over the experts of total[0..E), by the whole workgroup
+// (E <= 1024 threads); returns the total of all.  scan: 1024 words of LDS.
+__device__ int prefix_experts(int mine, int* scan) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  int v = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  if (lane == 63) scan[tid >> 6] = v;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < (tid >> 6); ++w) before += scan[w];
+  return before + v - mine;
+}
+
+// Rows of this chunk: position base[e] + the number of earlier tokens of the
+// chunk that chose e.
+__device__ void place(const RouteArgs& p, int64_t t0, int n, const uint32_t* bits,
+                      const int* base) {
+  const int words = p.chunk / 32;
+  for (int i = threadIdx.x; i < n * p.k; i += kRouteThreads) {
+    const int at = i / p.k;
+    const int64_t c = t0 * p.k + i;
+    const int id = p.ids[c];
+    int pos = -1;
+    if (id >= 0) {
+      const uint32_t* b = bits + id * words;
+      int rank = __popc(b[at / 32] & ((1u << (at & 31)) - 1u));
+      for (int w = 0; w < at / 32; ++w) rank += __popc(b[w]);
+      pos = base[id] + rank;
+      p.row_token[pos] = (int32_t)(t0 + at);
+    }
+    p.row_pos[c] = pos;
+  }
+}
+
+// LDS: bits [E * words], then base [E].
+extern __shared__ uint32_t route_lds[];
+
+// One workgroup for all tokens (T <= chunk): everything in one launch.
+template <int TYPE, int L, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_one_kernel(RouteArgs p) {
+  __shared__ int scan[16], routed;
+  const int tid = threadIdx.x, words = p.chunk / 32;
+  uint32_t* bits = route_lds;
+  int* base = (int*)(route_lds + p.E * words);
+  for (int i = tid; i < p.E * words; i += kRouteThreads) bits[i] = 0;
+  __syncthreads();
+  choose<TYPE, L, V>(p, 0, (int)p.T, bits);
+  __syncthreads();
+  int mine = 0;
+  if (tid < p.E)
+    for (int w = 0; w < words; ++w) mine += __popc(bits[tid * words + w]);
+  const int at = prefix_experts(mine, scan);
+  if (tid < p.E) {
+    base[tid] = at;
+    p.m_splits[tid] = mine;
+  }
+  if (tid == p.E - 1) routed = at + mine;
+  __syncthreads();
+  place(p, 0, (int)p.T, bits, base);
+  for (int64_t i = routed + tid; i < p.T * p.k; i += kRouteThreads) p.row_token[i] = -1;
+}
+
+// Several workgroups: choice and the chunk's counts, then, in a second launch
+// that sees all counts, the positions.
+template <int TYPE, int L, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs p) {
+  const int tid = threadIdx.x, words = p.chunk / 32;
+  const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+  const int n = (int)min((int64_t)p.chunk, p.T - t0);
+  for (int i = tid; i < p.E * words; i += kRouteThreads) route_lds[i] = 0;
+  __syncthreads();
+  choose<TYPE, L, V>(p, t0, n, route_lds);
+  __syncthreads();
+  if (tid < p.E) {
+    int mine = 0;
+    for (int w = 0; w < words; ++w) mine += __popc(route_lds[tid * words + w]);
+    p.hist[(int64_t)blockIdx.x * p.E + tid] = (uint16_t)mine;
+  }
+}
+
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs p) {
+  __shared__ int scan[16], routed;
+  __shared__ int part[2][kRouteThreads];
+  const int tid = threadIdx.x, words = p.chunk / 32;
+  uint32_t* bits = route_lds;
+  int* base = (int*)(route_lds + p.E * words);
+  const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+  const int n = (int)min((int64_t)p.chunk, p.T - t0);
+  for (int i = tid; i < p.E * words; i += kRouteThreads) bits[i] = 0;
+  // counts of every chunk: slice s of the workgroup sums chunks s, s + slices, ...
+  // for its expert, apart for all chunks and for those before this one
+  const int slices = max(1, kRouteThreads / p.E), s = tid / p.E, e = tid % p.E;
+  int all = 0, before = 0;
+  if (s < slices)
+    for (int b = s; b < p.blocks; b += slices) {
+      const int h = p.hist[(int64_t)b * p.E + e];
+      all += h;
+      if (b < (int)blockIdx.x) before += h;
+    }
+  part[0][tid] = all;
+  part[1][tid] = before;
+  __syncthreads();
+  for (int i = tid; i < n * p.k; i += kRouteThreads) {
+    const int id = p.ids[t0 * p.k + i], at = i / p.k;
+    if (id >= 0) atomicOr(&bits[id * words + at / 32], 1u << (at & 31));
+  }
+  all = before = 0;
+  if (tid < p.E)
+    for (int i = 0; i < slices; ++i) {
+      all += part[0][i * p.E + tid];
+      before += part[1][i * p.E + tid];
+    }
+  const int at = prefix_experts(all, scan);
+  if (tid < p.E) {
+    base[tid] = at + before;
+    if (blockIdx.x == 0) p.m_splits[tid] = all;
+  }
+  if (tid == p.E - 1) routed = at + all;
+  __syncthreads();
+  place(p, t0, n, bits, base);
+  for (int64_t i = routed + (int64_t)blockIdx.x * kRouteThreads + tid; i < p.T * p.k;
+       i += (int64_t)gridDim.x * kRouteThreads)
+    p.row_token[i] = -1;
+}
+
+struct RouteBwdArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* weights;
+  const float* dweights;
+  void* dlogits;
+  int64_t T;
+  int32_t E, k, renorm;
+};
+
+template <int TYPE, int L, int V>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
+  const int sub = threadIdx.x % L;
+  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const bool on = t < p.T;
+  // lane j holds choice j
+  int id = -1;
+  float w = 0.f, d = 0.f;
+  if (on && sub < p.k) {
+    id = p.ids[t * p.k + sub];
+    if (id >= 0) {
+      w = p.weights[t * p.k + sub];
+      d = p.dweights[t * p.k + sub];
+    }
+  }
+  const float inner = lanes_sum<L>(w * d);
+  float g[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) g[i] = 0.f;
+  const int first = __shfl(id, (threadIdx.x & 63) / L * L, 64);
+  if (!p.renorm) {
+    float v[V];
+    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on && first >= 0, v);
+    float top = v[0], sum = 0.f;
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = fmaxf(top, v[i]);
+    top = lanes_max<L>(top);
+    if (!(top > -INFINITY)) top = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += v[i] = expf(v[i] - top);
+    sum = lanes_sum<L>(sum);
+    if (first >= 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = -inner * (v[i] / sum);
+    }
+  }
+  const float add = p.renorm ? w * (d - inner) : w * d;
+  for (int j = 0; j < p.k; ++j) {
+    const int src = (threadIdx.x & 63) / L * L + j;
+    const int ej = __shfl(id, src, 64);
+    const float aj = __shfl(add, src, 64);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ej == sub + i * L) g[i] += aj;
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = sub + i * L;
+    if (e < p.E) store_float<TYPE>(p.dlogits, t * p.E + e, g[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The experts' rows joined for each token.
+// ---------------------------------------------------------------------------
+constexpr int kJoinWidth = 8;   // values of a thread at a time (16 bytes)
+
+struct JoinArgs {
+  const void* y;            // [R, H]
+  const void* dout;         // [T, H]
+  const int32_t* pos;       // [T, k]
+  const float* weights;     // [T, k] or NULL (all 1)
+  void* out;                // [T, H]; backward: dy [R, H] or NULL
+  float* dweights;          // [T, k] or NULL
+  int64_t T, R, H;
+  int32_t k;
+};
+
+template <int TYPE>
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
+  uint16_t e[kJoinWidth];
+  if (n == kJoinWidth) {
+    __builtin_memcpy(e, p, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kJoinWidth; ++i) e[i] = i < n ? p[i] : (uint16_t)0;
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinWidth; ++i) v[i] = load_float<TYPE>(e, i);
+}
+template <int TYPE>
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float* v) {
+  uint16_t e[kJoinWidth];
+#pragma unroll
+  for (int i = 0; i < kJoinWidth; ++i) store_float<TYPE>(e, i, v[i]);
+  if (n == kJoinWidth) {
+    __builtin_memcpy(p, e, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kJoinWidth; ++i)
+      if (i < n) p[i] = e[i];
+  }
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
+  const int64_t chunks = (p.H + kJoinWidth - 1) / kJoinWidth;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.T * chunks) return;
+  const int64_t t = i / chunks, h = i % chunks * kJoinWidth;
+  const int n = (int)min((int64_t)kJoinWidth, p.H - h);
+  float sum[kJoinWidth] = {};
+  for (int j = 0; j < p.k; ++j) {
+    const int64_t row = p.pos[t * p.k + j];
+    if (row < 0 || row >= p.R) continue;
+    const float w = p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
+    float v[kJoinWidth];
+    load8<TYPE>((const uint16_t*)p.y + row * p.H + h, n, v);
+#pragma unroll
+    for (int e = 0; e < kJoinWidth; ++e) sum[e] += w * v[e];
+  }
+  store8<TYPE>((uint16_t*)p.out + t * p.H + h, n, sum);
+}
+
+// One workgroup per token.
+template <int TYPE>
+__global__ __launch_bounds__(256) void join_bwd_kernel(JoinArgs p) {
+  __shared__ float part[4][kMaxTopK];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float dot[kMaxTopK];
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) dot[j] = 0.f;
+  for (int64_t h = (int64_t)threadIdx.x * kJoinWidth; h < p.H; h += 256 * kJoinWidth) {
+    const int n = (int)min((int64_t)kJoinWidth, p.H - h);
+    float d[kJoinWidth];
+    load8<TYPE>((const uint16_t*)p.dout + t * p.H + h, n, d);
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) {
+      if (j >= p.k) break;
+      const int64_t row = p.pos[t * p.k + j];
+      if (row < 0 || row >= p.R) continue;
+      float v[kJoinWidth];
+      if (p.dweights != nullptr) {
+        load8<TYPE>((const uint16_t*)p.y + row * p.H + h, n, v);
+#pragma unroll
+        for (int e = 0; e < kJoinWidth; ++e) dot[j] += v[e] * d[e];
+      }
+      if (p.out != nullptr) {
+        const float w = p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
+#pragma unroll
+        for (int e = 0; e < kJoinWidth; ++e) v[e] = w * d[e];
+        store8<TYPE>((uint16_t*)p.out + row * p.H + h, n, v);
+      }
+    }
+  }
+  if (p.dweights == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    if (j >= p.k) break;
+    const float s = lanes_sum<64>(dot[j]);
+    if (lane == 0) part[wave][j] = s;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < p.k)
+    p.dweights[t * p.k + threadIdx.x] = (part[0][threadIdx.x] + part[1][threadIdx.x]) +
+                                        (part[2][threadIdx.x] + part[3][threadIdx.x]);
+}
+
+// ---------------------------------------------------------------------------
+// Tokens to 8-bit integers: scale = amax / 127 (fp32, nearest), code = the
+// integer nearest to x / scale (ties to even) in exact arithmetic.  A row of
+// zeros has scale 0 and codes 0; a row with an infinity or NaN scale NaN.
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 256;
+constexpr int kQuantHeld = 4;   // chunks of 8 values a thread keeps: rows up to 8192 are read once
+
+__device__ __forceinline__ int code_int8(float x, float scale, float inv) {
+  // The product with the reciprocal is within 2 units in the last place of
+  // the quotient, so its nearest integer q is the right one or a neighbour
+  // across a border.  x - q scale is exact in one fused multiply-add (both are
+  // multiples of the last place of scale, the difference is at most about
+  // scale), and tells on which side of the border, or on it, x lies.
+  float q = rintf(x * inv);
+  const float r = __builtin_fmaf(-q, scale, x);
+  const float half = 0.5f * scale;
+  const bool odd = ((int)q & 1) != 0;
+  if (r > half || (r == half && odd)) q += 1.f;
+  else if (r < -half || (r == -half && odd)) q -= 1.f;
+  return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kQuantThreads) void quantize_int8_kernel(const void* x, int64_t ldx,
+                                                                      int64_t K, int8_t* q,
+                                                                      float* scale) {
+  __shared__ uint32_t part[kQuantThreads / 64];
+  const int64_t row = blockIdx.x;
+  const uint16_t* src = (const uint16_t*)x + row * ldx;
+  int8_t* dst = q + row * K;
+  const int64_t step = kQuantThreads * 8;
+  // the largest magnitude, compared as bits: infinities and NaN lie above all
+  uint32_t top = 0;
+  float held[kQuantHeld][8];
+  int64_t h = (int64_t)threadIdx.x * 8;
+#pragma unroll
+  for (int c = 0; c < kQuantHeld; ++c, h += step) {
+    if (h >= K) break;
+    load8<TYPE>(src + h, (int)min((int64_t)8, K - h), held[c]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(held[c][e]) & 0x7FFFFFFFu);
+  }
+  for (; h < K; h += step) {
+    float v[8];
+    load8<TYPE>(src + h, (int)min((int64_t)8, K - h), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 64; ++w) top = max(top, part[w]);
+  const float s = top >= 0x7F800000u ? NAN : __fdiv_rn(__uint_as_float(top), 127.f);
+  const bool none = !(s > 0.f);
+  // tiny scales are worked with 2^64 larger, values and all: the reciprocal
+  // of a subnormal overflows
+  const float up = s < 0x1p-90f ? 0x1p64f : 1.f;
+  const float su = s * up;
+  const float inv = none ? 0.f : 1.f / su;
+  if (threadIdx.x == 0) scale[row] = s;
+  auto put = [&](int64_t at, const float* v) {
+    const int n = (int)min((int64_t)8, K - at);
+    int8_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = none ? 0 : (int8_t)code_int8(v[e] * up, su, inv);
+    if (n == 8) {
+      __builtin_memcpy(dst + at, c, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) dst[at + e] = c[e];
+    }
+  };
+  h = (int64_t)threadIdx.x * 8;
+#pragma unroll
+  for (int c = 0; c < kQuantHeld; ++c, h += step) {
+    if (h >= K) break;
+    put(h, held[c]);
+  }
+  for (; h < K; h += step) {
+    float v[8];
+    load8<TYPE>(src + h, (int)min((int64_t)8, K - h), v);
+    put(h, v);
+  }
+}
+
+namespace {
+
+// Tokens of a workgroup: about 256 workgroups, 64 to 512 tokens each
+// at most, and at most 32 KiB of bits (chunk * E / 8 bytes).
+int route_chunk(int64_t T, int32_t E) {
+  const int64_t per = (T + 255) / 256;
+  const int64_t most = std::min<int64_t>(kMaxChunk, (1 << 18) / E / 32 * 32);
+  return (int)std::min<int64_t>(std::max<int64_t>((per + 63) / 64 * 64, 64), most);
+}
+// Tokens that one workgroup alone takes: the second launch of the other form
+// costs about as much as these.
+constexpr int64_t kOneLaunch = 256;
+
+template <int TYPE, int L, int V>
+hipError_t launch_route_lv(RouteArgs p, hipStream_t st) {
+  const bool one = p.T <= kOneLaunch;
+  p.chunk = one ? (int)std::max<int64_t>((p.T + 31) / 32 * 32, 32) : route_chunk(p.T, p.E);
+  p.blocks = (int)((p.T + p.chunk - 1) / p.chunk);
+  const size_t bits = (size_t)p.E * (p.chunk / 32) * 4, lds = bits + (size_t)p.E * 4;
+  if (one) {
+    route_one_kernel<TYPE, L, V><<<1, kRouteThreads, lds, st>>>(p);
+  } else {
+    route_choose_kernel<TYPE, L, V><<<p.blocks, kRouteThreads, bits, st>>>(p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    route_place_kernel<<<p.blocks, kRouteThreads, lds, st>>>(p);
+  }
+  return hipGetLastError();
+}
+
+template <int TYPE, int L, int V>
+hipError_t launch_bwd_lv(const RouteBwdArgs& p, hipStream_t st) {
+  const int64_t per = 256 / L;
+  route_bwd_kernel<TYPE, L, V><<<(uint32_t)((p.T + per - 1) / per), 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+// 16 lanes for a token up to 256 experts (4 tokens a wave, short reductions),
+// a whole wave above.
+#define MX_ROUTE_PICK(FN, TYPE, P)                        \
+  (P).E <= 16    ? FN<TYPE, 16, 1>(P, st)                 \
+  : (P).E <= 64  ? FN<TYPE, 16, 4>(P, st)                 \
+  : (P).E <= 128 ? FN<TYPE, 16, 8>(P, st)                 \
+  : (P).E <= 256 ? FN<TYPE, 16, 16>(P, st)                \
+  : (P).E <= 512 ? FN<TYPE, 64, 8>(P, st)                 \
+                 : FN<TYPE, 64, 16>(P, st)
+
+}  // namespace
+
+size_t route_workspace_bytes(int64_t T, int32_t E) {
+  if (T <= kOneLaunch || E <= 0) return 0;
+  const int64_t c = route_chunk(T, E);
+  return (size_t)((T + c - 1) / c) * (size_t)E * sizeof(uint16_t);
+}
+
+hipError_t launch_route(const void* logits, int type, int64_t T, int32_t E, int32_t k, bool renorm,
+                        const uint8_t* mask, int32_t* ids, float* weights, int64_t* m_splits,
+                        int32_t* row_token, int32_t* row_pos, void* ws, hipStream_t st) {
+  RouteArgs p{};
+  p.logits = logits;
+  p.mask = mask;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.renorm = renorm;
+  p.ids = ids;
+  p.weights = weights;
+  p.m_splits = m_splits;
+  p.row_token = row_token;
+  p.row_pos = row_pos;
+  p.hist = (uint16_t*)ws;
+  if (type == 0) return MX_ROUTE_PICK(launch_route_lv, 0, p);
+  if (type == 1) return MX_ROUTE_PICK(launch_route_lv, 1, p);
+  return MX_ROUTE_PICK(launch_route_lv, 2, p);
+}
+
+hipError_t launch_route_bwd(const void* logits, int type, int64_t T, int32_t E, int32_t k,
+                            bool renorm, const int32_t* ids, const float* weights,
+                            const float* dweights, void* dlogits, hipStream_t st) {
+  RouteBwdArgs p{logits, ids, weights, dweights, dlogits, T, E, k, renorm};
+  if (type == 0) return MX_ROUTE_PICK(launch_bwd_lv, 0, p);
+  if (type == 1) return MX_ROUTE_PICK(launch_bwd_lv, 1, p);
+  return MX_ROUTE_PICK(launch_bwd_lv, 2, p);
+}
+
+hipError_t launch_join(const void* y, bool f16, int64_t T, int64_t R, int64_t H, int32_t k,
+                       const int32_t* pos, const float* weights, void* out, hipStream_t st) {
+  JoinArgs p{};
+  p.y = y;
+  p.pos = pos;
+  p.weights = weights;
+  p.out = out;
+  p.T = T;
+  p.R = R;
+  p.H = H;
+  p.k = k;
+  const int64_t n = T * ((H + kJoinWidth - 1) / kJoinWidth);
+  const uint32_t blocks = (uint32_t)((n + 255) / 256);
+  if (f16) join_kernel<2><<<blocks, 256, 0, st>>>(p);
+  else join_kernel<1><<<blocks, 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_join_bwd(const void* dout, const void* y, bool f16, int64_t T, int64_t R,
+                           int64_t H, int32_t k, const int32_t* pos, const float* weights,
+                           void* dy, float* dweights, hipStream_t st) {
+  JoinArgs p{};
+  p.y = y;
+  p.dout = dout;
+  p.pos = pos;
+  p.weights = weights;
+  p.out = dy;
+  p.dweights = dweights;
+  p.T = T;
+  p.R = R;
+  p.H = H;
+  p.k = k;
+  if (f16) join_bwd_kernel<2><<<(uint32_t)T, 256, 0, st>>>(p);
+  else join_bwd_kernel<1><<<(uint32_t)T, 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,
+                                int8_t* q, float* scale, hipStream_t st) {
+  if (f16)
+    quantize_int8_kernel<2><<<(uint32_t)T, kQuantThreads, 0, st>>>(x, ldx, K, q, scale);
+  else
+    quantize_int8_kernel<1><<<(uint32_t)T, kQuantThreads, 0, st>>>(x, ldx, K, q, scale);
+  return hipGetLastError();
+}
+
+}  // namespace mx

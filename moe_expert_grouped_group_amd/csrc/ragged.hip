@@ -287,10 +287,33 @@ hipError_t launch_layout(int layout, const RaggedArgs& p, hipStream_t st) {
   return launch_any<T, O, 2>(p, st);
 }
 
+bool on16(const void* p, int64_t stride_bytes) {
+  return (uintptr_t)p % 16 == 0 && stride_bytes % 16 == 0;
+}
+
+// Whether the large tiles take these operands: rows on 16 bytes, the contiguous
+// contraction and the result's rows multiples of 16 bytes, and lane offsets (256
+// rows, 64 contraction rows, any gathered row) within 32 bits.
+bool ragged_tile_takes(int layout, int esize, int osize, const RaggedArgs& p) {
+  const int64_t ea = p.lda * esize, eb = p.ldb * esize, ec = p.ldc * osize;
+  const int64_t span = (int64_t)kSpan;
+  if (!on16(p.a, ea) || !on16(p.b, eb) || !on16(p.c, ec)) return false;
+  if ((layout == 0 ? p.N : p.K) * osize % 16 != 0) return false;
+  if (256 * ea > span || 256 * eb > span || 256 * ec > span) return false;
+  if (layout == 0 && p.K * esize % 16 != 0) return false;
+  if (layout == 1 && p.N * esize % 16 != 0) return false;
+  if (p.row_index != nullptr && (p.S == 0 || p.S * (layout == 2 ? eb : ea) > span)) return false;
+  return true;
+}
+
 }  // namespace
 
 hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p,
                               hipStream_t st) {
+  if (ragged_tile_takes(layout, 2, out == 0 ? 4 : 2, p))
+    return layout == 0   ? launch_ragged_tile_nt(f16, out, p, st)
+           : layout == 1 ? launch_ragged_tile_nn(f16, out, p, st)
+                         : launch_ragged_tile_tn(f16, out, p, st);
   if (f16) {
     if (out == 0) return launch_layout<TypeF16, OutF32>(layout, p, st);
     return launch_layout<TypeF16, OutF16>(layout, p, st);
@@ -300,6 +323,7 @@ hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p
 }
 
 hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st) {
+  if (ragged_tile_takes(0, 1, out == 0 ? 4 : 2, p)) return launch_ragged_tile_int8(out, p, st);
   if (out == 0) return launch_any<TypeI8, OutF32, 0>(p, st);
   if (out == 1) return launch_any<TypeI8, OutBf16, 0>(p, st);
   return launch_any<TypeI8, OutF16, 0>(p, st);

@@ -33,6 +33,16 @@ struct RaggedArgs {
   int32_t G;
 };
 
+// The large-tile form (ragged_tile.h), by layout.
+hipError_t launch_ragged_tile_nt(bool f16, int out, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_tile_nn(bool f16, int out, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_tile_tn(bool f16, int out, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_tile_int8(int out, const RaggedArgs& p, hipStream_t st);
+
+// Longest range of a bounded operand (32-bit offsets, less what marks a lane that
+// is out of it).
+constexpr uint64_t kSpan = 0xFFFFFE00ull;
+
 // Element types: every one is handled as 16-byte chunks of the contraction
 // (8 values of 16 bits, 16 of 8), which is what one lane hands to one
 // matrix instruction.  Which contraction indices a lane's chunk holds does not

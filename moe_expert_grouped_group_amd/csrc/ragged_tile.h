@@ -1,0 +1,688 @@
+// Large tiles of the products grouped by expert (ragged.hip has the formulas
+// and the form for any alignment): operands whose rows start on 16 bytes.
+//
+// One workgroup per CU walks output tiles of 64 FA x 256; 4 waves, 2 x 2, each
+// 32 FA x 128.  Operands go from memory to LDS without passing registers (buffer
+// loads to LDS, 16 bytes a lane), in stages of 128 contraction bytes (64 values of
+// 16 bits, 128 of 8) in two slots.
+//
+// Two kinds of operand:
+//  * contraction contiguous (X and W in NT, dY in NN): a stage is [rows][128 B],
+//    16-byte chunk c of row r at chunk c ^ (r & 7): the 8 rows that one LDS
+//    access phase reads use 8 different bank groups.
+//  * contraction over rows (W in NN, dY and X in TN): a stage is [64][512 B],
+//    chunk c of row r at chunk c ^ {0, 4, 10, 14}[r & 3].  Fragments come through
+//    the transposing LDS read: in each group of 16 lanes, lane l hands in the
+//    address of 4 columns of contraction row l / 4 and gets 4 contraction rows
+//    of column l.  The 4 rows x 32 columns of 32 lanes lie in 256 different
+//    bytes of bank space.
+// What lies outside an operand (rows past an expert's in TN, past N in
+// NN, past K in a last stage, row indexes out of range) is zero because the
+// buffer loads are bounded: such a lane's offset fails the range check and the
+// load writes zeros.  Rows of other experts that a tile of NT or NN takes along
+// reach only result rows that are not stored.
+//
+// The matrix instructions take the column operand first, so that a lane holds
+// 4 consecutive columns of one row and stores 16 bytes at a time.
+#pragma once
+
+#include <type_traits>
+
+#include "ragged_common.h"
+
+namespace mx {
+
+constexpr int kTileN = 256;
+constexpr int kStageK = 128;                     // contraction bytes of a stage
+constexpr uint32_t kOut = 0xFFFFFF00u;           // a lane offset that no range check passes
+
+typedef __attribute__((address_space(3))) const u32x4_t lds_u32x4_t;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// Buffer load to LDS: lane i writes LDS bytes [lds + 16 i, lds + 16 i + 16) (4 for
+// the dword form) from rsrc's base + voff + soff, zeros where the range check
+// fails.  Inline assembly so that the compiler's counters do not see it: the
+// explicit waits below order the copies.  One wait state between the write of
+// M0 and its use.
+__device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(rsrc), "s"(soff)
+               : "m0", "memory");
+}
+__device__ __forceinline__ void copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(rsrc), "s"(soff)
+               : "m0", "memory");
+}
+
+__device__ __forceinline__ i32x4 bounded(const void* base, int64_t bytes) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  const uint64_t n = bytes < 0 ? 0 : ((uint64_t)bytes < kSpan ? (uint64_t)bytes : kSpan);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu));
+  r[2] = __builtin_amdgcn_readfirstlane((int)(uint32_t)n);
+  r[3] = 0x00020000;
+  return r;
+}
+
+// The same range for the compiler's buffer loads and stores.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  const uint64_t n = bytes < 0 ? 0 : ((uint64_t)bytes < kSpan ? (uint64_t)bytes : kSpan);
+  const uint64_t u = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32) |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)u, 0,
+                                           __builtin_amdgcn_readfirstlane((int)(uint32_t)n), 0x00020000);
+}
+
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unroll(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unroll<N, I + 1>(f);
+  }
+}
+
+__device__ __forceinline__ uint32_t hide(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kLgkmWait0 = 0xC07F;
+
+// Prefix sums of the experts' row tiles and rows.
+struct RaggedTable {
+  int32_t tiles[kRaggedMaxGroups + 1];
+  int32_t rows[kRaggedMaxGroups + 1];
+};
+__device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int G, int64_t R,
+                                                   int tile, RaggedTable* t, int32_t* scan) {
+  const int tid = threadIdx.x;
+  constexpr int per = kRaggedMaxGroups / 256;
+  int64_t rows[per], rs = 0;
+  int32_t ts = 0;
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    const int g = tid * per + i;
+    rows[i] = g < G ? split_rows(m_splits, g, R) : 0;
+    rs += rows[i];
+  }
+  // rows before this thread's experts, cut at R (sums of up to 1024 splits of at
+  // most R each, in 64 bits)
+  int64_t* s64 = (int64_t*)scan;
+  s64[tid] = rs;
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int64_t u = tid >= d ? s64[tid - d] : 0;
+    __syncthreads();
+    s64[tid] += u;
+    __syncthreads();
+  }
+  int64_t r0 = s64[tid] - rs;
+  __syncthreads();
+  int32_t off[per + 1];
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    off[i] = (int32_t)(r0 < R ? r0 : R);
+    r0 += rows[i];
+    off[i + 1] = (int32_t)(r0 < R ? r0 : R);
+    ts += (off[i + 1] - off[i] + tile - 1) / tile;
+  }
+  scan[tid] = ts;
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int32_t u = tid >= d ? scan[tid - d] : 0;
+    __syncthreads();
+    scan[tid] += u;
+    __syncthreads();
+  }
+  int32_t t0 = scan[tid] - ts;
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    t->tiles[tid * per + i] = t0;
+    t->rows[tid * per + i] = off[i];
+    t0 += (off[i + 1] - off[i] + tile - 1) / tile;
+  }
+  if (tid == 255) {
+    t->tiles[kRaggedMaxGroups] = t0;
+    t->rows[kRaggedMaxGroups] = off[per];
+  }
+  __syncthreads();
+}
+
+template <typename T, typename O, int LAYOUT, int FA, bool GATHER>
+__global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
+  typedef typename T::elem E;
+  constexpr bool kInt8 = sizeof(E) == 1;
+  constexpr bool kColA = LAYOUT == 2, kColB = LAYOUT != 0;   // contraction over rows
+  constexpr int kTileM = 64 * FA;
+  constexpr int kOffB = kTileM * kStageK;
+  constexpr int kStage = kOffB + kTileN * kStageK;
+  constexpr int kPartsA = 2 * FA, kParts = kPartsA + 8;      // copies of a wave for a stage
+  constexpr int kMfma = 8 * FA;                              // of a half stage
+  constexpr int kReads = 2 * (FA + 4);
+  constexpr int kEarly = 3 * kParts / 8;                     // copies in the first half
+  constexpr int kStores = sizeof(typename O::elem) == 4 ? 16 * FA : 8 * FA;
+  static_assert(!kColA || FA == 4, "");
+  // row indexes, per wave: TN the 64 of each of 8 stages, NT the wave's rows of
+  // the next tile
+  constexpr int kRing = !GATHER ? 16 : (kColA ? 4 * 8 * 256 : 4 * 256);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRing];
+  __shared__ RaggedTable table;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+  build_ragged_table(p.m_splits, p.G, p.R, kTileM, &table, (int32_t*)smem);
+
+  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
+  const int32_t ctiles = (int32_t)((cols + kTileN - 1) / kTileN);
+  const int32_t band = (int32_t)((p.N + kTileM - 1) / kTileM);           // TN: row tiles of an expert
+  const uint32_t rtiles = kColA ? (uint32_t)p.G * (uint32_t)band
+                                : (uint32_t)__builtin_amdgcn_readfirstlane(table.tiles[kRaggedMaxGroups]);
+  const uint32_t ntiles = rtiles * (uint32_t)ctiles;   // below 2^31 (checked by the caller)
+
+  // Order of the tiles: 8 row tiles by all column tiles at a time, columns
+  // outermost; of each round of the grid, XCD x (workgroups x, x + 8, ...)
+  // takes consecutive ones, so that its 32 workgroups share 8 row and 4 column
+  // panels in its L2.
+  const bool xcd = gridDim.x % 8 == 0;
+  auto place = [&](uint32_t i) -> uint32_t {
+    if (!xcd) return i;
+    const uint32_t b = i % gridDim.x, from = i - b;
+    if (from + gridDim.x > ntiles) return i;   // the last round as it comes
+    return from + (b & 7) * (gridDim.x / 8) + (b >> 3);
+  };
+
+  struct Tile {
+    i32x4 sa, sb;        // bounded operands at contraction 0
+    int64_t na, nb;      // contraction over rows: bytes left of each operand
+    const uint8_t *pa, *pb;
+    int32_t ns;          // stages
+    int32_t len;         // contraction length (TN)
+    int32_t lo;          // first row of the expert (TN), of the tile (NT, NN)
+    int32_t rows;        // rows to store
+    int32_t n0;          // first column
+    int32_t m0;          // first result row
+    int32_t g;
+  };
+  const int64_t ea = p.lda * (int64_t)sizeof(E), eb = p.ldb * (int64_t)sizeof(E);
+  const int64_t con = LAYOUT == 0 ? p.K : p.N;   // NT, NN
+  auto describe = [&](uint32_t i) {
+    Tile t;
+    const uint32_t at = place(i);
+    const uint32_t per = 8u * (uint32_t)ctiles;
+    int32_t mt, nt;
+    if (kColA) {
+      const uint32_t all = (uint32_t)band * (uint32_t)ctiles;
+      t.g = __builtin_amdgcn_readfirstlane((int32_t)(at / all));
+      const uint32_t rem = at % all;
+      const int32_t grp = (int32_t)(rem / per), in = (int32_t)(rem % per);
+      const int32_t wide = min(8, band - 8 * grp);
+      mt = 8 * grp + in % wide;
+      nt = in / wide;
+      t.lo = table.rows[t.g];
+      t.len = table.rows[t.g + 1] - t.lo;
+      t.m0 = mt * kTileM;
+      t.rows = (int32_t)min((int64_t)kTileM, p.N - t.m0);
+      t.n0 = nt * kTileN;
+      t.ns = (int32_t)(((int64_t)t.len * sizeof(E) + kStageK - 1) / kStageK);
+      // columns m0.. of dY and n0.. of X, the expert's rows
+      t.pa = (const uint8_t*)p.a + (int64_t)t.lo * ea + (int64_t)t.m0 * sizeof(E);
+      t.na = t.len == 0 ? 0 : (int64_t)(t.len - 1) * ea + (p.N - t.m0) * (int64_t)sizeof(E);
+      if (GATHER) {
+        t.pb = (const uint8_t*)p.b + (int64_t)t.n0 * sizeof(E);
+        t.nb = p.S == 0 ? 0 : (p.S - 1) * eb + (p.K - t.n0) * (int64_t)sizeof(E);
+      } else {
+        t.pb = (const uint8_t*)p.b + (int64_t)t.lo * eb + (int64_t)t.n0 * sizeof(E);
+        t.nb = t.len == 0 ? 0 : (int64_t)(t.len - 1) * eb + (p.K - t.n0) * (int64_t)sizeof(E);
+      }
+    } else {
+      const int32_t grp = (int32_t)(at / per), in = (int32_t)(at % per);
+      const int32_t wide = min(8, (int32_t)rtiles - 8 * grp);
+      mt = 8 * grp + in % wide;
+      nt = in / wide;
+      int lo = 0, hi = p.G;   // tiles[lo] <= mt < tiles[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (table.tiles[mid] <= mt) lo = mid; else hi = mid;
+      }
+      t.g = lo;
+      t.lo = table.rows[lo] + (mt - table.tiles[lo]) * kTileM;
+      t.m0 = t.lo;
+      t.rows = min(kTileM, table.rows[lo + 1] - t.lo);
+      t.n0 = nt * kTileN;
+      t.len = 0;
+      t.ns = (int32_t)((con * (int64_t)sizeof(E) + kStageK - 1) / kStageK);
+      if (GATHER) {
+        t.pa = (const uint8_t*)p.a;
+        t.na = p.S == 0 ? 0 : (p.S - 1) * ea + con * (int64_t)sizeof(E);
+      } else {
+        t.pa = (const uint8_t*)p.a + (int64_t)t.lo * ea;
+        t.na = (p.R - 1 - t.lo) * ea + con * (int64_t)sizeof(E);
+      }
+      const uint8_t* w = (const uint8_t*)p.b + (int64_t)t.g * p.N * p.K * (int64_t)sizeof(E);
+      if (LAYOUT == 0) {
+        t.pb = w + (int64_t)t.n0 * eb;
+        t.nb = (p.N - 1 - t.n0) * eb + con * (int64_t)sizeof(E);
+      } else {
+        t.pb = w + (int64_t)t.n0 * sizeof(E);
+        t.nb = (p.N - 1) * eb + (p.K - t.n0) * (int64_t)sizeof(E);
+      }
+    }
+    t.sa = bounded(t.pa, t.na);
+    t.sb = bounded(t.pb, t.nb);
+    t.ns = __builtin_amdgcn_readfirstlane(t.ns);
+    t.len = __builtin_amdgcn_readfirstlane(t.len);
+    t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+    t.g = __builtin_amdgcn_readfirstlane(t.g);
+    return t;
+  };
+
+  // Lane offsets of the copies.  Contiguous: part j copies rows 8 (parts wave + j)
+  // + lane / 8, chunk position lane % 8.  Over rows: part j copies contraction
+  // rows 16 wave + 2 j + lane / 32, chunk position lane % 32.
+  const uint32_t chunk_k = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+  auto chunk_c = [&](int j) {
+    const int r = 2 * (j & 1) + (lane >> 5);
+    const int x = (r & 1) * 4 + (r >> 1) * 10;
+    return (uint32_t)((lane & 31) ^ x) * 16;
+  };
+  uint32_t va[kPartsA], vb[8];
+#pragma unroll
+  for (int j = 0; j < kPartsA; ++j)
+    va[j] = kColA ? (uint32_t)((16 * wave + 2 * j + (lane >> 5)) * ea) + chunk_c(j)
+                  : (uint32_t)((8 * (kPartsA * wave + j) + (lane >> 3)) * ea) + chunk_k;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    vb[j] = kColB ? (uint32_t)((16 * wave + 2 * j + (lane >> 5)) * eb) + chunk_c(j)
+                  : (uint32_t)((8 * (8 * wave + j) + (lane >> 3)) * eb) + chunk_k;
+  // contiguous contraction: lanes past its end in the last stage
+  const uint32_t last_bytes = (uint32_t)((con * (int64_t)sizeof(E) - 1) % kStageK) + 1;
+  const uint32_t past = !kColA && chunk_k >= last_bytes ? kOut : 0u;
+
+  // Addresses of the fragments in a stage.
+  uint32_t ra[kColA ? FA : 4], rb[kColB ? 4 : 4];
+  {
+    const int xr = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 1) * 10;
+    auto col = [&](int first) {   // first: the fragment's first column
+      return (uint32_t)(((lane >> 2) & 3) * 512 + (lane >> 5) * 4096 +
+                        (((first >> 3) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ xr) * 16 +
+                        (lane & 1) * 8);
+    };
+    auto row = [&](int first, int s) {
+      return (uint32_t)((first + (lane & 31)) * kStageK + (((2 * s + (lane >> 5)) ^ (lane & 7)) * 16));
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kColA) {
+        if (i < FA) ra[i] = lds0 + col(wm * 32 * FA + 32 * i);
+      } else {
+        ra[i] = lds0 + row(wm * 32 * FA, i);
+      }
+      rb[i] = lds0 + kOffB + (kColB ? col(wn * 128 + 32 * i) : row(wn * 128, i));
+    }
+  }
+  auto transposed = [](uint32_t at) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 2048));
+    const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
+    return u32x4_t{a[0], a[1], b[0], b[1]};
+  };
+
+  typename T::acc acc[FA][4];
+  u32x4_t fa[2][2][FA], fb[2][2][4];
+
+  Tile t;              // the tile whose operands are copied
+  int slot0 = 0;       // slot of the computed tile's stage 0
+  int ring_at = 0;     // place of its stage 0 in the ring of row indexes
+
+  // Row indexes of the gathered operand go to LDS beside the stages: no load
+  // of theirs is waited for.
+  const uint32_t ring0 = (uint32_t)(uintptr_t)ring + (uint32_t)(wave * (kColA ? 2048 : 256));
+  auto copy_index = [&](const Tile& n, int st, int at) {   // TN: stage st of n
+    const i32x4 si = bounded(p.row_index + n.lo + 64 * st, ((int64_t)n.len - 64 * st) * 4);
+    copy4(si, (uint32_t)(lane * 4), 0u, ring0 + (uint32_t)(at & 7) * 256u);
+  };
+  auto copy_rows = [&](const Tile& n) {   // NT: the wave's rows of n
+    const i32x4 si = bounded(p.row_index + n.lo, (int64_t)n.rows * 4);
+    copy4(si, (uint32_t)(lane * 4 + wave * 8 * kPartsA * 4), 0u, ring0);
+  };
+  auto take_rows = [&](const Tile& n) {   // NT: lane offsets from them
+#pragma unroll
+    for (int j = 0; j < kPartsA; ++j) {
+      const uint32_t r = (uint32_t)(8 * j + (lane >> 3));
+      const uint32_t row = *(__attribute__((address_space(3))) const uint32_t*)(ring0 + r * 4);
+      const bool ok = ((int)(8 * kPartsA * wave + r) < n.rows) & (row < (uint32_t)p.S);
+      va[j] = (row * (uint32_t)ea + chunk_k) | (ok ? 0u : kOut);
+    }
+  };
+
+  struct Stage {
+    int st, len, at;
+    uint32_t soff, lds, kill;
+    i32x4 sa, sb;
+  };
+  // Stage st of the copied tile; v: its number counted from the computed tile's
+  // stage 0.
+  auto stage = [&](int st, int v) {
+    const Tile& n = t;
+    // A stage past the last copies zeros: every lane out of range.  The range
+    // check takes soff from the range, so soff must not pass it: it is 0 there,
+    // and within a row otherwise.
+    const bool none = st >= n.ns;
+    Stage s;
+    s.st = st;
+    s.len = none ? 0 : n.len;
+    s.at = ring_at + v;
+    s.lds = lds0 + (uint32_t)(((slot0 + v) & 1) * kStage);
+    s.soff = none ? 0u : (uint32_t)st * kStageK;
+    s.kill = none ? kOut : (st == n.ns - 1 ? past : 0u);
+    s.sa = n.sa;
+    s.sb = n.sb;
+    if (kColA)
+      s.sa = bounded(n.pa + (int64_t)st * 64 * ea, none ? 0 : n.na - (int64_t)st * 64 * ea);
+    if (kColB && !(GATHER && kColA))
+      s.sb = bounded(n.pb + (int64_t)st * 64 * eb, none ? 0 : n.nb - (int64_t)st * 64 * eb);
+    // the same in every lane, which the compiler does not always see
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s.sa[i] = __builtin_amdgcn_readfirstlane(s.sa[i]);
+      s.sb[i] = __builtin_amdgcn_readfirstlane(s.sb[i]);
+    }
+    s.lds = __builtin_amdgcn_readfirstlane(s.lds);
+    s.soff = __builtin_amdgcn_readfirstlane(s.soff);
+    return s;
+  };
+  // copy c of a stage: A and B parts in turn (then what is left of B)
+  auto copy = [&](const Stage& s, auto C) {
+    constexpr int c = decltype(C)::value;
+    constexpr bool isA = c < 2 * kPartsA && c % 2 == 0;
+    constexpr int j = isA ? c / 2 : (c < 2 * kPartsA ? c / 2 : c - kPartsA);
+    if constexpr (isA) {
+      const uint32_t at = s.lds + (uint32_t)(wave * kPartsA * 1024 + j * 1024);
+      copy16(s.sa, kColA ? va[j] : (va[j] | s.kill), kColA ? 0u : s.soff, at);
+    } else {
+      const uint32_t at = s.lds + kOffB + (uint32_t)(wave * 8192 + j * 1024);
+      if constexpr (GATHER && kColA) {
+        // the row index of this lane's contraction row, from the ring
+        const uint32_t r = (uint32_t)(16 * wave + 2 * j) + (uint32_t)(lane >> 5);
+        const uint32_t row = *(__attribute__((address_space(3))) const uint32_t*)(
+            ring0 + (uint32_t)(s.at & 7) * 256u + r * 4);
+        const bool ok = ((int)(s.st * 64 + r) < s.len) & (row < (uint32_t)p.S);
+        copy16(s.sb, (row * (uint32_t)eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
+      } else {
+        copy16(s.sb, kColB ? vb[j] : (vb[j] | s.kill), kColB ? 0u : s.soff, at);
+      }
+    }
+  };
+  // fragment r (0 .. kReads) of half h of a stage into register set h; at: the
+  // slot's offset
+  struct Base {
+    uint32_t a[4], b[4];
+  };
+  auto base = [&](int slot, auto H) {
+    constexpr int h = decltype(H)::value;
+    Base x;
+    const uint32_t off = (uint32_t)slot * kStage;
+#pragma unroll
+    for (int i = 0; i < (kColA ? FA : 2); ++i) x.a[i] = hide(ra[kColA ? i : 2 * h + i] + off);
+#pragma unroll
+    for (int i = 0; i < (kColB ? 4 : 2); ++i) x.b[i] = hide(rb[kColB ? i : 2 * h + i] + off);
+    return x;
+  };
+  auto read = [&](const Base& x, auto H, auto R) {
+    constexpr int h = decltype(H)::value, r = decltype(R)::value;
+    constexpr int s = r / (FA + 4), q = r % (FA + 4);   // step of the half, fragment
+    constexpr bool isA = q < 2 * FA ? q % 2 == 0 : false;
+    constexpr int i = isA ? q / 2 : (q < 2 * FA ? q / 2 : q - FA);
+    if constexpr (isA) {
+      if constexpr (kColA) fa[h][s][i] = transposed(x.a[i] + (2 * h + s) * 8192);
+      else fa[h][s][i] = *(lds_u32x4_t*)(x.a[s] + i * 4096);
+    } else {
+      if constexpr (kColB) fb[h][s][i] = transposed(x.b[i] + (2 * h + s) * 8192);
+      else fb[h][s][i] = *(lds_u32x4_t*)(x.b[s] + i * 4096);
+    }
+  };
+  auto mma = [&](auto H, auto Q) {
+    constexpr int h = decltype(H)::value, q = decltype(Q)::value;
+    constexpr int s = q / (4 * FA), i = q % (4 * FA) / 4, j = q % 4;
+    acc[i][j] = T::mma(fb[h][s][j], fa[h][s][i], acc[i][j]);
+    asm volatile("" : "+a"(acc[i][j]));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using H0 = std::integral_constant<int, 0>;
+  using H1 = std::integral_constant<int, 1>;
+
+  // A tile from the start: its first two stages (and the indexes before them),
+  // waited for, and its first fragments.
+  auto start = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (GATHER && kColA) {
+#pragma unroll
+      for (int st = 0; st < 4; ++st) copy_index(t, st, ring_at + st);
+      __builtin_amdgcn_s_waitcnt(vm_wait(0));
+    }
+    if constexpr (GATHER && !kColA) {
+      copy_rows(t);
+      __builtin_amdgcn_s_waitcnt(vm_wait(0));
+      take_rows(t);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    for (int st = 0; st < 2; ++st) {   // a stage past the last copies zeros
+      const Stage s = stage(st, st);
+      unroll<kParts>([&](auto C) { copy(s, C); });
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vm_wait(0));
+    __syncthreads();
+    const Base x = base(slot0 & 1, H0{});
+    unroll<kReads>([&](auto R) { read(x, H0{}, R); });
+  };
+
+  // First half of a stage: matrix instructions on set 0; the second half's
+  // fragments are read in their first half, then the slot is free (each wave
+  // has waited for its reads) and the copies of the stage two ahead begin.
+  auto first_half = [&](int st, const Stage& cp) {
+    const Base x = base((slot0 + st) & 1, H1{});
+    __builtin_amdgcn_sched_barrier(0);
+    unroll<kMfma>([&](auto Q) {
+      constexpr int q = decltype(Q)::value, m = kMfma / 2;
+      mma(H0{}, Q);
+      unroll<kReads>([&](auto R) {
+        if constexpr (decltype(R)::value * m / kReads == q) read(x, H1{}, R);
+      });
+      if constexpr (q == m) {
+        __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+        __syncthreads();
+      }
+      unroll<kEarly>([&](auto C) {
+        if constexpr (m + 1 + decltype(C)::value * (m - 1) / kEarly == q) copy(cp, C);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // Second half: the next stage has landed (only the copies just begun, and the
+  // stores of the tile before, may be in flight), its first fragments are read,
+  // the rest of the copies go out.
+  auto second_half = [&](int st, const Stage& cp, bool stores) {
+    if (stores) __builtin_amdgcn_s_waitcnt(vm_wait(kStores + kEarly < 63 ? kStores + kEarly : 63));
+    else __builtin_amdgcn_s_waitcnt(vm_wait(kEarly));
+    __syncthreads();
+    const Base x = base((slot0 + st + 1) & 1, H0{});
+    __builtin_amdgcn_sched_barrier(0);
+    unroll<kMfma>([&](auto Q) {
+      constexpr int q = decltype(Q)::value, left = kParts - kEarly;
+      mma(H1{}, Q);
+      unroll<kReads>([&](auto R) {
+        if constexpr (decltype(R)::value * kMfma / kReads == q) read(x, H0{}, R);
+      });
+      unroll<left>([&](auto C) {
+        if constexpr (1 + decltype(C)::value * (kMfma - 2) / left == q)
+          copy(cp, std::integral_constant<int, decltype(C)::value + kEarly>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  uint32_t tile = blockIdx.x;
+  if (tile >= ntiles) return;
+  t = describe(tile);
+  start();
+  bool chained = false;   // the previous tile's last stages carried this one's first two
+
+  for (;;) {
+    const int ns = t.ns;
+    // what the stores need of this tile
+    const int32_t rows = t.rows, n0 = t.n0, m0 = t.m0, g = t.g;
+    const uint32_t next = tile + gridDim.x;
+    // Chain: the last two stages of a tile carry the copies of the next tile's
+    // first two and read its first fragments, as if the contraction went on.
+    // Otherwise they copy nothing (an empty range) and the next tile starts
+    // anew.  The indexes of gathered rows go ahead, from four stages before
+    // the end.
+    bool chain = next < ntiles && ns >= (GATHER ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    for (int st = 0; st < ns; ++st) {
+      int from = st + 2;
+      if (st >= ns - 2) {
+        from -= ns;
+        if (st == ns - 2 || ns == 1) {
+          if (chain) {
+            t = describe(next);
+            chain = t.ns >= 2;
+            if constexpr (GATHER && !kColA) take_rows(t);
+          }
+          if (!chain) t.ns = 0;
+        }
+      }
+      const Stage cp = stage(from, st + 2);
+      first_half(st, cp);
+      second_half(st, cp, chained && st == 0);
+      if constexpr (GATHER) {
+        if constexpr (kColA) {
+          if (st + 4 < ns) copy_index(t, st + 4, ring_at + st + 4);
+        }
+        if (chain && st == ns - 4) {
+          const Tile n = describe(next);
+          if constexpr (kColA) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) copy_index(n, s, ring_at + ns + s);
+          } else {
+            copy_rows(n);
+          }
+        }
+      }
+    }
+
+    // the lane number anew for each tile: addresses formed from it would otherwise
+    // be kept, and spilled, through the whole loop
+    const int ln = (int)hide((uint32_t)lane);
+    float srow[FA];
+    u32x4_t scol[4][4];
+    if constexpr (kInt8) {
+      // scales of the tile's rows and columns (0 outside)
+      const auto si = make_rsrc(p.row_index + m0, (int64_t)rows * 4);
+      const auto sr = GATHER ? make_rsrc(p.sa, p.S * 4) : make_rsrc(p.sa + m0, (int64_t)rows * 4);
+      const auto sc = make_rsrc(p.sb + (int64_t)g * p.N + n0, (cols - n0) * 4);
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        const int m = wm * 32 * FA + 32 * i + (ln & 31);
+        const uint32_t row = GATHER ? __builtin_amdgcn_raw_buffer_load_b32(si, (uint32_t)m * 4u, 0, 0)
+                                    : (uint32_t)m;
+        const bool ok = (m < rows) & (!GATHER | (row < (uint32_t)p.S));
+        srow[i] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(sr, (row * 4u) | (ok ? 0u : kOut), 0, 0));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          scol[j][q] = __builtin_amdgcn_raw_buffer_load_b128(
+              sc, (uint32_t)(wn * 128 + 32 * j + 8 * q + 4 * (ln >> 5)) * 4u, 0, 0);
+    }
+
+    // Stores, bounded like the loads: lanes past the tile's rows or columns get an
+    // offset that stores nothing, so that every tile issues the same stores
+    // (the waits count on it).
+    typedef typename O::elem OE;
+    OE* c = (OE*)p.c + (kColA ? ((int64_t)g * p.N + m0) * p.K : m0 * p.ldc) + n0;
+    const uint32_t ec = (uint32_t)(p.ldc * sizeof(OE));
+    const int64_t room = (int64_t)(rows - 1) * ec + (cols - n0) * (int64_t)sizeof(OE);
+    const auto out = make_rsrc(c, room);
+    const int right = (int)min((int64_t)kTileN, cols - n0);   // columns of the tile
+    auto value = [&](int i, int j, int r) {
+      if constexpr (kInt8)
+        return (float)acc[i][j][r] * srow[i] * __uint_as_float(scol[j][r >> 2][r & 3]);
+      else
+        return acc[i][j][r];
+    };
+    constexpr int kNt = 2;   // non-temporal: not read again here
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+      const int m = wm * 32 * FA + 32 * i + (ln & 31);
+      const uint32_t roff = m < rows ? (uint32_t)m * ec : kOut;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(OE) == 4) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = wn * 128 + 32 * j + 8 * q + 4 * (ln >> 5);
+            const u32x4_t v = {__float_as_uint(value(i, j, 4 * q)), __float_as_uint(value(i, j, 4 * q + 1)),
+                               __float_as_uint(value(i, j, 4 * q + 2)),
+                               __float_as_uint(value(i, j, 4 * q + 3))};
+            const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 4u : kOut;
+            __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // 8 consecutive columns: lanes l and l + 32 trade a half each
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * h + 2 * e;
+              w[e] = (uint32_t)O::cvt(value(i, j, r)) | ((uint32_t)O::cvt(value(i, j, r + 1)) << 16);
+            }
+            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+            const u32x4_t v = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+            const int n = wn * 128 + 32 * j + 16 * h + 8 * (ln >> 5);
+            const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 2u : kOut;
+            __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (next >= ntiles) return;
+    slot0 = (slot0 + ns) & 1;
+    ring_at += ns;
+    chained = chain;
+    tile = next;
+    if (!chain) {
+      // this wave's copies (of nothing) are done, every wave has read the
+      // last fragments: both slots are free
+      __builtin_amdgcn_s_waitcnt(vm_wait(0));
+      __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+      __syncthreads();
+      t = describe(tile);
+      start();
+    }
+  }
+}
+
+}  // namespace mx

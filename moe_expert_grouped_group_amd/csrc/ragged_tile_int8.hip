@@ -1,0 +1,12 @@
+// Large tiles of the forward product in 8-bit integers.
+#include "ragged_tile_launch.h"
+
+namespace mx {
+
+hipError_t launch_ragged_tile_int8(int out, const RaggedArgs& p, hipStream_t st) {
+  if (out == 0) return launch_tile_gather<TypeI8, OutF32, 0>(p, st);
+  if (out == 1) return launch_tile_gather<TypeI8, OutBf16, 0>(p, st);
+  return launch_tile_gather<TypeI8, OutF16, 0>(p, st);
+}
+
+}  // namespace mx

@@ -1,0 +1,34 @@
+// The launch of one large-tile product (ragged_tile.h).  Each layout's kernels
+// are compiled in a file of their own.
+#pragma once
+
+#include <algorithm>
+
+#include "ragged_tile.h"
+
+namespace mx {
+
+inline int compute_units() {
+  int dev = 0, cus = 256;
+  if (hipGetDevice(&dev) == hipSuccess)
+    (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  return cus;
+}
+
+template <typename T, typename O, int LAYOUT, int FA, bool GATHER>
+hipError_t launch_tile(const RaggedArgs& p, hipStream_t st) {
+  const int64_t m = 64 * FA, cols = ((LAYOUT == 0 ? p.N : p.K) + kTileN - 1) / kTileN;
+  const int64_t most = cols * (LAYOUT == 2 ? p.G * ((p.N + m - 1) / m)
+                                           : p.R / m + std::min<int64_t>(p.G, p.R));
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, compute_units()));
+  ragged_tile_kernel<T, O, LAYOUT, FA, GATHER><<<dim3(grid), dim3(256), 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O, int LAYOUT>
+hipError_t launch_tile_gather(const RaggedArgs& p, hipStream_t st) {
+  return p.row_index != nullptr ? launch_tile<T, O, LAYOUT, 4, true>(p, st)
+                                : launch_tile<T, O, LAYOUT, 4, false>(p, st);
+}
+
+}  // namespace mx

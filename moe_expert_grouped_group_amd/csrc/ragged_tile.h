@@ -8,8 +8,9 @@
 //
 // Two kinds of operand:
 //  * contraction contiguous (X and W in NT, dY in NN): a stage is [rows][128 B],
-//    16-byte chunk c of row r at chunk c ^ (r & 7): the 8 rows that one LDS
-//    access phase reads use 8 different bank groups.
+//    16-byte chunk c of row r at chunk c ^ ((r >> 1) & 7): two rows fill the
+//    256 bytes of the banks, and the 16 rows that one LDS access phase reads use
+//    16 different places there.
 //  * contraction over rows (W in NN, dY and X in TN): a stage is [64][512 B],
 //    chunk c of row r at chunk c ^ {0, 4, 10, 14}[r & 3].  Fragments come through
 //    the transposing LDS read: in each group of 16 lanes, lane l hands in the
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   // Lane offsets of the copies.  Contiguous: part j copies rows 8 (parts wave + j)
   // + lane / 8, chunk position lane % 8.  Over rows: part j copies contraction
   // rows 16 wave + 2 j + lane / 32, chunk position lane % 32.
-  const uint32_t chunk_k = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+  auto chunk_k = [&](int j) { return (uint32_t)((lane & 7) ^ (4 * (j & 1) + (lane >> 4))) * 16; };
   auto chunk_c = [&](int j) {
     const int r = 2 * (j & 1) + (lane >> 5);
     const int x = (r & 1) * 4 + (r >> 1) * 10;
@@ -300,14 +301,16 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
 #pragma unroll
   for (int j = 0; j < kPartsA; ++j)
     va[j] = kColA ? (uint32_t)((16 * wave + 2 * j + (lane >> 5)) * ea) + chunk_c(j)
-                  : (uint32_t)((8 * (kPartsA * wave + j) + (lane >> 3)) * ea) + chunk_k;
+                  : (uint32_t)((8 * (kPartsA * wave + j) + (lane >> 3)) * ea) + chunk_k(j);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     vb[j] = kColB ? (uint32_t)((16 * wave + 2 * j + (lane >> 5)) * eb) + chunk_c(j)
-                  : (uint32_t)((8 * (8 * wave + j) + (lane >> 3)) * eb) + chunk_k;
+                  : (uint32_t)((8 * (8 * wave + j) + (lane >> 3)) * eb) + chunk_k(j);
   // contiguous contraction: lanes past its end in the last stage
   const uint32_t last_bytes = (uint32_t)((con * (int64_t)sizeof(E) - 1) % kStageK) + 1;
-  const uint32_t past = !kColA && chunk_k >= last_bytes ? kOut : 0u;
+  uint32_t past[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) past[j] = !kColA && chunk_k(j) >= last_bytes ? kOut : 0u;
 
   // Addresses of the fragments in a stage.
   uint32_t ra[kColA ? FA : 4], rb[kColB ? 4 : 4];
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
                         (lane & 1) * 8);
     };
     auto row = [&](int first, int s) {
-      return (uint32_t)((first + (lane & 31)) * kStageK + (((2 * s + (lane >> 5)) ^ (lane & 7)) * 16));
+      return (uint32_t)((first + (lane & 31)) * kStageK + (((2 * s + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16));
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -362,13 +365,13 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       const uint32_t r = (uint32_t)(8 * j + (lane >> 3));
       const uint32_t row = *(__attribute__((address_space(3))) const uint32_t*)(ring0 + r * 4);
       const bool ok = ((int)(8 * kPartsA * wave + r) < n.rows) & (row < (uint32_t)p.S);
-      va[j] = (row * (uint32_t)ea + chunk_k) | (ok ? 0u : kOut);
+      va[j] = (row * (uint32_t)ea + chunk_k(j)) | (ok ? 0u : kOut);
     }
   };
 
   struct Stage {
     int st, len, at;
-    uint32_t soff, lds, kill;
+    uint32_t soff, lds, kill[2];
     i32x4 sa, sb;
   };
   // Stage st of the copied tile; v: its number counted from the computed tile's
@@ -385,7 +388,8 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     s.at = ring_at + v;
     s.lds = lds0 + (uint32_t)(((slot0 + v) & 1) * kStage);
     s.soff = none ? 0u : (uint32_t)st * kStageK;
-    s.kill = none ? kOut : (st == n.ns - 1 ? past : 0u);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s.kill[j] = none ? kOut : (st == n.ns - 1 ? past[j] : 0u);
     s.sa = n.sa;
     s.sb = n.sb;
     if (kColA)
@@ -409,7 +413,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     constexpr int j = isA ? c / 2 : (c < 2 * kPartsA ? c / 2 : c - kPartsA);
     if constexpr (isA) {
       const uint32_t at = s.lds + (uint32_t)(wave * kPartsA * 1024 + j * 1024);
-      copy16(s.sa, kColA ? va[j] : (va[j] | s.kill), kColA ? 0u : s.soff, at);
+      copy16(s.sa, kColA ? va[j] : (va[j] | s.kill[j & 1]), kColA ? 0u : s.soff, at);
     } else {
       const uint32_t at = s.lds + kOffB + (uint32_t)(wave * 8192 + j * 1024);
       if constexpr (GATHER && kColA) {
@@ -420,7 +424,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         const bool ok = ((int)(s.st * 64 + r) < s.len) & (row < (uint32_t)p.S);
         copy16(s.sb, (row * (uint32_t)eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
       } else {
-        copy16(s.sb, kColB ? vb[j] : (vb[j] | s.kill), kColB ? 0u : s.soff, at);
+        copy16(s.sb, kColB ? vb[j] : (vb[j] | s.kill[j & 1]), kColB ? 0u : s.soff, at);
       }
     }
   };
@@ -630,7 +634,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       else
         return acc[i][j][r];
     };
-    constexpr int kNt = 2;   // non-temporal: not read again here
+    constexpr int kNt = 0;
 #pragma unroll
     for (int i = 0; i < FA; ++i) {
       const int m = wm * 32 * FA + 32 * i + (ln & 31);

@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp8moe.so")
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "ragged.hip", "ragged_tile_nt.hip",
+SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "ragged.hip", "ragged_few.hip", "ragged_tile_nt.hip",
            "ragged_tile_nn.hip", "ragged_tile_tn.hip", "ragged_tile_int8.hip", "routing.hip"]
 ARCH = "gfx950"
 

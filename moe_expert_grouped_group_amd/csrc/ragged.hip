@@ -308,8 +308,13 @@ bool ragged_tile_takes(int layout, int esize, int osize, const RaggedArgs& p) {
 
 }  // namespace
 
+// Whether experts have few rows (64 on average, of those that can have any): the
+// forward product is then bound by reading the weights.
+bool few_rows(const RaggedArgs& p) { return p.R <= 64 * std::min<int64_t>(p.G, p.R); }
+
 hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p,
                               hipStream_t st) {
+  if (layout == 0 && few_rows(p)) return launch_ragged_few(f16, out, p, st);
   if (ragged_tile_takes(layout, 2, out == 0 ? 4 : 2, p))
     return layout == 0   ? launch_ragged_tile_nt(f16, out, p, st)
            : layout == 1 ? launch_ragged_tile_nn(f16, out, p, st)
@@ -323,6 +328,7 @@ hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p
 }
 
 hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st) {
+  if (few_rows(p)) return launch_ragged_few_int8(out, p, st);
   if (ragged_tile_takes(0, 1, out == 0 ? 4 : 2, p)) return launch_ragged_tile_int8(out, p, st);
   if (out == 0) return launch_any<TypeI8, OutF32, 0>(p, st);
   if (out == 1) return launch_any<TypeI8, OutBf16, 0>(p, st);
@@ -332,6 +338,10 @@ hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st)
 // Workgroups that any call may launch at most (the grid's limit).
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G) {
   const int64_t cols = ((layout == 0 ? N : K) + kAnyT - 1) / kAnyT;
+  if (layout == 0)   // the smallest tiles: 16 rows by 16 columns
+    return std::max(cols * (R / kAnyT + std::min<int64_t>(G, R)),
+                    R <= 64 * std::min<int64_t>(G, R)
+                        ? ((N + 15) / 16) * (R / 16 + std::min<int64_t>(G, R)) : 0);
   return cols * (layout == 2 ? (int64_t)G * ((N + kAnyT - 1) / kAnyT)
                              : R / kAnyT + std::min<int64_t>(G, R));
 }

@@ -33,6 +33,9 @@ struct RaggedArgs {
   int32_t G;
 };
 
+// Forward products of experts with few rows (ragged_few.hip).
+hipError_t launch_ragged_few(bool f16, int out, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_few_int8(int out, const RaggedArgs& p, hipStream_t st);
 // The large-tile form (ragged_tile.h), by layout.
 hipError_t launch_ragged_tile_nt(bool f16, int out, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_nn(bool f16, int out, const RaggedArgs& p, hipStream_t st);

@@ -1,0 +1,254 @@
+// Forward products where experts have few rows (decoding): bound by reading
+// the weights once.
+//
+// One workgroup takes up to 16 MR rows of one expert and 16 CF output columns;
+// its waves split the contraction by 128-byte lines (wave w takes lines w,
+// w + waves, ...), so that few columns still give many loads in flight, and
+// their sums are joined in LDS in a fixed order.  Weights go from memory straight to
+// the registers of the matrix instruction, as its first operand (16 columns by 64
+// contraction bytes; rows of tokens are the second), at element alignment: no size or
+// stride is special.
+#include <algorithm>
+
+#include "ragged_common.h"
+
+namespace mx {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Small;
+template <>
+struct Small<TypeBf16> {
+  typedef f32x4 acc;
+  static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
+    typedef TypeBf16::vec v;
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v, a), __builtin_bit_cast(v, b),
+                                                   c, 0, 0, 0);
+  }
+};
+template <>
+struct Small<TypeF16> {
+  typedef f32x4 acc;
+  static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
+    typedef TypeF16::vec v;
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v, a), __builtin_bit_cast(v, b),
+                                                  c, 0, 0, 0);
+  }
+};
+template <>
+struct Small<TypeI8> {
+  typedef i32x4 acc;
+  static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                                 c, 0, 0, 0);
+  }
+};
+
+// 16 bytes at p, of which the contraction holds n (n <= 0: none): zeros behind.
+template <typename E>
+__device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
+  u32x4_t v = {0, 0, 0, 0};
+  if (n >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (n > 0) {
+    E e[16 / sizeof(E)];
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(E)); ++i)
+      e[i] = (int64_t)(i * sizeof(E)) < n ? ((const E*)p)[i] : (E)0;
+    __builtin_memcpy(&v, e, 16);
+  }
+  return v;
+}
+
+template <typename T, typename O, int MR, int CF, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
+  typedef typename T::elem E;
+  typedef typename Small<T>::acc Acc;
+  constexpr bool kInt8 = sizeof(E) == 1;
+  __shared__ Acc part[WAVES][MR * CF][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t ctiles = (p.N + 16 * CF - 1) / (16 * CF);
+  const int64_t rt = (int64_t)blockIdx.x / ctiles;
+  const int64_t n0 = (int64_t)blockIdx.x % ctiles * (16 * CF);
+
+  // The row tile's expert: each wave for itself, 16 experts a lane in a row.
+  int g = -1, rows = 0;
+  int64_t row0 = 0;
+  {
+    constexpr int per = kRaggedMaxGroups / 64;
+    int64_t before_r = 0, before_t = 0;
+    for (int i = 0; i < per && 64 * i < p.G; ++i) {
+      const int e = 64 * i + lane;
+      const int64_t m = e < p.G ? split_rows(p.m_splits, e, p.R) : 0;
+      // rows and tiles of experts up to this one, over the wave
+      int64_t r = m;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int64_t u = __shfl_up(r, d, 64);
+        if (lane >= d) r += u;
+      }
+      // rows cut at R
+      const int64_t hi = min(before_r + r, p.R), lo = min(before_r + r - m, p.R);
+      const int64_t t = (hi - lo + 16 * MR - 1) / (16 * MR);
+      int64_t ts = t;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int64_t u = __shfl_up(ts, d, 64);
+        if (lane >= d) ts += u;
+      }
+      const int64_t first = before_t + ts - t;
+      const bool mine = rt >= first && rt < first + t;
+      const uint64_t who = __ballot(mine);
+      if (who != 0) {
+        const int src = __builtin_ctzll(who);
+        const int64_t at = lo + (rt - first) * (16 * MR);
+        g = 64 * i + src;
+        row0 = __shfl(at, src, 64);
+        rows = (int)min((int64_t)(16 * MR), __shfl(hi, src, 64) - row0);
+        break;
+      }
+      before_r += __shfl(r, 63, 64);
+      before_t += __shfl(ts, 63, 64);
+    }
+  }
+  if (g < 0) return;
+
+  const int64_t kb = p.K * (int64_t)sizeof(E);
+  const int64_t lines = (kb + 127) / 128;
+  const int sub = lane >> 4;   // 16-byte chunk of a 64-byte step
+  // this lane's weight rows and token rows; rows past the end repeat the last
+  const uint8_t* w[CF];
+#pragma unroll
+  for (int c = 0; c < CF; ++c) {
+    const int64_t n = min(n0 + 16 * c + (lane & 15), p.N - 1);
+    w[c] = (const uint8_t*)p.b + ((int64_t)g * p.N + n) * kb + sub * 16;
+  }
+  const uint8_t* x[MR];
+  int64_t token[MR];   // -1: a row of zeros
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    const int64_t r = row0 + min(16 * m + (lane & 15), rows - 1);
+    const int64_t s = p.row_index != nullptr ? p.row_index[r] : r;
+    token[m] = s >= 0 && s < p.S ? s : -1;
+    // any readable row of K values does for a row of zeros
+    x[m] = (token[m] >= 0 ? (const uint8_t*)p.a + s * p.lda * (int64_t)sizeof(E) : w[0] - sub * 16) +
+           sub * 16;
+  }
+
+  Acc acc[MR][CF];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int c = 0; c < CF; ++c) acc[m][c] = Acc{0, 0, 0, 0};
+  auto mma = [&](const u32x4_t* wv, const u32x4_t* xv) {
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+      for (int c = 0; c < CF; ++c) acc[m][c] = Small<T>::mma(wv[c], xv[m], acc[m][c]);
+  };
+  // whole lines, kUnroll at a time
+  constexpr int kUnroll = CF * 2 >= 8 ? 2 : 4;
+  const int64_t whole = kb / 128;
+  int64_t l = wave;
+  for (; l + (kUnroll - 1) * WAVES < whole; l += kUnroll * WAVES) {
+    u32x4_t wv[kUnroll][2][CF], xv[kUnroll][2][MR];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = (l + u * WAVES) * 128 + h * 64;
+#pragma unroll
+        for (int c = 0; c < CF; ++c) __builtin_memcpy(&wv[u][h][c], w[c] + at, 16);
+#pragma unroll
+        for (int m = 0; m < MR; ++m) __builtin_memcpy(&xv[u][h][m], x[m] + at, 16);
+      }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) mma(wv[u][h], xv[u][h]);
+  }
+  for (; l < lines; l += WAVES) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = l * 128 + h * 64;
+      const int64_t n = kb - at - sub * 16;
+      u32x4_t wv[CF], xv[MR];
+#pragma unroll
+      for (int c = 0; c < CF; ++c) wv[c] = chunk_end<E>(w[c] + at, n);
+#pragma unroll
+      for (int m = 0; m < MR; ++m) xv[m] = chunk_end<E>(x[m] + at, n);
+      mma(wv, xv);
+    }
+  }
+
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int c = 0; c < CF; ++c) part[wave][m * CF + c][lane] = acc[m][c];
+  __syncthreads();
+  // block i: token 16 (i / CF) + lane % 16, columns 16 (i % CF) + 4 (lane / 16) + 0..3
+  for (int i = wave; i < MR * CF; i += WAVES) {
+    Acc sum = part[0][i][lane];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) sum += part[v][i][lane];
+    const int m = i / CF, r = 16 * m + (lane & 15);
+    if (r >= rows) continue;
+    int64_t s = -1;
+#pragma unroll
+    for (int j = 0; j < MR; ++j)
+      if (j == m) s = token[j];
+    typename O::elem* c = (typename O::elem*)p.c + (row0 + r) * p.ldc;
+    const float sa = kInt8 && s >= 0 ? p.sa[s] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t n = n0 + 16 * (i % CF) + 4 * sub + e;
+      if (n >= p.N) continue;
+      float v = (float)sum[e];
+      if (kInt8) v = v * sa * p.sb[(int64_t)g * p.N + n];
+      c[n] = O::cvt(s >= 0 ? v : 0.f);
+    }
+  }
+}
+
+namespace {
+
+template <typename T, typename O, int MR, int CF, int WAVES>
+hipError_t launch_few(const RaggedArgs& p, hipStream_t st) {
+  const int64_t rt = p.R / (16 * MR) + std::min<int64_t>(p.G, p.R);
+  const int64_t ct = (p.N + 16 * CF - 1) / (16 * CF);
+  ragged_few_kernel<T, O, MR, CF, WAVES><<<dim3((uint32_t)(rt * ct)), dim3(64 * WAVES), 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t launch_rows(const RaggedArgs& p, hipStream_t st) {
+  // rows of an expert on average, over experts that can have any
+  const int64_t groups = std::min<int64_t>(p.G, p.R);
+  const int64_t mean = (p.R + groups - 1) / groups;
+  // 64 columns a workgroup where that gives every CU two of them, else 16
+  // columns and twice the waves on the contraction
+  const bool wide = groups * ((p.N + 63) / 64) >= 512;
+  if (mean <= 16)
+    return wide ? launch_few<T, O, 1, 4, 4>(p, st) : launch_few<T, O, 1, 1, 8>(p, st);
+  if (mean <= 32)
+    return wide ? launch_few<T, O, 2, 4, 4>(p, st) : launch_few<T, O, 2, 1, 8>(p, st);
+  return wide ? launch_few<T, O, 4, 4, 4>(p, st) : launch_few<T, O, 4, 1, 8>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_ragged_few(bool f16, int out, const RaggedArgs& p, hipStream_t st) {
+  if (f16)
+    return out == 0 ? launch_rows<TypeF16, OutF32>(p, st) : launch_rows<TypeF16, OutF16>(p, st);
+  return out == 0 ? launch_rows<TypeBf16, OutF32>(p, st) : launch_rows<TypeBf16, OutBf16>(p, st);
+}
+
+hipError_t launch_ragged_few_int8(int out, const RaggedArgs& p, hipStream_t st) {
+  if (out == 0) return launch_rows<TypeI8, OutF32>(p, st);
+  if (out == 1) return launch_rows<TypeI8, OutBf16>(p, st);
+  return launch_rows<TypeI8, OutF16>(p, st);
+}
+
+}  // namespace mx

@@ -497,6 +497,11 @@ typedef enum mxfp8_type {
  * other rows never reach a result (infinities and NaN included).
  * Strides are in elements.  Faster where pointers, strides and the contraction
  * length are multiples of 16 bytes; right for all.
+ *   workspace  NULL, or device memory, 16-byte aligned, of
+ *           mxfp8_ragged_gemm_workspace_bytes() bytes that no other call running at
+ *           the same time uses; needs no initialisation.  With it, tiles that
+ *           do not fill the GPU are split along the contraction and joined in
+ *           a fixed order (a smaller one is not used).
  * Errors: EINVAL for NULL pointers, sizes < 1 (R, S >= 0), strides shorter than
  * a row, G out of range, host m_splits, row_index with NN, S != R without
  * row_index, over 2^31 - 1 rows, columns or tiles; ENOTSUP for other types.
@@ -505,7 +510,8 @@ mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int6
                                const void* b, int64_t ldb, void* c, int64_t ldc, int32_t c_type,
                                int64_t R, int64_t S, int64_t N, int64_t K,
                                const int64_t* m_splits, int32_t G, const int32_t* row_index,
-                               void* stream);
+                               void* workspace, size_t workspace_bytes, void* stream);
+size_t mxfp8_ragged_gemm_workspace_bytes(void);
 
 /*
  * mxfp8_quantize_int8 -- a tensor's rows as 8-bit integers with a scale each:
@@ -534,7 +540,7 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
                                     const int8_t* w, const float* w_scale, void* c, int64_t ldc,
                                     int32_t c_type, int64_t R, int64_t S, int64_t N, int64_t K,
                                     const int64_t* m_splits, int32_t G, const int32_t* row_index,
-                                    void* stream);
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * mxfp8_moe_route -- the top_k experts of each token, their weights, and the

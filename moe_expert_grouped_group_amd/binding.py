@@ -543,7 +543,28 @@ def _row_index(row_index, like):
     return row_index
 
 
-def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None, stream=None):
+def ragged_gemm_workspace_bytes():
+    return int(_lib().mxfp8_ragged_gemm_workspace_bytes())
+
+
+def _ragged_workspace(workspace, like):
+    """The caller's buffer, or one for this call (torch's allocator hands the
+    same memory out again)."""
+    global _ragged_bytes
+    if not _ragged_bytes:
+        _ragged_bytes = ragged_gemm_workspace_bytes()
+    if workspace is None:
+        return _empty((_ragged_bytes,), torch.uint8, like)
+    if not workspace.is_cuda or workspace.numel() * workspace.element_size() < _ragged_bytes:
+        raise ValueError(f"workspace must be a device buffer of at least {_ragged_bytes} bytes")
+    return workspace
+
+
+_ragged_bytes = 0
+
+
+def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None, stream=None,
+                workspace=None):
     """One product of an expert linear whose experts have any number of rows.
 
     layout "NT" (forward): a = X [S, K], b = W [G, N, K] -> [R, N]
@@ -554,7 +575,9 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
     consecutive rows of R.  row_index (int32 [R], NT and TN): row r of the
     product is row row_index[r] of X; without it S = R.  a, X and out may
     have a row stride.  out_dtype: the operands' (default) or float32.  Rows
-    past the last expert's are not written (mxfp8_ragged_gemm).
+    past the last expert's are not written (mxfp8_ragged_gemm).  workspace:
+    optional device buffer of ragged_gemm_workspace_bytes(), not shared by calls
+    that may run at the same time; allocated for the call where there is none.
     """
     lib = _lib()
     lay = _LAYOUTS[layout]
@@ -598,9 +621,15 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
         if out is None:
             out = _empty(shape, out_dtype, a)
         ldc = _rows_of(out, out_dtype, shape, "out")
-    _same_device(a, b=b, m_splits=ms, row_index=index, out=out)
+    ws = None
+    if not (lay == LAYOUT_NT and r <= 64 * g and workspace is None):   # few rows take none
+        ws = _ragged_workspace(workspace, a)
+    _same_device(a, b=b, m_splits=ms, row_index=index, out=out, workspace=ws)
+    if ws is not None and stream is not None:
+        ws.record_stream(stream)
     st = lib.mxfp8_ragged_gemm(lay, ty, _ptr(a), lda, _ptr(b), ldb, _ptr(out), ldc,
                                _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
+                               _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                                _stream(stream))
     _native.check(st, "mxfp8_ragged_gemm")
     return out
@@ -626,10 +655,11 @@ def quantize_int8(x, out=None, stream=None):
 
 
 def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=torch.bfloat16,
-                     out=None, stream=None):
+                     out=None, stream=None, workspace=None):
     """Forward product in 8-bit integers: q [S, K] int8 with scale [S] (as
     quantize_int8 gives them), w [G, N, K] int8 with w_scale [G, N] -> [R, N],
-    (sum of q w) * scale * w_scale.  row_index and m_splits as ragged_gemm."""
+    (sum of q w) * scale * w_scale.  row_index, m_splits and workspace as
+    ragged_gemm."""
     lib = _lib()
     ms = _splits(m_splits)
     g = ms.numel()
@@ -648,9 +678,14 @@ def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=t
     if out is None:
         out = _empty((r, n), out_dtype, q)
     ldc = _rows_of(out, out_dtype, (r, n), "out")
-    _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out)
+    ws = _ragged_workspace(workspace, q) if r > 64 * g or workspace is not None else None
+    _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out,
+                 workspace=ws)
+    if ws is not None and stream is not None:
+        ws.record_stream(stream)
     st = lib.mxfp8_ragged_gemm_int8(_ptr(q), ldq, _ptr(scale), _ptr(w), _ptr(w_scale), _ptr(out),
                                     ldc, _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
+                                    _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                                     _stream(stream))
     _native.check(st, "mxfp8_ragged_gemm_int8")
     return out

@@ -486,13 +486,19 @@ mxfp8_status check_ragged(const char* fn, int layout, int64_t R, int64_t S, int6
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+void* usable_workspace(void* ws, size_t bytes) {
+  return bytes >= mx::ragged_workspace_bytes() && aligned_to(ws, 16) ? ws : nullptr;
+}
+
 }  // namespace
+
+size_t mxfp8_ragged_gemm_workspace_bytes(void) { return mx::ragged_workspace_bytes(); }
 
 mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int64_t lda,
                                const void* b, int64_t ldb, void* c, int64_t ldc, int32_t c_type,
                                int64_t R, int64_t S, int64_t N, int64_t K,
                                const int64_t* m_splits, int32_t G, const int32_t* row_index,
-                               void* stream) {
+                               void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "mxfp8_ragged_gemm";
   REQUIRE(layout == MXFP8_LAYOUT_NT || layout == MXFP8_LAYOUT_NN || layout == MXFP8_LAYOUT_TN,
           "%s: unknown layout %d", fn, (int)layout);
@@ -529,6 +535,7 @@ mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int6
   p.m_splits = m_splits;
   p.row_index = row_index;
   p.G = G;
+  p.ws = usable_workspace(workspace, workspace_bytes);
   return hip_status(
       mx::launch_ragged_gemm(layout, type == MXFP8_TYPE_F16, c_type, p, as_stream(stream)), fn);
 }
@@ -555,7 +562,7 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
                                     const int8_t* w, const float* w_scale, void* c, int64_t ldc,
                                     int32_t c_type, int64_t R, int64_t S, int64_t N, int64_t K,
                                     const int64_t* m_splits, int32_t G, const int32_t* row_index,
-                                    void* stream) {
+                                    void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "mxfp8_ragged_gemm_int8";
   if (c_type != MXFP8_TYPE_F32 && c_type != MXFP8_TYPE_BF16 && c_type != MXFP8_TYPE_F16)
     return fail(MXFP8_ENOTSUP, "%s: output type %d is not supported", fn, (int)c_type);
@@ -586,6 +593,7 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
   p.sa = scale;
   p.sb = w_scale;
   p.G = G;
+  p.ws = usable_workspace(workspace, workspace_bytes);
   return hip_status(mx::launch_ragged_gemm_int8(c_type, p, as_stream(stream)), fn);
 }
 

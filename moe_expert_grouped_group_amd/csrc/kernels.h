@@ -64,6 +64,7 @@ hipError_t launch_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* sa, const
 struct RaggedArgs;
 hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st);
+size_t ragged_workspace_bytes();   // a partial 256 x 256 tile for each CU
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G);
 hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,
                                 int8_t* q, float* scale, hipStream_t st);

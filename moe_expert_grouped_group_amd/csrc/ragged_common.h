@@ -31,6 +31,7 @@ struct RaggedArgs {
   const float* sa;      // int8: scale of each row of X [S]
   const float* sb;      // int8: scale of each output channel [G, N]
   int32_t G;
+  void* ws;             // partial sums of split tiles (large tiles), or NULL
 };
 
 // Forward products of experts with few rows (ragged_few.hip).
@@ -101,6 +102,54 @@ struct OutF16 {
 __device__ __forceinline__ int64_t split_rows(const int64_t* m_splits, int g, int64_t R) {
   const int64_t m = m_splits[g];
   return m < 0 ? 0 : (m < R ? m : R);
+}
+
+// The expert, first row and row count of row tile rt (tiles of `tile` rows), by one
+// wave; g = -1 past the last.  total: row tiles of all experts (only if asked for).
+struct RowSpan {
+  int g, rows;
+  int64_t row0, total;
+};
+__device__ __forceinline__ RowSpan wave_row_tile(const int64_t* m_splits, int G, int64_t R, int tile,
+                                                 int64_t rt, bool want_total) {
+  const int lane = threadIdx.x & 63;
+  RowSpan s;
+  s.g = -1;
+  s.rows = 0;
+  s.row0 = 0;
+  int64_t before_r = 0, before_t = 0;
+  for (int base = 0; base < G; base += 64) {
+    const int e = base + lane;
+    const int64_t m = e < G ? split_rows(m_splits, e, R) : 0;
+    // rows, then tiles, of the experts up to this one
+    int64_t r = m;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t u = __shfl_up(r, d, 64);
+      if (lane >= d) r += u;
+    }
+    const int64_t hi = min(before_r + r, R), lo = min(before_r + r - m, R);   // cut at R
+    const int64_t t = (hi - lo + tile - 1) / tile;
+    int64_t ts = t;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t u = __shfl_up(ts, d, 64);
+      if (lane >= d) ts += u;
+    }
+    const int64_t first = before_t + ts - t;
+    const uint64_t who = __ballot(rt >= first && rt < first + t);
+    if (who != 0) {
+      const int src = __builtin_ctzll(who);
+      s.g = base + src;
+      s.row0 = __shfl(lo + (rt - first) * tile, src, 64);
+      s.rows = (int)min((int64_t)tile, __shfl(hi, src, 64) - s.row0);
+      if (!want_total) break;
+    }
+    before_r += __shfl(r, 63, 64);
+    before_t += __shfl(ts, 63, 64);
+  }
+  s.total = before_t;
+  return s;
 }
 
 }  // namespace mx

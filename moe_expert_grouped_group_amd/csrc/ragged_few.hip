@@ -73,46 +73,9 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
   const int64_t rt = (int64_t)blockIdx.x / ctiles;
   const int64_t n0 = (int64_t)blockIdx.x % ctiles * (16 * CF);
 
-  // The row tile's expert: each wave for itself, 16 experts a lane in a row.
-  int g = -1, rows = 0;
-  int64_t row0 = 0;
-  {
-    constexpr int per = kRaggedMaxGroups / 64;
-    int64_t before_r = 0, before_t = 0;
-    for (int i = 0; i < per && 64 * i < p.G; ++i) {
-      const int e = 64 * i + lane;
-      const int64_t m = e < p.G ? split_rows(p.m_splits, e, p.R) : 0;
-      // rows and tiles of experts up to this one, over the wave
-      int64_t r = m;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int64_t u = __shfl_up(r, d, 64);
-        if (lane >= d) r += u;
-      }
-      // rows cut at R
-      const int64_t hi = min(before_r + r, p.R), lo = min(before_r + r - m, p.R);
-      const int64_t t = (hi - lo + 16 * MR - 1) / (16 * MR);
-      int64_t ts = t;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int64_t u = __shfl_up(ts, d, 64);
-        if (lane >= d) ts += u;
-      }
-      const int64_t first = before_t + ts - t;
-      const bool mine = rt >= first && rt < first + t;
-      const uint64_t who = __ballot(mine);
-      if (who != 0) {
-        const int src = __builtin_ctzll(who);
-        const int64_t at = lo + (rt - first) * (16 * MR);
-        g = 64 * i + src;
-        row0 = __shfl(at, src, 64);
-        rows = (int)min((int64_t)(16 * MR), __shfl(hi, src, 64) - row0);
-        break;
-      }
-      before_r += __shfl(r, 63, 64);
-      before_t += __shfl(ts, 63, 64);
-    }
-  }
+  const RowSpan at = wave_row_tile(p.m_splits, p.G, p.R, 16 * MR, rt, false);
+  const int g = at.g, rows = at.rows;
+  const int64_t row0 = at.row0;
   if (g < 0) return;
 
   const int64_t kb = p.K * (int64_t)sizeof(E);

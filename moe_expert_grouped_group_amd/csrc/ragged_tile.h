@@ -79,6 +79,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
                                            __builtin_amdgcn_readfirstlane((int)(uint32_t)n), 0x00020000);
 }
 
+// The same value in every lane, in scalar registers.
+template <typename V>
+__device__ __forceinline__ V uniform(V v) {
+  const uint64_t b = (uint64_t)v;
+  return (V)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32) |
+             (uint32_t)__builtin_amdgcn_readfirstlane((int)b));
+}
+
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void unroll(F&& f) {
   if constexpr (I < N) {
@@ -154,6 +162,41 @@ __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int 
   __syncthreads();
 }
 
+// Units of work of a launch.  Tiles that fill whole rounds of the grid are one unit
+// each; where the rest fills less than half of a round, each of its tiles is
+// split along the contraction into `parts` units, whose sums go to the
+// workspace and are joined by ragged_join_kernel.
+constexpr int kMinPart = 4;   // stages of a part
+struct Units {
+  uint32_t full, rem, parts;
+};
+__device__ __forceinline__ Units units_of(uint32_t ntiles, uint32_t grid, int64_t stages, bool ws) {
+  Units u;
+  u.full = ntiles / grid * grid;
+  u.rem = ntiles - u.full;
+  u.parts = 1;
+  if (ws && u.rem > 0) {
+    const uint32_t most = (uint32_t)(stages / kMinPart < 1 ? 1 : stages / kMinPart);
+    u.parts = min(grid / u.rem, most);
+  }
+  return u;
+}
+// Row and column tile of tile `at`: 8 row tiles by all column tiles at a
+// time, columns outermost.
+__device__ __forceinline__ void tile_order(uint32_t at, uint32_t rtiles, uint32_t ctiles, int32_t* mt,
+                                           int32_t* nt) {
+  const uint32_t per = 8u * ctiles, grp = at / per, in = at % per;
+  const uint32_t wide = min(8u, rtiles - 8u * grp);
+  *mt = (int32_t)(8u * grp + in % wide);
+  *nt = (int32_t)(in / wide);
+}
+// Stages of the contraction that the number of parts goes by: all of it, or the
+// rows of an expert on average.
+__device__ __forceinline__ int64_t part_stages(int layout, const RaggedArgs& p, int esize) {
+  const int64_t con = layout == 0 ? p.K : (layout == 1 ? p.N : p.R / p.G);
+  return (con * esize + kStageK - 1) / kStageK;
+}
+
 template <typename T, typename O, int LAYOUT, int FA, bool GATHER>
 __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   typedef typename T::elem E;
@@ -173,7 +216,15 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   constexpr int kRing = !GATHER ? 16 : (kColA ? 4 * 8 * 256 : 4 * 256);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRing];
+  // int8: scales of the rows and columns of two tiles
+  __shared__ __attribute__((aligned(16))) float scales[2][2][kInt8 ? 256 : 4];
   __shared__ RaggedTable table;
+  // What only the start and the end of a tile need is kept in LDS, not in
+  // scalar registers: they would spill.
+  __shared__ RaggedArgs args;
+  __shared__ struct {
+    uint32_t full, rem, parts, rtiles, ctiles, band;
+  } plan;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -181,23 +232,36 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
   build_ragged_table(p.m_splits, p.G, p.R, kTileM, &table, (int32_t*)smem);
 
-  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
-  const int32_t ctiles = (int32_t)((cols + kTileN - 1) / kTileN);
-  const int32_t band = (int32_t)((p.N + kTileM - 1) / kTileM);           // TN: row tiles of an expert
-  const uint32_t rtiles = kColA ? (uint32_t)p.G * (uint32_t)band
-                                : (uint32_t)__builtin_amdgcn_readfirstlane(table.tiles[kRaggedMaxGroups]);
-  const uint32_t ntiles = rtiles * (uint32_t)ctiles;   // below 2^31 (checked by the caller)
+  uint32_t nunits;
+  {
+    const int64_t cols = LAYOUT == 0 ? p.N : p.K;
+    const uint32_t ctiles = (uint32_t)((cols + kTileN - 1) / kTileN);
+    const uint32_t band = (uint32_t)((p.N + kTileM - 1) / kTileM);       // TN: row tiles of an expert
+    const uint32_t rtiles = kColA ? (uint32_t)p.G * band : (uint32_t)table.tiles[kRaggedMaxGroups];
+    // tiles: below 2^31 (checked by the caller)
+    const Units u =
+        units_of(rtiles * ctiles, gridDim.x, part_stages(LAYOUT, p, sizeof(E)), p.ws != nullptr);
+    nunits = (uint32_t)__builtin_amdgcn_readfirstlane((int)(u.full + u.rem * u.parts));
+    if (tid == 0) {
+      plan.full = u.full;
+      plan.rem = u.rem;
+      plan.parts = u.parts;
+      plan.rtiles = rtiles;
+      plan.ctiles = ctiles;
+      plan.band = band;
+      args = p;
+    }
+  }
+  __syncthreads();
 
-  // Order of the tiles: 8 row tiles by all column tiles at a time, columns
-  // outermost; of each round of the grid, XCD x (workgroups x, x + 8, ...)
-  // takes consecutive ones, so that its 32 workgroups share 8 row and 4 column
-  // panels in its L2.
-  const bool xcd = gridDim.x % 8 == 0;
+  // Order of the tiles (tile_order); of each full round of the grid, XCD x
+  // (workgroups x, x + 8, ...) takes consecutive ones, so that its 32 workgroups
+  // share 8 row and 4 column panels in its L2.
   auto place = [&](uint32_t i) -> uint32_t {
-    if (!xcd) return i;
-    const uint32_t b = i % gridDim.x, from = i - b;
-    if (from + gridDim.x > ntiles) return i;   // the last round as it comes
-    return from + (b & 7) * (gridDim.x / 8) + (b >> 3);
+    const uint32_t n = gridDim.x;
+    if (n % 8 != 0 || i >= plan.full) return i;   // a last round that is not full as it comes
+    const uint32_t b = i % n;
+    return i - b + (b & 7) * (n / 8) + (b >> 3);
   };
 
   struct Tile {
@@ -211,22 +275,27 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     int32_t n0;          // first column
     int32_t m0;          // first result row
     int32_t g;
+    int32_t split;       // a part: its number among the units that store partial sums, or -1
+    int32_t last;        // its last stage is the contraction's
   };
-  const int64_t ea = p.lda * (int64_t)sizeof(E), eb = p.ldb * (int64_t)sizeof(E);
-  const int64_t con = LAYOUT == 0 ? p.K : p.N;   // NT, NN
+  // row strides in bytes: 256 of them lie within 32 bits
+  const uint32_t ea = (uint32_t)(p.lda * (int64_t)sizeof(E)), eb = (uint32_t)(p.ldb * (int64_t)sizeof(E));
   auto describe = [&](uint32_t i) {
     Tile t;
-    const uint32_t at = place(i);
-    const uint32_t per = 8u * (uint32_t)ctiles;
+    const RaggedArgs& p = args;
+    const uint32_t ctiles = plan.ctiles, rtiles = plan.rtiles, band = plan.band;
+    const uint32_t ufull = plan.full, urem = plan.rem, uparts = plan.parts;
+    const int64_t con = LAYOUT == 0 ? p.K : p.N;   // NT, NN
+    const int64_t la = ea, lb = eb;
+    const bool part = i >= ufull && uparts > 1;
+    const uint32_t v = i - ufull;
+    const uint32_t at = part ? ufull + v % urem : place(i);
     int32_t mt, nt;
+    t.split = part ? (int32_t)v : -1;
     if (kColA) {
-      const uint32_t all = (uint32_t)band * (uint32_t)ctiles;
+      const uint32_t all = band * ctiles;
       t.g = __builtin_amdgcn_readfirstlane((int32_t)(at / all));
-      const uint32_t rem = at % all;
-      const int32_t grp = (int32_t)(rem / per), in = (int32_t)(rem % per);
-      const int32_t wide = min(8, band - 8 * grp);
-      mt = 8 * grp + in % wide;
-      nt = in / wide;
+      tile_order(at % all, band, ctiles, &mt, &nt);
       t.lo = table.rows[t.g];
       t.len = table.rows[t.g + 1] - t.lo;
       t.m0 = mt * kTileM;
@@ -234,20 +303,17 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       t.n0 = nt * kTileN;
       t.ns = (int32_t)(((int64_t)t.len * sizeof(E) + kStageK - 1) / kStageK);
       // columns m0.. of dY and n0.. of X, the expert's rows
-      t.pa = (const uint8_t*)p.a + (int64_t)t.lo * ea + (int64_t)t.m0 * sizeof(E);
-      t.na = t.len == 0 ? 0 : (int64_t)(t.len - 1) * ea + (p.N - t.m0) * (int64_t)sizeof(E);
+      t.pa = (const uint8_t*)p.a + (int64_t)t.lo * la + (int64_t)t.m0 * sizeof(E);
+      t.na = t.len == 0 ? 0 : (int64_t)(t.len - 1) * la + (p.N - t.m0) * (int64_t)sizeof(E);
       if (GATHER) {
         t.pb = (const uint8_t*)p.b + (int64_t)t.n0 * sizeof(E);
-        t.nb = p.S == 0 ? 0 : (p.S - 1) * eb + (p.K - t.n0) * (int64_t)sizeof(E);
+        t.nb = p.S == 0 ? 0 : (p.S - 1) * lb + (p.K - t.n0) * (int64_t)sizeof(E);
       } else {
-        t.pb = (const uint8_t*)p.b + (int64_t)t.lo * eb + (int64_t)t.n0 * sizeof(E);
-        t.nb = t.len == 0 ? 0 : (int64_t)(t.len - 1) * eb + (p.K - t.n0) * (int64_t)sizeof(E);
+        t.pb = (const uint8_t*)p.b + (int64_t)t.lo * lb + (int64_t)t.n0 * sizeof(E);
+        t.nb = t.len == 0 ? 0 : (int64_t)(t.len - 1) * lb + (p.K - t.n0) * (int64_t)sizeof(E);
       }
     } else {
-      const int32_t grp = (int32_t)(at / per), in = (int32_t)(at % per);
-      const int32_t wide = min(8, (int32_t)rtiles - 8 * grp);
-      mt = 8 * grp + in % wide;
-      nt = in / wide;
+      tile_order(at, rtiles, ctiles, &mt, &nt);
       int lo = 0, hi = p.G;   // tiles[lo] <= mt < tiles[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -262,22 +328,46 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       t.ns = (int32_t)((con * (int64_t)sizeof(E) + kStageK - 1) / kStageK);
       if (GATHER) {
         t.pa = (const uint8_t*)p.a;
-        t.na = p.S == 0 ? 0 : (p.S - 1) * ea + con * (int64_t)sizeof(E);
+        t.na = p.S == 0 ? 0 : (p.S - 1) * la + con * (int64_t)sizeof(E);
       } else {
-        t.pa = (const uint8_t*)p.a + (int64_t)t.lo * ea;
-        t.na = (p.R - 1 - t.lo) * ea + con * (int64_t)sizeof(E);
+        t.pa = (const uint8_t*)p.a + (int64_t)t.lo * la;
+        t.na = (p.R - 1 - t.lo) * la + con * (int64_t)sizeof(E);
       }
       const uint8_t* w = (const uint8_t*)p.b + (int64_t)t.g * p.N * p.K * (int64_t)sizeof(E);
       if (LAYOUT == 0) {
-        t.pb = w + (int64_t)t.n0 * eb;
-        t.nb = (p.N - 1 - t.n0) * eb + con * (int64_t)sizeof(E);
+        t.pb = w + (int64_t)t.n0 * lb;
+        t.nb = (p.N - 1 - t.n0) * lb + con * (int64_t)sizeof(E);
       } else {
         t.pb = w + (int64_t)t.n0 * sizeof(E);
-        t.nb = (p.N - 1) * eb + (p.K - t.n0) * (int64_t)sizeof(E);
+        t.nb = (p.N - 1) * lb + (p.K - t.n0) * (int64_t)sizeof(E);
+      }
+    }
+    t.last = 1;
+    if (part) {   // stages [s0, s1)
+      const int32_t which = (int32_t)(v / urem), n = (int32_t)uparts;
+      const int32_t each = t.ns / n, more = t.ns % n;   // the first `more` parts have one stage more
+      const int32_t s0 = which * each + min(which, more), s1 = s0 + each + (which < more ? 1 : 0);
+      t.last = s1 == t.ns;
+      t.ns = s1 - s0;
+      const int64_t da = kColA ? (int64_t)s0 * 64 * la : (int64_t)s0 * kStageK;
+      const int64_t db = kColB ? (int64_t)s0 * 64 * lb : (int64_t)s0 * kStageK;
+      t.pa += da;
+      t.na -= da;
+      if (!(GATHER && kColA)) {   // gathered rows move with their indexes
+        t.pb += db;
+        t.nb -= db;
+      }
+      if (kColA) {
+        t.lo += s0 * 64;
+        t.len -= s0 * 64;
       }
     }
     t.sa = bounded(t.pa, t.na);
     t.sb = bounded(t.pb, t.nb);
+    if (kColA) t.pa = uniform(t.pa), t.na = uniform(t.na);
+    if (kColB) t.pb = uniform(t.pb), t.nb = uniform(t.nb);
+    t.split = __builtin_amdgcn_readfirstlane(t.split);
+    t.last = __builtin_amdgcn_readfirstlane(t.last);
     t.ns = __builtin_amdgcn_readfirstlane(t.ns);
     t.len = __builtin_amdgcn_readfirstlane(t.len);
     t.lo = __builtin_amdgcn_readfirstlane(t.lo);
@@ -307,7 +397,8 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     vb[j] = kColB ? (uint32_t)((16 * wave + 2 * j + (lane >> 5)) * eb) + chunk_c(j)
                   : (uint32_t)((8 * (8 * wave + j) + (lane >> 3)) * eb) + chunk_k(j);
   // contiguous contraction: lanes past its end in the last stage
-  const uint32_t last_bytes = (uint32_t)((con * (int64_t)sizeof(E) - 1) % kStageK) + 1;
+  const uint32_t last_bytes =
+      (uint32_t)(((LAYOUT == 0 ? p.K : p.N) * (int64_t)sizeof(E) - 1) % kStageK) + 1;
   uint32_t past[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) past[j] = !kColA && chunk_k(j) >= last_bytes ? kOut : 0u;
@@ -365,8 +456,24 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       const uint32_t r = (uint32_t)(8 * j + (lane >> 3));
       const uint32_t row = *(__attribute__((address_space(3))) const uint32_t*)(ring0 + r * 4);
       const bool ok = ((int)(8 * kPartsA * wave + r) < n.rows) & (row < (uint32_t)p.S);
-      va[j] = (row * (uint32_t)ea + chunk_k(j)) | (ok ? 0u : kOut);
+      va[j] = (row * ea + chunk_k(j)) | (ok ? 0u : kOut);
     }
+  };
+
+  // int8: scales of tile n's rows (this wave's 64, of the rows that copy_rows
+  // brought) and columns (64) to LDS, with the copies; zeros outside.
+  int side = 0;   // place of the computed tile's
+  auto copy_scales = [&](const Tile& n, int at) {
+    const RaggedArgs& p = args;
+    const uint32_t to = (uint32_t)(uintptr_t)scales + (uint32_t)(at * 2048 + wave * 256);
+    const uint32_t r = (uint32_t)(64 * wave + lane);
+    uint32_t row = r;
+    if (GATHER) row = *(__attribute__((address_space(3))) const uint32_t*)(ring0 + (uint32_t)lane * 4);
+    const i32x4 rs = GATHER ? bounded(p.sa, p.S * 4) : bounded(p.sa + n.lo, (int64_t)n.rows * 4);
+    const bool ok = ((int)r < n.rows) & (!GATHER | (row < (uint32_t)p.S));
+    const i32x4 cs = bounded(p.sb + (int64_t)n.g * p.N + n.n0, (p.N - n.n0) * 4);
+    copy4(rs, (row * 4u) | (ok ? 0u : kOut), 0u, __builtin_amdgcn_readfirstlane(to));
+    copy4(cs, r * 4u, 0u, __builtin_amdgcn_readfirstlane(to + 1024u));
   };
 
   struct Stage {
@@ -389,13 +496,15 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     s.lds = lds0 + (uint32_t)(((slot0 + v) & 1) * kStage);
     s.soff = none ? 0u : (uint32_t)st * kStageK;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) s.kill[j] = none ? kOut : (st == n.ns - 1 ? past[j] : 0u);
+    for (int j = 0; j < 2; ++j) s.kill[j] = none ? kOut : (st == n.ns - 1 && n.last ? past[j] : 0u);
     s.sa = n.sa;
     s.sb = n.sb;
     if (kColA)
-      s.sa = bounded(n.pa + (int64_t)st * 64 * ea, none ? 0 : n.na - (int64_t)st * 64 * ea);
+      s.sa = bounded(n.pa + (uint64_t)(64u * (uint32_t)st) * ea,
+                     none ? 0 : n.na - (int64_t)((uint64_t)(64u * (uint32_t)st) * ea));
     if (kColB && !(GATHER && kColA))
-      s.sb = bounded(n.pb + (int64_t)st * 64 * eb, none ? 0 : n.nb - (int64_t)st * 64 * eb);
+      s.sb = bounded(n.pb + (uint64_t)(64u * (uint32_t)st) * eb,
+                     none ? 0 : n.nb - (int64_t)((uint64_t)(64u * (uint32_t)st) * eb));
     // the same in every lane, which the compiler does not always see
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -422,7 +531,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         const uint32_t row = *(__attribute__((address_space(3))) const uint32_t*)(
             ring0 + (uint32_t)(s.at & 7) * 256u + r * 4);
         const bool ok = ((int)(s.st * 64 + r) < s.len) & (row < (uint32_t)p.S);
-        copy16(s.sb, (row * (uint32_t)eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
+        copy16(s.sb, (row * eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
       } else {
         copy16(s.sb, kColB ? vb[j] : (vb[j] | s.kill[j & 1]), kColB ? 0u : s.soff, at);
       }
@@ -480,6 +589,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       __builtin_amdgcn_s_waitcnt(vm_wait(0));
       take_rows(t);
     }
+    if constexpr (kInt8) copy_scales(t, side);
     __builtin_amdgcn_sched_barrier(0);
     for (int st = 0; st < 2; ++st) {   // a stage past the last copies zeros
       const Stage s = stage(st, st);
@@ -538,7 +648,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   };
 
   uint32_t tile = blockIdx.x;
-  if (tile >= ntiles) return;
+  if (tile >= nunits) return;
   t = describe(tile);
   start();
   bool chained = false;   // the previous tile's last stages carried this one's first two
@@ -546,14 +656,15 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   for (;;) {
     const int ns = t.ns;
     // what the stores need of this tile
-    const int32_t rows = t.rows, n0 = t.n0, m0 = t.m0, g = t.g;
+    const int32_t rows = t.rows, n0 = t.n0, m0 = t.m0, g = t.g, split = t.split;
     const uint32_t next = tile + gridDim.x;
     // Chain: the last two stages of a tile carry the copies of the next tile's
     // first two and read its first fragments, as if the contraction went on.
     // Otherwise they copy nothing (an empty range) and the next tile starts
     // anew.  The indexes of gathered rows go ahead, from four stages before
-    // the end.
-    bool chain = next < ntiles && ns >= (GATHER ? 4 : 2);
+    // the end; int8's scales take the place that the previous tile's had, so a
+    // barrier of this tile lies between.
+    bool chain = next < nunits && ns >= (GATHER ? 4 : (kInt8 ? 3 : 2));
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
@@ -569,6 +680,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
             t = describe(next);
             chain = t.ns >= 2;
             if constexpr (GATHER && !kColA) take_rows(t);
+            if constexpr (kInt8) copy_scales(t, side ^ 1);
           }
           if (!chain) t.ns = 0;
         }
@@ -595,28 +707,38 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     // the lane number anew for each tile: addresses formed from it would otherwise
     // be kept, and spilled, through the whole loop
     const int ln = (int)hide((uint32_t)lane);
+    const RaggedArgs& p = args;
+    const int64_t cols = LAYOUT == 0 ? p.N : p.K;
+    if (split >= 0) {
+      // a part (the last unit of its workgroup): the accumulators as they lie
+      const auto ws = make_rsrc((const uint8_t*)p.ws + (int64_t)split * (kTileM * kTileN * 4),
+                                kTileM * kTileN * 4);
+#pragma unroll
+      for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // (values of this branch's own: moved ahead of the branch, all 256
+          // accumulators would be spilled)
+          asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const auto x = acc[i][j][4 * q + e];   // (a bit cast of the element itself reads element 0)
+              v[e] = __builtin_bit_cast(uint32_t, x);
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(
+                v, ws, (uint32_t)((((wave * FA + i) * 4 + j) * 4 + q) * 1024 + ln * 16), 0, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      return;
+    }
     float srow[FA];
-    u32x4_t scol[4][4];
     if constexpr (kInt8) {
-      // scales of the tile's rows and columns (0 outside)
-      const auto si = make_rsrc(p.row_index + m0, (int64_t)rows * 4);
-      const auto sr = GATHER ? make_rsrc(p.sa, p.S * 4) : make_rsrc(p.sa + m0, (int64_t)rows * 4);
-      const auto sc = make_rsrc(p.sb + (int64_t)g * p.N + n0, (cols - n0) * 4);
 #pragma unroll
-      for (int i = 0; i < FA; ++i) {
-        const int m = wm * 32 * FA + 32 * i + (ln & 31);
-        const uint32_t row = GATHER ? __builtin_amdgcn_raw_buffer_load_b32(si, (uint32_t)m * 4u, 0, 0)
-                                    : (uint32_t)m;
-        const bool ok = (m < rows) & (!GATHER | (row < (uint32_t)p.S));
-        srow[i] = __uint_as_float(
-            __builtin_amdgcn_raw_buffer_load_b32(sr, (row * 4u) | (ok ? 0u : kOut), 0, 0));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          scol[j][q] = __builtin_amdgcn_raw_buffer_load_b128(
-              sc, (uint32_t)(wn * 128 + 32 * j + 8 * q + 4 * (ln >> 5)) * 4u, 0, 0);
+      for (int i = 0; i < FA; ++i) srow[i] = scales[side][0][wm * 32 * FA + 32 * i + (ln & 31)];
     }
 
     // Stores, bounded like the loads: lanes past the tile's rows or columns get an
@@ -630,7 +752,8 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     const int right = (int)min((int64_t)kTileN, cols - n0);   // columns of the tile
     auto value = [&](int i, int j, int r) {
       if constexpr (kInt8)
-        return (float)acc[i][j][r] * srow[i] * __uint_as_float(scol[j][r >> 2][r & 3]);
+        return (float)acc[i][j][r] * srow[i] *
+               scales[side][1][wn * 128 + 32 * j + 8 * (r >> 2) + 4 * (ln >> 5) + (r & 3)];
       else
         return acc[i][j][r];
     };
@@ -641,6 +764,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       const uint32_t roff = m < rows ? (uint32_t)m * ec : kOut;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        asm volatile("" : "+a"(acc[i][j]));
         if constexpr (sizeof(OE) == 4) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -672,9 +796,10 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (next >= ntiles) return;
+    if (next >= nunits) return;
     slot0 = (slot0 + ns) & 1;
     ring_at += ns;
+    if (kInt8) side ^= 1;
     chained = chain;
     tile = next;
     if (!chain) {
@@ -685,6 +810,76 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       __syncthreads();
       t = describe(tile);
       start();
+    }
+  }
+}
+
+// Sums of the parts of split tiles, in order, with the conversion and stores of the kernel above.
+// Workgroup b takes 32-row strips b, b + grid, ... of the split tiles (strip: one wave's fragment row).
+template <typename T, typename O, int LAYOUT, int FA>
+__global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t tile_grid) {
+  constexpr bool kInt8 = sizeof(typename T::elem) == 1;
+  constexpr int kTileM = 64 * FA;
+  constexpr int kStrips = 4 * FA;
+  const int lane = threadIdx.x & 63, j = threadIdx.x >> 6;
+  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
+  const uint32_t ctiles = (uint32_t)((cols + kTileN - 1) / kTileN);
+  const uint32_t band = (uint32_t)((p.N + kTileM - 1) / kTileM);
+  uint32_t rtiles = (uint32_t)p.G * band;
+  if (LAYOUT != 2)
+    rtiles = (uint32_t)wave_row_tile(p.m_splits, p.G, p.R, kTileM, -1, true).total;
+  const Units u = units_of(rtiles * ctiles, tile_grid, part_stages(LAYOUT, p, sizeof(typename T::elem)), true);
+  if (u.parts < 2) return;
+  for (uint32_t b = blockIdx.x; b < u.rem * kStrips; b += gridDim.x) {
+    const uint32_t v = b / kStrips, strip = b % kStrips, at = u.full + v;
+    const int wave = (int)strip / FA, i = (int)strip % FA;
+    int32_t mt, nt, g;
+    int64_t m0, rows;
+    if (LAYOUT == 2) {
+      g = (int32_t)(at / (band * ctiles));
+      tile_order(at % (band * ctiles), band, ctiles, &mt, &nt);
+      m0 = (int64_t)mt * kTileM;
+      rows = min((int64_t)kTileM, p.N - m0);
+    } else {
+      tile_order(at, rtiles, ctiles, &mt, &nt);
+      const RowSpan s = wave_row_tile(p.m_splits, p.G, p.R, kTileM, mt, false);
+      g = s.g;
+      m0 = s.row0;
+      rows = s.rows;
+    }
+    typedef typename std::conditional<kInt8, i32x4, float __attribute__((ext_vector_type(4)))>::type V;
+    V sum[4];
+    for (uint32_t part = 0; part < u.parts; ++part) {
+      const uint8_t* ws = (const uint8_t*)p.ws + (int64_t)(part * u.rem + v) * (kTileM * kTileN * 4) +
+                          ((wave * FA + i) * 4 + j) * 4096 + lane * 16;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const V x = *(const V*)(ws + q * 1024);
+        if (part == 0) sum[q] = x;
+        else sum[q] += x;
+      }
+    }
+    const int m = (wave >> 1) * 32 * FA + 32 * i + (lane & 31);
+    if (m >= rows) continue;
+    float sa = 0.f;
+    if (kInt8) {
+      const int64_t row = p.row_index != nullptr ? p.row_index[m0 + m] : m0 + m;
+      if (row >= 0 && row < p.S) sa = p.sa[row];
+    }
+    typedef typename O::elem OE;
+    OE* c = (OE*)p.c + (LAYOUT == 2 ? ((int64_t)g * p.N + m0 + m) * p.K : (m0 + m) * p.ldc);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t n = (int64_t)nt * kTileN + (wave & 1) * 128 + 32 * j + 8 * q + 4 * (lane >> 5);
+      if (n >= cols) continue;   // columns come in fours (rows are multiples of 16 bytes)
+      OE o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = (float)sum[q][e];
+        if (kInt8) x = x * sa * p.sb[(int64_t)g * p.N + n + e];
+        o[e] = O::cvt(x);
+      }
+      __builtin_memcpy(__builtin_assume_aligned(c + n, sizeof(o)), o, sizeof(o));
     }
   }
 }

@@ -9,4 +9,6 @@ hipError_t launch_ragged_tile_int8(int out, const RaggedArgs& p, hipStream_t st)
   return launch_tile_gather<TypeI8, OutF16, 0>(p, st);
 }
 
+size_t ragged_workspace_bytes() { return (size_t)compute_units() * 256 * 256 * 4; }
+
 }  // namespace mx

@@ -18,10 +18,17 @@ inline int compute_units() {
 template <typename T, typename O, int LAYOUT, int FA, bool GATHER>
 hipError_t launch_tile(const RaggedArgs& p, hipStream_t st) {
   const int64_t m = 64 * FA, cols = ((LAYOUT == 0 ? p.N : p.K) + kTileN - 1) / kTileN;
-  const int64_t most = cols * (LAYOUT == 2 ? p.G * ((p.N + m - 1) / m)
+  // one workgroup per CU; fewer where there are fewer tiles than CUs and no
+  // workspace to split them
+  const int64_t most = p.ws != nullptr ? INT32_MAX : cols * (LAYOUT == 2 ? p.G * ((p.N + m - 1) / m)
                                            : p.R / m + std::min<int64_t>(p.G, p.R));
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, compute_units()));
   ragged_tile_kernel<T, O, LAYOUT, FA, GATHER><<<dim3(grid), dim3(256), 0, st>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ws == nullptr) return e;
+  // half the tiles of a round at most are split, 4 FA strips each
+  const unsigned strips = std::max(1u, grid / 2) * 4 * FA;
+  ragged_join_kernel<T, O, LAYOUT, FA><<<dim3(std::min(strips, 1024u)), dim3(256), 0, st>>>(p, grid);
   return hipGetLastError();
 }
 

@@ -26,7 +26,7 @@ def lib():
 
 def _gemm(lib, layout=NT, type=BF16, a=FAKE, lda=64, b=FAKE, ldb=64, c=FAKE, ldc=64, c_type=BF16, R=8, S=8,
           N=64, K=64, ms=FAKE, G=2, index=None):
-    st = lib.mxfp8_ragged_gemm(layout, type, a, lda, b, ldb, c, ldc, c_type, R, S, N, K, ms, G, index, None)
+    st = lib.mxfp8_ragged_gemm(layout, type, a, lda, b, ldb, c, ldc, c_type, R, S, N, K, ms, G, index, None, 0, None)
     return st, lib.mxfp8_last_error().decode()
 
 
@@ -64,7 +64,7 @@ def test_quantize_refuses(lib):
 def test_int8_gemm_refuses(lib):
     def call(q=FAKE, ldq=64, sc=FAKE, w=FAKE, ws=FAKE, c=FAKE, ldc=64, ct=BF16, R=8, S=8, N=64, K=64, ms=FAKE,
              G=2, index=None):
-        return lib.mxfp8_ragged_gemm_int8(q, ldq, sc, w, ws, c, ldc, ct, R, S, N, K, ms, G, index, None)
+        return lib.mxfp8_ragged_gemm_int8(q, ldq, sc, w, ws, c, ldc, ct, R, S, N, K, ms, G, index, None, 0, None)
     assert call(ct=3) == 2
     for kw in ({"N": 0}, {"K": 0}, {"G": 0}, {"G": 2000}, {"S": 9}, {"ms": None}, {"R": -1, "S": -1}):
         assert call(**kw) == 1, kw

@@ -7,6 +7,7 @@ torch stream (or the stream given).  The entry points have the C names
 without the ``mxfp8_`` prefix.
 """
 
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -43,8 +44,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The raw stream: the one given, or torch's current one (without making
+    the stream object, which costs as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, dtype, shape, name):
@@ -529,8 +533,9 @@ def _type_of(t, name, floats=(torch.bfloat16, torch.float16)):
 
 
 def _same_device(like, **tensors):
+    at = like.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != like.device:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
 
 
@@ -703,6 +708,7 @@ class Route:
     renormalize: bool = True
 
 
+@functools.lru_cache(maxsize=256)
 def moe_route_workspace_bytes(tokens, experts):
     return int(_lib().mxfp8_moe_route_workspace_bytes(tokens, experts))
 
@@ -727,13 +733,14 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
                     _empty((e,), torch.int64, logits),
                     _empty((t * top_k,), torch.int32, logits),
                     _empty((t, top_k), torch.int32, logits))
+    else:
+        _need(out.ids, torch.int32, (t, top_k), "ids")
+        _need(out.weights, torch.float32, (t, top_k), "weights")
+        _need(out.m_splits, torch.int64, (e,), "m_splits")
+        _need(out.row_token, torch.int32, (t * top_k,), "row_token")
+        _need(out.row_pos, torch.int32, (t, top_k), "row_pos")
     out.renormalize = bool(renormalize)
-    _need(out.ids, torch.int32, (t, top_k), "ids")
-    _need(out.weights, torch.float32, (t, top_k), "weights")
-    _need(out.m_splits, torch.int64, (e,), "m_splits")
-    _need(out.row_token, torch.int32, (t * top_k,), "row_token")
-    _need(out.row_pos, torch.int32, (t, top_k), "row_pos")
-    need = lib.mxfp8_moe_route_workspace_bytes(t, e)
+    need = moe_route_workspace_bytes(t, e)
     size = need
     if workspace is not None:
         size = workspace.numel() * workspace.element_size()

@@ -617,7 +617,6 @@ mxfp8_status check_join(const char* fn, int32_t type, int64_t T, int64_t R, int6
   REQUIRE(T >= 0 && R >= 0 && T <= kI32Max && R <= kI32Max,
           "%s: T = %lld and R = %lld must be 0 to 2^31 - 1", fn, (long long)T, (long long)R);
   REQUIRE(H >= 1 && H <= kI32Max, "%s: H = %lld must be 1 to 2^31 - 1", fn, (long long)H);
-  REQUIRE(T * ((H + 7) / 8) / 256 < kI32Max, "%s: T * H is too large", fn);
   REQUIRE(top_k >= 1 && top_k <= 16, "%s: top_k = %d must be 1 to 16", fn, (int)top_k);
   return MXFP8_OK;
 }
@@ -643,7 +642,7 @@ mxfp8_status mxfp8_moe_route(const void* logits, int32_t type, int64_t T, int32_
           "%s: needs a workspace of %zu bytes", fn, need);
   REQUIRE(aligned_to(logits, type == 0 ? 4 : 2) && aligned_to(ids, 4) && aligned_to(weights, 4) &&
               aligned_to(m_splits, 8) && aligned_to(row_token, 4) && aligned_to(row_pos, 4) &&
-              (need == 0 || aligned_to(workspace, 2)),
+              (need == 0 || aligned_to(workspace, 4)),
           "%s: a pointer is not aligned to its element", fn);
   return hip_status(mx::launch_route(logits, type, T, E, top_k, renormalize != 0, token_mask, ids,
                                      weights, m_splits, row_token, row_pos, workspace,

@@ -515,6 +515,15 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     s.soff = __builtin_amdgcn_readfirstlane(s.soff);
     return s;
   };
+  // TN: the row indexes of this lane's contraction rows in a stage, from the
+  // ring: read together ahead of the stage's copies, so that no copy waits.
+  uint32_t rows_at[8];
+  auto read_index = [&](const Stage& s) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      rows_at[j] = *(__attribute__((address_space(3))) const uint32_t*)(
+          ring0 + (uint32_t)(s.at & 7) * 256u + (uint32_t)(16 * wave + 2 * j + (lane >> 5)) * 4u);
+  };
   // copy c of a stage: A and B parts in turn (then what is left of B)
   auto copy = [&](const Stage& s, auto C) {
     constexpr int c = decltype(C)::value;
@@ -526,12 +535,9 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     } else {
       const uint32_t at = s.lds + kOffB + (uint32_t)(wave * 8192 + j * 1024);
       if constexpr (GATHER && kColA) {
-        // the row index of this lane's contraction row, from the ring
-        const uint32_t r = (uint32_t)(16 * wave + 2 * j) + (uint32_t)(lane >> 5);
-        const uint32_t row = *(__attribute__((address_space(3))) const uint32_t*)(
-            ring0 + (uint32_t)(s.at & 7) * 256u + r * 4);
-        const bool ok = ((int)(s.st * 64 + r) < s.len) & (row < (uint32_t)p.S);
-        copy16(s.sb, (row * eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
+        const int r = 16 * wave + 2 * j + (lane >> 5);
+        const bool ok = (s.st * 64 + r < s.len) & (rows_at[j] < (uint32_t)p.S);
+        copy16(s.sb, (rows_at[j] * eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
       } else {
         copy16(s.sb, kColB ? vb[j] : (vb[j] | s.kill[j & 1]), kColB ? 0u : s.soff, at);
       }
@@ -593,6 +599,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     __builtin_amdgcn_sched_barrier(0);
     for (int st = 0; st < 2; ++st) {   // a stage past the last copies zeros
       const Stage s = stage(st, st);
+      if constexpr (GATHER && kColA) read_index(s);
       unroll<kParts>([&](auto C) { copy(s, C); });
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -607,6 +614,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   // has waited for its reads) and the copies of the stage two ahead begin.
   auto first_half = [&](int st, const Stage& cp) {
     const Base x = base((slot0 + st) & 1, H1{});
+    if constexpr (GATHER && kColA) read_index(cp);
     __builtin_amdgcn_sched_barrier(0);
     unroll<kMfma>([&](auto Q) {
       constexpr int q = decltype(Q)::value, m = kMfma / 2;

@@ -39,24 +39,42 @@ __device__ __forceinline__ void store_float(void* p, int64_t i, float v) {
   else ((_Float16*)p)[i] = (_Float16)v;
 }
 
-// Reductions over the L consecutive lanes (L a power of two) that share a token.
+// Reductions over the L = 16 or 64 lanes that share a token, every lane getting
+// the result: rotations within rows of 16 lanes (DPP, no LDS), then the
+// gfx950 swaps of rows and halves.
+template <int CTRL>
+__device__ __forceinline__ float rotate(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int L, typename F>
+__device__ __forceinline__ float lanes_all(float v, F f) {
+  v = f(v, rotate<0x128>(v));   // row_ror:8, 4, 2, 1
+  v = f(v, rotate<0x124>(v));
+  v = f(v, rotate<0x122>(v));
+  v = f(v, rotate<0x121>(v));
+  if (L == 64) {
+    const uint32_t u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = f(__uint_as_float((uint32_t)r[0]), __uint_as_float((uint32_t)r[1]));
+    const uint32_t w = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    v = f(__uint_as_float((uint32_t)h[0]), __uint_as_float((uint32_t)h[1]));
+  }
+  return v;
+}
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+  return lanes_all<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  return lanes_all<L>(v, [](float a, float b) { return a + b; });
 }
 template <int L>
 __device__ __forceinline__ int lanes_min(int v) {
-#pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) v = min(v, __shfl_xor(v, d, 64));
-  return v;
+  return __float_as_int(lanes_all<L>(__int_as_float(v), [](float a, float b) {
+    return __int_as_float(min(__float_as_int(a), __float_as_int(b)));
+  }));
 }
 
 struct RouteArgs {
@@ -71,75 +89,113 @@ struct RouteArgs {
   int64_t* m_splits;        // [E]
   int32_t* row_token;       // [T k]
   int32_t* row_pos;         // [T, k]
-  uint16_t* hist;           // workspace [blocks, E]: rows of each expert in a chunk
+  uint16_t* hist;           // workspace [blocks, E rounded up to 2]: rows of each expert in a chunk
+  int32_t vec;              // logits rows lie on 4 values
 };
 
-// A token's logits, E / L (rounded up) in each of its L lanes: lane s holds
-// experts s, s + L, ...  NaN and what lies past E become -inf.
+// A token's logits in its L lanes: lane s holds experts 4 s .. 4 s + 3, then
+// 4 (L + s) ..., V of them (expert_of).  NaN and what lies past E become -inf.
+template <int L>
+__device__ __forceinline__ int expert_of(int sub, int i) {
+  return ((i >> 2) * L + sub) * 4 + (i & 3);
+}
 template <int TYPE, int L, int V>
 __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, int sub,
-                                            bool on, float* v) {
+                                            bool on, bool vec, float* v) {
+  constexpr int kSize = TYPE == 0 ? 4 : 2;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = sub + i * L;
-    const float x = on && e < E ? load_float<TYPE>(logits, t * E + e) : -INFINITY;
-    v[i] = x == x ? x : -INFINITY;
+  for (int i = 0; i < V; i += 4) {
+    const int e = expert_of<L>(sub, i);
+    char raw[4 * kSize];
+    if (vec) {   // E is a multiple of 4: all four or none
+      if (on && e < E)
+        __builtin_memcpy(raw, __builtin_assume_aligned((const char*)logits + (t * E + e) * kSize, 4 * kSize),
+                         sizeof(raw));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (on && e + c < E)
+          __builtin_memcpy(raw + c * kSize, (const char*)logits + (t * E + e + c) * kSize, kSize);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float x = load_float<TYPE>(raw, c);
+      v[i + c] = on && e + c < E && x == x ? x : -INFINITY;
+    }
   }
 }
 
 // Choice and weights of one workgroup's tokens, and which tokens of the chunk
-// each expert got (bits[e * words + t / 32]).
-template <int TYPE, int L, int V>
-__device__ void choose(const RouteArgs& p, int64_t t0, int n, uint32_t* bits) {
-  constexpr int kTokens = kRouteThreads / L;   // tokens at a time
+// each expert got (bits[e * words + t / 32]).  U tokens for each group of L lanes
+// at a time: their loads and reductions overlap.
+template <int TYPE, int L, int V, int U>
+__device__ __forceinline__ void choose_some(const RouteArgs& p, int64_t t0, int n, int base,
+                                            uint32_t* bits) {
+  constexpr int kTokens = kRouteThreads / L;
   const int sub = threadIdx.x % L, words = p.chunk / 32;
-  for (int base = 0; base < n; base += kTokens) {
-    const int at = base + (int)threadIdx.x / L;
-    const int64_t t = t0 + at;
-    const bool on = at < n && (p.mask == nullptr || p.mask[t] != 0);
-    float v[V];
-    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on, v);
-    float top = -INFINITY, sum = 0.f, mine_w = 0.f;
-    int mine_id = -1;
-    float all = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      float best = v[0];
+  float v[U][V], top[U], all[U], mine[U];
+  int at[U], mine_id[U];
 #pragma unroll
-      for (int i = 1; i < V; ++i) best = fmaxf(best, v[i]);
+  for (int u = 0; u < U; ++u) {
+    at[u] = base + u * kTokens + (int)threadIdx.x / L;
+    const int64_t t = t0 + at[u];
+    const bool on = at[u] < n && (p.mask == nullptr || p.mask[t] != 0);
+    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on, p.vec != 0, v[u]);
+    top[u] = 0.f;
+    all[u] = 0.f;
+    mine[u] = -INFINITY;
+    mine_id[u] = -1;
+  }
+  for (int j = 0; j < p.k; ++j) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float best = v[u][0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = fmaxf(best, v[u][i]);
       best = lanes_max<L>(best);
       int id = INT32_MAX;
 #pragma unroll
       for (int i = V - 1; i >= 0; --i)
-        if (v[i] == best) id = sub + i * L;
+        if (v[u][i] == best) id = expert_of<L>(sub, i);
       id = lanes_min<L>(id);
       const bool live = best > -INFINITY;
       if (j == 0) {
-        top = live ? best : 0.f;
+        top[u] = live ? best : 0.f;
         if (!p.renorm) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) all += expf(v[i] - top);
-          all = lanes_sum<L>(all);
+          for (int i = 0; i < V; ++i) all[u] += expf(v[u][i] - top[u]);
+          all[u] = lanes_sum<L>(all[u]);
         }
       }
-      const float w = live ? expf(best - top) : 0.f;
-      sum += w;
-      // the chosen one leaves
+      // the chosen one leaves; lane j keeps choice j (k <= 16 <= L)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (live && id == sub + i * L) v[i] = -INFINITY;
-      if (live && sub == 0) atomicOr(&bits[id * words + at / 32], 1u << (at & 31));
-      // lane j % L keeps choice j (k <= 16 <= L)
-      if (sub == j) {
-        mine_w = w;
-        mine_id = live ? id : -1;
+        if (live && id == expert_of<L>(sub, i)) v[u][i] = -INFINITY;
+      if (sub == j && live) {
+        mine[u] = best;
+        mine_id[u] = id;
+        atomicOr(&bits[id * words + at[u] / 32], 1u << (at[u] & 31));
       }
     }
-    const float z = p.renorm ? sum : all;
-    if (at < n && sub < p.k) {
-      p.ids[t * p.k + sub] = mine_id;
-      p.weights[t * p.k + sub] = mine_id >= 0 ? mine_w / z : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float w = mine_id[u] >= 0 ? expf(mine[u] - top[u]) : 0.f;
+    const float z = p.renorm ? lanes_sum<L>(w) : all[u];
+    if (at[u] < n && sub < p.k) {
+      const int64_t c = (t0 + at[u]) * p.k + sub;
+      p.ids[c] = mine_id[u];
+      p.weights[c] = mine_id[u] >= 0 ? w / z : 0.f;
     }
   }
+}
+template <int TYPE, int L, int V>
+__device__ __forceinline__ void choose(const RouteArgs& p, int64_t t0, int n, uint32_t* bits) {
+  constexpr int kTokens = kRouteThreads / L;
+  int base = 0;
+  if (V <= 8)
+    for (; base + kTokens < n; base += 2 * kTokens) choose_some<TYPE, L, V, 2>(p, t0, n, base, bits);
+  for (; base < n; base += kTokens) choose_some<TYPE, L, V, 1>(p, t0, n, base, bits);
 }
 
 // Exclusive prefix over the experts of total[0..E), by the whole workgroup
@@ -159,28 +215,15 @@ __device__ int prefix_experts(int mine, int* scan) {
   return before + v - mine;
 }
 
-// Rows of this chunk: position base[e] + the number of earlier tokens of the
-// chunk that chose e.
-__device__ void place(const RouteArgs& p, int64_t t0, int n, const uint32_t* bits,
-                      const int* base) {
-  const int words = p.chunk / 32;
-  for (int i = threadIdx.x; i < n * p.k; i += kRouteThreads) {
-    const int at = i / p.k;
-    const int64_t c = t0 * p.k + i;
-    const int id = p.ids[c];
-    int pos = -1;
-    if (id >= 0) {
-      const uint32_t* b = bits + id * words;
-      int rank = __popc(b[at / 32] & ((1u << (at & 31)) - 1u));
-      for (int w = 0; w < at / 32; ++w) rank += __popc(b[w]);
-      pos = base[id] + rank;
-      p.row_token[pos] = (int32_t)(t0 + at);
-    }
-    p.row_pos[c] = pos;
-  }
+// The rank of choice i of the chunk: earlier tokens of the chunk with the same expert.
+__device__ __forceinline__ int rank_of(const uint32_t* bits, int words, int id, int at) {
+  const uint32_t* b = bits + id * words;
+  int rank = __popc(b[at / 32] & ((1u << (at & 31)) - 1u));
+  for (int w = 0; w < at / 32; ++w) rank += __popc(b[w]);
+  return rank;
 }
 
-// LDS: bits [E * words], then base [E].
+// LDS: bits [E * words] (and base [E] in the one-launch form).
 extern __shared__ uint32_t route_lds[];
 
 // One workgroup for all tokens (T <= chunk): everything in one launch.
@@ -204,12 +247,22 @@ __global__ __launch_bounds__(kRouteThreads) void route_one_kernel(RouteArgs p) {
   }
   if (tid == p.E - 1) routed = at + mine;
   __syncthreads();
-  place(p, 0, (int)p.T, bits, base);
-  for (int64_t i = routed + tid; i < p.T * p.k; i += kRouteThreads) p.row_token[i] = -1;
+  const int n = (int)p.T * p.k;
+  for (int i = tid; i < n; i += kRouteThreads) {
+    const int t = i / p.k, id = p.ids[i];
+    int pos = -1;
+    if (id >= 0) {
+      pos = base[id] + rank_of(bits, words, id, t);
+      p.row_token[pos] = t;
+    }
+    p.row_pos[i] = pos;
+  }
+  for (int i = routed + tid; i < n; i += kRouteThreads) p.row_token[i] = -1;
 }
 
-// Several workgroups: choice and the chunk's counts, then, in a second launch
-// that sees all counts, the positions.
+// Several workgroups: choice, the chunk's counts, and each choice's rank within
+// its chunk (left in row_pos); then, in a second launch that sees all counts,
+// the positions.
 template <int TYPE, int L, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs p) {
   const int tid = threadIdx.x, words = p.chunk / 32;
@@ -222,41 +275,47 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose_kernel(RouteArgs p
   if (tid < p.E) {
     int mine = 0;
     for (int w = 0; w < words; ++w) mine += __popc(route_lds[tid * words + w]);
-    p.hist[(int64_t)blockIdx.x * p.E + tid] = (uint16_t)mine;
+    p.hist[(int64_t)blockIdx.x * ((p.E + 1) & ~1) + tid] = (uint16_t)mine;
+  }
+  for (int i = tid; i < n * p.k; i += kRouteThreads) {
+    const int id = p.ids[t0 * p.k + i];
+    p.row_pos[t0 * p.k + i] = id >= 0 ? rank_of(route_lds, words, id, i / p.k) : -1;
   }
 }
 
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs p) {
-  __shared__ int scan[16], routed;
-  __shared__ int part[2][kRouteThreads];
-  const int tid = threadIdx.x, words = p.chunk / 32;
-  uint32_t* bits = route_lds;
-  int* base = (int*)(route_lds + p.E * words);
+  __shared__ int scan[16], routed, base[kRouteThreads];
+  __shared__ uint32_t part[2][kRouteThreads][2];
+  const int tid = threadIdx.x, pairs = (p.E + 1) / 2;
   const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
   const int n = (int)min((int64_t)p.chunk, p.T - t0);
-  for (int i = tid; i < p.E * words; i += kRouteThreads) bits[i] = 0;
   // counts of every chunk: slice s of the workgroup sums chunks s, s + slices, ...
-  // for its expert, apart for all chunks and for those before this one
-  const int slices = max(1, kRouteThreads / p.E), s = tid / p.E, e = tid % p.E;
-  int all = 0, before = 0;
-  if (s < slices)
+  // for a pair of experts, apart for all chunks and for those before this one
+  const int slices = kRouteThreads / pairs, s = tid / pairs, e2 = tid % pairs;
+  uint32_t all0 = 0, all1 = 0, bef0 = 0, bef1 = 0;
+  if (s < slices) {
+    const uint32_t* h = (const uint32_t*)p.hist + e2;
+#pragma unroll 4
     for (int b = s; b < p.blocks; b += slices) {
-      const int h = p.hist[(int64_t)b * p.E + e];
-      all += h;
-      if (b < (int)blockIdx.x) before += h;
+      const uint32_t x = h[(int64_t)b * pairs];
+      all0 += x & 0xFFFFu;
+      all1 += x >> 16;
+      if (b < (int)blockIdx.x) {
+        bef0 += x & 0xFFFFu;
+        bef1 += x >> 16;
+      }
     }
-  part[0][tid] = all;
-  part[1][tid] = before;
-  __syncthreads();
-  for (int i = tid; i < n * p.k; i += kRouteThreads) {
-    const int id = p.ids[t0 * p.k + i], at = i / p.k;
-    if (id >= 0) atomicOr(&bits[id * words + at / 32], 1u << (at & 31));
   }
-  all = before = 0;
+  part[0][tid][0] = all0;
+  part[0][tid][1] = all1;
+  part[1][tid][0] = bef0;
+  part[1][tid][1] = bef1;
+  __syncthreads();
+  int all = 0, before = 0;
   if (tid < p.E)
     for (int i = 0; i < slices; ++i) {
-      all += part[0][i * p.E + tid];
-      before += part[1][i * p.E + tid];
+      all += (int)part[0][i * pairs + tid / 2][tid & 1];
+      before += (int)part[1][i * pairs + tid / 2][tid & 1];
     }
   const int at = prefix_experts(all, scan);
   if (tid < p.E) {
@@ -265,7 +324,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs p)
   }
   if (tid == p.E - 1) routed = at + all;
   __syncthreads();
-  place(p, t0, n, bits, base);
+  for (int i = tid; i < n * p.k; i += kRouteThreads) {
+    const int64_t c = t0 * p.k + i;
+    const int id = p.ids[c];
+    if (id < 0) continue;   // row_pos is -1 already
+    const int pos = base[id] + p.row_pos[c];
+    p.row_token[pos] = (int32_t)(t0 + i / p.k);
+    p.row_pos[c] = pos;
+  }
   for (int64_t i = routed + (int64_t)blockIdx.x * kRouteThreads + tid; i < p.T * p.k;
        i += (int64_t)gridDim.x * kRouteThreads)
     p.row_token[i] = -1;
@@ -278,7 +344,7 @@ struct RouteBwdArgs {
   const float* dweights;
   void* dlogits;
   int64_t T;
-  int32_t E, k, renorm;
+  int32_t E, k, renorm, vec;
 };
 
 template <int TYPE, int L, int V>
@@ -303,7 +369,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
   const int first = __shfl(id, (threadIdx.x & 63) / L * L, 64);
   if (!p.renorm) {
     float v[V];
-    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on && first >= 0, v);
+    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on && first >= 0, p.vec != 0, v);
     float top = v[0], sum = 0.f;
 #pragma unroll
     for (int i = 1; i < V; ++i) top = fmaxf(top, v[i]);
@@ -324,13 +390,24 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
     const float aj = __shfl(add, src, 64);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (ej == sub + i * L) g[i] += aj;
+      if (ej == expert_of<L>(sub, i)) g[i] += aj;
   }
   if (!on) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = sub + i * L;
-    if (e < p.E) store_float<TYPE>(p.dlogits, t * p.E + e, g[i]);
+  for (int i = 0; i < V; i += 4) {
+    constexpr int kSize = TYPE == 0 ? 4 : 2;
+    const int e = expert_of<L>(sub, i);
+    char raw[4 * kSize];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) store_float<TYPE>(raw, c, g[i + c]);
+    char* to = (char*)p.dlogits + (t * p.E + e) * kSize;
+    if (p.vec) {
+      if (e < p.E) __builtin_memcpy(__builtin_assume_aligned(to, 4 * kSize), raw, sizeof(raw));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e + c < p.E) __builtin_memcpy(to + c * kSize, raw + c * kSize, kSize);
+    }
   }
 }
 
@@ -350,17 +427,30 @@ struct JoinArgs {
   int32_t k;
 };
 
-template <int TYPE>
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
-  uint16_t e[kJoinWidth];
+// n (up to 8) values of 16 bits as they lie, zeros behind; and as fp32.  Apart, so
+// that several loads can be in flight before the first conversion waits.
+__device__ __forceinline__ u32x4_t load_raw(const uint16_t* p, int n) {
+  u32x4_t raw = {0, 0, 0, 0};
   if (n == kJoinWidth) {
-    __builtin_memcpy(e, p, 16);
+    __builtin_memcpy(&raw, p, 16);
   } else {
+    uint16_t e[kJoinWidth];
 #pragma unroll
     for (int i = 0; i < kJoinWidth; ++i) e[i] = i < n ? p[i] : (uint16_t)0;
+    __builtin_memcpy(&raw, e, 16);
   }
+  return raw;
+}
+template <int TYPE>
+__device__ __forceinline__ void to_floats(u32x4_t raw, float* v) {
+  uint16_t e[kJoinWidth];
+  __builtin_memcpy(e, &raw, 16);
 #pragma unroll
   for (int i = 0; i < kJoinWidth; ++i) v[i] = load_float<TYPE>(e, i);
+}
+template <int TYPE>
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
+  to_floats<TYPE>(load_raw(p, n), v);
 }
 template <int TYPE>
 __device__ __forceinline__ void store8(uint16_t* p, int n, const float* v) {
@@ -376,69 +466,105 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, const float* v) {
   }
 }
 
-template <int TYPE>
-__global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
-  const int64_t chunks = (p.H + kJoinWidth - 1) / kJoinWidth;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.T * chunks) return;
-  const int64_t t = i / chunks, h = i % chunks * kJoinWidth;
-  const int n = (int)min((int64_t)kJoinWidth, p.H - h);
-  float sum[kJoinWidth] = {};
-  for (int j = 0; j < p.k; ++j) {
-    const int64_t row = p.pos[t * p.k + j];
-    if (row < 0 || row >= p.R) continue;
-    const float w = p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
-    float v[kJoinWidth];
-    load8<TYPE>((const uint16_t*)p.y + row * p.H + h, n, v);
+// K rows a token at most (p.k of them): a thread has the chunks of all of them
+// in flight before it adds the first.  Workgroups are rows of `lanes` threads
+// for each of 256 / lanes tokens.
+template <int TYPE, int K>
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs p, int lanes) {
+  const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+  if (t >= p.T) return;
+  int64_t row[K];
+  float w[K];
 #pragma unroll
-    for (int e = 0; e < kJoinWidth; ++e) sum[e] += w * v[e];
+  for (int j = 0; j < K; ++j) {
+    const int64_t r = j < p.k ? p.pos[t * p.k + j] : -1;
+    row[j] = r >= 0 && r < p.R ? r : -1;
+    w[j] = j < p.k && p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
   }
-  store8<TYPE>((uint16_t*)p.out + t * p.H + h, n, sum);
+  for (int64_t h = (int64_t)(threadIdx.x % lanes) * kJoinWidth; h < p.H; h += lanes * kJoinWidth) {
+    const int n = (int)min((int64_t)kJoinWidth, p.H - h);
+    u32x4_t raw[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      raw[j] = u32x4_t{0, 0, 0, 0};
+      if (row[j] >= 0) raw[j] = load_raw((const uint16_t*)p.y + row[j] * p.H + h, n);
+    }
+    float sum[kJoinWidth] = {};
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (row[j] >= 0) {
+        float v[kJoinWidth];
+        to_floats<TYPE>(raw[j], v);
+#pragma unroll
+        for (int e = 0; e < kJoinWidth; ++e) sum[e] += w[j] * v[e];
+      }
+    store8<TYPE>((uint16_t*)p.out + t * p.H + h, n, sum);
+  }
 }
 
-// One workgroup per token.
-template <int TYPE>
-__global__ __launch_bounds__(256) void join_bwd_kernel(JoinArgs p) {
-  __shared__ float part[4][kMaxTopK];
-  const int64_t t = blockIdx.x;
+// dy and dweights: tokens as above; a token's dot products are joined over its
+// lanes (lanes is 64 or 256).
+template <int TYPE, int K>
+__global__ __launch_bounds__(256) void join_bwd_kernel(JoinArgs p, int lanes) {
+  __shared__ float part[4][K];
+  const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+  const bool on = t < p.T;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float dot[kMaxTopK];
+  int64_t row[K];
+  float w[K], dot[K];
 #pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) dot[j] = 0.f;
-  for (int64_t h = (int64_t)threadIdx.x * kJoinWidth; h < p.H; h += 256 * kJoinWidth) {
+  for (int j = 0; j < K; ++j) {
+    const int64_t r = on && j < p.k ? p.pos[t * p.k + j] : -1;
+    row[j] = r >= 0 && r < p.R ? r : -1;
+    w[j] = on && j < p.k && p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
+    dot[j] = 0.f;
+  }
+  for (int64_t h = (int64_t)(threadIdx.x % lanes) * kJoinWidth; on && h < p.H; h += lanes * kJoinWidth) {
     const int n = (int)min((int64_t)kJoinWidth, p.H - h);
     float d[kJoinWidth];
     load8<TYPE>((const uint16_t*)p.dout + t * p.H + h, n, d);
+    if (p.dweights != nullptr) {
+      u32x4_t raw[K];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= p.k) break;
-      const int64_t row = p.pos[t * p.k + j];
-      if (row < 0 || row >= p.R) continue;
-      float v[kJoinWidth];
-      if (p.dweights != nullptr) {
-        load8<TYPE>((const uint16_t*)p.y + row * p.H + h, n, v);
-#pragma unroll
-        for (int e = 0; e < kJoinWidth; ++e) dot[j] += v[e] * d[e];
+      for (int j = 0; j < K; ++j) {
+        raw[j] = u32x4_t{0, 0, 0, 0};
+        if (row[j] >= 0) raw[j] = load_raw((const uint16_t*)p.y + row[j] * p.H + h, n);
       }
-      if (p.out != nullptr) {
-        const float w = p.weights != nullptr ? p.weights[t * p.k + j] : 1.f;
 #pragma unroll
-        for (int e = 0; e < kJoinWidth; ++e) v[e] = w * d[e];
-        store8<TYPE>((uint16_t*)p.out + row * p.H + h, n, v);
-      }
+      for (int j = 0; j < K; ++j)
+        if (row[j] >= 0) {
+          float v[kJoinWidth];
+          to_floats<TYPE>(raw[j], v);
+#pragma unroll
+          for (int e = 0; e < kJoinWidth; ++e) dot[j] += v[e] * d[e];
+        }
+    }
+    if (p.out != nullptr) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (row[j] >= 0) {
+          float v[kJoinWidth];
+#pragma unroll
+          for (int e = 0; e < kJoinWidth; ++e) v[e] = w[j] * d[e];
+          store8<TYPE>((uint16_t*)p.out + row[j] * p.H + h, n, v);
+        }
     }
   }
   if (p.dweights == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) {
-    if (j >= p.k) break;
-    const float s = lanes_sum<64>(dot[j]);
-    if (lane == 0) part[wave][j] = s;
+  for (int j = 0; j < K; ++j) dot[j] = lanes_sum<64>(dot[j]);
+  if (lanes == 64) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (on && lane == j && j < p.k) p.dweights[t * p.k + j] = dot[j];
+    return;
   }
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    if (lane == 0) part[wave][j] = dot[j];
   __syncthreads();
-  if ((int)threadIdx.x < p.k)
-    p.dweights[t * p.k + threadIdx.x] = (part[0][threadIdx.x] + part[1][threadIdx.x]) +
-                                        (part[2][threadIdx.x] + part[3][threadIdx.x]);
+  const int j = (int)threadIdx.x;
+  if (on && j < p.k) p.dweights[t * p.k + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
 }
 
 // ---------------------------------------------------------------------------
@@ -548,41 +674,64 @@ hipError_t launch_route_lv(RouteArgs p, hipStream_t st) {
   const bool one = p.T <= kOneLaunch;
   p.chunk = one ? (int)std::max<int64_t>((p.T + 31) / 32 * 32, 32) : route_chunk(p.T, p.E);
   p.blocks = (int)((p.T + p.chunk - 1) / p.chunk);
-  const size_t bits = (size_t)p.E * (p.chunk / 32) * 4, lds = bits + (size_t)p.E * 4;
+  p.vec = p.E % 4 == 0 && (uintptr_t)p.logits % (TYPE == 0 ? 16 : 8) == 0;
+  const size_t bits = (size_t)p.E * (p.chunk / 32) * 4;
   if (one) {
-    route_one_kernel<TYPE, L, V><<<1, kRouteThreads, lds, st>>>(p);
+    route_one_kernel<TYPE, L, V><<<1, kRouteThreads, bits + (size_t)p.E * 4, st>>>(p);
   } else {
     route_choose_kernel<TYPE, L, V><<<p.blocks, kRouteThreads, bits, st>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_place_kernel<<<p.blocks, kRouteThreads, lds, st>>>(p);
+    route_place_kernel<<<p.blocks, kRouteThreads, 0, st>>>(p);
   }
   return hipGetLastError();
 }
 
 template <int TYPE, int L, int V>
-hipError_t launch_bwd_lv(const RouteBwdArgs& p, hipStream_t st) {
+hipError_t launch_bwd_lv(RouteBwdArgs p, hipStream_t st) {
+  const uintptr_t on = (uintptr_t)p.logits | (uintptr_t)p.dlogits;
+  p.vec = p.E % 4 == 0 && on % (TYPE == 0 ? 16 : 8) == 0;
   const int64_t per = 256 / L;
   route_bwd_kernel<TYPE, L, V><<<(uint32_t)((p.T + per - 1) / per), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
 // 16 lanes for a token up to 256 experts (4 tokens a wave, short reductions),
-// a whole wave above.
-#define MX_ROUTE_PICK(FN, TYPE, P)                        \
-  (P).E <= 16    ? FN<TYPE, 16, 1>(P, st)                 \
-  : (P).E <= 64  ? FN<TYPE, 16, 4>(P, st)                 \
-  : (P).E <= 128 ? FN<TYPE, 16, 8>(P, st)                 \
-  : (P).E <= 256 ? FN<TYPE, 16, 16>(P, st)                \
-  : (P).E <= 512 ? FN<TYPE, 64, 8>(P, st)                 \
+// a whole wave above, and for few tokens, whose latency counts: fewer logits
+// a lane.
+#define MX_ROUTE_PICK(FN, TYPE, P)                                     \
+  (P).T <= 64 && (P).E <= 256 ? FN<TYPE, 64, 4>(P, st)                 \
+  : (P).E <= 64  ? FN<TYPE, 16, 4>(P, st)                              \
+  : (P).E <= 128 ? FN<TYPE, 16, 8>(P, st)                              \
+  : (P).E <= 256 ? FN<TYPE, 16, 16>(P, st)                             \
+  : (P).E <= 512 ? FN<TYPE, 64, 8>(P, st)                              \
                  : FN<TYPE, 64, 16>(P, st)
+
+template <int TYPE, int K>
+hipError_t launch_join_k(const JoinArgs& p, bool bwd, hipStream_t st) {
+  // threads for a token: one wave for rows up to 1024 values, else the workgroup
+  const int lanes = p.H <= 64 * kJoinWidth * 2 ? 64 : 256;
+  const int64_t per = 256 / lanes;
+  const uint32_t blocks = (uint32_t)((p.T + per - 1) / per);
+  if (bwd) join_bwd_kernel<TYPE, K><<<blocks, 256, 0, st>>>(p, lanes);
+  else join_kernel<TYPE, K><<<blocks, 256, 0, st>>>(p, lanes);
+  return hipGetLastError();
+}
+template <int TYPE>
+hipError_t launch_join_type(const JoinArgs& p, bool bwd, hipStream_t st) {
+  if (p.k == 1) return launch_join_k<TYPE, 1>(p, bwd, st);
+  if (p.k == 2) return launch_join_k<TYPE, 2>(p, bwd, st);
+  if (p.k <= 4) return launch_join_k<TYPE, 4>(p, bwd, st);
+  if (p.k <= 8) return launch_join_k<TYPE, 8>(p, bwd, st);
+  return launch_join_k<TYPE, kMaxTopK>(p, bwd, st);
+}
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int32_t E) {
   if (T <= kOneLaunch || E <= 0) return 0;
   const int64_t c = route_chunk(T, E);
-  return (size_t)((T + c - 1) / c) * (size_t)E * sizeof(uint16_t);
+  return (size_t)((T + c - 1) / c) * (size_t)((E + 1) & ~1) * sizeof(uint16_t);
 }
 
 hipError_t launch_route(const void* logits, int type, int64_t T, int32_t E, int32_t k, bool renorm,
@@ -609,7 +758,7 @@ hipError_t launch_route(const void* logits, int type, int64_t T, int32_t E, int3
 hipError_t launch_route_bwd(const void* logits, int type, int64_t T, int32_t E, int32_t k,
                             bool renorm, const int32_t* ids, const float* weights,
                             const float* dweights, void* dlogits, hipStream_t st) {
-  RouteBwdArgs p{logits, ids, weights, dweights, dlogits, T, E, k, renorm};
+  RouteBwdArgs p{logits, ids, weights, dweights, dlogits, T, E, k, renorm, 0};
   if (type == 0) return MX_ROUTE_PICK(launch_bwd_lv, 0, p);
   if (type == 1) return MX_ROUTE_PICK(launch_bwd_lv, 1, p);
   return MX_ROUTE_PICK(launch_bwd_lv, 2, p);
@@ -626,11 +775,7 @@ hipError_t launch_join(const void* y, bool f16, int64_t T, int64_t R, int64_t H,
   p.R = R;
   p.H = H;
   p.k = k;
-  const int64_t n = T * ((H + kJoinWidth - 1) / kJoinWidth);
-  const uint32_t blocks = (uint32_t)((n + 255) / 256);
-  if (f16) join_kernel<2><<<blocks, 256, 0, st>>>(p);
-  else join_kernel<1><<<blocks, 256, 0, st>>>(p);
-  return hipGetLastError();
+  return f16 ? launch_join_type<2>(p, false, st) : launch_join_type<1>(p, false, st);
 }
 
 hipError_t launch_join_bwd(const void* dout, const void* y, bool f16, int64_t T, int64_t R,
@@ -647,9 +792,7 @@ hipError_t launch_join_bwd(const void* dout, const void* y, bool f16, int64_t T,
   p.R = R;
   p.H = H;
   p.k = k;
-  if (f16) join_bwd_kernel<2><<<(uint32_t)T, 256, 0, st>>>(p);
-  else join_bwd_kernel<1><<<(uint32_t)T, 256, 0, st>>>(p);
-  return hipGetLastError();
+  return f16 ? launch_join_type<2>(p, true, st) : launch_join_type<1>(p, true, st);
 }
 
 hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,

@@ -1,13 +1,15 @@
 // Forward products where experts have few rows (decoding): bound by reading
 // the weights once.
 //
-// One workgroup takes up to 16 MR rows of one expert and 16 CF output columns;
-// its waves split the contraction by 128-byte lines (wave w takes lines w,
-// w + waves, ...), so that few columns still give many loads in flight, and
-// their sums are joined in LDS in a fixed order.  Weights go from memory straight to
-// the registers of the matrix instruction, as its first operand (16 columns by 64
-// contraction bytes; rows of tokens are the second), at element alignment: no size or
-// stride is special.
+// One workgroup takes up to 16 MR rows of one expert and 16 output columns; its
+// waves split the contraction in runs of U 128-byte lines, so that few columns
+// still give many loads in flight, and their sums are joined in LDS in a fixed
+// order.  Weights go from memory straight to the registers of the matrix
+// instruction, as its first operand (16 columns by 64 contraction bytes; rows of
+// tokens are the second), at element alignment: no size or stride is special.
+// 16 columns and runs of 1 KB read the weights fastest: 8 experts of 14336 x
+// 4096 bf16, 16 rows, took 137 us (6.0 TB/s); 32 columns took 178, 64 took 175,
+// runs of 512 B 140, and non-temporal loads 155.
 #include <algorithm>
 
 #include "ragged_common.h"
@@ -61,17 +63,17 @@ __device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
   return v;
 }
 
-template <typename T, typename O, int MR, int CF, int WAVES>
+template <typename T, typename O, int MR, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
   typedef typename T::elem E;
   typedef typename Small<T>::acc Acc;
   constexpr bool kInt8 = sizeof(E) == 1;
-  __shared__ Acc part[WAVES][MR * CF][64];
+  __shared__ Acc part[WAVES][MR][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t ctiles = (p.N + 16 * CF - 1) / (16 * CF);
-  const int64_t rt = (int64_t)blockIdx.x / ctiles;
-  const int64_t n0 = (int64_t)blockIdx.x % ctiles * (16 * CF);
+  const uint32_t ctiles = (uint32_t)((p.N + 15) / 16);
+  const int64_t rt = blockIdx.x / ctiles;
+  const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 16;
 
   const RowSpan at = wave_row_tile(p.m_splits, p.G, p.R, 16 * MR, rt, false);
   const int g = at.g, rows = at.rows;
@@ -79,15 +81,10 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
   if (g < 0) return;
 
   const int64_t kb = p.K * (int64_t)sizeof(E);
-  const int64_t lines = (kb + 127) / 128;
   const int sub = lane >> 4;   // 16-byte chunk of a 64-byte step
-  // this lane's weight rows and token rows; rows past the end repeat the last
-  const uint8_t* w[CF];
-#pragma unroll
-  for (int c = 0; c < CF; ++c) {
-    const int64_t n = min(n0 + 16 * c + (lane & 15), p.N - 1);
-    w[c] = (const uint8_t*)p.b + ((int64_t)g * p.N + n) * kb + sub * 16;
-  }
+  // this lane's weight row and token rows; rows past the end repeat the last
+  const uint8_t* w = (const uint8_t*)p.b +
+                     ((int64_t)g * p.N + min(n0 + (lane & 15), p.N - 1)) * kb + sub * 16;
   const uint8_t* x[MR];
   int64_t token[MR];   // -1: a row of zeros
 #pragma unroll
@@ -96,67 +93,50 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
     const int64_t s = p.row_index != nullptr ? p.row_index[r] : r;
     token[m] = s >= 0 && s < p.S ? s : -1;
     // any readable row of K values does for a row of zeros
-    x[m] = (token[m] >= 0 ? (const uint8_t*)p.a + s * p.lda * (int64_t)sizeof(E) : w[0] - sub * 16) +
-           sub * 16;
+    x[m] = token[m] >= 0 ? (const uint8_t*)p.a + s * p.lda * (int64_t)sizeof(E) + sub * 16 : w;
   }
 
-  Acc acc[MR][CF];
+  Acc acc[MR];
 #pragma unroll
-  for (int m = 0; m < MR; ++m)
+  for (int m = 0; m < MR; ++m) acc[m] = Acc{0, 0, 0, 0};
+  // whole runs of U lines, wave by wave
+  const int64_t runs = kb / (128 * U);
+  for (int64_t run = wave; run < runs; run += WAVES) {
+    u32x4_t wv[2 * U], xv[2 * U][MR];
 #pragma unroll
-    for (int c = 0; c < CF; ++c) acc[m][c] = Acc{0, 0, 0, 0};
-  auto mma = [&](const u32x4_t* wv, const u32x4_t* xv) {
+    for (int i = 0; i < 2 * U; ++i) {
+      const int64_t at = run * (128 * U) + i * 64;
+      __builtin_memcpy(&wv[i], w + at, 16);
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
+      for (int m = 0; m < MR; ++m) __builtin_memcpy(&xv[i][m], x[m] + at, 16);
+    }
 #pragma unroll
-      for (int c = 0; c < CF; ++c) acc[m][c] = Small<T>::mma(wv[c], xv[m], acc[m][c]);
-  };
-  // whole lines, kUnroll at a time
-  constexpr int kUnroll = CF * 2 >= 8 ? 2 : 4;
-  const int64_t whole = kb / 128;
-  int64_t l = wave;
-  for (; l + (kUnroll - 1) * WAVES < whole; l += kUnroll * WAVES) {
-    u32x4_t wv[kUnroll][2][CF], xv[kUnroll][2][MR];
+    for (int i = 0; i < 2 * U; ++i)
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = (l + u * WAVES) * 128 + h * 64;
-#pragma unroll
-        for (int c = 0; c < CF; ++c) __builtin_memcpy(&wv[u][h][c], w[c] + at, 16);
-#pragma unroll
-        for (int m = 0; m < MR; ++m) __builtin_memcpy(&xv[u][h][m], x[m] + at, 16);
-      }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) mma(wv[u][h], xv[u][h]);
+      for (int m = 0; m < MR; ++m) acc[m] = Small<T>::mma(wv[i], xv[i][m], acc[m]);
   }
-  for (; l < lines; l += WAVES) {
+  // the lines that are left, each to the next wave; the last may be partial
+  const int64_t lines = (kb + 127) / 128;
+  for (int64_t l = runs * U + (wave + WAVES - (int)(runs % WAVES)) % WAVES; l < lines; l += WAVES) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t at = l * 128 + h * 64;
       const int64_t n = kb - at - sub * 16;
-      u32x4_t wv[CF], xv[MR];
+      const u32x4_t wv = chunk_end<E>(w + at, n);
 #pragma unroll
-      for (int c = 0; c < CF; ++c) wv[c] = chunk_end<E>(w[c] + at, n);
-#pragma unroll
-      for (int m = 0; m < MR; ++m) xv[m] = chunk_end<E>(x[m] + at, n);
-      mma(wv, xv);
+      for (int m = 0; m < MR; ++m) acc[m] = Small<T>::mma(wv, chunk_end<E>(x[m] + at, n), acc[m]);
     }
   }
 
 #pragma unroll
-  for (int m = 0; m < MR; ++m)
-#pragma unroll
-    for (int c = 0; c < CF; ++c) part[wave][m * CF + c][lane] = acc[m][c];
+  for (int m = 0; m < MR; ++m) part[wave][m][lane] = acc[m];
   __syncthreads();
-  // block i: token 16 (i / CF) + lane % 16, columns 16 (i % CF) + 4 (lane / 16) + 0..3
-  for (int i = wave; i < MR * CF; i += WAVES) {
-    Acc sum = part[0][i][lane];
+  // block m: token 16 m + lane % 16, columns 4 (lane / 16) + 0..3
+  for (int m = wave; m < MR; m += WAVES) {
+    Acc sum = part[0][m][lane];
 #pragma unroll
-    for (int v = 1; v < WAVES; ++v) sum += part[v][i][lane];
-    const int m = i / CF, r = 16 * m + (lane & 15);
+    for (int v = 1; v < WAVES; ++v) sum += part[v][m][lane];
+    const int r = 16 * m + (lane & 15);
     if (r >= rows) continue;
     int64_t s = -1;
 #pragma unroll
@@ -166,7 +146,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
     const float sa = kInt8 && s >= 0 ? p.sa[s] : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int64_t n = n0 + 16 * (i % CF) + 4 * sub + e;
+      const int64_t n = n0 + 4 * sub + e;
       if (n >= p.N) continue;
       float v = (float)sum[e];
       if (kInt8) v = v * sa * p.sb[(int64_t)g * p.N + n];
@@ -177,11 +157,11 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
 
 namespace {
 
-template <typename T, typename O, int MR, int CF, int WAVES>
+template <typename T, typename O, int MR, int U, int WAVES>
 hipError_t launch_few(const RaggedArgs& p, hipStream_t st) {
   const int64_t rt = p.R / (16 * MR) + std::min<int64_t>(p.G, p.R);
-  const int64_t ct = (p.N + 16 * CF - 1) / (16 * CF);
-  ragged_few_kernel<T, O, MR, CF, WAVES><<<dim3((uint32_t)(rt * ct)), dim3(64 * WAVES), 0, st>>>(p);
+  const int64_t blocks = rt * ((p.N + 15) / 16);
+  ragged_few_kernel<T, O, MR, U, WAVES><<<dim3((uint32_t)blocks), dim3(64 * WAVES), 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -190,14 +170,17 @@ hipError_t launch_rows(const RaggedArgs& p, hipStream_t st) {
   // rows of an expert on average, over experts that can have any
   const int64_t groups = std::min<int64_t>(p.G, p.R);
   const int64_t mean = (p.R + groups - 1) / groups;
-  // 64 columns a workgroup where that gives every CU two of them, else 16
-  // columns and twice the waves on the contraction
-  const bool wide = groups * ((p.N + 63) / 64) >= 512;
-  if (mean <= 16)
-    return wide ? launch_few<T, O, 1, 4, 4>(p, st) : launch_few<T, O, 1, 1, 8>(p, st);
-  if (mean <= 32)
-    return wide ? launch_few<T, O, 2, 4, 4>(p, st) : launch_few<T, O, 2, 1, 8>(p, st);
-  return wide ? launch_few<T, O, 4, 4, 4>(p, st) : launch_few<T, O, 4, 1, 8>(p, st);
+  // Four workgroups of four waves for each CU fill it; with fewer workgroups
+  // twice the waves share the contraction, in shorter runs.  Runs of 8 lines want
+  // a contraction that has one for each wave.
+  const bool many = groups * ((p.N + 15) / 16) >= 1024;
+  const bool longk = p.K * (int64_t)sizeof(typename T::elem) >= 4 * 8 * 128;
+  if (mean <= 16) {
+    if (!many) return launch_few<T, O, 1, 2, 8>(p, st);
+    return longk ? launch_few<T, O, 1, 8, 4>(p, st) : launch_few<T, O, 1, 2, 4>(p, st);
+  }
+  if (mean <= 32) return many ? launch_few<T, O, 2, 4, 4>(p, st) : launch_few<T, O, 2, 2, 8>(p, st);
+  return many ? launch_few<T, O, 4, 2, 4>(p, st) : launch_few<T, O, 4, 2, 8>(p, st);
 }
 
 }  // namespace

@@ -497,11 +497,15 @@ typedef enum mxfp8_type {
  * other rows never reach a result (infinities and NaN included).
  * Strides are in elements.  Faster where pointers, strides and the contraction
  * length are multiples of 16 bytes; right for all.
- *   workspace  NULL, or device memory, 16-byte aligned, of
- *           mxfp8_ragged_gemm_workspace_bytes() bytes that no other call running at
- *           the same time uses; needs no initialisation.  With it, tiles that
- *           do not fill the GPU are split along the contraction and joined in
- *           a fixed order (a smaller one is not used).
+ *   workspace  NULL, or device memory, 16-byte aligned, that no other call running
+ *           at the same time uses; needs no initialisation.  With
+ *           mxfp8_ragged_gemm_workspace_bytes() bytes of it, tiles that do not fill
+ *           the GPU are split along the contraction and joined in a fixed order,
+ *           and operands whose rows do not start on 16 bytes are laid out anew
+ *           where that pays.  Results do not depend on it but for the order of
+ *           sums.
+ * mxfp8_ragged_gemm_workspace_bytes: for operands of elem_bytes (2, or 1 for
+ * mxfp8_ragged_gemm_int8); 0 where none is used.
  * Errors: EINVAL for NULL pointers, sizes < 1 (R, S >= 0), strides shorter than
  * a row, G out of range, host m_splits, row_index with NN, S != R without
  * row_index, over 2^31 - 1 rows, columns or tiles; ENOTSUP for other types.
@@ -511,7 +515,8 @@ mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int6
                                int64_t R, int64_t S, int64_t N, int64_t K,
                                const int64_t* m_splits, int32_t G, const int32_t* row_index,
                                void* workspace, size_t workspace_bytes, void* stream);
-size_t mxfp8_ragged_gemm_workspace_bytes(void);
+size_t mxfp8_ragged_gemm_workspace_bytes(int32_t layout, int32_t elem_bytes, int64_t R, int64_t S,
+                                         int64_t N, int64_t K, int32_t G);
 
 /*
  * mxfp8_quantize_int8 -- a tensor's rows as 8-bit integers with a scale each:

@@ -59,7 +59,7 @@ SIGNATURES = {
     "mxfp8_convert_sweep": (c_i32, [c_i32, c_vp, c_size, c_vp]),
     "mxfp8_ragged_gemm": (c_i32, [c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
                                   c_i64, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
-    "mxfp8_ragged_gemm_workspace_bytes": (c_size, []),
+    "mxfp8_ragged_gemm_workspace_bytes": (c_size, [c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, c_i32]),
     "mxfp8_quantize_int8": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "mxfp8_ragged_gemm_int8": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64,
                                        c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),

@@ -548,24 +548,29 @@ def _row_index(row_index, like):
     return row_index
 
 
-def ragged_gemm_workspace_bytes():
-    return int(_lib().mxfp8_ragged_gemm_workspace_bytes())
+@functools.lru_cache(maxsize=4096)
+def ragged_gemm_workspace_bytes(layout, dtype, rows, x_rows, n, k, groups):
+    """Workspace of ragged_gemm (bf16, fp16) or ragged_gemm_int8 (int8, "NT")
+    for these sizes; 0 where none is used."""
+    return int(_lib().mxfp8_ragged_gemm_workspace_bytes(_LAYOUTS[layout], dtype.itemsize, rows,
+                                                        x_rows, n, k, groups))
 
 
-def _ragged_workspace(workspace, like):
-    """The caller's buffer, or one for this call (torch's allocator hands the
-    same memory out again)."""
-    global _ragged_bytes
-    if not _ragged_bytes:
-        _ragged_bytes = ragged_gemm_workspace_bytes()
+def _ragged_workspace(workspace, like, stream, *sizes):
+    """(buffer, its bytes): the caller's, or one for this call (torch's
+    allocator hands the same memory out again)."""
+    need = ragged_gemm_workspace_bytes(*sizes)
     if workspace is None:
-        return _empty((_ragged_bytes,), torch.uint8, like)
-    if not workspace.is_cuda or workspace.numel() * workspace.element_size() < _ragged_bytes:
-        raise ValueError(f"workspace must be a device buffer of at least {_ragged_bytes} bytes")
-    return workspace
-
-
-_ragged_bytes = 0
+        if need == 0:
+            return None, 0
+        workspace = _empty((need,), torch.uint8, like)
+        if stream is not None:
+            workspace.record_stream(stream)
+        return workspace, need
+    size = workspace.numel() * workspace.element_size()
+    if not workspace.is_cuda or size < need:
+        raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
+    return workspace, size
 
 
 def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None, stream=None,
@@ -581,7 +586,7 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
     product is row row_index[r] of X; without it S = R.  a, X and out may
     have a row stride.  out_dtype: the operands' (default) or float32.  Rows
     past the last expert's are not written (mxfp8_ragged_gemm).  workspace:
-    optional device buffer of ragged_gemm_workspace_bytes(), not shared by calls
+    optional device buffer of ragged_gemm_workspace_bytes(...), not shared by calls
     that may run at the same time; allocated for the call where there is none.
     """
     lib = _lib()
@@ -626,16 +631,11 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
         if out is None:
             out = _empty(shape, out_dtype, a)
         ldc = _rows_of(out, out_dtype, shape, "out")
-    ws = None
-    if not (lay == LAYOUT_NT and r <= 64 * g and workspace is None):   # few rows take none
-        ws = _ragged_workspace(workspace, a)
+    ws, ws_bytes = _ragged_workspace(workspace, a, stream, lay, a.dtype, r, s, n, k, g)
     _same_device(a, b=b, m_splits=ms, row_index=index, out=out, workspace=ws)
-    if ws is not None and stream is not None:
-        ws.record_stream(stream)
     st = lib.mxfp8_ragged_gemm(lay, ty, _ptr(a), lda, _ptr(b), ldb, _ptr(out), ldc,
                                _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
-                               _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                               _stream(stream))
+                               _ptr(ws), ws_bytes, _stream(stream))
     _native.check(st, "mxfp8_ragged_gemm")
     return out
 
@@ -683,15 +683,12 @@ def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=t
     if out is None:
         out = _empty((r, n), out_dtype, q)
     ldc = _rows_of(out, out_dtype, (r, n), "out")
-    ws = _ragged_workspace(workspace, q) if r > 64 * g or workspace is not None else None
+    ws, ws_bytes = _ragged_workspace(workspace, q, stream, LAYOUT_NT, torch.int8, r, s, n, k, g)
     _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out,
                  workspace=ws)
-    if ws is not None and stream is not None:
-        ws.record_stream(stream)
     st = lib.mxfp8_ragged_gemm_int8(_ptr(q), ldq, _ptr(scale), _ptr(w), _ptr(w_scale), _ptr(out),
                                     ldc, _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
-                                    _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                                    _stream(stream))
+                                    _ptr(ws), ws_bytes, _stream(stream))
     _native.check(st, "mxfp8_ragged_gemm_int8")
     return out
 

@@ -486,13 +486,17 @@ mxfp8_status check_ragged(const char* fn, int layout, int64_t R, int64_t S, int6
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-void* usable_workspace(void* ws, size_t bytes) {
-  return bytes >= mx::ragged_workspace_bytes() && aligned_to(ws, 16) ? ws : nullptr;
-}
+void* usable_workspace(void* ws) { return aligned_to(ws, 16) ? ws : nullptr; }
 
 }  // namespace
 
-size_t mxfp8_ragged_gemm_workspace_bytes(void) { return mx::ragged_workspace_bytes(); }
+size_t mxfp8_ragged_gemm_workspace_bytes(int32_t layout, int32_t elem_bytes, int64_t R, int64_t S,
+                                         int64_t N, int64_t K, int32_t G) {
+  if (layout < 0 || layout > 2 || (elem_bytes != 1 && elem_bytes != 2) || R < 0 || S < 0 || N < 1 ||
+      K < 1 || G < 1 || R > kI32Max || S > kI32Max || N > kI32Max || K > kI32Max)
+    return 0;
+  return mx::ragged_workspace_bytes(layout, elem_bytes, R, S, N, K, G);
+}
 
 mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int64_t lda,
                                const void* b, int64_t ldb, void* c, int64_t ldc, int32_t c_type,
@@ -535,9 +539,11 @@ mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int6
   p.m_splits = m_splits;
   p.row_index = row_index;
   p.G = G;
-  p.ws = usable_workspace(workspace, workspace_bytes);
+  p.ws = usable_workspace(workspace);
   return hip_status(
-      mx::launch_ragged_gemm(layout, type == MXFP8_TYPE_F16, c_type, p, as_stream(stream)), fn);
+      mx::launch_ragged_gemm(layout, type == MXFP8_TYPE_F16, c_type, p,
+                             p.ws != nullptr ? workspace_bytes : 0, as_stream(stream)),
+      fn);
 }
 
 mxfp8_status mxfp8_quantize_int8(const void* x, int32_t type, int64_t T, int64_t K, int64_t ldx,
@@ -593,8 +599,10 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
   p.sa = scale;
   p.sb = w_scale;
   p.G = G;
-  p.ws = usable_workspace(workspace, workspace_bytes);
-  return hip_status(mx::launch_ragged_gemm_int8(c_type, p, as_stream(stream)), fn);
+  p.ws = usable_workspace(workspace);
+  return hip_status(mx::launch_ragged_gemm_int8(
+                        c_type, p, p.ws != nullptr ? workspace_bytes : 0, as_stream(stream)),
+                    fn);
 }
 
 namespace {

@@ -62,9 +62,10 @@ hipError_t launch_grouped_gemm_swiglu(const uint8_t* a, const uint8_t* sa, const
 // Products grouped by expert with ragged row counts (ragged.hip); layout and
 // out as in the C header's enums.
 struct RaggedArgs;
-hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p, hipStream_t st);
-hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st);
-size_t ragged_workspace_bytes();   // a partial 256 x 256 tile for each CU
+hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p, size_t ws_bytes,
+                              hipStream_t st);
+hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
+size_t ragged_workspace_bytes(int layout, int esize, int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G);
 hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,
                                 int8_t* q, float* scale, hipStream_t st);

@@ -290,35 +290,170 @@ hipError_t launch_layout(int layout, const RaggedArgs& p, hipStream_t st) {
 bool on16(const void* p, int64_t stride_bytes) {
   return (uintptr_t)p % 16 == 0 && stride_bytes % 16 == 0;
 }
+int64_t pad16(int64_t n, int64_t size) { return (n * size + 15) / 16 * 16 / size; }
 
-// Whether the large tiles take these operands: rows on 16 bytes, the contiguous
-// contraction and the result's rows multiples of 16 bytes, and lane offsets (256
-// rows, 64 contraction rows, any gathered row) within 32 bits.
-bool ragged_tile_takes(int layout, int esize, int osize, const RaggedArgs& p) {
+// Whether experts have few rows, so that the forward product is bound by reading
+// the weights and ragged_few.hip takes it.  Measured (MI355X, weights of W MB, m
+// rows an expert): about W (0.16 + 0.0071 m) us there, 30 + 0.19 W us for the
+// large tiles, e.g. 940 MB: 166 and 178 us at 4 rows, 191 and 182 at 8; 34 MB:
+// 38 and 34 us at 64 rows of 1 expert.
+bool few_rows(const RaggedArgs& p, int esize) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
+  const double mb = 1e-6 * (double)groups * (double)p.N * (double)p.K * esize;
+  return p.R < (1 << 20) && (mean <= 4 || (double)(mean - 4) * mb <= 4200.0);
+}
+
+// What the large tiles want and an operand may lack: rows on 16 bytes, the
+// contiguous contraction and the result's rows multiples of 16 bytes.  Such an
+// operand is laid out anew in the workspace first (zeros behind its rows), a
+// result is copied from there.
+struct Repack {
+  bool a, b, c;
+  int64_t lda, ldb, ldc;      // of the copies
+  int64_t rows_b, rows_c;
+  size_t bytes_a, bytes_b, bytes_c;
+  size_t bytes() const { return bytes_a + bytes_b + bytes_c; }
+};
+Repack repack_of(int layout, int esize, int osize, const RaggedArgs& p) {
+  Repack r{};
+  const int64_t cols = layout == 0 ? p.N : p.K, ca = layout == 0 ? p.K : p.N;
+  const bool odd = layout != 2 && ca * esize % 16 != 0;
+  r.a = odd || !on16(p.a, p.lda * esize);
+  r.b = (layout == 0 && odd) || !on16(p.b, p.ldb * esize);
+  r.c = !on16(p.c, p.ldc * osize) || cols * osize % 16 != 0;
+  r.rows_b = layout == 2 ? p.S : (int64_t)p.G * p.N;
+  r.rows_c = layout == 2 ? (int64_t)p.G * p.N : p.R;
+  r.lda = pad16(ca, esize);
+  r.ldb = pad16(p.K, esize);
+  r.ldc = pad16(cols, osize);
+  r.bytes_a = r.a ? (size_t)(layout == 0 ? p.S : p.R) * r.lda * esize : 0;
+  r.bytes_b = r.b ? (size_t)r.rows_b * r.ldb * esize : 0;
+  r.bytes_c = r.c ? (size_t)r.rows_c * r.ldc * osize : 0;
+  return r;
+}
+// Copying pays where the arithmetic is long enough: ragged_any_kernel reaches
+// 560 (NT), 250 (NN) and 150 (TN) TFLOP/s on 16384 rows of 8 x 4096 x 14336, the
+// large tiles 1150 and more; a copy moves its bytes twice at about 4 TB/s.
+bool repack_pays(int layout, const RaggedArgs& p, size_t bytes) {
+  const double tflop = 2e-12 * (double)p.R * (double)p.N * (double)p.K;
+  const double any = tflop / (layout == 0 ? 560.0 : layout == 1 ? 250.0 : 150.0);
+  return bytes <= ((size_t)8 << 30) && any > tflop / 1150.0 + 2.0 * (double)bytes / 4e12 + 30e-6;
+}
+size_t split_bytes() { return ragged_split_bytes(); }
+
+// Lane offsets (256 rows, 64 contraction rows, any gathered row) within 32 bits.
+bool tile_spans(int layout, int esize, int osize, const RaggedArgs& p) {
   const int64_t ea = p.lda * esize, eb = p.ldb * esize, ec = p.ldc * osize;
   const int64_t span = (int64_t)kSpan;
-  if (!on16(p.a, ea) || !on16(p.b, eb) || !on16(p.c, ec)) return false;
-  if ((layout == 0 ? p.N : p.K) * osize % 16 != 0) return false;
   if (256 * ea > span || 256 * eb > span || 256 * ec > span) return false;
-  if (layout == 0 && p.K * esize % 16 != 0) return false;
-  if (layout == 1 && p.N * esize % 16 != 0) return false;
-  if (p.row_index != nullptr && (p.S == 0 || p.S * (layout == 2 ? eb : ea) > span)) return false;
-  return true;
+  return p.row_index == nullptr || (p.S > 0 && p.S * (layout == 2 ? eb : ea) <= span);
+}
+
+// Rows of `bytes` bytes from one pitch to another, 16 bytes a lane, zeros up to
+// `fill` bytes.  splits: only the experts' rows.
+template <typename E>
+__global__ __launch_bounds__(256) void repack_kernel(const uint8_t* src, int64_t src_pitch, uint8_t* dst,
+                                                     int64_t dst_pitch, int64_t rows, int64_t bytes,
+                                                     int64_t fill, const int64_t* m_splits, int G) {
+  if (m_splits != nullptr) rows = wave_row_tile(m_splits, G, rows, 1, -1, true).total;
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4)
+    for (int64_t at = lane * 16; at < fill; at += 64 * 16) {
+      const u32x4_t v = load_chunk<E>((const E*)(src + r * src_pitch + at), (bytes - at) / (int64_t)sizeof(E));
+      uint8_t* to = dst + r * dst_pitch + at;
+      if (at + 16 <= fill) {
+        __builtin_memcpy(to, &v, 16);
+      } else {
+        E e[16 / sizeof(E)];
+        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+        for (int i = 0; i < (int)(16 / sizeof(E)); ++i)
+          if (at + (int64_t)((i + 1) * sizeof(E)) <= fill) ((E*)to)[i] = e[i];
+      }
+    }
+}
+template <typename E>
+hipError_t repack(const void* src, int64_t ld_src, void* dst, int64_t ld_dst, int64_t rows, int64_t n,
+                  int64_t fill, const int64_t* m_splits, int G, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  const int64_t size = sizeof(E);
+  repack_kernel<E><<<dim3((uint32_t)std::min<int64_t>((rows + 3) / 4, 4096)), dim3(256), 0, st>>>(
+      (const uint8_t*)src, ld_src * size, (uint8_t*)dst, ld_dst * size, rows, n * size, fill * size, m_splits, G);
+  return hipGetLastError();
+}
+
+// Runs `launch` with operands that the large tiles take; *done is false where
+// they cannot (no room in the workspace, too large, or not worth it).
+template <typename E, typename F>
+hipError_t with_tiles(int layout, int osize, RaggedArgs p, size_t ws_bytes, hipStream_t st, bool* done,
+                      F launch) {
+  const int esize = sizeof(E);
+  const int64_t cols = layout == 0 ? p.N : p.K, ca = layout == 0 ? p.K : p.N;
+  const Repack r = repack_of(layout, esize, osize, p);
+  *done = false;
+  uint8_t* ws = (uint8_t*)p.ws;
+  if (r.bytes() > 0 && (ws == nullptr || ws_bytes < split_bytes() + r.bytes() ||
+                        !repack_pays(layout, p, r.bytes())))
+    return hipSuccess;
+  RaggedArgs q = p;
+  if (ws_bytes < split_bytes()) q.ws = nullptr;
+  uint8_t* at = ws + split_bytes();
+  if (r.a) q.a = at, q.lda = r.lda, at += r.bytes_a;
+  if (r.b) q.b = at, q.ldb = r.ldb, at += r.bytes_b;
+  if (r.c) q.c = at, q.ldc = r.ldc;
+  q.con = layout == 2 ? 0 : (r.a ? r.lda : ca);
+  q.ccols = r.c ? r.ldc : cols;
+  if (!tile_spans(layout, esize, osize, q)) return hipSuccess;
+  *done = true;
+  hipError_t e = hipSuccess;
+  if (r.a)
+    e = repack<E>(p.a, p.lda, (void*)q.a, r.lda, layout == 0 ? p.S : p.R, ca, r.lda, nullptr, 0, st);
+  if (e == hipSuccess && r.b) e = repack<E>(p.b, p.ldb, (void*)q.b, r.ldb, r.rows_b, p.K, r.ldb, nullptr, 0, st);
+  if (e == hipSuccess) e = launch(q);
+  if (e == hipSuccess && r.c) {
+    const int64_t* rows = layout == 2 ? nullptr : p.m_splits;
+    if (osize == 4) e = repack<uint32_t>(q.c, r.ldc, p.c, p.ldc, r.rows_c, cols, cols, rows, p.G, st);
+    else e = repack<uint16_t>(q.c, r.ldc, p.c, p.ldc, r.rows_c, cols, cols, rows, p.G, st);
+  }
+  return e;
 }
 
 }  // namespace
 
-// Whether experts have few rows (64 on average, of those that can have any): the
-// forward product is then bound by reading the weights.
-bool few_rows(const RaggedArgs& p) { return p.R <= 64 * std::min<int64_t>(p.G, p.R); }
+// Workspace that a product of these sizes uses (0: none), operands contiguous.
+size_t ragged_workspace_bytes(int layout, int esize, int64_t R, int64_t S, int64_t N, int64_t K, int32_t G) {
+  if (R == 0) return 0;
+  RaggedArgs p{};
+  p.R = R;
+  p.S = S;
+  p.N = N;
+  p.K = K;
+  p.G = G;
+  p.lda = layout == 0 ? K : N;
+  p.ldb = K;
+  p.ldc = layout == 0 ? N : K;
+  if (layout == 0 && few_rows(p, esize)) return 0;
+  size_t most = 0;
+  for (int osize = 2; osize <= 4; osize += 2) {
+    const size_t n = repack_of(layout, esize, osize, p).bytes();
+    if (n > 0 && repack_pays(layout, p, n)) most = std::max(most, n);
+  }
+  return split_bytes() + most;
+}
 
-hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p,
+hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p, size_t ws_bytes,
                               hipStream_t st) {
-  if (layout == 0 && few_rows(p)) return launch_ragged_few(f16, out, p, st);
-  if (ragged_tile_takes(layout, 2, out == 0 ? 4 : 2, p))
-    return layout == 0   ? launch_ragged_tile_nt(f16, out, p, st)
-           : layout == 1 ? launch_ragged_tile_nn(f16, out, p, st)
-                         : launch_ragged_tile_tn(f16, out, p, st);
+  if (layout == 0 && few_rows(p, 2)) return launch_ragged_few(f16, out, p, st);
+  if (p.R > 0) {
+    bool done = false;
+    const hipError_t e = with_tiles<uint16_t>(
+        layout, out == 0 ? 4 : 2, p, ws_bytes, st, &done, [&](const RaggedArgs& q) {
+          return layout == 0   ? launch_ragged_tile_nt(f16, out, q, st)
+                 : layout == 1 ? launch_ragged_tile_nn(f16, out, q, st)
+                               : launch_ragged_tile_tn(f16, out, q, st);
+        });
+    if (done || e != hipSuccess) return e;
+  }
   if (f16) {
     if (out == 0) return launch_layout<TypeF16, OutF32>(layout, p, st);
     return launch_layout<TypeF16, OutF16>(layout, p, st);
@@ -327,9 +462,13 @@ hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p
   return launch_layout<TypeBf16, OutBf16>(layout, p, st);
 }
 
-hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st) {
-  if (few_rows(p)) return launch_ragged_few_int8(out, p, st);
-  if (ragged_tile_takes(0, 1, out == 0 ? 4 : 2, p)) return launch_ragged_tile_int8(out, p, st);
+hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, size_t ws_bytes, hipStream_t st) {
+  if (few_rows(p, 1)) return launch_ragged_few_int8(out, p, st);
+  bool done = false;
+  const hipError_t e = with_tiles<uint8_t>(
+      0, out == 0 ? 4 : 2, p, ws_bytes, st, &done,
+      [&](const RaggedArgs& q) { return launch_ragged_tile_int8(out, q, st); });
+  if (done || e != hipSuccess) return e;
   if (out == 0) return launch_any<TypeI8, OutF32, 0>(p, st);
   if (out == 1) return launch_any<TypeI8, OutBf16, 0>(p, st);
   return launch_any<TypeI8, OutF16, 0>(p, st);
@@ -338,10 +477,9 @@ hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, hipStream_t st)
 // Workgroups that any call may launch at most (the grid's limit).
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G) {
   const int64_t cols = ((layout == 0 ? N : K) + kAnyT - 1) / kAnyT;
-  if (layout == 0)   // the smallest tiles: 16 rows by 16 columns
+  if (layout == 0)   // the smallest tiles: 16 rows by 16 columns, where rows are few
     return std::max(cols * (R / kAnyT + std::min<int64_t>(G, R)),
-                    R <= 64 * std::min<int64_t>(G, R)
-                        ? ((N + 15) / 16) * (R / 16 + std::min<int64_t>(G, R)) : 0);
+                    R < (1 << 20) ? ((N + 15) / 16) * (R / 16 + std::min<int64_t>(G, R)) : 0);
   return cols * (layout == 2 ? (int64_t)G * ((N + kAnyT - 1) / kAnyT)
                              : R / kAnyT + std::min<int64_t>(G, R));
 }

@@ -31,6 +31,9 @@ struct RaggedArgs {
   const float* sa;      // int8: scale of each row of X [S]
   const float* sb;      // int8: scale of each output channel [G, N]
   int32_t G;
+  // for the large tiles
+  int64_t con;          // NT, NN: contraction with its zero padding
+  int64_t ccols;        // columns that a row of C has room for
   void* ws;             // partial sums of split tiles (large tiles), or NULL
 };
 
@@ -42,6 +45,7 @@ hipError_t launch_ragged_tile_nt(bool f16, int out, const RaggedArgs& p, hipStre
 hipError_t launch_ragged_tile_nn(bool f16, int out, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_tn(bool f16, int out, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_int8(int out, const RaggedArgs& p, hipStream_t st);
+size_t ragged_split_bytes();   // a partial 256 x 256 tile for each CU
 
 // Longest range of a bounded operand (32-bit offsets, less what marks a lane that
 // is out of it).

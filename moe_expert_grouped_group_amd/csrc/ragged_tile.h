@@ -79,6 +79,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
                                            __builtin_amdgcn_readfirstlane((int)(uint32_t)n), 0x00020000);
 }
 
+// The range check goes by dwords: one that the last value fills half of counts.
+__device__ __forceinline__ int64_t whole_dwords(int64_t bytes) { return (bytes + 3) & ~(int64_t)3; }
+
 // The same value in every lane, in scalar registers.
 template <typename V>
 __device__ __forceinline__ V uniform(V v) {
@@ -176,8 +179,12 @@ __device__ __forceinline__ Units units_of(uint32_t ntiles, uint32_t grid, int64_
   u.rem = ntiles - u.full;
   u.parts = 1;
   if (ws && u.rem > 0) {
+    // A part's sums cost a write and a read of a tile each, for all `rem` tiles as
+    // long as about rem / 7 stages of one: with p parts the round takes about
+    // stages / p + p rem / 7.
     const uint32_t most = (uint32_t)(stages / kMinPart < 1 ? 1 : stages / kMinPart);
-    u.parts = min(grid / u.rem, most);
+    const uint32_t best = (uint32_t)sqrtf(7.f * (float)stages / (float)u.rem);
+    u.parts = max(1u, min(min(grid / u.rem, most), best));
   }
   return u;
 }
@@ -193,7 +200,7 @@ __device__ __forceinline__ void tile_order(uint32_t at, uint32_t rtiles, uint32_
 // Stages of the contraction that the number of parts goes by: all of it, or the
 // rows of an expert on average.
 __device__ __forceinline__ int64_t part_stages(int layout, const RaggedArgs& p, int esize) {
-  const int64_t con = layout == 0 ? p.K : (layout == 1 ? p.N : p.R / p.G);
+  const int64_t con = layout == 2 ? p.R / p.G : p.con;
   return (con * esize + kStageK - 1) / kStageK;
 }
 
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     const RaggedArgs& p = args;
     const uint32_t ctiles = plan.ctiles, rtiles = plan.rtiles, band = plan.band;
     const uint32_t ufull = plan.full, urem = plan.rem, uparts = plan.parts;
-    const int64_t con = LAYOUT == 0 ? p.K : p.N;   // NT, NN
+    const int64_t con = p.con;   // NT, NN
     const int64_t la = ea, lb = eb;
     const bool part = i >= ufull && uparts > 1;
     const uint32_t v = i - ufull;
@@ -304,13 +311,13 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       t.ns = (int32_t)(((int64_t)t.len * sizeof(E) + kStageK - 1) / kStageK);
       // columns m0.. of dY and n0.. of X, the expert's rows
       t.pa = (const uint8_t*)p.a + (int64_t)t.lo * la + (int64_t)t.m0 * sizeof(E);
-      t.na = t.len == 0 ? 0 : (int64_t)(t.len - 1) * la + (p.N - t.m0) * (int64_t)sizeof(E);
+      t.na = t.len == 0 ? 0 : (int64_t)(t.len - 1) * la + whole_dwords((p.N - t.m0) * (int64_t)sizeof(E));
       if (GATHER) {
         t.pb = (const uint8_t*)p.b + (int64_t)t.n0 * sizeof(E);
-        t.nb = p.S == 0 ? 0 : (p.S - 1) * lb + (p.K - t.n0) * (int64_t)sizeof(E);
+        t.nb = p.S == 0 ? 0 : (p.S - 1) * lb + whole_dwords((p.K - t.n0) * (int64_t)sizeof(E));
       } else {
         t.pb = (const uint8_t*)p.b + (int64_t)t.lo * lb + (int64_t)t.n0 * sizeof(E);
-        t.nb = t.len == 0 ? 0 : (int64_t)(t.len - 1) * lb + (p.K - t.n0) * (int64_t)sizeof(E);
+        t.nb = t.len == 0 ? 0 : (int64_t)(t.len - 1) * lb + whole_dwords((p.K - t.n0) * (int64_t)sizeof(E));
       }
     } else {
       tile_order(at, rtiles, ctiles, &mt, &nt);
@@ -333,13 +340,13 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         t.pa = (const uint8_t*)p.a + (int64_t)t.lo * la;
         t.na = (p.R - 1 - t.lo) * la + con * (int64_t)sizeof(E);
       }
-      const uint8_t* w = (const uint8_t*)p.b + (int64_t)t.g * p.N * p.K * (int64_t)sizeof(E);
+      const uint8_t* w = (const uint8_t*)p.b + (int64_t)t.g * p.N * lb;
       if (LAYOUT == 0) {
         t.pb = w + (int64_t)t.n0 * lb;
         t.nb = (p.N - 1 - t.n0) * lb + con * (int64_t)sizeof(E);
       } else {
         t.pb = w + (int64_t)t.n0 * sizeof(E);
-        t.nb = (p.N - 1) * lb + (p.K - t.n0) * (int64_t)sizeof(E);
+        t.nb = (p.N - 1) * lb + whole_dwords((p.K - t.n0) * (int64_t)sizeof(E));
       }
     }
     t.last = 1;
@@ -398,7 +405,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
                   : (uint32_t)((8 * (8 * wave + j) + (lane >> 3)) * eb) + chunk_k(j);
   // contiguous contraction: lanes past its end in the last stage
   const uint32_t last_bytes =
-      (uint32_t)(((LAYOUT == 0 ? p.K : p.N) * (int64_t)sizeof(E) - 1) % kStageK) + 1;
+      (uint32_t)((p.con * (int64_t)sizeof(E) - 1) % kStageK) + 1;
   uint32_t past[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) past[j] = !kColA && chunk_k(j) >= last_bytes ? kOut : 0u;
@@ -460,20 +467,24 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     }
   };
 
-  // int8: scales of tile n's rows (this wave's 64, of the rows that copy_rows
-  // brought) and columns (64) to LDS, with the copies; zeros outside.
+  // int8: scales of tile n's rows (this wave's and on, as copy_rows
+  // brought their indexes) and columns (64) to LDS, with the copies; zeros outside.
   int side = 0;   // place of the computed tile's
   auto copy_scales = [&](const Tile& n, int at) {
     const RaggedArgs& p = args;
-    const uint32_t to = (uint32_t)(uintptr_t)scales + (uint32_t)(at * 2048 + wave * 256);
-    const uint32_t r = (uint32_t)(64 * wave + lane);
+    // (with fewer than 64 rows a wave, waves write rows of the next one too, the
+    // same values)
+    const uint32_t to = (uint32_t)(uintptr_t)scales + (uint32_t)(at * 2048);
+    const uint32_t r = (uint32_t)(8 * kPartsA * wave + lane),
+                   c = (uint32_t)(64 * wave + lane);
     uint32_t row = r;
     if (GATHER) row = *(__attribute__((address_space(3))) const uint32_t*)(ring0 + (uint32_t)lane * 4);
     const i32x4 rs = GATHER ? bounded(p.sa, p.S * 4) : bounded(p.sa + n.lo, (int64_t)n.rows * 4);
     const bool ok = ((int)r < n.rows) & (!GATHER | (row < (uint32_t)p.S));
     const i32x4 cs = bounded(p.sb + (int64_t)n.g * p.N + n.n0, (p.N - n.n0) * 4);
-    copy4(rs, (row * 4u) | (ok ? 0u : kOut), 0u, __builtin_amdgcn_readfirstlane(to));
-    copy4(cs, r * 4u, 0u, __builtin_amdgcn_readfirstlane(to + 1024u));
+    copy4(rs, (row * 4u) | (ok ? 0u : kOut), 0u,
+          __builtin_amdgcn_readfirstlane(to + (uint32_t)(wave * kPartsA * 32)));
+    copy4(cs, c * 4u, 0u, __builtin_amdgcn_readfirstlane(to + 1024u + (uint32_t)(wave * 256)));
   };
 
   struct Stage {
@@ -716,7 +727,6 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     // be kept, and spilled, through the whole loop
     const int ln = (int)hide((uint32_t)lane);
     const RaggedArgs& p = args;
-    const int64_t cols = LAYOUT == 0 ? p.N : p.K;
     if (split >= 0) {
       // a part (the last unit of its workgroup): the accumulators as they lie
       const auto ws = make_rsrc((const uint8_t*)p.ws + (int64_t)split * (kTileM * kTileN * 4),
@@ -725,6 +735,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          if (wm * 32 * FA + 32 * i >= rows) continue;   // not read by the join either
           // (values of this branch's own: moved ahead of the branch, all 256
           // accumulators would be spilled)
           asm volatile("" : "+a"(acc[i][j]));
@@ -753,11 +764,11 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     // offset that stores nothing, so that every tile issues the same stores
     // (the waits count on it).
     typedef typename O::elem OE;
-    OE* c = (OE*)p.c + (kColA ? ((int64_t)g * p.N + m0) * p.K : m0 * p.ldc) + n0;
+    OE* c = (OE*)p.c + ((kColA ? (int64_t)g * p.N : 0) + m0) * p.ldc + n0;
     const uint32_t ec = (uint32_t)(p.ldc * sizeof(OE));
-    const int64_t room = (int64_t)(rows - 1) * ec + (cols - n0) * (int64_t)sizeof(OE);
+    const int64_t room = (int64_t)(rows - 1) * ec + (p.ccols - n0) * (int64_t)sizeof(OE);
     const auto out = make_rsrc(c, room);
-    const int right = (int)min((int64_t)kTileN, cols - n0);   // columns of the tile
+    const int right = (int)min((int64_t)kTileN, p.ccols - n0);   // columns to store
     auto value = [&](int i, int j, int r) {
       if constexpr (kInt8)
         return (float)acc[i][j][r] * srow[i] *
@@ -855,6 +866,7 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
       m0 = s.row0;
       rows = s.rows;
     }
+    if ((wave >> 1) * 32 * FA + 32 * i >= rows) continue;
     typedef typename std::conditional<kInt8, i32x4, float __attribute__((ext_vector_type(4)))>::type V;
     V sum[4];
     for (uint32_t part = 0; part < u.parts; ++part) {
@@ -875,16 +887,16 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
       if (row >= 0 && row < p.S) sa = p.sa[row];
     }
     typedef typename O::elem OE;
-    OE* c = (OE*)p.c + (LAYOUT == 2 ? ((int64_t)g * p.N + m0 + m) * p.K : (m0 + m) * p.ldc);
+    OE* c = (OE*)p.c + ((LAYOUT == 2 ? (int64_t)g * p.N : 0) + m0 + m) * p.ldc;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t n = (int64_t)nt * kTileN + (wave & 1) * 128 + 32 * j + 8 * q + 4 * (lane >> 5);
-      if (n >= cols) continue;   // columns come in fours (rows are multiples of 16 bytes)
+      if (n >= p.ccols) continue;   // columns come in fours (rows are multiples of 16 bytes)
       OE o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float x = (float)sum[q][e];
-        if (kInt8) x = x * sa * p.sb[(int64_t)g * p.N + n + e];
+        if (kInt8) x = n + e < cols ? x * sa * p.sb[(int64_t)g * p.N + n + e] : 0.f;
         o[e] = O::cvt(x);
       }
       __builtin_memcpy(__builtin_assume_aligned(c + n, sizeof(o)), o, sizeof(o));

@@ -5,10 +5,10 @@ namespace mx {
 
 hipError_t launch_ragged_tile_nt(bool f16, int out, const RaggedArgs& p, hipStream_t st) {
   if (f16)
-    return out == 0 ? launch_tile_gather<TypeF16, OutF32, 0>(p, st)
-                    : launch_tile_gather<TypeF16, OutF16, 0>(p, st);
-  return out == 0 ? launch_tile_gather<TypeBf16, OutF32, 0>(p, st)
-                  : launch_tile_gather<TypeBf16, OutBf16, 0>(p, st);
+    return out == 0 ? launch_tile_rows<TypeF16, OutF32>(p, st)
+                    : launch_tile_rows<TypeF16, OutF16>(p, st);
+  return out == 0 ? launch_tile_rows<TypeBf16, OutF32>(p, st)
+                  : launch_tile_rows<TypeBf16, OutBf16>(p, st);
 }
 
 }  // namespace mx

@@ -415,6 +415,118 @@ def test_int8_longest_sum():
     assert (got.double() + 127.0 * 128 * k).abs().max() <= 127 * 128 * k * 2.0 ** -24
 
 
+# Weights so large that few rows do not pay for the forward form of few rows:
+# the large tiles of 64, 128 and 256 rows.  (K, N): contractions that end inside
+# a 16-byte chunk's stage, are one stage or less, columns that end inside a tile.
+TILED = [(6152, 4104, [20, 0, 41, 1, 64, 33]), (6208, 4136, [63, 65, 0, 130, 100, 1]),
+         (6144, 4104, [300, 257, 0, 1, 255, 256]), (72, 300008, [30, 64, 0, 40]),
+         (136, 160040, [129, 128, 0, 127]), (8, 1000008, [70, 80]), (64, 260040, [200, 0, 150, 1])]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("k,n,splits", TILED)
+def test_forward_large_tiles(k, n, splits, gather):
+    rows, g = sum(splits), len(splits)
+    x, w = _normal((rows, k), 1, BF), _normal((g, n, k), 2, BF)
+    index = None
+    if gather:
+        index = torch.randperm(rows, generator=torch.Generator().manual_seed(3)).int().cuda()
+        index[0], index[5] = -1, rows
+    _forward(x, w, splits, index, mx.ragged_gemm("NT", x, w, _ms(splits), row_index=index), rows)
+    if k > 64:
+        got = mx.ragged_gemm("NT", x, w, _ms(splits), row_index=index, out_dtype=F32)
+        _forward(x, w, splits, index, got, rows)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("k,n,splits", [(12304, 4104, [20, 0, 41, 1, 64, 33]), (12416, 4136, [63, 65, 0, 130, 100, 1]),
+                                        (12288, 4104, [300, 257, 0, 1, 255, 256]), (144, 300016, [30, 64, 0, 40]),
+                                        (272, 160048, [129, 128, 0, 127]), (16, 1000016, [70, 80])])
+def test_int8_large_tiles(k, n, splits, gather):
+    rows, g = sum(splits), len(splits)
+    gen = torch.Generator("cuda").manual_seed(2)
+    q = torch.randint(-127, 128, (rows, k), generator=gen, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (g, n, k), generator=gen, device="cuda", dtype=torch.int8)
+    sc, ws = torch.rand(rows, generator=gen, device="cuda"), torch.rand((g, n), generator=gen, device="cuda")
+    index = None
+    if gather:
+        index = torch.randperm(rows, generator=torch.Generator().manual_seed(3)).int().cuda()
+        index[0], index[5] = -1, rows
+    got = mx.ragged_gemm_int8(q, sc, w, ws, _ms(splits), row_index=index, out_dtype=BF)
+    _int8_check(q, sc, w, ws, splits, index, got, rows)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("k,n,pad", [(2111, 4011, 0), (2112, 4011, 3), (2111, 4008, 5)])
+def test_odd_operands_laid_out_anew(k, n, pad, dtype):
+    """Rows that do not start on 16 bytes, and work enough that they are copied
+    first; rows past the last expert's are neither read nor written."""
+    splits, rows = [1200, 0, 1, 900, 850], 3000
+    g, end = len(splits), sum(splits)
+    wide = lambda t: torch.nn.functional.pad(t, (0, pad), value=math.nan)[:, :t.shape[1]]  # noqa: E731
+    x, dy = _normal((rows, k), 1, dtype), _normal((rows, n), 3, dtype)
+    x[end:], dy[end:] = math.nan, math.inf
+    x, dy, w, ms = wide(x), wide(dy), _normal((g, n, k), 2, dtype), _ms(splits)
+    index = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device="cuda")
+    xr = x.flip(0).contiguous()          # the same rows through the index
+    for out in (dtype, F32):
+        y = wide(torch.full((rows, n), 7.0, dtype=out, device="cuda"))
+        mx.ragged_gemm("NT", x, w, ms, out=y, out_dtype=out)
+        _forward(x, w, splits, None, y, rows)
+        assert (y[end:] == 7.0).all()
+        y2 = mx.ragged_gemm("NT", xr, w, ms, row_index=index, out_dtype=out)
+        assert torch.equal(y2[:end], y[:end])
+        dx = torch.full((rows, k), 7.0, dtype=out, device="cuda")
+        mx.ragged_gemm("NN", dy, w, ms, out=dx, out_dtype=out)
+        _dgrad(dy, w, splits, dx)
+        assert (dx[end:] == 7.0).all()
+        dw = mx.ragged_gemm("TN", dy, x, ms, out_dtype=out)
+        _wgrad(dy, x, splits, None, dw)
+        assert torch.equal(mx.ragged_gemm("TN", dy, xr, ms, row_index=index, out_dtype=out), dw)
+
+
+def test_int8_odd_laid_out_anew():
+    splits, k, n, rows = [1200, 0, 1, 900, 850], 2111, 4011, 3000
+    gen = torch.Generator("cuda").manual_seed(2)
+    q = torch.randint(-127, 128, (rows, k), generator=gen, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (5, n, k), generator=gen, device="cuda", dtype=torch.int8)
+    sc, ws = torch.rand(rows, generator=gen, device="cuda"), torch.rand((5, n), generator=gen, device="cuda")
+    for out in (F32, BF, HF):
+        _int8_check(q, sc * 1e-3, w, ws * 1e-3, splits, None,
+                    mx.ragged_gemm_int8(q, sc * 1e-3, w, ws * 1e-3, _ms(splits), out_dtype=out), rows)
+
+
+def test_wgrad_odd_columns_of_padded_rows():
+    """Odd widths in rows that do start on 16 bytes: the last value of the last row."""
+    splits, k, n = [70, 0, 130], 37, 51
+    x, dy = torch.zeros((200, 40), dtype=BF, device="cuda")[:, :k], torch.zeros((200, 56), dtype=BF, device="cuda")[:, :n]
+    x.copy_(_normal((200, k), 1, BF))
+    dy.copy_(_normal((200, n), 2, BF))
+    _wgrad(dy, x, splits, None, mx.ragged_gemm("TN", dy, x, _ms(splits)))
+    k = 40
+    x = _normal((200, k), 1, BF)
+    _wgrad(dy, x, splits, None, mx.ragged_gemm("TN", dy, x, _ms(splits), out_dtype=F32))
+
+
+def test_small_workspace_and_none():
+    """A workspace that is larger than needed, and the C entry without one."""
+    from moe_expert_grouped_group_amd import _native
+    splits, k, n = [300, 0, 700], 1032, 520
+    x, w, dy, ms = _normal((1000, k), 1, BF), _normal((3, n, k), 2, BF), _normal((1000, n), 3, BF), _ms(splits)
+    need = mx.ragged_gemm_workspace_bytes("NN", BF, 1000, 1000, n, k, 3)
+    big = torch.empty(need + 4096, dtype=torch.uint8, device="cuda")
+    a = mx.ragged_gemm("NN", dy, w, ms, out_dtype=F32, workspace=big)
+    assert torch.equal(a, mx.ragged_gemm("NN", dy, w, ms, out_dtype=F32))
+    with pytest.raises(ValueError):
+        mx.ragged_gemm("NN", dy, w, ms, workspace=big[:need - 1])
+    b = torch.empty_like(a)
+    lib = _native.load()
+    st = lib.mxfp8_ragged_gemm(1, 1, dy.data_ptr(), n, w.data_ptr(), k, b.data_ptr(), k, 0, 1000, 1000, n, k,
+                               ms.data_ptr(), 3, None, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    _dgrad(dy, w, splits, b)
+
+
 def test_offsets_past_32_bits():
     """Weights, gathered tokens and outputs over 4 GiB."""
     g, n, k = 33, 8192, 8192                      # W: 4.4 GB

@@ -331,13 +331,17 @@ Repack repack_of(int layout, int esize, int osize, const RaggedArgs& p) {
   r.bytes_c = r.c ? (size_t)r.rows_c * r.ldc * osize : 0;
   return r;
 }
-// Copying pays where the arithmetic is long enough: ragged_any_kernel reaches
-// 560 (NT), 250 (NN) and 150 (TN) TFLOP/s on 16384 rows of 8 x 4096 x 14336, the
-// large tiles 1150 and more; a copy moves its bytes twice at about 4 TB/s.
-bool repack_pays(int layout, const RaggedArgs& p, size_t bytes) {
+// Copying pays where the arithmetic is long enough.  Measured: ragged_any_kernel
+// reaches 560 (NT), 250 (NN) and 150 (TN) TFLOP/s on 16384 rows of 8 x 4096 x 14336
+// and takes about 1.7 us for each step of its contraction however small the
+// product (NN, 9 rows, 3103 x 147: 179 us); the large tiles reach 1150 TFLOP/s and
+// take 30 us at least; a copy moves its bytes twice at about 4 TB/s.
+bool repack_pays(int layout, int esize, const RaggedArgs& p, size_t bytes) {
   const double tflop = 2e-12 * (double)p.R * (double)p.N * (double)p.K;
-  const double any = tflop / (layout == 0 ? 560.0 : layout == 1 ? 250.0 : 150.0);
-  return bytes <= ((size_t)8 << 30) && any > tflop / 1150.0 + 2.0 * (double)bytes / 4e12 + 30e-6;
+  const double rate = layout == 0 ? 560.0 : layout == 1 ? 250.0 : 150.0;
+  const double con = layout == 0 ? (double)p.K : layout == 1 ? (double)p.N : (double)p.R / p.G;
+  const double any = std::max(tflop / rate, 1.7e-6 * con * esize / kAnyBytes);
+  return bytes <= ((size_t)8 << 30) && any > tflop / 1150.0 + 2.0 * (double)bytes / 4e12 + 40e-6;
 }
 size_t split_bytes() { return ragged_split_bytes(); }
 
@@ -393,7 +397,7 @@ hipError_t with_tiles(int layout, int osize, RaggedArgs p, size_t ws_bytes, hipS
   *done = false;
   uint8_t* ws = (uint8_t*)p.ws;
   if (r.bytes() > 0 && (ws == nullptr || ws_bytes < split_bytes() + r.bytes() ||
-                        !repack_pays(layout, p, r.bytes())))
+                        !repack_pays(layout, esize, p, r.bytes())))
     return hipSuccess;
   RaggedArgs q = p;
   if (ws_bytes < split_bytes()) q.ws = nullptr;
@@ -436,7 +440,7 @@ size_t ragged_workspace_bytes(int layout, int esize, int64_t R, int64_t S, int64
   size_t most = 0;
   for (int osize = 2; osize <= 4; osize += 2) {
     const size_t n = repack_of(layout, esize, osize, p).bytes();
-    if (n > 0 && repack_pays(layout, p, n)) most = std::max(most, n);
+    if (n > 0 && repack_pays(layout, esize, p, n)) most = std::max(most, n);
   }
   return split_bytes() + most;
 }

@@ -296,11 +296,12 @@ int64_t pad16(int64_t n, int64_t size) { return (n * size + 15) / 16 * 16 / size
 // the weights and ragged_few.hip takes it.  Measured (MI355X, weights of W MB, m
 // rows an expert): about W (0.16 + 0.0071 m) us there, 30 + 0.19 W us for the
 // large tiles, e.g. 940 MB: 166 and 178 us at 4 rows, 191 and 182 at 8; 34 MB:
-// 38 and 34 us at 64 rows of 1 expert.
+// 38 and 34 us at 64 rows of 1 expert.  The fit holds to some 256 rows; 22 experts of
+// 808 x 151 with 760 rows each took 130 us there.
 bool few_rows(const RaggedArgs& p, int esize) {
   const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
   const double mb = 1e-6 * (double)groups * (double)p.N * (double)p.K * esize;
-  return p.R < (1 << 20) && (mean <= 4 || (double)(mean - 4) * mb <= 4200.0);
+  return p.R < (1 << 20) && mean <= 256 && (mean <= 4 || (double)(mean - 4) * mb <= 4200.0);
 }
 
 // What the large tiles want and an operand may lack: rows on 16 bytes, the
@@ -334,14 +335,15 @@ Repack repack_of(int layout, int esize, int osize, const RaggedArgs& p) {
 // Copying pays where the arithmetic is long enough.  Measured: ragged_any_kernel
 // reaches 560 (NT), 250 (NN) and 150 (TN) TFLOP/s on 16384 rows of 8 x 4096 x 14336
 // and takes about 1.7 us for each step of its contraction however small the
-// product (NN, 9 rows, 3103 x 147: 179 us); the large tiles reach 1150 TFLOP/s and
-// take 30 us at least; a copy moves its bytes twice at about 4 TB/s.
+// product (NN, 9 rows, 3103 x 147: 179 us; NT, 1777 x 1031 x 517: 48 us); the large
+// tiles reach 1150 TFLOP/s and with three copies take 57 us at least; a copy moves
+// its bytes twice at about 4 TB/s.
 bool repack_pays(int layout, int esize, const RaggedArgs& p, size_t bytes) {
   const double tflop = 2e-12 * (double)p.R * (double)p.N * (double)p.K;
   const double rate = layout == 0 ? 560.0 : layout == 1 ? 250.0 : 150.0;
   const double con = layout == 0 ? (double)p.K : layout == 1 ? (double)p.N : (double)p.R / p.G;
   const double any = std::max(tflop / rate, 1.7e-6 * con * esize / kAnyBytes);
-  return bytes <= ((size_t)8 << 30) && any > tflop / 1150.0 + 2.0 * (double)bytes / 4e12 + 40e-6;
+  return bytes <= ((size_t)8 << 30) && any > tflop / 1150.0 + 2.0 * (double)bytes / 4e12 + 57e-6;
 }
 size_t split_bytes() { return ragged_split_bytes(); }
 

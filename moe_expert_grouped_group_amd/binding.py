@@ -526,6 +526,15 @@ def _matrix(t, name):
     return t.shape
 
 
+def _fresh(shape, dtype, like, stream):
+    """A buffer that this call allocates; torch is told when another stream than
+    its own is to use it."""
+    t = _empty(shape, dtype, like)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _type_of(t, name, floats=(torch.bfloat16, torch.float16)):
     if t.dtype not in floats:
         raise NotImplementedError(f"{name} of {t.dtype} is not supported")
@@ -563,10 +572,7 @@ def _ragged_workspace(workspace, like, stream, *sizes):
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = _empty((need,), torch.uint8, like)
-        if stream is not None:
-            workspace.record_stream(stream)
-        return workspace, need
+        return _fresh((need,), torch.uint8, like, stream), need
     size = workspace.numel() * workspace.element_size()
     if not workspace.is_cuda or size < need:
         raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
@@ -623,13 +629,13 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
         raise NotImplementedError(f"output dtype {out_dtype} is not supported")
     if lay == LAYOUT_TN:
         if out is None:
-            out = _empty((g, n, k), out_dtype, a)
+            out = _fresh((g, n, k), out_dtype, a, stream)
         _need(out, out_dtype, (g, n, k), "out")
         ldc = k
     else:
         shape = (r, n if lay == LAYOUT_NT else k)
         if out is None:
-            out = _empty(shape, out_dtype, a)
+            out = _fresh(shape, out_dtype, a, stream)
         ldc = _rows_of(out, out_dtype, shape, "out")
     ws, ws_bytes = _ragged_workspace(workspace, a, stream, lay, a.dtype, r, s, n, k, g)
     _same_device(a, b=b, m_splits=ms, row_index=index, out=out, workspace=ws)
@@ -649,8 +655,8 @@ def quantize_int8(x, out=None, stream=None):
     ty = _type_of(x, "x")
     ldx = _rows_of(x, x.dtype, (t, k), "x")
     q, scale = (None, None) if out is None else out
-    q = _empty((t, k), torch.int8, x) if q is None else q
-    scale = _empty((t,), torch.float32, x) if scale is None else scale
+    q = _fresh((t, k), torch.int8, x, stream) if q is None else q
+    scale = _fresh((t,), torch.float32, x, stream) if scale is None else scale
     _need(q, torch.int8, (t, k), "q")
     _need(scale, torch.float32, (t,), "scale")
     _same_device(x, q=q, scale=scale)
@@ -681,7 +687,7 @@ def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=t
     if out_dtype not in _TYPE:
         raise NotImplementedError(f"output dtype {out_dtype} is not supported")
     if out is None:
-        out = _empty((r, n), out_dtype, q)
+        out = _fresh((r, n), out_dtype, q, stream)
     ldc = _rows_of(out, out_dtype, (r, n), "out")
     ws, ws_bytes = _ragged_workspace(workspace, q, stream, LAYOUT_NT, torch.int8, r, s, n, k, g)
     _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out,
@@ -725,11 +731,11 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
             token_mask = token_mask.view(torch.uint8)
         _need(token_mask, torch.uint8, (t,), "token_mask")
     if out is None:
-        out = Route(_empty((t, top_k), torch.int32, logits),
-                    _empty((t, top_k), torch.float32, logits),
-                    _empty((e,), torch.int64, logits),
-                    _empty((t * top_k,), torch.int32, logits),
-                    _empty((t, top_k), torch.int32, logits))
+        out = Route(_fresh((t, top_k), torch.int32, logits, stream),
+                    _fresh((t, top_k), torch.float32, logits, stream),
+                    _fresh((e,), torch.int64, logits, stream),
+                    _fresh((t * top_k,), torch.int32, logits, stream),
+                    _fresh((t, top_k), torch.int32, logits, stream))
     else:
         _need(out.ids, torch.int32, (t, top_k), "ids")
         _need(out.weights, torch.float32, (t, top_k), "weights")
@@ -744,7 +750,7 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
         if not workspace.is_cuda or size < need:
             raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
     elif need:
-        workspace = _empty((need,), torch.uint8, logits)
+        workspace = _fresh((need,), torch.uint8, logits, stream)
     _same_device(logits, token_mask=token_mask, ids=out.ids, weights=out.weights,
                  m_splits=out.m_splits, row_token=out.row_token, row_pos=out.row_pos,
                  workspace=workspace)
@@ -767,7 +773,7 @@ def moe_route_bwd(logits, route, dweights, out=None, stream=None):
     _need(route.weights, torch.float32, (t, k), "weights")
     _need(dweights, torch.float32, (t, k), "dweights")
     if out is None:
-        out = torch.empty_like(logits)
+        out = _fresh((t, e), logits.dtype, logits, stream)
     _need(out, logits.dtype, (t, e), "out")
     _same_device(logits, ids=route.ids, weights=route.weights, dweights=dweights, out=out)
     st = lib.mxfp8_moe_route_bwd(_ptr(logits), ty, t, e, k, int(route.renormalize),
@@ -790,7 +796,7 @@ def moe_combine(y, row_pos, weights=None, out=None, stream=None):
     if weights is not None:
         _need(weights, torch.float32, (t, k), "weights")
     if out is None:
-        out = _empty((t, h), y.dtype, y)
+        out = _fresh((t, h), y.dtype, y, stream)
     _need(out, y.dtype, (t, h), "out")
     _same_device(y, row_pos=row_pos, weights=weights, out=out)
     st = lib.mxfp8_moe_combine(_ptr(y), ty, t, r, h, k, _ptr(row_pos), _ptr(weights), _ptr(out),
@@ -816,12 +822,12 @@ def moe_combine_bwd(dout, y, row_pos, weights=None, want_dy=True, want_dweights=
         _need(weights, torch.float32, (t, k), "weights")
     dy, dw = (None, None) if out is None else out
     if want_dy:
-        dy = torch.empty_like(y) if dy is None else dy
+        dy = _fresh((r, h), y.dtype, y, stream) if dy is None else dy
         _need(dy, dout.dtype, (r, h), "dy")
     else:
         dy = None
     if want_dweights:
-        dw = _empty((t, k), torch.float32, dout) if dw is None else dw
+        dw = _fresh((t, k), torch.float32, dout, stream) if dw is None else dw
         _need(dw, torch.float32, (t, k), "dweights")
     else:
         dw = None

@@ -13,6 +13,7 @@ namespace mx {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kRaggedMaxGroups = 1024;
@@ -63,6 +64,12 @@ struct TypeBf16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(vec, a),
                                                    __builtin_bit_cast(vec, b), c, 0, 0, 0);
   }
+  // 16 x 16 results, 64 contraction bytes
+  typedef f32x4 acc16;
+  static __device__ __forceinline__ acc16 mma16(u32x4_t a, u32x4_t b, acc16 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec, a),
+                                                   __builtin_bit_cast(vec, b), c, 0, 0, 0);
+  }
 };
 struct TypeF16 {
   typedef uint16_t elem;
@@ -72,6 +79,12 @@ struct TypeF16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(vec, a),
                                                   __builtin_bit_cast(vec, b), c, 0, 0, 0);
   }
+  // 16 x 16 results, 64 contraction bytes
+  typedef f32x4 acc16;
+  static __device__ __forceinline__ acc16 mma16(u32x4_t a, u32x4_t b, acc16 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec, a),
+                                                  __builtin_bit_cast(vec, b), c, 0, 0, 0);
+  }
 };
 // 8-bit integers: products and sums are exact in 32 bits for K <= 131071.
 struct TypeI8 {
@@ -79,6 +92,11 @@ struct TypeI8 {
   typedef i32x16 acc;
   static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+  }
+  typedef i32x4 acc16;
+  static __device__ __forceinline__ acc16 mma16(u32x4_t a, u32x4_t b, acc16 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
                                                  __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
   }
 };

@@ -16,37 +16,6 @@
 
 namespace mx {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-template <typename T>
-struct Small;
-template <>
-struct Small<TypeBf16> {
-  typedef f32x4 acc;
-  static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
-    typedef TypeBf16::vec v;
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v, a), __builtin_bit_cast(v, b),
-                                                   c, 0, 0, 0);
-  }
-};
-template <>
-struct Small<TypeF16> {
-  typedef f32x4 acc;
-  static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
-    typedef TypeF16::vec v;
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v, a), __builtin_bit_cast(v, b),
-                                                  c, 0, 0, 0);
-  }
-};
-template <>
-struct Small<TypeI8> {
-  typedef i32x4 acc;
-  static __device__ __forceinline__ acc mma(u32x4_t a, u32x4_t b, acc c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
-                                                 c, 0, 0, 0);
-  }
-};
-
 // 16 bytes at p, of which the contraction holds n (n <= 0: none): zeros behind.
 template <typename E>
 __device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
@@ -66,7 +35,7 @@ __device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
 template <typename T, typename O, int MR, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
   typedef typename T::elem E;
-  typedef typename Small<T>::acc Acc;
+  typedef typename T::acc16 Acc;
   constexpr bool kInt8 = sizeof(E) == 1;
   __shared__ Acc part[WAVES][MR][64];
   const int lane = threadIdx.x & 63;
@@ -113,7 +82,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
 #pragma unroll
     for (int i = 0; i < 2 * U; ++i)
 #pragma unroll
-      for (int m = 0; m < MR; ++m) acc[m] = Small<T>::mma(wv[i], xv[i][m], acc[m]);
+      for (int m = 0; m < MR; ++m) acc[m] = T::mma16(wv[i], xv[i][m], acc[m]);
   }
   // the lines that are left, each to the next wave; the last may be partial
   const int64_t lines = (kb + 127) / 128;
@@ -124,7 +93,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
       const int64_t n = kb - at - sub * 16;
       const u32x4_t wv = chunk_end<E>(w + at, n);
 #pragma unroll
-      for (int m = 0; m < MR; ++m) acc[m] = Small<T>::mma(wv, chunk_end<E>(x[m] + at, n), acc[m]);
+      for (int m = 0; m < MR; ++m) acc[m] = T::mma16(wv, chunk_end<E>(x[m] + at, n), acc[m]);
     }
   }
 

@@ -12,19 +12,23 @@
 //    256 bytes of the banks, and the 16 rows that one LDS access phase reads use
 //    16 different places there.
 //  * contraction over rows (W in NN, dY and X in TN): a stage is [64][512 B],
-//    chunk c of row r at chunk c ^ {0, 4, 10, 14}[r & 3].  Fragments come through
-//    the transposing LDS read: in each group of 16 lanes, lane l hands in the
-//    address of 4 columns of contraction row l / 4 and gets 4 contraction rows
-//    of column l.  The 4 rows x 32 columns of 32 lanes lie in 256 different
-//    bytes of bank space.
+//    chunk c of row r at chunk c ^ {0, 4, 10, 14}[r & 3] ^ 2 (r / 8 % 2).  Fragments
+//    come through the transposing LDS read: in each group of 16 lanes, lane l
+//    hands in the address of 4 columns of contraction row l / 4 and gets 4
+//    contraction rows of column l.  The 8 rows (two groups of 4, 8 apart) x 16
+//    columns of 32 lanes lie in 256 different bytes of bank space.
 // What lies outside an operand (rows past an expert's in TN, past N in
 // NN, past K in a last stage, row indexes out of range) is zero because the
 // buffer loads are bounded: such a lane's offset fails the range check and the
 // load writes zeros.  Rows of other experts that a tile of NT or NN takes along
 // reach only result rows that are not stored.
 //
-// The matrix instructions take the column operand first, so that a lane holds
-// 4 consecutive columns of one row and stores 16 bytes at a time.
+// The matrix instructions are the 16 x 16 ones: for each product they read and write
+// half as many accumulators as the 32 x 32 ones, and under this load the chip's
+// clock goes by the power it draws.  Measured in turn on 8 x 4096 x 14336: forward
+// 1.67 ms with 32 x 32 and 1.59 with 16 x 16, int8 0.93 and 0.90.  They take the
+// column operand first, so that a lane holds 4 consecutive columns of one row and
+// stores 16 bytes at a time.
 #pragma once
 
 #include <type_traits>
@@ -213,8 +217,9 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   constexpr int kOffB = kTileM * kStageK;
   constexpr int kStage = kOffB + kTileN * kStageK;
   constexpr int kPartsA = 2 * FA, kParts = kPartsA + 8;      // copies of a wave for a stage
-  constexpr int kMfma = 8 * FA;                              // of a half stage
-  constexpr int kReads = 2 * (FA + 4);
+  constexpr int kRowsF = 2 * FA;                             // fragments of 16 rows; 8 of 16 columns
+  constexpr int kMfma = 8 * kRowsF;                          // of a half stage: 64 contraction bytes
+  constexpr int kReads = kRowsF + 8;
   constexpr int kEarly = 3 * kParts / 8;                     // copies in the first half
   constexpr int kStores = sizeof(typename O::elem) == 4 ? 16 * FA : 8 * FA;
   static_assert(!kColA || FA == 4, "");
@@ -391,7 +396,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   auto chunk_k = [&](int j) { return (uint32_t)((lane & 7) ^ (4 * (j & 1) + (lane >> 4))) * 16; };
   auto chunk_c = [&](int j) {
     const int r = 2 * (j & 1) + (lane >> 5);
-    const int x = (r & 1) * 4 + (r >> 1) * 10;
+    const int x = ((r & 1) * 4 + (r >> 1) * 10) ^ (2 * (j >> 2));   // row 2 j + .. of 16
     return (uint32_t)((lane & 31) ^ x) * 16;
   };
   uint32_t va[kPartsA], vb[8];
@@ -410,26 +415,24 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) past[j] = !kColA && chunk_k(j) >= last_bytes ? kOut : 0u;
 
-  // Addresses of the fragments in a stage.
-  uint32_t ra[kColA ? FA : 4], rb[kColB ? 4 : 4];
+  // Address of the first fragment of each half of a stage.  Contiguous: fragment i
+  // 16 rows (2048 bytes) on.  Over rows: columns 16 i on, address bits 5..7 changed
+  // by 32 i; the halves 32 contraction rows apart.
+  uint32_t ra[2], rb[2];
   {
-    const int xr = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 1) * 10;
-    auto col = [&](int first) {   // first: the fragment's first column
-      return (uint32_t)(((lane >> 2) & 3) * 512 + (lane >> 5) * 4096 +
-                        (((first >> 3) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ xr) * 16 +
-                        (lane & 1) * 8);
+    const int xr = (((lane >> 2) & 1) * 4 + ((lane >> 3) & 1) * 10) ^ (2 * ((lane >> 4) & 1));
+    auto col = [&](int first, int h) {
+      return (uint32_t)((32 * h + 8 * (lane >> 4) + ((lane >> 2) & 3)) * 512 +
+                        (((first >> 3) + ((lane >> 1) & 1)) ^ xr) * 16 + (lane & 1) * 8);
     };
-    auto row = [&](int first, int s) {
-      return (uint32_t)((first + (lane & 31)) * kStageK + (((2 * s + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16));
+    auto row = [&](int first, int h) {
+      return (uint32_t)((first + (lane & 15)) * kStageK +
+                        (((4 * h + (lane >> 4)) ^ ((lane >> 1) & 7)) * 16));
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (kColA) {
-        if (i < FA) ra[i] = lds0 + col(wm * 32 * FA + 32 * i);
-      } else {
-        ra[i] = lds0 + row(wm * 32 * FA, i);
-      }
-      rb[i] = lds0 + kOffB + (kColB ? col(wn * 128 + 32 * i) : row(wn * 128, i));
+    for (int h = 0; h < 2; ++h) {
+      ra[h] = lds0 + (kColA ? col(wm * 32 * FA, h) : row(wm * 32 * FA, h));
+      rb[h] = lds0 + kOffB + (kColB ? col(wn * 128, h) : row(wn * 128, h));
     }
   }
   auto transposed = [](uint32_t at) {
@@ -439,8 +442,8 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     return u32x4_t{a[0], a[1], b[0], b[1]};
   };
 
-  typename T::acc acc[FA][4];
-  u32x4_t fa[2][2][FA], fb[2][2][4];
+  typename T::acc16 acc[kRowsF][8];
+  u32x4_t fa[2][kRowsF], fb[2][8];
 
   Tile t;              // the tile whose operands are copied
   int slot0 = 0;       // slot of the computed tile's stage 0
@@ -536,56 +539,62 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
           ring0 + (uint32_t)(s.at & 7) * 256u + (uint32_t)(16 * wave + 2 * j + (lane >> 5)) * 4u);
   };
   // copy c of a stage: A and B parts in turn (then what is left of B)
-  auto copy = [&](const Stage& s, auto C) {
+  // Copy c of a stage: its addresses first, behind a matrix instruction of their
+  // own, then the copy behind the next (all five instructions behind one are more
+  // than its 16 cycles hide: 8 x 4096 x 14336 forward 1.59 ms, so 1.55).
+  struct Part {
+    uint32_t off, at;
+  } part[kParts];
+  auto prepare = [&](const Stage& s, auto C) {
     constexpr int c = decltype(C)::value;
     constexpr bool isA = c < 2 * kPartsA && c % 2 == 0;
     constexpr int j = isA ? c / 2 : (c < 2 * kPartsA ? c / 2 : c - kPartsA);
+    uint32_t off;
     if constexpr (isA) {
-      const uint32_t at = s.lds + (uint32_t)(wave * kPartsA * 1024 + j * 1024);
-      copy16(s.sa, kColA ? va[j] : (va[j] | s.kill[j & 1]), kColA ? 0u : s.soff, at);
+      off = kColA ? va[j] : (va[j] | s.kill[j & 1]);
+    } else if constexpr (GATHER && kColA) {
+      const int r = 16 * wave + 2 * j + (lane >> 5);
+      const bool ok = (s.st * 64 + r < s.len) & (rows_at[j] < (uint32_t)p.S);
+      off = (rows_at[j] * eb + chunk_c(j)) | (ok ? 0u : kOut);
     } else {
-      const uint32_t at = s.lds + kOffB + (uint32_t)(wave * 8192 + j * 1024);
-      if constexpr (GATHER && kColA) {
-        const int r = 16 * wave + 2 * j + (lane >> 5);
-        const bool ok = (s.st * 64 + r < s.len) & (rows_at[j] < (uint32_t)p.S);
-        copy16(s.sb, (rows_at[j] * eb + chunk_c(j)) | (ok ? 0u : kOut), 0u, at);
-      } else {
-        copy16(s.sb, kColB ? vb[j] : (vb[j] | s.kill[j & 1]), kColB ? 0u : s.soff, at);
-      }
+      off = kColB ? vb[j] : (vb[j] | s.kill[j & 1]);
     }
+    uint32_t at = s.lds + (isA ? (uint32_t)(wave * kPartsA * 1024 + j * 1024)
+                               : kOffB + (uint32_t)(wave * 8192 + j * 1024));
+    asm volatile("" : "+s"(at));
+    part[c] = {hide(off), at};
   };
-  // fragment r (0 .. kReads) of half h of a stage into register set h; at: the
-  // slot's offset
+  auto copy = [&](const Stage& s, auto C) {
+    constexpr int c = decltype(C)::value;
+    constexpr bool isA = c < 2 * kPartsA && c % 2 == 0;
+    if constexpr (isA) copy16(s.sa, part[c].off, kColA ? 0u : s.soff, part[c].at);
+    else copy16(s.sb, part[c].off, kColB ? 0u : s.soff, part[c].at);
+  };
+  // fragment r (0 .. kReads) of half h of a stage into register set h
   struct Base {
-    uint32_t a[4], b[4];
+    uint32_t a, b;
   };
   auto base = [&](int slot, auto H) {
     constexpr int h = decltype(H)::value;
-    Base x;
     const uint32_t off = (uint32_t)slot * kStage;
-#pragma unroll
-    for (int i = 0; i < (kColA ? FA : 2); ++i) x.a[i] = hide(ra[kColA ? i : 2 * h + i] + off);
-#pragma unroll
-    for (int i = 0; i < (kColB ? 4 : 2); ++i) x.b[i] = hide(rb[kColB ? i : 2 * h + i] + off);
-    return x;
+    return Base{hide(ra[h] + off), hide(rb[h] + off)};
   };
   auto read = [&](const Base& x, auto H, auto R) {
     constexpr int h = decltype(H)::value, r = decltype(R)::value;
-    constexpr int s = r / (FA + 4), q = r % (FA + 4);   // step of the half, fragment
-    constexpr bool isA = q < 2 * FA ? q % 2 == 0 : false;
-    constexpr int i = isA ? q / 2 : (q < 2 * FA ? q / 2 : q - FA);
+    constexpr bool isA = r < 2 * kRowsF && r % 2 == 0;
+    constexpr int i = r < 2 * kRowsF ? r / 2 : r - kRowsF;
     if constexpr (isA) {
-      if constexpr (kColA) fa[h][s][i] = transposed(x.a[i] + (2 * h + s) * 8192);
-      else fa[h][s][i] = *(lds_u32x4_t*)(x.a[s] + i * 4096);
+      if constexpr (kColA) fa[h][i] = transposed(x.a ^ (uint32_t)(32 * i));
+      else fa[h][i] = *(lds_u32x4_t*)(x.a + i * 2048);
     } else {
-      if constexpr (kColB) fb[h][s][i] = transposed(x.b[i] + (2 * h + s) * 8192);
-      else fb[h][s][i] = *(lds_u32x4_t*)(x.b[s] + i * 4096);
+      if constexpr (kColB) fb[h][i] = transposed(x.b ^ (uint32_t)(32 * i));
+      else fb[h][i] = *(lds_u32x4_t*)(x.b + i * 2048);
     }
   };
   auto mma = [&](auto H, auto Q) {
     constexpr int h = decltype(H)::value, q = decltype(Q)::value;
-    constexpr int s = q / (4 * FA), i = q % (4 * FA) / 4, j = q % 4;
-    acc[i][j] = T::mma(fb[h][s][j], fa[h][s][i], acc[i][j]);
+    constexpr int i = q / 8, j = q % 8;
+    acc[i][j] = T::mma16(fb[h][j], fa[h][i], acc[i][j]);
     asm volatile("" : "+a"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -611,7 +620,10 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     for (int st = 0; st < 2; ++st) {   // a stage past the last copies zeros
       const Stage s = stage(st, st);
       if constexpr (GATHER && kColA) read_index(s);
-      unroll<kParts>([&](auto C) { copy(s, C); });
+      unroll<kParts>([&](auto C) {
+        prepare(s, C);
+        copy(s, C);
+      });
     }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(vm_wait(0));
@@ -638,7 +650,9 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         __syncthreads();
       }
       unroll<kEarly>([&](auto C) {
-        if constexpr (m + 1 + decltype(C)::value * (m - 1) / kEarly == q) copy(cp, C);
+        constexpr int at = m + 1 + decltype(C)::value * (m - 1) / kEarly;
+        if constexpr (at - 1 == q) prepare(cp, C);
+        if constexpr (at == q) copy(cp, C);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -659,8 +673,10 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         if constexpr (decltype(R)::value * kMfma / kReads == q) read(x, H0{}, R);
       });
       unroll<left>([&](auto C) {
-        if constexpr (1 + decltype(C)::value * (kMfma - 2) / left == q)
-          copy(cp, std::integral_constant<int, decltype(C)::value + kEarly>{});
+        constexpr int at = decltype(C)::value * (kMfma / 4) / left * 4 + 2;   // between two reads
+        using Part_ = std::integral_constant<int, decltype(C)::value + kEarly>;
+        if constexpr (at - 1 == q) prepare(cp, Part_{});
+        if constexpr (at == q) copy(cp, Part_{});
       });
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -685,11 +701,12 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     // barrier of this tile lies between.
     bool chain = next < nunits && ns >= (GATHER ? 4 : (kInt8 ? 3 : 2));
 #pragma unroll
-    for (int i = 0; i < FA; ++i)
+    for (int i = 0; i < kRowsF; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+      for (int j = 0; j < 8; ++j) {
+        acc[i][j] = typename T::acc16{0, 0, 0, 0};
+        asm volatile("" : "+a"(acc[i][j]));
+      }
     for (int st = 0; st < ns; ++st) {
       int from = st + 2;
       if (st >= ns - 2) {
@@ -732,32 +749,25 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       const auto ws = make_rsrc((const uint8_t*)p.ws + (int64_t)split * (kTileM * kTileN * 4),
                                 kTileM * kTileN * 4);
 #pragma unroll
-      for (int i = 0; i < FA; ++i)
+      for (int i = 0; i < kRowsF; ++i) {
+        if (wm * 32 * FA + 16 * i >= rows) continue;   // not read by the join either
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (wm * 32 * FA + 32 * i >= rows) continue;   // not read by the join either
+        for (int j = 0; j < 8; ++j) {
           // (values of this branch's own: moved ahead of the branch, all 256
           // accumulators would be spilled)
           asm volatile("" : "+a"(acc[i][j]));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            u32x4_t v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const auto x = acc[i][j][4 * q + e];   // (a bit cast of the element itself reads element 0)
-              v[e] = __builtin_bit_cast(uint32_t, x);
-            }
-            __builtin_amdgcn_raw_buffer_store_b128(
-                v, ws, (uint32_t)((((wave * FA + i) * 4 + j) * 4 + q) * 1024 + ln * 16), 0, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4_t, acc[i][j]), ws,
+              (uint32_t)(((wave * kRowsF + i) * 8 + j) * 1024 + ln * 16), 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
       return;
     }
-    float srow[FA];
+    float srow[kRowsF];
     if constexpr (kInt8) {
 #pragma unroll
-      for (int i = 0; i < FA; ++i) srow[i] = scales[side][0][wm * 32 * FA + 32 * i + (ln & 31)];
+      for (int i = 0; i < kRowsF; ++i) srow[i] = scales[side][0][wm * 32 * FA + 16 * i + (ln & 15)];
     }
 
     // Stores, bounded like the loads: lanes past the tile's rows or columns get an
@@ -769,48 +779,45 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     const int64_t room = (int64_t)(rows - 1) * ec + (p.ccols - n0) * (int64_t)sizeof(OE);
     const auto out = make_rsrc(c, room);
     const int right = (int)min((int64_t)kTileN, p.ccols - n0);   // columns to store
-    auto value = [&](int i, int j, int r) {
+    auto value = [&](int i, int j, int e) {
       if constexpr (kInt8)
-        return (float)acc[i][j][r] * srow[i] *
-               scales[side][1][wn * 128 + 32 * j + 8 * (r >> 2) + 4 * (ln >> 5) + (r & 3)];
+        return (float)acc[i][j][e] * srow[i] * scales[side][1][wn * 128 + 16 * j + 4 * (ln >> 4) + e];
       else
-        return acc[i][j][r];
+        return acc[i][j][e];
     };
+    // Accumulator e of block (i, j) in lane l: row 16 i + l % 16, column
+    // 16 j + 4 (l / 16) + e.
     constexpr int kNt = 0;
 #pragma unroll
-    for (int i = 0; i < FA; ++i) {
-      const int m = wm * 32 * FA + 32 * i + (ln & 31);
+    for (int i = 0; i < kRowsF; ++i) {
+      const int m = wm * 32 * FA + 16 * i + (ln & 15);
       const uint32_t roff = m < rows ? (uint32_t)m * ec : kOut;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        asm volatile("" : "+a"(acc[i][j]));
+      for (int j = 0; j < 8; j += 2) {
+        asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
         if constexpr (sizeof(OE) == 4) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = wn * 128 + 32 * j + 8 * q + 4 * (ln >> 5);
-            const u32x4_t v = {__float_as_uint(value(i, j, 4 * q)), __float_as_uint(value(i, j, 4 * q + 1)),
-                               __float_as_uint(value(i, j, 4 * q + 2)),
-                               __float_as_uint(value(i, j, 4 * q + 3))};
+          for (int k = j; k < j + 2; ++k) {
+            const int n = wn * 128 + 16 * k + 4 * (ln >> 4);
+            const u32x4_t v = {__float_as_uint(value(i, k, 0)), __float_as_uint(value(i, k, 1)),
+                               __float_as_uint(value(i, k, 2)), __float_as_uint(value(i, k, 3))};
             const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 4u : kOut;
             __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
           }
         } else {
+          // 8 consecutive columns a lane: rows of 16 lanes trade, so that rows 0 and 2
+          // of lanes take block j (columns 0.. and 8..), rows 1 and 3 block j + 1
+          uint32_t w[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // 8 consecutive columns: lanes l and l + 32 trade a half each
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 8 * h + 2 * e;
-              w[e] = (uint32_t)O::cvt(value(i, j, r)) | ((uint32_t)O::cvt(value(i, j, r + 1)) << 16);
-            }
-            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-            const u32x4_t v = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
-            const int n = wn * 128 + 32 * j + 16 * h + 8 * (ln >> 5);
-            const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 2u : kOut;
-            __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
-          }
+          for (int k = 0; k < 4; ++k)
+            w[k] = (uint32_t)O::cvt(value(i, j + (k >> 1), 2 * (k & 1))) |
+                   ((uint32_t)O::cvt(value(i, j + (k >> 1), 2 * (k & 1) + 1)) << 16);
+          const auto s0 = __builtin_amdgcn_permlane16_swap(w[0], w[2], false, false);
+          const auto s1 = __builtin_amdgcn_permlane16_swap(w[1], w[3], false, false);
+          const u32x4_t v = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+          const int n = wn * 128 + 16 * (j + ((ln >> 4) & 1)) + 8 * (ln >> 5);
+          const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 2u : kOut;
+          __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -834,13 +841,13 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
 }
 
 // Sums of the parts of split tiles, in order, with the conversion and stores of the kernel above.
-// Workgroup b takes 32-row strips b, b + grid, ... of the split tiles (strip: one wave's fragment row).
+// Workgroup b takes strips b, b + grid, ... of the split tiles (strip: a wave's 16 rows).
 template <typename T, typename O, int LAYOUT, int FA>
 __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t tile_grid) {
   constexpr bool kInt8 = sizeof(typename T::elem) == 1;
   constexpr int kTileM = 64 * FA;
-  constexpr int kStrips = 4 * FA;
-  const int lane = threadIdx.x & 63, j = threadIdx.x >> 6;
+  constexpr int kRowsF = 2 * FA, kStrips = 4 * kRowsF;
+  const int lane = threadIdx.x & 63;
   const int64_t cols = LAYOUT == 0 ? p.N : p.K;
   const uint32_t ctiles = (uint32_t)((cols + kTileN - 1) / kTileN);
   const uint32_t band = (uint32_t)((p.N + kTileM - 1) / kTileM);
@@ -851,7 +858,7 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
   if (u.parts < 2) return;
   for (uint32_t b = blockIdx.x; b < u.rem * kStrips; b += gridDim.x) {
     const uint32_t v = b / kStrips, strip = b % kStrips, at = u.full + v;
-    const int wave = (int)strip / FA, i = (int)strip % FA;
+    const int wave = (int)strip / kRowsF, i = (int)strip % kRowsF;
     int32_t mt, nt, g;
     int64_t m0, rows;
     if (LAYOUT == 2) {
@@ -866,20 +873,21 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
       m0 = s.row0;
       rows = s.rows;
     }
-    if ((wave >> 1) * 32 * FA + 32 * i >= rows) continue;
-    typedef typename std::conditional<kInt8, i32x4, float __attribute__((ext_vector_type(4)))>::type V;
-    V sum[4];
+    if ((wave >> 1) * 32 * FA + 16 * i >= rows) continue;
+    // blocks threadIdx.x / 64 and 4 on of the strip's 8
+    typedef typename T::acc16 V;
+    V sum[2];
     for (uint32_t part = 0; part < u.parts; ++part) {
       const uint8_t* ws = (const uint8_t*)p.ws + (int64_t)(part * u.rem + v) * (kTileM * kTileN * 4) +
-                          ((wave * FA + i) * 4 + j) * 4096 + lane * 16;
+                          ((wave * kRowsF + i) * 8 + (threadIdx.x >> 6)) * 1024 + lane * 16;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const V x = *(const V*)(ws + q * 1024);
+      for (int q = 0; q < 2; ++q) {
+        const V x = *(const V*)(ws + q * 4096);
         if (part == 0) sum[q] = x;
         else sum[q] += x;
       }
     }
-    const int m = (wave >> 1) * 32 * FA + 32 * i + (lane & 31);
+    const int m = (wave >> 1) * 32 * FA + 16 * i + (lane & 15);
     if (m >= rows) continue;
     float sa = 0.f;
     if (kInt8) {
@@ -889,8 +897,9 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
     typedef typename O::elem OE;
     OE* c = (OE*)p.c + ((LAYOUT == 2 ? (int64_t)g * p.N : 0) + m0 + m) * p.ldc;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t n = (int64_t)nt * kTileN + (wave & 1) * 128 + 32 * j + 8 * q + 4 * (lane >> 5);
+    for (int q = 0; q < 2; ++q) {
+      const int64_t n = (int64_t)nt * kTileN + (wave & 1) * 128 + 16 * (int)(threadIdx.x >> 6) + 64 * q +
+                        4 * (lane >> 4);
       if (n >= p.ccols) continue;   // columns come in fours (rows are multiples of 16 bytes)
       OE o[4];
 #pragma unroll

@@ -26,8 +26,8 @@ hipError_t launch_tile(const RaggedArgs& p, hipStream_t st) {
   ragged_tile_kernel<T, O, LAYOUT, FA, GATHER><<<dim3(grid), dim3(256), 0, st>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.ws == nullptr) return e;
-  // half the tiles of a round at most are split, 4 FA strips each
-  const unsigned strips = std::max(1u, grid / 2) * 4 * FA;
+  // half the tiles of a round at most are split, 8 FA strips each
+  const unsigned strips = std::max(1u, grid / 2) * 8 * FA;
   ragged_join_kernel<T, O, LAYOUT, FA><<<dim3(std::min(strips, 1024u)), dim3(256), 0, st>>>(p, grid);
   return hipGetLastError();
 }

@@ -3,10 +3,12 @@
 Argument marshalling only: shapes and dtypes are checked, outputs are
 allocated with torch when the caller does not pass them, and every step of
 the computation runs in the HIP kernels of libmxfp8moe.so on the current
-torch stream (or the stream given).  The entry points have the C names
-without the ``mxfp8_`` prefix.
+torch stream (or the stream given, from whose pool its buffers then come; the
+caller orders that stream behind the inputs and ahead of the results' use).
+The entry points have the C names without the ``mxfp8_`` prefix.
 """
 
+import contextlib
 import functools
 from dataclasses import dataclass
 from typing import Optional
@@ -62,8 +64,29 @@ def _need(t, dtype, shape, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _empty(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _pool(stream):
+    """The context in which memory comes from the pool of the stream that will use
+    it.  A block of another stream's pool may still be in use by work queued
+    there, which nothing here is ordered behind."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output that this call allocates.  The caller reads it on the current
+    stream, which the allocator is told."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    reader = torch.cuda.current_stream(device)
+    with _pool(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(reader)
+    return t
+
+
+def _scratch(size, device, stream):
+    """A workspace for this call alone: only `stream` ever uses it."""
+    with _pool(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def _as_shape(t, shape, name):
@@ -88,19 +111,19 @@ def _splits(m_splits, name="m_splits"):
     return m_splits
 
 
-def _mx_outputs(out, usage, t, k, like):
+def _mx_outputs(out, usage, t, k, like, stream):
     """Allocate (or check) the requested row-/column-wise buffers of a [t, k] tensor."""
     out = out or MXFP8Tensor()
     if usage & ROWWISE:
         if out.row_data is None:
-            out.row_data = _empty((t, k), torch.uint8, like)
-            out.row_scale = _empty((t, k // 32), torch.uint8, like)
+            out.row_data = _empty((t, k), torch.uint8, like.device, stream)
+            out.row_scale = _empty((t, k // 32), torch.uint8, like.device, stream)
         _need(out.row_data, torch.uint8, (t, k), "row_data")
         _need(out.row_scale, torch.uint8, (t, k // 32), "row_scale")
     if usage & COLWISE:
         if out.col_data is None:
-            out.col_data = _empty((k, t), torch.uint8, like)
-            out.col_scale = _empty((k, t // 32), torch.uint8, like)
+            out.col_data = _empty((k, t), torch.uint8, like.device, stream)
+            out.col_scale = _empty((k, t // 32), torch.uint8, like.device, stream)
         _need(out.col_data, torch.uint8, (k, t), "col_data")
         _need(out.col_scale, torch.uint8, (k, t // 32), "col_scale")
     return out
@@ -122,10 +145,11 @@ def group_quantize(x, usage=ROWWISE, out: Optional[MXFP8Tensor] = None, noop_fla
     """
     lib = _lib()
     if x.dim() != 2:
-        x = x.reshape(-1, x.shape[-1])
+        with _pool(stream):   # a copy, where it takes one, is made and used on one stream
+            x = x.reshape(-1, x.shape[-1])
     t, k = x.shape
     _need(x, torch.bfloat16, (t, k), "x")
-    out = _mx_outputs(out, usage, t, k, x)
+    out = _mx_outputs(out, usage, t, k, x, stream)
     if noop_flag is not None:
         _need(noop_flag, torch.int32, (1,), "noop_flag")
     st = lib.mxfp8_group_quantize(_ptr(x), t, k, usage, *_mx_ptrs(out, usage), _ptr(noop_flag),
@@ -142,7 +166,7 @@ def swiglu_quantize(h, usage=ROWWISE | COLWISE, out: Optional[MXFP8Tensor] = Non
     t, f2 = h.shape
     f = f2 // 2
     _need(h, torch.bfloat16, (t, 2 * f), "h")
-    out = _mx_outputs(out, usage, t, f, h)
+    out = _mx_outputs(out, usage, t, f, h, stream)
     st = lib.mxfp8_swiglu_quantize(_ptr(h), t, f, usage, *_mx_ptrs(out, usage), _stream(stream))
     _native.check(st, "mxfp8_swiglu_quantize")
     return out
@@ -152,10 +176,10 @@ def dbias_workspace_bytes(t, n):
     return int(_lib().mxfp8_dbias_workspace_bytes(t, n))
 
 
-def _workspace(t, n, like, workspace):
+def _workspace(t, n, like, workspace, stream):
     need = dbias_workspace_bytes(t, n)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
+        workspace = _scratch(max(need, 1), like.device, stream)
     if not workspace.is_cuda or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
     return workspace
@@ -170,8 +194,8 @@ def requant_colwise(row_data, row_scale, m_splits=None, with_dbias=False, out=No
     _need(row_scale, torch.uint8, (t, k // 32), "row_scale")
     out = out or MXFP8Tensor(row_data=row_data, row_scale=row_scale)
     if out.col_data is None:
-        out.col_data = _empty((k, t), torch.uint8, row_data)
-        out.col_scale = _empty((k, t // 32), torch.uint8, row_data)
+        out.col_data = _empty((k, t), torch.uint8, row_data.device, stream)
+        out.col_scale = _empty((k, t // 32), torch.uint8, row_data.device, stream)
     _need(out.col_data, torch.uint8, (k, t), "col_data")
     _need(out.col_scale, torch.uint8, (k, t // 32), "col_scale")
     g = 0
@@ -180,9 +204,9 @@ def requant_colwise(row_data, row_scale, m_splits=None, with_dbias=False, out=No
         ms = _splits(m_splits)
         g = ms.numel()
         if dbias is None:
-            dbias = _empty((g, k), torch.float32, row_data)
+            dbias = _empty((g, k), torch.float32, row_data.device, stream)
         _need(dbias, torch.float32, (g, k), "dbias")
-        workspace = _workspace(t, k, row_data, workspace)
+        workspace = _workspace(t, k, row_data, workspace, stream)
     st = lib.mxfp8_requant_colwise(
         _ptr(row_data), _ptr(row_scale), t, k, _ptr(out.col_data), _ptr(out.col_scale),
         _ptr(ms), g, _ptr(dbias) if with_dbias else None,
@@ -201,16 +225,16 @@ def group_quantize_requant(x, m_splits=None, with_dbias=False, out=None, dbias=N
     lib = _lib()
     t, k = x.shape
     _need(x, torch.bfloat16, (t, k), "x")
-    out = _mx_outputs(out, ROWWISE | COLWISE, t, k, x)
+    out = _mx_outputs(out, ROWWISE | COLWISE, t, k, x, stream)
     g = 0
     ms = None
     if with_dbias:
         ms = _splits(m_splits)
         g = ms.numel()
         if dbias is None:
-            dbias = _empty((g, k), torch.float32, x)
+            dbias = _empty((g, k), torch.float32, x.device, stream)
         _need(dbias, torch.float32, (g, k), "dbias")
-        workspace = _workspace(t, k, x, workspace)
+        workspace = _workspace(t, k, x, workspace, stream)
     st = lib.mxfp8_group_quantize_requant(
         _ptr(x), t, k, _ptr(out.row_data), _ptr(out.row_scale), _ptr(out.col_data),
         _ptr(out.col_scale), _ptr(ms), g, _ptr(dbias) if with_dbias else None,
@@ -233,14 +257,14 @@ def group_quantize_requant_noalloc(x, m_splits=None, with_dbias=False, out=None,
     lib = _lib()
     t, k = x.shape
     _need(x, torch.bfloat16, (t, k), "x")
-    out = _mx_outputs(out, ROWWISE | COLWISE, t, k, x)
+    out = _mx_outputs(out, ROWWISE | COLWISE, t, k, x, stream)
     g = 0
     ms = None
     if with_dbias:
         ms = _splits(m_splits)
         g = ms.numel()
         if dbias is None:
-            dbias = _empty((g, k), torch.float32, x)
+            dbias = _empty((g, k), torch.float32, x.device, stream)
         _need(dbias, torch.float32, (g, k), "dbias")
     st = lib.mxfp8_group_quantize_requant_noalloc(
         _ptr(x), t, k, _ptr(out.row_data), _ptr(out.row_scale), _ptr(out.col_data),
@@ -258,9 +282,9 @@ def grouped_dbias(row_data, row_scale, m_splits, dbias=None, workspace=None, str
     ms = _splits(m_splits)
     g = ms.numel()
     if dbias is None:
-        dbias = _empty((g, n), torch.float32, row_data)
+        dbias = _empty((g, n), torch.float32, row_data.device, stream)
     _need(dbias, torch.float32, (g, n), "dbias")
-    workspace = _workspace(t, n, row_data, workspace)
+    workspace = _workspace(t, n, row_data, workspace, stream)
     st = lib.mxfp8_grouped_dbias(_ptr(row_data), _ptr(row_scale), t, n, _ptr(ms), g,
                                  _ptr(dbias), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream))
@@ -285,19 +309,20 @@ def grouped_scaled_bias_grad(row_data, row_scale, m_splits, scales=None, bias=No
     dbias, dscales = (None, None) if out is None else out
     if want_dbias:
         _need(scales, torch.float32, (t,), "scales")
-        dbias = _empty((g, n), torch.float32, row_data) if dbias is None else dbias
+        dbias = _empty((g, n), torch.float32, row_data.device, stream) if dbias is None else dbias
         _need(dbias, torch.float32, (g, n), "dbias")
     else:
         dbias = None
     if want_dscales:
         _need(bias, torch.float32, (g, n), "bias")
-        dscales = _empty((t,), torch.float32, row_data) if dscales is None else dscales
+        if dscales is None:
+            dscales = _empty((t,), torch.float32, row_data.device, stream)
         _need(dscales, torch.float32, (t,), "dscales")
     else:
         dscales = None
     need = lib.mxfp8_scaled_bias_workspace_bytes(t, n)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=row_data.device)
+        workspace = _scratch(max(need, 1), row_data.device, stream)
     st = lib.mxfp8_grouped_scaled_bias_grad(
         _ptr(row_data), _ptr(row_scale), t, n, _ptr(ms), g, _ptr(scales) if want_dbias else None,
         _ptr(bias) if want_dscales else None, _ptr(dbias), _ptr(dscales), _ptr(workspace),
@@ -346,7 +371,7 @@ def grouped_gemm(layout, a_data, a_scale, b_data, b_scale, m_splits, tokens, n, 
     b2 = _as_shape(b_data, shapes[2], "b_data")
     bs2 = _as_shape(b_scale, shapes[3], "b_scale")
     if out is None:
-        out = _empty(shapes[4], out_dtype, a2)
+        out = _empty(shapes[4], out_dtype, a2.device, stream)
     _need(out, out_dtype, shapes[4], "out")
     if workspace is None:
         st = lib.mxfp8_grouped_gemm(lay, _ptr(a2), _ptr(as2), _ptr(b2), _ptr(bs2), _ptr(out),
@@ -376,9 +401,9 @@ def grouped_gemm_swiglu_quantize(a_data, a_scale, b_data, b_scale, m_splits, tok
     b2 = _as_shape(b_data, (g * 2 * f, k), "b_data")
     bs2 = _as_shape(b_scale, (g * 2 * f, k // 32), "b_scale")
     if h is None:
-        h = _empty((t, 2 * f), torch.bfloat16, a2)
+        h = _empty((t, 2 * f), torch.bfloat16, a2.device, stream)
     _need(h, torch.bfloat16, (t, 2 * f), "h")
-    out = _mx_outputs(out, usage, t, f, a2)
+    out = _mx_outputs(out, usage, t, f, a2, stream)
     st = lib.mxfp8_grouped_gemm_swiglu_quantize(
         _ptr(a2), _ptr(as2), _ptr(b2), _ptr(bs2), _ptr(h), t, f, k, _ptr(ms), g, usage,
         *_mx_ptrs(out, usage), _stream(stream))
@@ -419,7 +444,7 @@ def validate_splits(m_splits, tokens, flag=None, stream=None):
     lib = _lib()
     ms = _splits(m_splits)
     if flag is None:
-        flag = _empty((1,), torch.int32, ms)
+        flag = _empty((1,), torch.int32, ms.device, stream)
     st = lib.mxfp8_validate_splits(_ptr(ms), ms.numel(), tokens, _ptr(flag), _stream(stream))
     _native.check(st, "mxfp8_validate_splits")
     return flag
@@ -432,7 +457,7 @@ def swiglu_fwd(h, out=None, stream=None):
     f = f2 // 2
     _need(h, torch.bfloat16, (t, 2 * f), "h")
     if out is None:
-        out = _empty((t, f), torch.bfloat16, h)
+        out = _empty((t, f), torch.bfloat16, h.device, stream)
     _need(out, torch.bfloat16, (t, f), "out")
     _native.check(lib.mxfp8_swiglu_fwd(_ptr(h), t, f, _ptr(out), _stream(stream)),
                   "mxfp8_swiglu_fwd")
@@ -450,16 +475,16 @@ def swiglu_bwd_quantize(h, da, m_splits=None, with_dbias=False, out=None, dbias=
     f = k // 2
     _need(h, torch.bfloat16, (t, 2 * f), "h")
     _need(da, torch.bfloat16, (t, f), "da")
-    out = _mx_outputs(out, ROWWISE | COLWISE, t, k, h)
+    out = _mx_outputs(out, ROWWISE | COLWISE, t, k, h, stream)
     g = 0
     ms = None
     if with_dbias:
         ms = _splits(m_splits)
         g = ms.numel()
         if dbias is None:
-            dbias = _empty((g, k), torch.float32, h)
+            dbias = _empty((g, k), torch.float32, h.device, stream)
         _need(dbias, torch.float32, (g, k), "dbias")
-        workspace = _workspace(t, k, h, workspace)
+        workspace = _workspace(t, k, h, workspace, stream)
     st = lib.mxfp8_swiglu_bwd_quantize(
         _ptr(h), _ptr(da), t, f, _ptr(out.row_data), _ptr(out.row_scale), _ptr(out.col_data),
         _ptr(out.col_scale), _ptr(ms), g, _ptr(dbias) if with_dbias else None,
@@ -477,7 +502,7 @@ def swiglu_bwd(h, da, out=None, stream=None):
     _need(h, torch.bfloat16, (t, 2 * f), "h")
     _need(da, torch.bfloat16, (t, f), "da")
     if out is None:
-        out = _empty((t, 2 * f), torch.bfloat16, h)
+        out = _empty((t, 2 * f), torch.bfloat16, h.device, stream)
     _need(out, torch.bfloat16, (t, 2 * f), "out")
     _native.check(lib.mxfp8_swiglu_bwd(_ptr(h), _ptr(da), t, f, _ptr(out), _stream(stream)),
                   "mxfp8_swiglu_bwd")
@@ -491,7 +516,7 @@ def convert_sweep(mode, stream=None):
     need = lib.mxfp8_convert_sweep_bytes(mode)
     if need == 0:
         raise ValueError(f"unknown sweep mode {mode}")
-    out = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = _empty((need,), torch.uint8, torch.device("cuda"), stream)
     st = lib.mxfp8_convert_sweep(mode, _ptr(out), need, _stream(stream))
     _native.check(st, "mxfp8_convert_sweep")
     return out
@@ -524,15 +549,6 @@ def _matrix(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
     return t.shape
-
-
-def _fresh(shape, dtype, like, stream):
-    """A buffer that this call allocates; torch is told when another stream than
-    its own is to use it."""
-    t = _empty(shape, dtype, like)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _type_of(t, name, floats=(torch.bfloat16, torch.float16)):
@@ -572,7 +588,7 @@ def _ragged_workspace(workspace, like, stream, *sizes):
     if workspace is None:
         if need == 0:
             return None, 0
-        return _fresh((need,), torch.uint8, like, stream), need
+        return _scratch(need, like.device, stream), need
     size = workspace.numel() * workspace.element_size()
     if not workspace.is_cuda or size < need:
         raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
@@ -629,13 +645,13 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
         raise NotImplementedError(f"output dtype {out_dtype} is not supported")
     if lay == LAYOUT_TN:
         if out is None:
-            out = _fresh((g, n, k), out_dtype, a, stream)
+            out = _empty((g, n, k), out_dtype, a.device, stream)
         _need(out, out_dtype, (g, n, k), "out")
         ldc = k
     else:
         shape = (r, n if lay == LAYOUT_NT else k)
         if out is None:
-            out = _fresh(shape, out_dtype, a, stream)
+            out = _empty(shape, out_dtype, a.device, stream)
         ldc = _rows_of(out, out_dtype, shape, "out")
     ws, ws_bytes = _ragged_workspace(workspace, a, stream, lay, a.dtype, r, s, n, k, g)
     _same_device(a, b=b, m_splits=ms, row_index=index, out=out, workspace=ws)
@@ -655,8 +671,8 @@ def quantize_int8(x, out=None, stream=None):
     ty = _type_of(x, "x")
     ldx = _rows_of(x, x.dtype, (t, k), "x")
     q, scale = (None, None) if out is None else out
-    q = _fresh((t, k), torch.int8, x, stream) if q is None else q
-    scale = _fresh((t,), torch.float32, x, stream) if scale is None else scale
+    q = _empty((t, k), torch.int8, x.device, stream) if q is None else q
+    scale = _empty((t,), torch.float32, x.device, stream) if scale is None else scale
     _need(q, torch.int8, (t, k), "q")
     _need(scale, torch.float32, (t,), "scale")
     _same_device(x, q=q, scale=scale)
@@ -687,7 +703,7 @@ def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=t
     if out_dtype not in _TYPE:
         raise NotImplementedError(f"output dtype {out_dtype} is not supported")
     if out is None:
-        out = _fresh((r, n), out_dtype, q, stream)
+        out = _empty((r, n), out_dtype, q.device, stream)
     ldc = _rows_of(out, out_dtype, (r, n), "out")
     ws, ws_bytes = _ragged_workspace(workspace, q, stream, LAYOUT_NT, torch.int8, r, s, n, k, g)
     _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out,
@@ -731,11 +747,11 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
             token_mask = token_mask.view(torch.uint8)
         _need(token_mask, torch.uint8, (t,), "token_mask")
     if out is None:
-        out = Route(_fresh((t, top_k), torch.int32, logits, stream),
-                    _fresh((t, top_k), torch.float32, logits, stream),
-                    _fresh((e,), torch.int64, logits, stream),
-                    _fresh((t * top_k,), torch.int32, logits, stream),
-                    _fresh((t, top_k), torch.int32, logits, stream))
+        out = Route(_empty((t, top_k), torch.int32, logits.device, stream),
+                    _empty((t, top_k), torch.float32, logits.device, stream),
+                    _empty((e,), torch.int64, logits.device, stream),
+                    _empty((t * top_k,), torch.int32, logits.device, stream),
+                    _empty((t, top_k), torch.int32, logits.device, stream))
     else:
         _need(out.ids, torch.int32, (t, top_k), "ids")
         _need(out.weights, torch.float32, (t, top_k), "weights")
@@ -750,7 +766,7 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
         if not workspace.is_cuda or size < need:
             raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
     elif need:
-        workspace = _fresh((need,), torch.uint8, logits, stream)
+        workspace = _scratch(need, logits.device, stream)
     _same_device(logits, token_mask=token_mask, ids=out.ids, weights=out.weights,
                  m_splits=out.m_splits, row_token=out.row_token, row_pos=out.row_pos,
                  workspace=workspace)
@@ -773,7 +789,7 @@ def moe_route_bwd(logits, route, dweights, out=None, stream=None):
     _need(route.weights, torch.float32, (t, k), "weights")
     _need(dweights, torch.float32, (t, k), "dweights")
     if out is None:
-        out = _fresh((t, e), logits.dtype, logits, stream)
+        out = _empty((t, e), logits.dtype, logits.device, stream)
     _need(out, logits.dtype, (t, e), "out")
     _same_device(logits, ids=route.ids, weights=route.weights, dweights=dweights, out=out)
     st = lib.mxfp8_moe_route_bwd(_ptr(logits), ty, t, e, k, int(route.renormalize),
@@ -796,7 +812,7 @@ def moe_combine(y, row_pos, weights=None, out=None, stream=None):
     if weights is not None:
         _need(weights, torch.float32, (t, k), "weights")
     if out is None:
-        out = _fresh((t, h), y.dtype, y, stream)
+        out = _empty((t, h), y.dtype, y.device, stream)
     _need(out, y.dtype, (t, h), "out")
     _same_device(y, row_pos=row_pos, weights=weights, out=out)
     st = lib.mxfp8_moe_combine(_ptr(y), ty, t, r, h, k, _ptr(row_pos), _ptr(weights), _ptr(out),
@@ -822,12 +838,12 @@ def moe_combine_bwd(dout, y, row_pos, weights=None, want_dy=True, want_dweights=
         _need(weights, torch.float32, (t, k), "weights")
     dy, dw = (None, None) if out is None else out
     if want_dy:
-        dy = _fresh((r, h), y.dtype, y, stream) if dy is None else dy
+        dy = _empty((r, h), y.dtype, y.device, stream) if dy is None else dy
         _need(dy, dout.dtype, (r, h), "dy")
     else:
         dy = None
     if want_dweights:
-        dw = _fresh((t, k), torch.float32, dout, stream) if dw is None else dw
+        dw = _empty((t, k), torch.float32, dout.device, stream) if dw is None else dw
         _need(dw, torch.float32, (t, k), "dweights")
     else:
         dw = None

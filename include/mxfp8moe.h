@@ -505,7 +505,7 @@ typedef enum mxfp8_type {
  *           where that pays.  Results do not depend on it but for the order of
  *           sums.
  * mxfp8_ragged_gemm_workspace_bytes: for operands of elem_bytes (2, or 1 for
- * mxfp8_ragged_gemm_int8); 0 where none is used.
+ * mxfp8_ragged_gemm_int8); 0 where none is used, and for sizes that are refused.
  * Errors: EINVAL for NULL pointers, sizes < 1 (R, S >= 0), strides shorter than
  * a row, G out of range, host m_splits, row_index with NN, S != R without
  * row_index, over 2^31 - 1 rows, columns or tiles; ENOTSUP for other types.
@@ -564,7 +564,7 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
  *                             token; -1 past the last row
  *   row_pos int32 [T, top_k]  row of each choice, -1 where there is none
  *   workspace   of mxfp8_moe_route_workspace_bytes(T, E) bytes; needs no
- *               initialisation (NULL where that is 0)
+ *               initialisation (NULL where that is 0, as for sizes that are refused)
  * Errors: EINVAL for NULL, sizes out of range, T top_k >= 2^31, a small
  * workspace; ENOTSUP for other types.  T = 0 writes m_splits only.
  */

@@ -493,7 +493,8 @@ void* usable_workspace(void* ws) { return aligned_to(ws, 16) ? ws : nullptr; }
 size_t mxfp8_ragged_gemm_workspace_bytes(int32_t layout, int32_t elem_bytes, int64_t R, int64_t S,
                                          int64_t N, int64_t K, int32_t G) {
   if (layout < 0 || layout > 2 || (elem_bytes != 1 && elem_bytes != 2) || R < 0 || S < 0 || N < 1 ||
-      K < 1 || G < 1 || R > kI32Max || S > kI32Max || N > kI32Max || K > kI32Max)
+      K < 1 || G < 1 || G > mx::kRaggedMaxGroups || R > kI32Max || S > kI32Max || N > kI32Max ||
+      K > kI32Max)
     return 0;
   return mx::ragged_workspace_bytes(layout, elem_bytes, R, S, N, K, G);
 }
@@ -607,10 +608,13 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
 
 namespace {
 
+constexpr int32_t kRouteMaxExperts = 1024;
+
 mxfp8_status check_route(const char* fn, int32_t type, int64_t T, int32_t E, int32_t top_k) {
   if (type != MXFP8_TYPE_F32 && type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
     return fail(MXFP8_ENOTSUP, "%s: logits type %d is not supported", fn, (int)type);
-  REQUIRE(E >= 1 && E <= 1024, "%s: E = %d must be 1 to 1024", fn, (int)E);
+  REQUIRE(E >= 1 && E <= kRouteMaxExperts, "%s: E = %d must be 1 to %d", fn, (int)E,
+          kRouteMaxExperts);
   REQUIRE(top_k >= 1 && top_k <= 16 && top_k <= E, "%s: top_k = %d must be 1 to min(E, 16)", fn,
           (int)top_k);
   REQUIRE(T >= 0 && T <= kI32Max / top_k, "%s: T = %lld: T * top_k must be below 2^31", fn,
@@ -632,6 +636,7 @@ mxfp8_status check_join(const char* fn, int32_t type, int64_t T, int64_t R, int6
 }  // namespace
 
 size_t mxfp8_moe_route_workspace_bytes(int64_t T, int32_t E) {
+  if (T < 0 || T > kI32Max || E < 1 || E > kRouteMaxExperts) return 0;
   return mx::route_workspace_bytes(T, E);
 }
 

@@ -732,8 +732,9 @@ hipError_t launch_join_type(const JoinArgs& p, bool bwd, hipStream_t st) {
 
 }  // namespace
 
+// T and E as launch_route takes them.
 size_t route_workspace_bytes(int64_t T, int32_t E) {
-  if (T <= kOneLaunch || E <= 0) return 0;
+  if (T <= kOneLaunch) return 0;
   const int64_t c = route_chunk(T, E);
   return (size_t)((T + c - 1) / c) * (size_t)((E + 1) & ~1) * sizeof(uint16_t);
 }

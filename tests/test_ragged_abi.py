@@ -129,3 +129,30 @@ def test_binding_refuses(lib):
         mx.moe_combine(x, torch.zeros((2, 2), dtype=torch.int32))
     with pytest.raises(ValueError):
         mx.moe_combine_bwd(x, x, torch.zeros((2, 2), dtype=torch.int32))
+
+
+def test_workspace_queries_of_refused_sizes(lib):
+    """0, whatever the sizes: callers ask before the entry itself refuses."""
+    route, gemm = lib.mxfp8_moe_route_workspace_bytes, lib.mxfp8_ragged_gemm_workspace_bytes
+    for t, e in ((300, 10000), (300, 1025), (300, 0), (300, -1), (-1, 8), (1 << 31, 8), ((1 << 63) - 1, 1024),
+                 (300, (1 << 31) - 1)):
+        assert route(t, e) == 0, (t, e)
+    assert route((1 << 31) - 1, 1024) > 0
+    assert gemm(NN, 2, 300, 300, 64, 64, 1024) > 0
+    for args in ((NN, 2, 300, 300, 64, 64, 1025), (NN, 2, 300, 300, 64, 64, 0), (NN, 2, -1, 300, 64, 64, 2),
+                 (NN, 2, 300, 300, 0, 64, 2), (3, 2, 300, 300, 64, 64, 2), (NN, 4, 300, 300, 64, 64, 2)):
+        assert gemm(*args) == 0, args
+
+
+def test_route_of_too_many_experts_raises(lib, monkeypatch):
+    """The whole call on logits [300, 10000]: a ValueError from the entry."""
+    from moe_expert_grouped_group_amd import binding
+
+    class DeviceTensor(torch.Tensor):
+        is_cuda = True
+
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: real(*a, **kw).as_subclass(DeviceTensor))
+    monkeypatch.setattr(binding, "_stream", lambda s: 0)
+    with pytest.raises(ValueError, match="E = 10000"):
+        mx.moe_route(torch.zeros((300, 10000)).as_subclass(DeviceTensor), 2)

@@ -492,7 +492,9 @@ typedef enum mxfp8_type {
  *           Rows of C past the last expert's are not written, and rows past R
  *           not read, whatever the splits sum to
  *   row_index  NULL or device int32 [R] (NT, TN).  Entries outside [0, S) stand
- *           for a row of zeros; entries past the last expert's row are not read
+ *           for a row of zeros (of scale 0 in 8-bit integers): results are those
+ *           of an X that has such a row, NaN where it meets an infinity or NaN of
+ *           W, dY or w_scale.  Entries past the last expert's row are not read
  * TN writes zeros for an expert without rows.  Row values of experts that own
  * other rows never reach a result (infinities and NaN included).
  * Strides are in elements.  Faster where pointers, strides and the contraction

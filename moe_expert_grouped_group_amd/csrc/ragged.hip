@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p) {
           if (sizeof(E) == 1) {
             int64_t row = m0 + m;
             if (p.row_index != nullptr) row = p.row_index[row];
-            v = row >= 0 && row < p.S ? v * p.sa[row] * sb : 0.f;
+            v = v * (row >= 0 && row < p.S ? p.sa[row] : 0.f) * sb;
           }
           c[m * ldc + n] = O::cvt(v);
         }

@@ -118,7 +118,7 @@ __device__ void expert_rows(const int64_t* m_splits, int g, int64_t R, int64_t* 
 }
 
 template <typename T, typename O, int LAYOUT>
-__global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p) {
+__global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32_t first) {
   typedef typename T::elem E;
   constexpr int kPer = 16 / sizeof(E);             // elements of a chunk
   constexpr int kStep = kAnyBytes / sizeof(E);     // contraction elements per step
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p) {
   // the tile: rows [m0, m0 + rows) of A's output dimension, columns from n0
   const int64_t cols = LAYOUT == 0 ? p.N : p.K;
   const int64_t nt = (cols + kAnyT - 1) / kAnyT;
-  const int64_t ct = (int64_t)blockIdx.x % nt, rt = (int64_t)blockIdx.x / nt;
+  const int64_t at = first + blockIdx.x, ct = at % nt, rt = at / nt;
   const int64_t n0 = ct * kAnyT;
   int g;
   int64_t m0, rows, con, lo = 0;   // con: contraction length; lo: its first row (TN)
@@ -276,8 +276,9 @@ hipError_t launch_any(const RaggedArgs& p, hipStream_t st) {
   // expert that has rows
   const int64_t rt = LAYOUT == 2 ? p.G * ((p.N + kAnyT - 1) / kAnyT)
                                  : p.R / kAnyT + std::min<int64_t>(p.G, p.R);
-  ragged_any_kernel<T, O, LAYOUT><<<dim3((uint32_t)(nt * rt)), dim3(256), 0, st>>>(p);
-  return hipGetLastError();
+  return launch_in_parts(nt * rt, 256, [&](uint32_t first, uint32_t n) {
+    ragged_any_kernel<T, O, LAYOUT><<<dim3(n), dim3(256), 0, st>>>(p, first);
+  });
 }
 
 template <typename T, typename O>
@@ -480,7 +481,7 @@ hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, size_t ws_bytes
   return launch_any<TypeI8, OutF16, 0>(p, st);
 }
 
-// Workgroups that any call may launch at most (the grid's limit).
+// Workgroups that any call may need at most.
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G) {
   const int64_t cols = ((layout == 0 ? N : K) + kAnyT - 1) / kAnyT;
   if (layout == 0)   // the smallest tiles: 16 rows by 16 columns, where rows are few

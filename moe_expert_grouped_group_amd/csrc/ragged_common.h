@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace mx {
@@ -17,6 +19,20 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kRaggedMaxGroups = 1024;
+
+// Workgroups 0 .. blocks - 1 (below 2^32) of `threads` threads.  A launch holds fewer than
+// 2^32 threads, and one of more goes wrong without an error: larger grids go in parts, fn
+// launching `n` workgroups from number `first` on.
+template <typename F>
+hipError_t launch_in_parts(int64_t blocks, int threads, F fn) {
+  const int64_t most = 0xFFFFFFFFll / threads;
+  for (int64_t first = 0; first < blocks; first += most) {
+    fn((uint32_t)first, (uint32_t)std::min(most, blocks - first));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 // The arguments of one product.  X, dY and W are row-major with a contiguous
 // last dimension; strides are in elements.

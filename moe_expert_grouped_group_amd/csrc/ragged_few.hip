@@ -33,7 +33,7 @@ __device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
 }
 
 template <typename T, typename O, int MR, int U, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
+__global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, uint32_t first) {
   typedef typename T::elem E;
   typedef typename T::acc16 Acc;
   constexpr bool kInt8 = sizeof(E) == 1;
@@ -41,8 +41,9 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t ctiles = (uint32_t)((p.N + 15) / 16);
-  const int64_t rt = blockIdx.x / ctiles;
-  const int64_t n0 = (int64_t)(blockIdx.x % ctiles) * 16;
+  const uint32_t tile = first + blockIdx.x;
+  const int64_t rt = tile / ctiles;
+  const int64_t n0 = (int64_t)(tile % ctiles) * 16;
 
   const RowSpan at = wave_row_tile(p.m_splits, p.G, p.R, 16 * MR, rt, false);
   const int g = at.g, rows = at.rows;
@@ -151,8 +152,9 @@ template <typename T, typename O, int MR, int U, int WAVES>
 hipError_t launch_few(const RaggedArgs& p, hipStream_t st) {
   const int64_t rt = p.R / (16 * MR) + std::min<int64_t>(p.G, p.R);
   const int64_t blocks = rt * ((p.N + 15) / 16);
-  ragged_few_kernel<T, O, MR, U, WAVES><<<dim3((uint32_t)blocks), dim3(64 * WAVES), 0, st>>>(p);
-  return hipGetLastError();
+  return launch_in_parts(blocks, 64 * WAVES, [&](uint32_t first, uint32_t n) {
+    ragged_few_kernel<T, O, MR, U, WAVES><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
+  });
 }
 
 template <typename T, typename O>

@@ -23,7 +23,7 @@ namespace mx {
 
 constexpr int kRouteThreads = 1024;
 constexpr int kMaxTopK = 16;
-constexpr int kMaxChunk = 512;      // tokens of a workgroup at most
+constexpr int kMaxChunk = 512;      // tokens of a workgroup at most, twice that above 2^30
 
 // Element i of a 16- or 32-bit floating tensor as fp32.  type: 0 fp32, 1 bf16, 2 fp16.
 template <int TYPE>
@@ -348,9 +348,9 @@ struct RouteBwdArgs {
 };
 
 template <int TYPE, int L, int V>
-__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p, uint32_t first) {
   const int sub = threadIdx.x % L;
-  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int64_t t = (int64_t)(first + blockIdx.x) * (256 / L) + threadIdx.x / L;
   const bool on = t < p.T;
   // lane j holds choice j
   int id = -1;
@@ -366,10 +366,10 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
   float g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) g[i] = 0.f;
-  const int first = __shfl(id, (threadIdx.x & 63) / L * L, 64);
+  const int best = __shfl(id, (threadIdx.x & 63) / L * L, 64);
   if (!p.renorm) {
     float v[V];
-    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on && first >= 0, p.vec != 0, v);
+    load_logits<TYPE, L, V>(p.logits, t, p.E, sub, on && best >= 0, p.vec != 0, v);
     float top = v[0], sum = 0.f;
 #pragma unroll
     for (int i = 1; i < V; ++i) top = fmaxf(top, v[i]);
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) sum += v[i] = expf(v[i] - top);
     sum = lanes_sum<L>(sum);
-    if (first >= 0) {
+    if (best >= 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) g[i] = -inner * (v[i] / sum);
     }
@@ -470,8 +470,8 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, const float* v) {
 // in flight before it adds the first.  Workgroups are rows of `lanes` threads
 // for each of 256 / lanes tokens.
 template <int TYPE, int K>
-__global__ __launch_bounds__(256) void join_kernel(JoinArgs p, int lanes) {
-  const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs p, int lanes, uint32_t first) {
+  const int64_t t = (int64_t)(first + blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
   if (t >= p.T) return;
   int64_t row[K];
   float w[K];
@@ -505,9 +505,9 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs p, int lanes) {
 // dy and dweights: tokens as above; a token's dot products are joined over its
 // lanes (lanes is 64 or 256).
 template <int TYPE, int K>
-__global__ __launch_bounds__(256) void join_bwd_kernel(JoinArgs p, int lanes) {
+__global__ __launch_bounds__(256) void join_bwd_kernel(JoinArgs p, int lanes, uint32_t first) {
   __shared__ float part[4][K];
-  const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+  const int64_t t = (int64_t)(first + blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
   const bool on = t < p.T;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t row[K];
@@ -598,9 +598,9 @@ __device__ __forceinline__ int code_int8(float x, float scale, float inv) {
 template <int TYPE>
 __global__ __launch_bounds__(kQuantThreads) void quantize_int8_kernel(const void* x, int64_t ldx,
                                                                       int64_t K, int8_t* q,
-                                                                      float* scale) {
+                                                                      float* scale, uint32_t first) {
   __shared__ uint32_t part[kQuantThreads / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = first + blockIdx.x;
   const uint16_t* src = (const uint16_t*)x + row * ldx;
   int8_t* dst = q + row * K;
   const int64_t step = (int64_t)blockDim.x * 8;
@@ -663,10 +663,12 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_int8_kernel(const void
 namespace {
 
 // Tokens of a workgroup: about 256 workgroups, 64 to 512 tokens each
-// at most, and at most 32 KiB of bits (chunk * E / 8 bytes).
+// at most, and at most 32 KiB of bits (chunk * E / 8 bytes).  Above 2^30 tokens (of 256
+// experts at most: more would be 512 GiB of logits) 1024, as a launch holds fewer than
+// 2^32 threads.
 int route_chunk(int64_t T, int32_t E) {
-  const int64_t per = (T + 255) / 256;
-  const int64_t most = std::min<int64_t>(kMaxChunk, (1 << 18) / E / 32 * 32);
+  const int64_t per = (T + 255) / 256, cap = T > (1 << 30) ? 2 * kMaxChunk : kMaxChunk;
+  const int64_t most = std::min<int64_t>(cap, (1 << 18) / E / 32 * 32);
   return (int)std::min<int64_t>(std::max<int64_t>((per + 63) / 64 * 64, 64), most);
 }
 // Tokens that one workgroup alone takes: the second launch of the other form
@@ -696,8 +698,9 @@ hipError_t launch_bwd_lv(RouteBwdArgs p, hipStream_t st) {
   const uintptr_t on = (uintptr_t)p.logits | (uintptr_t)p.dlogits;
   p.vec = p.E % 4 == 0 && on % (TYPE == 0 ? 16 : 8) == 0;
   const int64_t per = 256 / L;
-  route_bwd_kernel<TYPE, L, V><<<(uint32_t)((p.T + per - 1) / per), 256, 0, st>>>(p);
-  return hipGetLastError();
+  return launch_in_parts((p.T + per - 1) / per, 256, [&](uint32_t first, uint32_t n) {
+    route_bwd_kernel<TYPE, L, V><<<n, 256, 0, st>>>(p, first);
+  });
 }
 
 // 16 lanes for a token up to 256 experts (4 tokens a wave, short reductions),
@@ -716,10 +719,10 @@ hipError_t launch_join_k(const JoinArgs& p, bool bwd, hipStream_t st) {
   // threads for a token: one wave for rows up to 1024 values, else the workgroup
   const int lanes = p.H <= 64 * kJoinWidth * 2 ? 64 : 256;
   const int64_t per = 256 / lanes;
-  const uint32_t blocks = (uint32_t)((p.T + per - 1) / per);
-  if (bwd) join_bwd_kernel<TYPE, K><<<blocks, 256, 0, st>>>(p, lanes);
-  else join_kernel<TYPE, K><<<blocks, 256, 0, st>>>(p, lanes);
-  return hipGetLastError();
+  return launch_in_parts((p.T + per - 1) / per, 256, [&](uint32_t first, uint32_t n) {
+    if (bwd) join_bwd_kernel<TYPE, K><<<n, 256, 0, st>>>(p, lanes, first);
+    else join_kernel<TYPE, K><<<n, 256, 0, st>>>(p, lanes, first);
+  });
 }
 template <int TYPE>
 hipError_t launch_join_type(const JoinArgs& p, bool bwd, hipStream_t st) {
@@ -806,11 +809,10 @@ hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, i
   // 7168 took 7.9 us with 256 threads each and 5.0 with 896.
   const int64_t most = T >= 1024 ? 256 : kQuantThreads;
   const uint32_t threads = (uint32_t)std::min<int64_t>(((K + 7) / 8 + 63) / 64 * 64, most);
-  if (f16)
-    quantize_int8_kernel<2><<<(uint32_t)T, threads, 0, st>>>(x, ldx, K, q, scale);
-  else
-    quantize_int8_kernel<1><<<(uint32_t)T, threads, 0, st>>>(x, ldx, K, q, scale);
-  return hipGetLastError();
+  return launch_in_parts(T, (int)threads, [&](uint32_t first, uint32_t n) {
+    if (f16) quantize_int8_kernel<2><<<n, threads, 0, st>>>(x, ldx, K, q, scale, first);
+    else quantize_int8_kernel<1><<<n, threads, 0, st>>>(x, ldx, K, q, scale, first);
+  });
 }
 
 }  // namespace mx

@@ -89,6 +89,14 @@ def _scratch(size, device, stream):
         return torch.empty(size, dtype=torch.uint8, device=device)
 
 
+def _sized(workspace, need):
+    """The bytes of a caller's workspace: the kernels write `need` from its pointer on."""
+    size = workspace.numel() * workspace.element_size()
+    if not workspace.is_cuda or not workspace.is_contiguous() or size < need:
+        raise ValueError(f"workspace must be a contiguous device buffer of at least {need} bytes")
+    return size
+
+
 def _as_shape(t, shape, name):
     """View a contiguous u8 operand with the expected number of bytes as `shape`."""
     n = 1
@@ -180,8 +188,7 @@ def _workspace(t, n, like, workspace, stream):
     need = dbias_workspace_bytes(t, n)
     if workspace is None:
         workspace = _scratch(max(need, 1), like.device, stream)
-    if not workspace.is_cuda or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
+    _sized(workspace, need)
     return workspace
 
 
@@ -323,6 +330,7 @@ def grouped_scaled_bias_grad(row_data, row_scale, m_splits, scales=None, bias=No
     need = lib.mxfp8_scaled_bias_workspace_bytes(t, n)
     if workspace is None:
         workspace = _scratch(max(need, 1), row_data.device, stream)
+    _sized(workspace, need)
     st = lib.mxfp8_grouped_scaled_bias_grad(
         _ptr(row_data), _ptr(row_scale), t, n, _ptr(ms), g, _ptr(scales) if want_dbias else None,
         _ptr(bias) if want_dscales else None, _ptr(dbias), _ptr(dscales), _ptr(workspace),
@@ -336,9 +344,7 @@ def gemm_workspace_bytes():
 
 
 def _gemm_workspace(workspace):
-    need = gemm_workspace_bytes()
-    if not workspace.is_cuda or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
+    _sized(workspace, gemm_workspace_bytes())
     return workspace
 
 
@@ -589,10 +595,7 @@ def _ragged_workspace(workspace, like, stream, *sizes):
         if need == 0:
             return None, 0
         return _scratch(need, like.device, stream), need
-    size = workspace.numel() * workspace.element_size()
-    if not workspace.is_cuda or size < need:
-        raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
-    return workspace, size
+    return workspace, _sized(workspace, need)
 
 
 def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None, stream=None,
@@ -762,9 +765,7 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
     need = moe_route_workspace_bytes(t, e)
     size = need
     if workspace is not None:
-        size = workspace.numel() * workspace.element_size()
-        if not workspace.is_cuda or size < need:
-            raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
+        size = _sized(workspace, need)
     elif need:
         workspace = _scratch(need, logits.device, stream)
     _same_device(logits, token_mask=token_mask, ids=out.ids, weights=out.weights,

@@ -132,3 +132,41 @@ def test_buffers_come_from_the_current_stream(pools, name):
     call(None)
     assert len(pools) == returned + scratch
     assert {pool for pool, _ in pools} == {"current"}
+
+
+# calls that take a workspace
+TAKES = {
+    "ragged_gemm": lambda w: mx.ragged_gemm("NN", T(8, 24), T(2, 24, 16), _ms(), workspace=w),
+    "ragged_gemm_int8": lambda w: mx.ragged_gemm_int8(
+        T(8, 16, dtype=I8), T(8, dtype=F32), T(2, 24, 16, dtype=I8), T(2, 24, dtype=F32), _ms(), workspace=w),
+    "moe_route": lambda w: mx.moe_route(T(6, 4, dtype=F32), 2, workspace=w),
+    "requant_colwise": lambda w: mx.requant_colwise(
+        T(128, 512, dtype=U8), T(128, 16, dtype=U8), _ms(), with_dbias=True, workspace=w),
+    "group_quantize_requant": lambda w: mx.group_quantize_requant(
+        T(128, 512), _ms(), with_dbias=True, workspace=w),
+    "grouped_dbias": lambda w: mx.grouped_dbias(
+        T(128, 512, dtype=U8), T(128, 16, dtype=U8), _ms(), workspace=w),
+    "grouped_scaled_bias_grad": lambda w: mx.grouped_scaled_bias_grad(
+        T(128, 512, dtype=U8), T(128, 16, dtype=U8), _ms(), T(128, dtype=F32), T(2, 512, dtype=F32), workspace=w),
+    "swiglu_bwd_quantize": lambda w: mx.swiglu_bwd_quantize(
+        T(128, 1024), T(128, 512), _ms(), with_dbias=True, workspace=w),
+    "grouped_gemm": lambda w: mx.grouped_gemm(
+        "NT", T(128, 512, dtype=U8), T(128, 16, dtype=U8), T(1024, 512, dtype=U8), T(1024, 16, dtype=U8), _ms(),
+        128, 512, 512, workspace=w),
+    "grouped_gemm_wgrad_accumulate": lambda w: mx.grouped_gemm_wgrad_accumulate(
+        T(512, 128, dtype=U8), T(512, 4, dtype=U8), T(512, 128, dtype=U8), T(512, 4, dtype=U8), _ms(), 128, 512, 512,
+        T(2, 512, 512, dtype=F32), workspace=w),
+}
+
+
+@pytest.mark.parametrize("name", TAKES)
+def test_workspaces_that_hold_less_than_they_count(pools, name):
+    """A workspace is `numel` elements from its pointer on: a view that lies on fewer or
+    on others is refused, as are a host buffer and one too short."""
+    call = TAKES[name]
+    call(T(4096, dtype=U8))
+    call(T(1024, dtype=F32))
+    for bad in (T(1, dtype=U8).expand(4096), T(8192, dtype=U8)[::2], T(4095, dtype=U8),
+                torch.zeros(4096, dtype=U8)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(bad)

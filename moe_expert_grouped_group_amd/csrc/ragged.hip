@@ -255,10 +255,10 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
         const int m = wm + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + (r & 3);
         if (m < rows && n < cols) {
           float v = (float)acc[i][j][r];
-          if (sizeof(E) == 1) {
+          if constexpr (sizeof(E) == 1) {
             int64_t row = m0 + m;
             if (p.row_index != nullptr) row = p.row_index[row];
-            v = v * (row >= 0 && row < p.S ? p.sa[row] : 0.f) * sb;
+            v = scaled<O>(acc[i][j][r], row >= 0 && row < p.S ? p.sa[row] : 0.f, sb);
           }
           c[m * ldc + n] = O::cvt(v);
         }

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 
@@ -134,6 +135,17 @@ struct OutF16 {
     return __builtin_bit_cast(uint16_t, (_Float16)v);
   }
 };
+
+// 8-bit integers: an exact sum, rounded to fp32, times the row's and the channel's scale,
+// rounded to fp32 before the output's conversion in every form and type.  Left to itself
+// the compiler multiplies and converts to fp16 in one instruction, which rounds once: one
+// result in 20000 differs in its last place.
+template <typename O>
+__device__ __forceinline__ float scaled(int sum, float row, float channel) {
+  float v = (float)sum * row * channel;
+  if (std::is_same<O, OutF16>::value) asm("" : "+v"(v));
+  return v;
+}
 
 // A split as the kernels take it: negative ones count as empty, and none is
 // longer than the R rows there are, so that sums cannot overflow.

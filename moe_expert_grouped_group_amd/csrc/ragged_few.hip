@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
       const int64_t n = n0 + 4 * sub + e;
       if (n >= p.N) continue;
       float v = (float)sum[e];
-      if (kInt8) v = v * sa * p.sb[(int64_t)g * p.N + n];
+      if constexpr (kInt8) v = scaled<O>(sum[e], sa, p.sb[(int64_t)g * p.N + n]);
       c[n] = O::cvt(v);
     }
   }

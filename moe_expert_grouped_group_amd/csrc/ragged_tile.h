@@ -781,7 +781,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     const int right = (int)min((int64_t)kTileN, p.ccols - n0);   // columns to store
     auto value = [&](int i, int j, int e) {
       if constexpr (kInt8)
-        return (float)acc[i][j][e] * srow[i] * scales[side][1][wn * 128 + 16 * j + 4 * (ln >> 4) + e];
+        return scaled<O>(acc[i][j][e], srow[i], scales[side][1][wn * 128 + 16 * j + 4 * (ln >> 4) + e]);
       else
         return acc[i][j][e];
     };
@@ -905,7 +905,8 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float x = (float)sum[q][e];
-        if (kInt8) x = n + e < cols ? x * sa * p.sb[(int64_t)g * p.N + n + e] : 0.f;
+        if constexpr (kInt8)
+          x = n + e < cols ? scaled<O>(sum[q][e], sa, p.sb[(int64_t)g * p.N + n + e]) : 0.f;
         o[e] = O::cvt(x);
       }
       __builtin_memcpy(__builtin_assume_aligned(c + n, sizeof(o)), o, sizeof(o));

@@ -294,15 +294,25 @@ bool on16(const void* p, int64_t stride_bytes) {
 int64_t pad16(int64_t n, int64_t size) { return (n * size + 15) / 16 * 16 / size; }
 
 // Whether experts have few rows, so that the forward product is bound by reading
-// the weights and ragged_few.hip takes it.  Measured (MI355X, weights of W MB, m
-// rows an expert): about W (0.16 + 0.0071 m) us there, 30 + 0.19 W us for the
-// large tiles, e.g. 940 MB: 166 and 178 us at 4 rows, 191 and 182 at 8; 34 MB:
-// 38 and 34 us at 64 rows of 1 expert.  The fit holds to some 256 rows; 22 experts of
-// 808 x 151 with 760 rows each took 130 us there.
+// the weights and ragged_few.hip takes it.  Measured with equal experts (us; here, in
+// the large tiles), by MB of weights (experts x N x K) and m rows an expert:
+//    34 (1 x 4096 x 4096)     m 16:  11,  30   64:  22,  34    96:  35,  35   192:  58,  44
+//    67 (8 x 2048 x 2048)     m 16:  18,  41   64:  41,  45    96:  70,  45
+//   134 (4 x 4096 x 4096)     m 16:  31,  43   20:  38,  44    32:  46,  44
+//   235 (4 x 7168 x 4096)     m 12:  48,  53   16:  53,  53    24:  67,  55
+//   268 (64 x 2048 x 1024)    m  8:  54,  56   12:  62,  57    16:  71,  58
+//   940 (8 x 14336 x 4096)    m  4: 165, 177    6: 177, 178     8: 195, 179
+//   8-bit, 470 (the same)     m  8: 103, 115   12: 115, 115    16: 129, 116
+// About W (0.16 + 0.0075 m) here; the tiles take some 25 us at least and 0.19 W or
+// 0.24 W (8-bit) where W is large.  Off by most with many experts of short rows (537,
+// 128 x 2048 x 1024: 116, 108 at m 4 already).  Up to 256 rows, though small weights
+// would stay ahead beyond (1 x 1024 x 1024 at 384: 14, 32), because 22 experts of 808 x 151
+// with 760 rows each took 130 us here.
 bool few_rows(const RaggedArgs& p, int esize) {
   const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
   const double mb = 1e-6 * (double)groups * (double)p.N * (double)p.K * esize;
-  return p.R < (1 << 20) && mean <= 256 && (mean <= 4 || (double)(mean - 4) * mb <= 4200.0);
+  const double most = mb < 100.0 ? 4200.0 : 3000.0;
+  return p.R < (1 << 20) && mean <= 256 && (mean <= 4 || (double)(mean - 4) * mb <= most);
 }
 
 // What the large tiles want and an operand may lack: rows on 16 bytes, the

@@ -156,3 +156,18 @@ def test_route_of_too_many_experts_raises(lib, monkeypatch):
     monkeypatch.setattr(binding, "_stream", lambda s: 0)
     with pytest.raises(ValueError, match="E = 10000"):
         mx.moe_route(torch.zeros((300, 10000)).as_subclass(DeviceTensor), 2)
+
+
+@pytest.mark.parametrize("g,n,k,size,rows,few", [
+    (1, 4096, 4096, 2, 16, True), (1, 4096, 4096, 2, 64, True), (1, 4096, 4096, 2, 192, False),
+    (8, 2048, 2048, 2, 64, True), (8, 2048, 2048, 2, 96, False),
+    (4, 4096, 4096, 2, 20, True), (4, 4096, 4096, 2, 32, False),
+    (4, 7168, 4096, 2, 12, True), (4, 7168, 4096, 2, 24, False),
+    (64, 2048, 1024, 2, 8, True), (64, 2048, 1024, 2, 16, False),
+    (8, 14336, 4096, 2, 4, True), (8, 14336, 4096, 2, 8, False),
+    (8, 14336, 4096, 1, 8, True), (8, 14336, 4096, 1, 16, False)])
+def test_form_that_measured_faster(lib, g, n, k, size, rows, few):
+    """The rule between the few-rows form, which uses no workspace, and the large tiles,
+    at sizes where both were timed and differ."""
+    need = lib.mxfp8_ragged_gemm_workspace_bytes(NT, size, g * rows, g * rows, n, k, g)
+    assert (need == 0) == few

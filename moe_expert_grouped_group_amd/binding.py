@@ -745,6 +745,8 @@ def moe_route(logits, top_k, renormalize=True, token_mask=None, out=None, worksp
     t, e = _matrix(logits, "logits")
     ty = _type_of(logits, "logits", tuple(_TYPE))
     _need(logits, logits.dtype, (t, e), "logits")
+    if not 1 <= top_k <= min(e, 16):
+        raise ValueError(f"top_k = {top_k} must be 1 to min(E, 16)")
     if token_mask is not None:
         if token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)

@@ -170,3 +170,13 @@ def test_workspaces_that_hold_less_than_they_count(pools, name):
                 torch.zeros(4096, dtype=U8)):
         with pytest.raises(ValueError, match="workspace"):
             call(bad)
+
+
+@pytest.mark.parametrize("top_k", [-1, 0, 5, 17, 1 << 40])
+def test_route_refuses_top_k_before_it_allocates(pools, top_k):
+    """The outputs' sizes go by top_k: a ValueError, not the allocator's error or its memory."""
+    with pytest.raises(ValueError, match="top_k"):
+        mx.moe_route(T(6, 4, dtype=F32), top_k)
+    with pytest.raises(ValueError, match="top_k"):
+        mx.moe_route(T(6, 40, dtype=F32), top_k if top_k != 5 else 41)
+    assert not pools

@@ -7,6 +7,7 @@
 // i(r) is row_index[r] or r.  Experts own consecutive rows, m_splits[g] of
 // them, read on the device; rows after the last expert's are not touched.
 #include <algorithm>
+#include <cmath>
 
 #include "ragged_common.h"
 
@@ -268,15 +269,18 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
 
 namespace {
 
+// Tiles of ragged_any_kernel.  An expert's last one may be partial: at most one more
+// for each expert that has rows.
+int64_t ragged_any_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G) {
+  const int64_t cols = ((layout == 0 ? N : K) + kAnyT - 1) / kAnyT;
+  return cols * (layout == 2 ? (int64_t)G * ((N + kAnyT - 1) / kAnyT)
+                             : R / kAnyT + std::min<int64_t>(G, R));
+}
+
 template <typename T, typename O, int LAYOUT>
 hipError_t launch_any(const RaggedArgs& p, hipStream_t st) {
-  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
-  const int64_t nt = (cols + kAnyT - 1) / kAnyT;
-  // an expert's last tile may be partial: at most one more tile for each
-  // expert that has rows
-  const int64_t rt = LAYOUT == 2 ? p.G * ((p.N + kAnyT - 1) / kAnyT)
-                                 : p.R / kAnyT + std::min<int64_t>(p.G, p.R);
-  return launch_in_parts(nt * rt, 256, [&](uint32_t first, uint32_t n) {
+  const int64_t blocks = ragged_any_blocks(LAYOUT, p.R, p.N, p.K, p.G);
+  return launch_in_parts(blocks, 256, [&](uint32_t first, uint32_t n) {
     ragged_any_kernel<T, O, LAYOUT><<<dim3(n), dim3(256), 0, st>>>(p, first);
   });
 }
@@ -343,18 +347,21 @@ Repack repack_of(int layout, int esize, int osize, const RaggedArgs& p) {
   r.bytes_c = r.c ? (size_t)r.rows_c * r.ldc * osize : 0;
   return r;
 }
-// Copying pays where the arithmetic is long enough.  Measured: ragged_any_kernel
-// reaches 560 (NT), 250 (NN) and 150 (TN) TFLOP/s on 16384 rows of 8 x 4096 x 14336
-// and takes about 1.7 us for each step of its contraction however small the
-// product (NN, 9 rows, 3103 x 147: 179 us; NT, 1777 x 1031 x 517: 48 us); the large
-// tiles reach 1150 TFLOP/s and with three copies take 57 us at least; a copy moves
-// its bytes twice at about 4 TB/s.
+// Copying pays where the arithmetic is long enough.  Measured (us: ragged_any_kernel, the
+// copies and the large tiles; rows, N x K, experts):
+//   NT  3000, 2011 x 1031, 3:  40,  68   4000, 1003 x 4011, 4: 118, 102   16384, 14331 x 4091, 8: 3830, 2011
+//       9000,  777 x 2051, 8:  82, 103   20000, 1021 x 515, 64: 70, 106   8-bit 4000, 1003 x 4011: 75, 89
+//   NN  1777,  517 x 1031, 5:  40,  52   3000, 2011 x 1031, 3: 132,  85   9000, 777 x 2051, 8: 154, 101
+//   TN  1777,  517 x 1031, 5:  43,  49   600, 4099 x 1003, 1:   94,  55   9000, 777 x 2051, 8: 291, 111
+// There a step of 64 contraction bytes takes 1.1 us (NT), 2.1 (NN) and 4.0 (TN) for each
+// round of two workgroups a CU, of 256; here 48 us, 1350 TFLOP/s and every byte twice at 4.5 TB/s.
 bool repack_pays(int layout, int esize, const RaggedArgs& p, size_t bytes) {
-  const double tflop = 2e-12 * (double)p.R * (double)p.N * (double)p.K;
-  const double rate = layout == 0 ? 560.0 : layout == 1 ? 250.0 : 150.0;
+  const double us = layout == 0 ? 1.1 : layout == 1 ? 2.1 : 4.0;
   const double con = layout == 0 ? (double)p.K : layout == 1 ? (double)p.N : (double)p.R / p.G;
-  const double any = std::max(tflop / rate, 1.7e-6 * con * esize / kAnyBytes);
-  return bytes <= ((size_t)8 << 30) && any > tflop / 1150.0 + 2.0 * (double)bytes / 4e12 + 57e-6;
+  const double rounds = std::max(1.0, (double)ragged_any_blocks(layout, p.R, p.N, p.K, p.G) / 512);
+  const double any = 1e-6 * us * std::ceil(con * esize / kAnyBytes) * rounds;
+  const double tflop = 2e-12 * (double)p.R * (double)p.N * (double)p.K;
+  return bytes <= ((size_t)8 << 30) && any > tflop / 1350.0 + 2.0 * (double)bytes / 4.5e12 + 48e-6;
 }
 size_t split_bytes() { return ragged_split_bytes(); }
 
@@ -493,12 +500,10 @@ hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, size_t ws_bytes
 
 // Workgroups that any call may need at most.
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G) {
-  const int64_t cols = ((layout == 0 ? N : K) + kAnyT - 1) / kAnyT;
-  if (layout == 0)   // the smallest tiles: 16 rows by 16 columns, where rows are few
-    return std::max(cols * (R / kAnyT + std::min<int64_t>(G, R)),
-                    R < (1 << 20) ? ((N + 15) / 16) * (R / 16 + std::min<int64_t>(G, R)) : 0);
-  return cols * (layout == 2 ? (int64_t)G * ((N + kAnyT - 1) / kAnyT)
-                             : R / kAnyT + std::min<int64_t>(G, R));
+  const int64_t any = ragged_any_blocks(layout, R, N, K, G);
+  // the smallest tiles: 16 rows by 16 columns, where rows are few
+  if (layout != 0 || R >= (1 << 20)) return any;
+  return std::max(any, ((N + 15) / 16) * (R / 16 + std::min<int64_t>(G, R)));
 }
 
 }  // namespace mx

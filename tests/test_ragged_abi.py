@@ -171,3 +171,19 @@ def test_form_that_measured_faster(lib, g, n, k, size, rows, few):
     at sizes where both were timed and differ."""
     need = lib.mxfp8_ragged_gemm_workspace_bytes(NT, size, g * rows, g * rows, n, k, g)
     assert (need == 0) == few
+
+
+@pytest.mark.parametrize("layout,size,g,rows,n,k,anew", [
+    (NT, 2, 8, 16384, 14331, 4091, True), (NT, 2, 5, 1777, 517, 1031, False), (NT, 2, 3, 3000, 2011, 1031, False),
+    (NT, 2, 4, 4000, 1003, 4011, True), (NT, 2, 1, 600, 4099, 1003, False), (NT, 2, 8, 9000, 777, 2051, False),
+    (NT, 2, 64, 20000, 1021, 515, False), (NT, 1, 8, 16384, 14331, 4091, True), (NT, 1, 4, 4000, 1003, 4011, False),
+    (NN, 2, 8, 16384, 14331, 4091, True), (NN, 2, 5, 1777, 517, 1031, False), (NN, 2, 3, 3000, 2011, 1031, True),
+    (NN, 2, 1, 600, 4099, 1003, True), (NN, 2, 8, 9000, 777, 2051, True), (NN, 2, 2, 9000, 1501, 517, True),
+    (NN, 2, 64, 20000, 1021, 515, True), (TN, 2, 8, 16384, 14331, 4091, True), (TN, 2, 5, 1777, 517, 1031, False),
+    (TN, 2, 3, 3000, 2011, 1031, True), (TN, 2, 1, 600, 4099, 1003, True), (TN, 2, 64, 20000, 1021, 515, True)])
+def test_layout_anew_that_measured_faster(lib, layout, size, g, rows, n, k, anew):
+    """The rule that lays odd operands out anew, for which it takes more workspace than
+    aligned ones, at sizes where both ways were timed."""
+    ask = lib.mxfp8_ragged_gemm_workspace_bytes
+    odd, even = ask(layout, size, rows, rows, n, k, g), ask(layout, size, rows, rows, n // 16 * 16, k // 16 * 16, g)
+    assert (odd > even) == anew

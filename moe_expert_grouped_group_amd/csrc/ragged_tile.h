@@ -538,8 +538,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       rows_at[j] = *(__attribute__((address_space(3))) const uint32_t*)(
           ring0 + (uint32_t)(s.at & 7) * 256u + (uint32_t)(16 * wave + 2 * j + (lane >> 5)) * 4u);
   };
-  // copy c of a stage: A and B parts in turn (then what is left of B)
-  // Copy c of a stage: its addresses first, behind a matrix instruction of their
+  // Copy c of a stage (A and B parts in turn, then what is left of B): its addresses first, behind a matrix instruction of their
   // own, then the copy behind the next (all five instructions behind one are more
   // than its 16 cycles hide: 8 x 4096 x 14336 forward 1.59 ms, so 1.55).
   struct Part {
@@ -787,7 +786,6 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     };
     // Accumulator e of block (i, j) in lane l: row 16 i + l % 16, column
     // 16 j + 4 (l / 16) + e.
-    constexpr int kNt = 0;
 #pragma unroll
     for (int i = 0; i < kRowsF; ++i) {
       const int m = wm * 32 * FA + 16 * i + (ln & 15);
@@ -802,7 +800,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
             const u32x4_t v = {__float_as_uint(value(i, k, 0)), __float_as_uint(value(i, k, 1)),
                                __float_as_uint(value(i, k, 2)), __float_as_uint(value(i, k, 3))};
             const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 4u : kOut;
-            __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
+            __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, 0);
           }
         } else {
           // 8 consecutive columns a lane: rows of 16 lanes trade, so that rows 0 and 2
@@ -817,7 +815,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
           const u32x4_t v = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
           const int n = wn * 128 + 16 * (j + ((ln >> 4) & 1)) + 8 * (ln >> 5);
           const uint32_t off = ((n < right) & (m < rows)) ? roff + (uint32_t)n * 2u : kOut;
-          __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, kNt);
+          __builtin_amdgcn_raw_buffer_store_b128(v, out, off, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
       }

@@ -507,7 +507,10 @@ typedef enum mxfp8_type {
  *           where that pays.  Results do not depend on it but for the order of
  *           sums.
  * mxfp8_ragged_gemm_workspace_bytes: for operands of elem_bytes (2, or 1 for
- * mxfp8_ragged_gemm_int8); 0 where none is used, and for sizes that are refused.
+ * mxfp8_ragged_gemm_int8) that are contiguous and on 16 bytes; 0 where none is used,
+ * and for sizes that are refused.  Strided or shifted operands whose rows start off
+ * 16 bytes find no room in it to be laid out anew, and a gathered X of 4 GiB or more
+ * is never: those take a form that is two to eight times slower on large products.
  * Errors: EINVAL for NULL pointers, sizes < 1 (R, S >= 0), strides shorter than
  * a row, G out of range, host m_splits, row_index with NN, S != R without
  * row_index, over 2^31 - 1 rows, columns or tiles; ENOTSUP for other types.
@@ -567,6 +570,8 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
  *   row_pos int32 [T, top_k]  row of each choice, -1 where there is none
  *   workspace   of mxfp8_moe_route_workspace_bytes(T, E) bytes; needs no
  *               initialisation (NULL where that is 0, as for sizes that are refused)
+ * Time grows with T, past some 10^6 tokens faster (128 experts: 0.5 ms for 2^20,
+ * 2.8 ms for 2^22).
  * Errors: EINVAL for NULL, sizes out of range, T top_k >= 2^31, a small
  * workspace; ENOTSUP for other types.  T = 0 writes m_splits only.
  */

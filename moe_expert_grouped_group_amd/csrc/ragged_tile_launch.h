@@ -37,11 +37,13 @@ hipError_t launch_tile_gather(const RaggedArgs& p, hipStream_t st) {
   return p.row_index != nullptr ? launch_tile<T, O, LAYOUT, FA, true>(p, st)
                                 : launch_tile<T, O, LAYOUT, FA, false>(p, st);
 }
+
 // Rows of a forward tile.  Experts of few rows want low tiles: what the copies
 // bring of other experts' rows is wasted.  Measured, 8 x 4096 x 14336 bf16, for
 // 64, 128 and 256 rows a tile: 210, 216 and 237 us at 32 rows an expert; 283, 224
 // and 249 at 96; 371, 310 and 261 at 192.  The bounds lie lower than the tile
-// heights because experts differ from the mean.
+// heights because experts differ from the mean, which is over all of them, those without
+// rows too: only the device knows the splits.
 template <typename T, typename O>
 hipError_t launch_tile_rows(const RaggedArgs& p, hipStream_t st) {
   const int64_t mean = p.R / std::min<int64_t>(p.G, p.R);

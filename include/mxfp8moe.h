@@ -616,6 +616,50 @@ mxfp8_status mxfp8_moe_combine_bwd(const void* dout, const void* y, int32_t type
                                    const float* weights, void* dy, float* dweights,
                                    void* stream);
 
+/*
+ * mxfp8_ragged_gemm_swiglu -- the gated feed-forward block of ragged experts up to its
+ * activation, in one kernel: both projections of mxfp8_ragged_gemm (NT), the activation
+ * and the product (the rows of W are the gate's, then the up projection's):
+ *   z[r, n] = sum_k X[i(r), k] W[g, n, k],  n in [0, 2F)
+ *   a[r, f] = silu(z[r, f]) * z[r, F + f],  h = z
+ * Sums and the activation are fp32; a and h are each rounded once from them (a does not go
+ * through the rounded h, as mxfp8_swiglu_fwd of h would).  A sigmoid below 2^-126 counts as 0.
+ *   type    MXFP8_TYPE_BF16 or MXFP8_TYPE_F16: X, W, a, h
+ *   x       [S, K], row stride ldx;  w [G, 2F, K]
+ *   a       [R, F], row stride lda;  h [R, 2F] (gate | up) or NULL: not kept
+ *   m_splits, G, row_index, workspace: as mxfp8_ragged_gemm, rows of a and h past the last
+ *   expert's are not written.  No output may overlap an input or the other output.
+ * Faster where pointers and ldx, lda, K and F are multiples of 16 bytes; right for all.
+ * Errors: as mxfp8_ragged_gemm with N = 2F.
+ */
+mxfp8_status mxfp8_ragged_gemm_swiglu(int32_t type, const void* x, int64_t ldx, const void* w, void* a,
+                                      int64_t lda, void* h, int64_t R, int64_t S, int64_t F, int64_t K,
+                                      const int64_t* m_splits, int32_t G, const int32_t* row_index,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mxfp8_ragged_gemm_swiglu_bwd -- the backward pass of that activation inside the down
+ * projection's input gradient (mxfp8_ragged_gemm NN), whose result da is never written:
+ *   da[r, f] = sum_n dY[r, n] W[g, n, f],  n in [0, N)
+ *   s = sigmoid(h[r, f]):  dh[r, f] = da * h[r, F + f] * s * (1 + h[r, f] * (1 - s))
+ *                          dh[r, F + f] = da * silu(h[r, f])
+ *   a[r, f] = silu(h[r, f]) * h[r, F + f]      anew, for the down projection's weight gradient
+ * Sums and derivatives are fp32, results are rounded once.
+ *   dy  [R, N], row stride lddy;  w [G, N, F];  h, dh [R, 2F] (gate | up);
+ *   a   [R, F] or NULL: not wanted
+ *   type, m_splits, G, workspace: as mxfp8_ragged_gemm.  dh and a may not overlap h, dy or w.
+ * The gradients of the weights and of X follow with mxfp8_ragged_gemm: TN of dy and a, TN of
+ * dh and X, NN of dh and the first weights.
+ * Errors: as mxfp8_ragged_gemm (NN) with K = F.
+ */
+mxfp8_status mxfp8_ragged_gemm_swiglu_bwd(int32_t type, const void* dy, int64_t lddy, const void* w,
+                                          const void* h, void* dh, void* a, int64_t R, int64_t N,
+                                          int64_t F, const int64_t* m_splits, int32_t G, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+/* Workspace of the two calls (backward: 0 or 1) for contiguous operands on 16 bytes; C is K of the
+ * first, N of the second.  0 where none is used, and for sizes that are refused. */
+size_t mxfp8_ragged_gemm_swiglu_workspace_bytes(int32_t backward, int64_t R, int64_t F, int64_t C, int32_t G);
+
 #ifdef __cplusplus
 }
 #endif

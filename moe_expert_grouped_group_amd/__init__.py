@@ -15,6 +15,7 @@ from .binding import (  # noqa: F401
     grouped_gemm_wgrad_accumulate,
     grouped_scaled_bias_grad, gemm_workspace_bytes, moe_combine, moe_combine_bwd, moe_route,
     moe_route_bwd, moe_route_workspace_bytes, quantize_int8, ragged_gemm, ragged_gemm_int8,
+    ragged_gemm_swiglu, ragged_gemm_swiglu_bwd, ragged_gemm_swiglu_workspace_bytes,
     ragged_gemm_workspace_bytes,
     requant_colwise, swiglu_bwd,
     swiglu_bwd_quantize, swiglu_fwd,

@@ -60,6 +60,11 @@ SIGNATURES = {
     "mxfp8_ragged_gemm": (c_i32, [c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
                                   c_i64, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
     "mxfp8_ragged_gemm_workspace_bytes": (c_size, [c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, c_i32]),
+    "mxfp8_ragged_gemm_swiglu": (c_i32, [c_i32, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64,
+                                         c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
+    "mxfp8_ragged_gemm_swiglu_bwd": (c_i32, [c_i32, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64,
+                                             c_vp, c_i32, c_vp, c_size, c_vp]),
+    "mxfp8_ragged_gemm_swiglu_workspace_bytes": (c_size, [c_i32, c_i64, c_i64, c_i64, c_i32]),
     "mxfp8_quantize_int8": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "mxfp8_ragged_gemm_int8": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64,
                                        c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),

@@ -665,6 +665,107 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
     return out
 
 
+def _on_current(t, name):
+    """Kernels run on the current device: a tensor of another one is refused."""
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+@functools.lru_cache(maxsize=4096)
+def ragged_gemm_swiglu_workspace_bytes(backward, rows, ffn, width, groups):
+    """Workspace of ragged_gemm_swiglu (width K) or, backward, of ragged_gemm_swiglu_bwd
+    (width N) for these sizes; 0 where none is used."""
+    return int(_lib().mxfp8_ragged_gemm_swiglu_workspace_bytes(int(backward), rows, ffn, width, groups))
+
+
+def _gated_workspace(workspace, like, stream, *sizes):
+    need = ragged_gemm_swiglu_workspace_bytes(*sizes)
+    if workspace is None:
+        return (None, 0) if need == 0 else (_scratch(need, like.device, stream), need)
+    return workspace, _sized(workspace, need)
+
+
+def ragged_gemm_swiglu(x, w, m_splits, row_index=None, want_h=True, h=None, out=None, stream=None,
+                       workspace=None):
+    """The gated feed-forward block of ragged experts up to its activation, in one kernel:
+    x [S, K], w [G, 2F, K] (gate rows, then up rows) -> (h [R, 2F], a [R, F]), h = x W_g^T
+    and a = silu(h[:, :F]) * h[:, F:], each rounded once from the fp32 sums.
+
+    bf16 or fp16; m_splits, row_index and workspace as ragged_gemm (NT), the workspace of
+    ragged_gemm_swiglu_workspace_bytes(False, R, F, K, G).  x and out may have a row stride.
+    want_h=False (serving): h is not written, None is returned for it.
+    """
+    lib = _lib()
+    ms = _splits(m_splits)
+    g = ms.numel()
+    s, k = _matrix(x, "x")
+    ty = _type_of(x, "x")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [G, 2F, K]")
+    if w.shape[1] % 2:
+        raise ValueError(f"w must have an even number of rows (gate | up), got {w.shape[1]}")
+    f = w.shape[1] // 2
+    index = _row_index(row_index, x)
+    r = s if index is None else index.numel()
+    ldx = _rows_of(x, x.dtype, (s, k), "x")
+    _need(w, x.dtype, (g, 2 * f, k), "w")
+    _on_current(x, "x")
+    if out is None:
+        out = _empty((r, f), x.dtype, x.device, stream)
+    lda = _rows_of(out, x.dtype, (r, f), "out")
+    if want_h:
+        h = _empty((r, 2 * f), x.dtype, x.device, stream) if h is None else h
+        _need(h, x.dtype, (r, 2 * f), "h")
+    else:
+        h = None
+    ws, ws_bytes = _gated_workspace(workspace, x, stream, False, r, f, k, g)
+    _same_device(x, w=w, m_splits=ms, row_index=index, out=out, h=h, workspace=ws)
+    st = lib.mxfp8_ragged_gemm_swiglu(ty, _ptr(x), ldx, _ptr(w), _ptr(out), lda, _ptr(h), r, s, f, k,
+                                      _ptr(ms), g, _ptr(index), _ptr(ws), ws_bytes, _stream(stream))
+    _native.check(st, "mxfp8_ragged_gemm_swiglu")
+    return h, out
+
+
+def ragged_gemm_swiglu_bwd(dy, w, h, m_splits, want_a=True, dh=None, out=None, stream=None,
+                           workspace=None):
+    """Backward of that activation inside the down projection's input gradient:
+    dy [R, N], w [G, N, F] (the down projection), h [R, 2F] as ragged_gemm_swiglu gave it ->
+    (dh [R, 2F], a [R, F]): the gradient of h for da = dy W_g, which is not written, and
+    the activation anew (None with want_a=False).
+
+    Then ragged_gemm gives the rest: "TN" of (dy, a) the down projection's gradient,
+    "TN" of (dh, x) and "NN" of (dh, w) of the first one those of its weights and input.
+    dy may have a row stride; workspace of
+    ragged_gemm_swiglu_workspace_bytes(True, R, F, N, G).
+    """
+    lib = _lib()
+    ms = _splits(m_splits)
+    g = ms.numel()
+    r, n = _matrix(dy, "dy")
+    ty = _type_of(dy, "dy")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [G, N, F]")
+    f = w.shape[2]
+    lddy = _rows_of(dy, dy.dtype, (r, n), "dy")
+    _need(w, dy.dtype, (g, n, f), "w")
+    _need(h, dy.dtype, (r, 2 * f), "h")
+    _on_current(dy, "dy")
+    if dh is None:
+        dh = _empty((r, 2 * f), dy.dtype, dy.device, stream)
+    _need(dh, dy.dtype, (r, 2 * f), "dh")
+    if want_a:
+        out = _empty((r, f), dy.dtype, dy.device, stream) if out is None else out
+        _need(out, dy.dtype, (r, f), "out")
+    else:
+        out = None
+    ws, ws_bytes = _gated_workspace(workspace, dy, stream, True, r, f, n, g)
+    _same_device(dy, w=w, h=h, m_splits=ms, dh=dh, out=out, workspace=ws)
+    st = lib.mxfp8_ragged_gemm_swiglu_bwd(ty, _ptr(dy), lddy, _ptr(w), _ptr(h), _ptr(dh), _ptr(out), r, n,
+                                          f, _ptr(ms), g, _ptr(ws), ws_bytes, _stream(stream))
+    _native.check(st, "mxfp8_ragged_gemm_swiglu_bwd")
+    return dh, out
+
+
 def quantize_int8(x, out=None, stream=None):
     """Rows of a bf16 / fp16 matrix as 8-bit integers: (q int8 [T, K], scale
     fp32 [T]) with x ~ q * scale, scale = max|row| / 127.  out: optional (q,

@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp8moe.so")
 SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "ragged.hip", "ragged_few.hip", "ragged_tile_nt.hip",
-           "ragged_tile_nn.hip", "ragged_tile_tn.hip", "ragged_tile_int8.hip", "routing.hip"]
+           "ragged_tile_nn.hip", "ragged_tile_tn.hip", "ragged_tile_int8.hip", "ragged_tile_gated.hip",
+           "ragged_tile_gated_f16.hip", "ragged_tile_gated_bwd.hip", "routing.hip"]
 ARCH = "gfx950"
 
 

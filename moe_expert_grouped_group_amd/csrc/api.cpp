@@ -547,6 +547,90 @@ mxfp8_status mxfp8_ragged_gemm(int32_t layout, int32_t type, const void* a, int6
       fn);
 }
 
+size_t mxfp8_ragged_gemm_swiglu_workspace_bytes(int32_t backward, int64_t R, int64_t F, int64_t C,
+                                                int32_t G) {
+  if (R < 0 || F < 1 || C < 1 || G < 1 || G > mx::kRaggedMaxGroups || R > kI32Max ||
+      F > kI32Max / 2 || C > kI32Max)
+    return 0;
+  return backward ? mx::ragged_gated_workspace_bytes(true, R, C, F, G)
+                  : mx::ragged_gated_workspace_bytes(false, R, 2 * F, C, G);
+}
+
+mxfp8_status mxfp8_ragged_gemm_swiglu(int32_t type, const void* x, int64_t ldx, const void* w, void* a,
+                                      int64_t lda, void* h, int64_t R, int64_t S, int64_t F, int64_t K,
+                                      const int64_t* m_splits, int32_t G, const int32_t* row_index,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "mxfp8_ragged_gemm_swiglu";
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: operand type %d is not supported", fn, (int)type);
+  REQUIRE(F >= 1 && F <= kI32Max / 2, "%s: F = %lld must be 1 to 2^30 - 1", fn, (long long)F);
+  mxfp8_status st = check_ragged(fn, MXFP8_LAYOUT_NT, R, S, 2 * F, K, m_splits, G, row_index);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(ldx >= K, "%s: ldx = %lld is shorter than a row", fn, (long long)ldx);
+  REQUIRE(lda >= F, "%s: lda = %lld is shorter than a row", fn, (long long)lda);
+  if (R == 0) return ok();
+  REQUIRE(a && w && (x || S == 0), "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(x, 2) && aligned_to(w, 2) && aligned_to(a, 2) && aligned_to(h, 2) &&
+              aligned_to(row_index, 4) && aligned_to(m_splits, 8),
+          "%s: a pointer is not aligned to its element", fn);
+  mx::RaggedArgs p{};
+  p.a = x;
+  p.b = w;
+  p.c = a;
+  p.h = h;
+  p.lda = ldx;
+  p.ldb = K;
+  p.ldc = lda;
+  p.R = R;
+  p.S = S;
+  p.N = 2 * F;
+  p.K = K;
+  p.m_splits = m_splits;
+  p.row_index = row_index;
+  p.G = G;
+  p.ws = usable_workspace(workspace);
+  return hip_status(mx::launch_ragged_gated(type == MXFP8_TYPE_F16, p, p.ws != nullptr ? workspace_bytes : 0,
+                                            as_stream(stream)),
+                    fn);
+}
+
+mxfp8_status mxfp8_ragged_gemm_swiglu_bwd(int32_t type, const void* dy, int64_t lddy, const void* w,
+                                          const void* h, void* dh, void* a, int64_t R, int64_t N,
+                                          int64_t F, const int64_t* m_splits, int32_t G, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  const char* fn = "mxfp8_ragged_gemm_swiglu_bwd";
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: operand type %d is not supported", fn, (int)type);
+  REQUIRE(F >= 1 && F <= kI32Max / 2, "%s: F = %lld must be 1 to 2^30 - 1", fn, (long long)F);
+  mxfp8_status st = check_ragged(fn, MXFP8_LAYOUT_NN, R, R, N, F, m_splits, G, nullptr);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(lddy >= N, "%s: lddy = %lld is shorter than a row", fn, (long long)lddy);
+  if (R == 0) return ok();
+  REQUIRE(dy && w && h && dh, "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(dy, 2) && aligned_to(w, 2) && aligned_to(h, 2) && aligned_to(dh, 2) &&
+              aligned_to(a, 2) && aligned_to(m_splits, 8),
+          "%s: a pointer is not aligned to its element", fn);
+  mx::RaggedArgs p{};
+  p.a = dy;
+  p.b = w;
+  p.c = dh;
+  p.h = const_cast<void*>(h);
+  p.act = a;
+  p.lda = lddy;
+  p.ldb = F;
+  p.ldc = 2 * F;
+  p.R = R;
+  p.S = R;
+  p.N = N;
+  p.K = F;
+  p.m_splits = m_splits;
+  p.G = G;
+  p.ws = usable_workspace(workspace);
+  return hip_status(mx::launch_ragged_gated_bwd(type == MXFP8_TYPE_F16, p,
+                                                p.ws != nullptr ? workspace_bytes : 0, as_stream(stream)),
+                    fn);
+}
+
 mxfp8_status mxfp8_quantize_int8(const void* x, int32_t type, int64_t T, int64_t K, int64_t ldx,
                                  int8_t* q, float* scale, void* stream) {
   const char* fn = "mxfp8_quantize_int8";

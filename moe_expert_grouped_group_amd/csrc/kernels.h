@@ -66,6 +66,10 @@ hipError_t launch_ragged_gemm(int layout, bool f16, int out, const RaggedArgs& p
                               hipStream_t st);
 hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
 size_t ragged_workspace_bytes(int layout, int esize, int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
+// Gated forward (p.N = 2F) and backward (p.K = F) products.
+hipError_t launch_ragged_gated(bool f16, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
+hipError_t launch_ragged_gated_bwd(bool f16, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
+size_t ragged_gated_workspace_bytes(bool bwd, int64_t R, int64_t N, int64_t K, int32_t G);
 int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G);
 hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,
                                 int8_t* q, float* scale, hipStream_t st);

@@ -118,9 +118,12 @@ __device__ void expert_rows(const int64_t* m_splits, int g, int64_t R, int64_t* 
   __syncthreads();
 }
 
-template <typename T, typename O, int LAYOUT>
+template <typename T, typename O, int LAYOUT, int EPI = kPlain>
 __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32_t first) {
   typedef typename T::elem E;
+  // gated: a tile is 64 gate columns and their up columns, in blocks of 32 in turn
+  constexpr bool kIsGated = EPI == kGated;
+  constexpr int kCols = kIsGated ? kAnyT / 2 : kAnyT;
   constexpr int kPer = 16 / sizeof(E);             // elements of a chunk
   constexpr int kStep = kAnyBytes / sizeof(E);     // contraction elements per step
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kAnyT * kAnyPitch];
@@ -128,10 +131,10 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 
   // the tile: rows [m0, m0 + rows) of A's output dimension, columns from n0
-  const int64_t cols = LAYOUT == 0 ? p.N : p.K;
-  const int64_t nt = (cols + kAnyT - 1) / kAnyT;
+  const int64_t cols = kIsGated ? p.N / 2 : LAYOUT == 0 ? p.N : p.K;
+  const int64_t nt = (cols + kCols - 1) / kCols;
   const int64_t at = first + blockIdx.x, ct = at % nt, rt = at / nt;
-  const int64_t n0 = ct * kAnyT;
+  const int64_t n0 = ct * kCols;
   int g;
   int64_t m0, rows, con, lo = 0;   // con: contraction length; lo: its first row (TN)
   if (LAYOUT != 2) {
@@ -175,8 +178,12 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
         ra[i] = load_chunk<E>(a + (lo + k) * p.lda + m0 + c, k < con ? p.N - m0 - c : 0);
       }
       if (LAYOUT == 0) {
-        const int64_t r = n0 + (tid >> 2) + 64 * i;
+        int64_t r = n0 + (tid >> 2) + 64 * i;
         const int64_t k = k0 + (tid & 3) * kPer;
+        if constexpr (kIsGated) {
+          const int c = (tid >> 2) + 64 * i, f = 32 * (c >> 6) + (c & 31);
+          r = n0 + f < cols ? n0 + f + ((c >> 5) & 1) * cols : p.N;
+        }
         rb[i] = load_chunk<E>(b + r * p.K + k, r < p.N ? con - k : 0);
       } else {
         const int64_t k = k0 + (tid >> 4) + 16 * i;
@@ -242,6 +249,34 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   // accumulator r of a 32 x 32 block in lane l: row 8 (r / 4) + 4 (l / 32) + r % 4,
   // column l % 32
   typename O::elem* c = (typename O::elem*)p.c;
+  if constexpr (EPI != kPlain) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < (kIsGated ? 1 : 2); ++j) {
+        const int64_t n = n0 + (kIsGated ? wn / 2 : wn) + 32 * j + (lane & 31);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int m = wm + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + (r & 3);
+          if (m >= rows || n >= cols) continue;
+          const int64_t at_h = (m0 + m) * 2 * cols + n;
+          if constexpr (kIsGated) {
+            c[(m0 + m) * p.ldc + n] = O::cvt(gated(acc[i][0][r], acc[i][1][r]));
+            if (p.h != nullptr) {
+              ((typename O::elem*)p.h)[at_h] = O::cvt(acc[i][0][r]);
+              ((typename O::elem*)p.h)[at_h + cols] = O::cvt(acc[i][1][r]);
+            }
+          } else {
+            const E* h = (const E*)p.h + at_h;
+            const GatedGrad d = gated_grad(acc[i][j][r], widen<T>(h[0]), widen<T>(h[cols]));
+            c[at_h] = O::cvt(d.gate);
+            c[at_h + cols] = O::cvt(d.up);
+            if (p.act != nullptr) ((typename O::elem*)p.act)[(m0 + m) * cols + n] = O::cvt(d.act);
+          }
+        }
+      }
+    return;
+  }
   const int64_t ldc = LAYOUT == 2 ? p.K : p.ldc;
   c += LAYOUT == 2 ? ((int64_t)g * p.N + m0) * p.K : m0 * ldc;
 #pragma unroll
@@ -277,11 +312,13 @@ int64_t ragged_any_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G
                              : R / kAnyT + std::min<int64_t>(G, R));
 }
 
-template <typename T, typename O, int LAYOUT>
+template <typename T, typename O, int LAYOUT, int EPI = kPlain>
 hipError_t launch_any(const RaggedArgs& p, hipStream_t st) {
-  const int64_t blocks = ragged_any_blocks(LAYOUT, p.R, p.N, p.K, p.G);
+  // gated: F columns in tiles of 64, as many as 2 (F rounded up to 64) in tiles of 128
+  const int64_t N = EPI == kGated ? (p.N / 2 + kAnyT / 2 - 1) / (kAnyT / 2) * kAnyT : p.N;
+  const int64_t blocks = ragged_any_blocks(LAYOUT, p.R, N, p.K, p.G);
   return launch_in_parts(blocks, 256, [&](uint32_t first, uint32_t n) {
-    ragged_any_kernel<T, O, LAYOUT><<<dim3(n), dim3(256), 0, st>>>(p, first);
+    ragged_any_kernel<T, O, LAYOUT, EPI><<<dim3(n), dim3(256), 0, st>>>(p, first);
   });
 }
 
@@ -496,6 +533,55 @@ hipError_t launch_ragged_gemm_int8(int out, const RaggedArgs& p, size_t ws_bytes
   if (out == 0) return launch_any<TypeI8, OutF32, 0>(p, st);
   if (out == 1) return launch_any<TypeI8, OutBf16, 0>(p, st);
   return launch_any<TypeI8, OutF16, 0>(p, st);
+}
+
+// Gated products: what the large tiles need of alignment and spans (32-bit lane offsets reach
+// the up rows of W and 256 rows of h).
+namespace {
+bool gated_tiles(bool bwd, const RaggedArgs& p) {
+  const int64_t F = bwd ? p.K : p.N / 2, con = bwd ? p.N : p.K, span = (int64_t)kSpan;
+  if (!on16(p.a, p.lda * 2) || !on16(p.b, p.ldb * 2) || con % 8 != 0 || F % 8 != 0) return false;
+  if (!on16(p.c, p.ldc * 2) || !on16(p.h, F * 4) || !on16(p.act, F * 2)) return false;
+  if (256 * p.lda * 2 > span || (bwd ? 256 : F + 256) * p.ldb * 2 > span || 256 * F * 4 > span ||
+      256 * p.ldc * 2 > span)
+    return false;
+  return p.row_index == nullptr || (p.S > 0 && p.S * p.lda * 2 <= span);
+}
+}  // namespace
+
+size_t ragged_gated_workspace_bytes(bool bwd, int64_t R, int64_t N, int64_t K, int32_t G) {
+  if (R == 0) return 0;
+  RaggedArgs p{};
+  p.R = R;
+  p.N = N;
+  p.K = K;
+  p.G = G;
+  const int64_t F = bwd ? K : N / 2, con = bwd ? N : K;
+  if (con % 8 != 0 || F % 8 != 0 || (!bwd && few_rows(p, 2))) return 0;
+  return split_bytes();
+}
+
+hipError_t launch_ragged_gated(bool f16, const RaggedArgs& p, size_t ws_bytes, hipStream_t st) {
+  if (few_rows(p, 2)) return launch_ragged_few_gated(f16, p, st);
+  if (gated_tiles(false, p)) {
+    RaggedArgs q = p;
+    q.con = p.K;
+    if (ws_bytes < split_bytes()) q.ws = nullptr;
+    return launch_ragged_tile_gated(f16, q, st);
+  }
+  return f16 ? launch_any<TypeF16, OutF16, 0, kGated>(p, st) : launch_any<TypeBf16, OutBf16, 0, kGated>(p, st);
+}
+
+hipError_t launch_ragged_gated_bwd(bool f16, const RaggedArgs& p, size_t ws_bytes, hipStream_t st) {
+  if (gated_tiles(true, p)) {
+    RaggedArgs q = p;
+    q.con = p.N;
+    q.ccols = p.K;
+    if (ws_bytes < split_bytes()) q.ws = nullptr;
+    return launch_ragged_tile_gated_bwd(f16, q, st);
+  }
+  return f16 ? launch_any<TypeF16, OutF16, 1, kGatedBwd>(p, st)
+             : launch_any<TypeBf16, OutBf16, 1, kGatedBwd>(p, st);
 }
 
 // Workgroups that any call may need at most.

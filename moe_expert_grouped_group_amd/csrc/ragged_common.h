@@ -53,7 +53,18 @@ struct RaggedArgs {
   int64_t con;          // NT, NN: contraction with its zero padding
   int64_t ccols;        // columns that a row of C has room for
   void* ws;             // partial sums of split tiles (large tiles), or NULL
+  // gated products (Epilogue): both projections [R, 2F], contiguous
+  void* h;              // kGated: written unless NULL; kGatedBwd: read
+  void* act;            // kGatedBwd: the activation [R, F], contiguous, or NULL
 };
+
+// What becomes of a product's sums.
+//  kGated (NT, W [G, 2F, K] gate rows then up rows): C[r, f] = silu(z[r, f]) z[r, F + f], z the
+//    sums; kGatedKeep writes h = z too.
+//  kGatedBwd (NN, K = F; h given): the sums are da; C [R, 2F] = da up silu'(gate) | da silu(gate),
+//    act = silu(gate) up.
+// Everything from the fp32 sums, each result rounded once.
+enum Epilogue { kPlain = 0, kGated = 1, kGatedKeep = 2, kGatedBwd = 3 };
 
 // Forward products of experts with few rows (ragged_few.hip).
 hipError_t launch_ragged_few(bool f16, int out, const RaggedArgs& p, hipStream_t st);
@@ -63,6 +74,10 @@ hipError_t launch_ragged_tile_nt(bool f16, int out, const RaggedArgs& p, hipStre
 hipError_t launch_ragged_tile_nn(bool f16, int out, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_tn(bool f16, int out, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_int8(int out, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_few_gated(bool f16, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_tile_gated(bool f16, const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_tile_gated_f16(const RaggedArgs& p, hipStream_t st);
+hipError_t launch_ragged_tile_gated_bwd(bool f16, const RaggedArgs& p, hipStream_t st);
 size_t ragged_split_bytes();   // a partial 256 x 256 tile for each CU
 
 // Longest range of a bounded operand (32-bit offsets, less what marks a lane that
@@ -118,6 +133,13 @@ struct TypeI8 {
   }
 };
 
+// The value of 16 stored bits.
+template <typename T>
+__device__ __forceinline__ float widen(uint16_t v) {
+  if constexpr (std::is_same<T, TypeF16>::value) return (float)__builtin_bit_cast(_Float16, v);
+  else return __uint_as_float((uint32_t)v << 16);
+}
+
 // Output conversion: one rounding (nearest even) of the fp32 value.
 struct OutF32 {
   typedef float elem;
@@ -145,6 +167,25 @@ __device__ __forceinline__ float scaled(int sum, float row, float channel) {
   float v = (float)sum * row * channel;
   if (std::is_same<O, OutF16>::value) asm("" : "+v"(v));
   return v;
+}
+
+// silu(g) = g sigmoid(g) with the hardware's exponential and reciprocal, 1 ulp each, ahead
+// of a rounding to 16 bits.  exp2 gives infinity for g below -88: sigmoid 0.
+__device__ __forceinline__ float sigmoid_of(float g) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
+__device__ __forceinline__ float gated(float gate, float up) { return gate * sigmoid_of(gate) * up; }
+struct GatedGrad {
+  float gate, up, act;
+};
+// silu'(g) = s (1 + g (1 - s)), s = sigmoid(g)
+__device__ __forceinline__ GatedGrad gated_grad(float da, float gate, float up) {
+  const float s = sigmoid_of(gate), silu = gate * s;
+  GatedGrad r;
+  r.gate = da * up * (s + silu * (1.f - s));
+  r.up = da * silu;
+  r.act = silu * up;
+  return r;
 }
 
 // A split as the kernels take it: negative ones count as empty, and none is

@@ -32,15 +32,20 @@ __device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
   return v;
 }
 
-template <typename T, typename O, int MR, int U, int WAVES>
+// GATED: 16 gate columns and their 16 up columns, the activation of both (and the
+// projections, where p.h is given).
+template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false>
 __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, uint32_t first) {
   typedef typename T::elem E;
   typedef typename T::acc16 Acc;
   constexpr bool kInt8 = sizeof(E) == 1;
-  __shared__ Acc part[WAVES][MR][64];
+  constexpr int NB = GATED ? 2 : 1;   // blocks of 16 weight rows
+  static_assert(!GATED || !kInt8, "");
+  __shared__ Acc part[WAVES][MR * NB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t ctiles = (uint32_t)((p.N + 15) / 16);
+  const int64_t cols = GATED ? p.N / 2 : p.N;
+  const uint32_t ctiles = (uint32_t)((cols + 15) / 16);
   const uint32_t tile = first + blockIdx.x;
   const int64_t rt = tile / ctiles;
   const int64_t n0 = (int64_t)(tile % ctiles) * 16;
@@ -53,8 +58,11 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
   const int64_t kb = p.K * (int64_t)sizeof(E);
   const int sub = lane >> 4;   // 16-byte chunk of a 64-byte step
   // this lane's weight row and token rows; rows past the end repeat the last
-  const uint8_t* w = (const uint8_t*)p.b +
-                     ((int64_t)g * p.N + min(n0 + (lane & 15), p.N - 1)) * kb + sub * 16;
+  const uint8_t* w[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    w[b] = (const uint8_t*)p.b +
+           ((int64_t)g * p.N + b * cols + min(n0 + (lane & 15), cols - 1)) * kb + sub * 16;
   const uint8_t* x[MR];
   int64_t token[MR];   // -1: a row of zeros
 #pragma unroll
@@ -63,27 +71,30 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
     const int64_t s = p.row_index != nullptr ? p.row_index[r] : r;
     token[m] = s >= 0 && s < p.S ? s : -1;
     // any readable row of K values does for a row of zeros: its sums are replaced below
-    x[m] = token[m] >= 0 ? (const uint8_t*)p.a + s * p.lda * (int64_t)sizeof(E) + sub * 16 : w;
+    x[m] = token[m] >= 0 ? (const uint8_t*)p.a + s * p.lda * (int64_t)sizeof(E) + sub * 16 : w[0];
   }
 
-  Acc acc[MR];
+  Acc acc[MR * NB];
 #pragma unroll
-  for (int m = 0; m < MR; ++m) acc[m] = Acc{0, 0, 0, 0};
+  for (int m = 0; m < MR * NB; ++m) acc[m] = Acc{0, 0, 0, 0};
   // whole runs of U lines, wave by wave
   const int64_t runs = kb / (128 * U);
   for (int64_t run = wave; run < runs; run += WAVES) {
-    u32x4_t wv[2 * U], xv[2 * U][MR];
+    u32x4_t wv[2 * U][NB], xv[2 * U][MR];
 #pragma unroll
     for (int i = 0; i < 2 * U; ++i) {
       const int64_t at = run * (128 * U) + i * 64;
-      __builtin_memcpy(&wv[i], w + at, 16);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) __builtin_memcpy(&wv[i][b], w[b] + at, 16);
 #pragma unroll
       for (int m = 0; m < MR; ++m) __builtin_memcpy(&xv[i][m], x[m] + at, 16);
     }
 #pragma unroll
     for (int i = 0; i < 2 * U; ++i)
 #pragma unroll
-      for (int m = 0; m < MR; ++m) acc[m] = T::mma16(wv[i], xv[i][m], acc[m]);
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[m * NB + b] = T::mma16(wv[i][b], xv[i][m], acc[m * NB + b]);
   }
   // the lines that are left, each to the next wave; the last may be partial
   const int64_t lines = (kb + 127) / 128;
@@ -92,9 +103,13 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
     for (int h = 0; h < 2; ++h) {
       const int64_t at = l * 128 + h * 64;
       const int64_t n = kb - at - sub * 16;
-      const u32x4_t wv = chunk_end<E>(w + at, n);
 #pragma unroll
-      for (int m = 0; m < MR; ++m) acc[m] = T::mma16(wv, chunk_end<E>(x[m] + at, n), acc[m]);
+      for (int b = 0; b < NB; ++b) {
+        const u32x4_t wv = chunk_end<E>(w[b] + at, n);
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+          acc[m * NB + b] = T::mma16(wv, chunk_end<E>(x[m] + at, n), acc[m * NB + b]);
+      }
     }
   }
 
@@ -106,27 +121,33 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
 #pragma unroll
   for (int m = 0; m < MR; ++m) gone |= token[m] < 0;
   if (__ballot(gone) != 0) {
-    Acc none = {0, 0, 0, 0};
-    if (!kInt8)
-      for (int64_t l = wave; l < lines; l += WAVES)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t at = l * 128 + h * 64;
-          none = T::mma16(chunk_end<E>(w + at, kb - at - sub * 16), u32x4_t{0, 0, 0, 0}, none);
-        }
+    for (int b = 0; b < NB; ++b) {
+      Acc none = {0, 0, 0, 0};
+      if (!kInt8)
+        for (int64_t l = wave; l < lines; l += WAVES)
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
-      if (token[m] < 0) acc[m] = none;
+          for (int h = 0; h < 2; ++h) {
+            const int64_t at = l * 128 + h * 64;
+            none = T::mma16(chunk_end<E>(w[b] + at, kb - at - sub * 16), u32x4_t{0, 0, 0, 0}, none);
+          }
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+        if (token[m] < 0) acc[m * NB + b] = none;
+    }
   }
 
 #pragma unroll
-  for (int m = 0; m < MR; ++m) part[wave][m][lane] = acc[m];
+  for (int m = 0; m < MR * NB; ++m) part[wave][m][lane] = acc[m];
   __syncthreads();
   // block m: token 16 m + lane % 16, columns 4 (lane / 16) + 0..3
   for (int m = wave; m < MR; m += WAVES) {
-    Acc sum = part[0][m][lane];
+    Acc sum = part[0][m * NB][lane], up = part[0][m * NB + NB - 1][lane];
 #pragma unroll
-    for (int v = 1; v < WAVES; ++v) sum += part[v][m][lane];
+    for (int v = 1; v < WAVES; ++v) {
+      sum += part[v][m * NB][lane];
+      if constexpr (GATED) up += part[v][m * NB + 1][lane];
+    }
     const int r = 16 * m + (lane & 15);
     if (r >= rows) continue;
     int64_t s = -1;
@@ -138,7 +159,16 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t n = n0 + 4 * sub + e;
-      if (n >= p.N) continue;
+      if (n >= cols) continue;
+      if constexpr (GATED) {
+        c[n] = O::cvt(gated(sum[e], up[e]));
+        if (p.h != nullptr) {
+          typename O::elem* h = (typename O::elem*)p.h + (row0 + r) * p.N + n;
+          h[0] = O::cvt(sum[e]);
+          h[cols] = O::cvt(up[e]);
+        }
+        continue;
+      }
       float v = (float)sum[e];
       if constexpr (kInt8) v = scaled<O>(sum[e], sa, p.sb[(int64_t)g * p.N + n]);
       c[n] = O::cvt(v);
@@ -148,12 +178,12 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
 
 namespace {
 
-template <typename T, typename O, int MR, int U, int WAVES>
+template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false>
 hipError_t launch_few(const RaggedArgs& p, hipStream_t st) {
   const int64_t rt = p.R / (16 * MR) + std::min<int64_t>(p.G, p.R);
-  const int64_t blocks = rt * ((p.N + 15) / 16);
+  const int64_t blocks = rt * (((GATED ? p.N / 2 : p.N) + 15) / 16);
   return launch_in_parts(blocks, 64 * WAVES, [&](uint32_t first, uint32_t n) {
-    ragged_few_kernel<T, O, MR, U, WAVES><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
+    ragged_few_kernel<T, O, MR, U, WAVES, GATED><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
   });
 }
 
@@ -175,7 +205,26 @@ hipError_t launch_rows(const RaggedArgs& p, hipStream_t st) {
   return many ? launch_few<T, O, 4, 2, 4>(p, st) : launch_few<T, O, 4, 2, 8>(p, st);
 }
 
+// Gated: a workgroup has twice the loads in flight for a row of tokens.
+template <typename T, typename O>
+hipError_t launch_rows_gated(const RaggedArgs& p, hipStream_t st) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R);
+  const int64_t mean = (p.R + groups - 1) / groups;
+  const bool many = groups * ((p.N / 2 + 15) / 16) >= 1024;
+  const bool longk = p.K * (int64_t)sizeof(typename T::elem) >= 4 * 4 * 128;
+  if (mean <= 16) {
+    if (!many) return launch_few<T, O, 1, 2, 8, true>(p, st);
+    return longk ? launch_few<T, O, 1, 4, 4, true>(p, st) : launch_few<T, O, 1, 2, 4, true>(p, st);
+  }
+  if (mean <= 32) return many ? launch_few<T, O, 2, 2, 4, true>(p, st) : launch_few<T, O, 2, 2, 8, true>(p, st);
+  return many ? launch_few<T, O, 4, 1, 4, true>(p, st) : launch_few<T, O, 4, 1, 8, true>(p, st);
+}
+
 }  // namespace
+
+hipError_t launch_ragged_few_gated(bool f16, const RaggedArgs& p, hipStream_t st) {
+  return f16 ? launch_rows_gated<TypeF16, OutF16>(p, st) : launch_rows_gated<TypeBf16, OutBf16>(p, st);
+}
 
 hipError_t launch_ragged_few(bool f16, int out, const RaggedArgs& p, hipStream_t st) {
   if (f16)

@@ -208,9 +208,126 @@ __device__ __forceinline__ int64_t part_stages(int layout, const RaggedArgs& p, 
   return (con * esize + kStageK - 1) / kStageK;
 }
 
-template <typename T, typename O, int LAYOUT, int FA, bool GATHER>
+// A wave's 32 FA rows by 64 gate columns (accumulators 0..3 of a row block) and their up
+// columns (4..7): the activation and, KEEP, both projections.  8 consecutive columns a lane as
+// in the plain stores below.
+template <typename O, int FA, bool KEEP, typename Acc>
+__device__ __forceinline__ void store_gated(const RaggedArgs& p, Acc (&acc)[2 * FA][8], int32_t m0, int32_t n0,
+                                            int32_t rows, int wm, int wn, int ln) {
+  const int64_t F = p.N / 2;
+  const uint32_t ec = (uint32_t)(p.ldc * 2), eh = (uint32_t)(F * 4);
+  const int right = (int)min((int64_t)(kTileN / 2), F - n0);
+  const auto out = make_rsrc((uint16_t*)p.c + (int64_t)m0 * p.ldc + n0, (int64_t)(rows - 1) * ec + (F - n0) * 2);
+  const auto gate = make_rsrc((uint16_t*)p.h + (int64_t)m0 * 2 * F + n0, (int64_t)(rows - 1) * eh + (F - n0) * 2);
+  const auto up = make_rsrc((uint16_t*)p.h + (int64_t)m0 * 2 * F + F + n0, (int64_t)(rows - 1) * eh + (F - n0) * 2);
+#pragma unroll
+  for (int i = 0; i < 2 * FA; ++i) {
+    const int m = wm * 32 * FA + 16 * i + (ln & 15);
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]), "+a"(acc[i][j + 4]), "+a"(acc[i][j + 5]));
+      const int n = wn * 64 + 16 * (j + ((ln >> 4) & 1)) + 8 * (ln >> 5);
+      const bool in = (n < right) & (m < rows);
+      auto pack = [&](auto value) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = (uint32_t)O::cvt(value(j + (k >> 1), 2 * (k & 1))) |
+                 ((uint32_t)O::cvt(value(j + (k >> 1), 2 * (k & 1) + 1)) << 16);
+        const auto s0 = __builtin_amdgcn_permlane16_swap(w[0], w[2], false, false);
+        const auto s1 = __builtin_amdgcn_permlane16_swap(w[1], w[3], false, false);
+        return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+      };
+      __builtin_amdgcn_raw_buffer_store_b128(
+          pack([&](int b, int e) { return gated(acc[i][b][e], acc[i][b + 4][e]); }), out,
+          in ? (uint32_t)m * ec + (uint32_t)n * 2u : kOut, 0, 0);
+      if constexpr (KEEP) {
+        const uint32_t at = in ? (uint32_t)m * eh + (uint32_t)n * 2u : kOut;
+        __builtin_amdgcn_raw_buffer_store_b128(pack([&](int b, int e) { return acc[i][b][e]; }), gate, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(pack([&](int b, int e) { return acc[i][b + 4][e]; }), up, at, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// A wave's 32 FA rows by 128 columns of da: both projections are read (16 rows ahead of their
+// use), their gradients and the activation written.
+template <typename T, typename O, int FA, typename Acc>
+__device__ __forceinline__ void store_gated_bwd(const RaggedArgs& p, Acc (&acc)[2 * FA][8], int32_t m0,
+                                                int32_t n0, int32_t rows, int wm, int wn, int ln) {
+  const int64_t F = p.K;
+  const uint32_t eh = (uint32_t)(F * 4), ea = (uint32_t)(F * 2);
+  const int right = (int)min((int64_t)kTileN, F - n0);
+  const int64_t at0 = (int64_t)m0 * 2 * F + n0, room = (int64_t)(rows - 1) * eh + (F - n0) * 2;
+  const auto hg = make_rsrc((const uint16_t*)p.h + at0, room), hu = make_rsrc((const uint16_t*)p.h + at0 + F, room);
+  const auto dg = make_rsrc((uint16_t*)p.c + at0, room), du = make_rsrc((uint16_t*)p.c + at0 + F, room);
+  const auto act = make_rsrc((uint16_t*)p.act + (int64_t)m0 * F + n0,
+                             p.act == nullptr ? 0 : (int64_t)(rows - 1) * ea + (F - n0) * 2);
+  auto col = [&](int j) { return wn * 128 + 16 * (j + ((ln >> 4) & 1)) + 8 * (ln >> 5); };
+  auto row = [&](int i) { return wm * 32 * FA + 16 * i + (ln & 15); };
+  u32x4_t g[2][4], u[2][4];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t at = ((col(2 * q) < right) & (row(i) < rows))
+                              ? (uint32_t)row(i) * eh + (uint32_t)col(2 * q) * 2u : kOut;
+      g[i & 1][q] = __builtin_amdgcn_raw_buffer_load_b128(hg, at, 0, 0);
+      u[i & 1][q] = __builtin_amdgcn_raw_buffer_load_b128(hu, at, 0, 0);
+    }
+  };
+  // 8 consecutive columns a lane, and back to 4 of each of two blocks: the exchange is its own inverse
+  auto swap = [](u32x4_t v) {
+    const auto s0 = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false);
+    const auto s1 = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
+    return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+  };
+  load(0);
+#pragma unroll
+  for (int i = 0; i < 2 * FA; ++i) {
+    if (i + 1 < 2 * FA) load(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int j = 2 * q;
+      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+      const u32x4_t vg = swap(g[i & 1][q]), vu = swap(u[i & 1][q]);
+      u32x4_t og, ou, oa;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        GatedGrad r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          r[e] = gated_grad(acc[i][j + (k >> 1)][2 * (k & 1) + e], widen<T>((uint16_t)(vg[k] >> (16 * e))),
+                            widen<T>((uint16_t)(vu[k] >> (16 * e))));
+        og[k] = (uint32_t)O::cvt(r[0].gate) | ((uint32_t)O::cvt(r[1].gate) << 16);
+        ou[k] = (uint32_t)O::cvt(r[0].up) | ((uint32_t)O::cvt(r[1].up) << 16);
+        oa[k] = (uint32_t)O::cvt(r[0].act) | ((uint32_t)O::cvt(r[1].act) << 16);
+      }
+      const bool in = (col(j) < right) & (row(i) < rows);
+      const uint32_t at = in ? (uint32_t)row(i) * eh + (uint32_t)col(j) * 2u : kOut;
+      __builtin_amdgcn_raw_buffer_store_b128(swap(og), dg, at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(swap(ou), du, at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(swap(oa), act,
+                                             in ? (uint32_t)row(i) * ea + (uint32_t)col(j) * 2u : kOut, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// Column tiles of a launch; a gated tile holds 128 gate columns and their 128 up columns.
+template <int LAYOUT, int EPI>
+__host__ __device__ __forceinline__ uint32_t column_tiles(const RaggedArgs& p) {
+  if (EPI == kGated || EPI == kGatedKeep) return (uint32_t)((p.N / 2 + kTileN / 2 - 1) / (kTileN / 2));
+  return (uint32_t)(((LAYOUT == 0 ? p.N : p.K) + kTileN - 1) / kTileN);
+}
+
+template <typename T, typename O, int LAYOUT, int FA, bool GATHER, int EPI = kPlain>
 __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   typedef typename T::elem E;
+  constexpr bool kIsGated = EPI == kGated || EPI == kGatedKeep;
+  static_assert(EPI == kPlain || (sizeof(typename O::elem) == 2 && sizeof(E) == 2), "");
+  static_assert(kIsGated ? LAYOUT == 0 : (EPI != kGatedBwd || LAYOUT == 1), "");
   constexpr bool kInt8 = sizeof(E) == 1;
   constexpr bool kColA = LAYOUT == 2, kColB = LAYOUT != 0;   // contraction over rows
   constexpr int kTileM = 64 * FA;
@@ -221,7 +338,9 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
   constexpr int kMfma = 8 * kRowsF;                          // of a half stage: 64 contraction bytes
   constexpr int kReads = kRowsF + 8;
   constexpr int kEarly = 3 * kParts / 8;                     // copies in the first half
-  constexpr int kStores = sizeof(typename O::elem) == 4 ? 16 * FA : 8 * FA;
+  // (at least: a wait that counts fewer than there are waits for some of them)
+  constexpr int kStores = EPI == kGated ? 4 * FA : EPI == kGatedKeep ? 12 * FA :
+                          sizeof(typename O::elem) == 4 || EPI == kGatedBwd ? 16 * FA : 8 * FA;
   static_assert(!kColA || FA == 4, "");
   // row indexes, per wave: TN the 64 of each of 8 stages, NT the wave's rows of
   // the next tile
@@ -246,8 +365,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
 
   uint32_t nunits;
   {
-    const int64_t cols = LAYOUT == 0 ? p.N : p.K;
-    const uint32_t ctiles = (uint32_t)((cols + kTileN - 1) / kTileN);
+    const uint32_t ctiles = column_tiles<LAYOUT, EPI>(p);
     const uint32_t band = (uint32_t)((p.N + kTileM - 1) / kTileM);       // TN: row tiles of an expert
     const uint32_t rtiles = kColA ? (uint32_t)p.G * band : (uint32_t)table.tiles[kRaggedMaxGroups];
     // tiles: below 2^31 (checked by the caller)
@@ -335,7 +453,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       t.lo = table.rows[lo] + (mt - table.tiles[lo]) * kTileM;
       t.m0 = t.lo;
       t.rows = min(kTileM, table.rows[lo + 1] - t.lo);
-      t.n0 = nt * kTileN;
+      t.n0 = nt * (kIsGated ? kTileN / 2 : kTileN);
       t.len = 0;
       t.ns = (int32_t)((con * (int64_t)sizeof(E) + kStageK - 1) / kStageK);
       if (GATHER) {
@@ -407,7 +525,14 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     vb[j] = kColB ? (uint32_t)((16 * wave + 2 * j + (lane >> 5)) * eb) + chunk_c(j)
-                  : (uint32_t)((8 * (8 * wave + j) + (lane >> 3)) * eb) + chunk_k(j);
+                  : (uint32_t)((kIsGated ? 64 * (wave >> 1) + 8 * j : 8 * (8 * wave + j)) + (lane >> 3)) * eb +
+                        chunk_k(j);
+  // gated: rows 64 (2 c + u) .. of the stage are gate (u = 0) and up (u = 1) rows of wave column c
+  if constexpr (kIsGated) {
+    const uint32_t up = (wave & 1) ? (uint32_t)(p.N / 2) * eb : 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vb[j] += up;
+  }
   // contiguous contraction: lanes past its end in the last stage
   const uint32_t last_bytes =
       (uint32_t)((p.con * (int64_t)sizeof(E) - 1) % kStageK) + 1;
@@ -773,6 +898,11 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
     // offset that stores nothing, so that every tile issues the same stores
     // (the waits count on it).
     typedef typename O::elem OE;
+    if constexpr (kIsGated) {
+      store_gated<O, FA, EPI == kGatedKeep>(p, acc, m0, n0, rows, wm, wn, ln);
+    } else if constexpr (EPI == kGatedBwd) {
+      store_gated_bwd<T, O, FA>(p, acc, m0, n0, rows, wm, wn, ln);
+    } else {
     OE* c = (OE*)p.c + ((kColA ? (int64_t)g * p.N : 0) + m0) * p.ldc + n0;
     const uint32_t ec = (uint32_t)(p.ldc * sizeof(OE));
     const int64_t room = (int64_t)(rows - 1) * ec + (p.ccols - n0) * (int64_t)sizeof(OE);
@@ -820,6 +950,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    }
     if (next >= nunits) return;
     slot0 = (slot0 + ns) & 1;
     ring_at += ns;
@@ -840,14 +971,15 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
 
 // Sums of the parts of split tiles, in order, with the conversion and stores of the kernel above.
 // Workgroup b takes strips b, b + grid, ... of the split tiles (strip: a wave's 16 rows).
-template <typename T, typename O, int LAYOUT, int FA>
+template <typename T, typename O, int LAYOUT, int FA, int EPI = kPlain>
 __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t tile_grid) {
   constexpr bool kInt8 = sizeof(typename T::elem) == 1;
+  constexpr bool kIsGated = EPI == kGated || EPI == kGatedKeep;
   constexpr int kTileM = 64 * FA;
   constexpr int kRowsF = 2 * FA, kStrips = 4 * kRowsF;
   const int lane = threadIdx.x & 63;
   const int64_t cols = LAYOUT == 0 ? p.N : p.K;
-  const uint32_t ctiles = (uint32_t)((cols + kTileN - 1) / kTileN);
+  const uint32_t ctiles = column_tiles<LAYOUT, EPI>(p);
   const uint32_t band = (uint32_t)((p.N + kTileM - 1) / kTileM);
   uint32_t rtiles = (uint32_t)p.G * band;
   if (LAYOUT != 2)
@@ -893,6 +1025,51 @@ __global__ __launch_bounds__(256) void ragged_join_kernel(RaggedArgs p, uint32_t
       if (row >= 0 && row < p.S) sa = p.sa[row];
     }
     typedef typename O::elem OE;
+    if constexpr (kIsGated) {
+      // the two blocks are a gate and its up block; columns come in eights
+      const int64_t F = p.N / 2;
+      const int64_t n = (int64_t)nt * (kTileN / 2) + (wave & 1) * 64 + 16 * (int)(threadIdx.x >> 6) + 4 * (lane >> 4);
+      if (n >= F) continue;
+      OE o[3][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[0][e] = O::cvt(gated(sum[0][e], sum[1][e]));
+        o[1][e] = O::cvt(sum[0][e]);
+        o[2][e] = O::cvt(sum[1][e]);
+      }
+      __builtin_memcpy(__builtin_assume_aligned((OE*)p.c + (m0 + m) * p.ldc + n, 8), o[0], 8);
+      if constexpr (EPI == kGatedKeep) {
+        OE* h = (OE*)p.h + (m0 + m) * 2 * F + n;
+        __builtin_memcpy(__builtin_assume_aligned(h, 8), o[1], 8);
+        __builtin_memcpy(__builtin_assume_aligned(h + F, 8), o[2], 8);
+      }
+      continue;
+    }
+    if constexpr (EPI == kGatedBwd) {
+      const int64_t F = p.K;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int64_t n = (int64_t)nt * kTileN + (wave & 1) * 128 + 16 * (int)(threadIdx.x >> 6) + 64 * q +
+                          4 * (lane >> 4);
+        if (n >= F) continue;
+        const int64_t at = (m0 + m) * 2 * F + n;
+        OE o[3][4], hg[4], hu[4];
+        __builtin_memcpy(hg, __builtin_assume_aligned((const OE*)p.h + at, 8), 8);
+        __builtin_memcpy(hu, __builtin_assume_aligned((const OE*)p.h + at + F, 8), 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const GatedGrad r = gated_grad((float)sum[q][e], widen<T>(hg[e]), widen<T>(hu[e]));
+          o[0][e] = O::cvt(r.gate);
+          o[1][e] = O::cvt(r.up);
+          o[2][e] = O::cvt(r.act);
+        }
+        __builtin_memcpy(__builtin_assume_aligned((OE*)p.c + at, 8), o[0], 8);
+        __builtin_memcpy(__builtin_assume_aligned((OE*)p.c + at + F, 8), o[1], 8);
+        if (p.act != nullptr)
+          __builtin_memcpy(__builtin_assume_aligned((OE*)p.act + (m0 + m) * F + n, 8), o[2], 8);
+      }
+      continue;
+    }
     OE* c = (OE*)p.c + ((LAYOUT == 2 ? (int64_t)g * p.N : 0) + m0 + m) * p.ldc;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {

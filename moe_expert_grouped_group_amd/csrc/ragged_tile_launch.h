@@ -15,27 +15,27 @@ inline int compute_units() {
   return cus;
 }
 
-template <typename T, typename O, int LAYOUT, int FA, bool GATHER>
+template <typename T, typename O, int LAYOUT, int FA, bool GATHER, int EPI = kPlain>
 hipError_t launch_tile(const RaggedArgs& p, hipStream_t st) {
-  const int64_t m = 64 * FA, cols = ((LAYOUT == 0 ? p.N : p.K) + kTileN - 1) / kTileN;
+  const int64_t m = 64 * FA, cols = column_tiles<LAYOUT, EPI>(p);
   // one workgroup per CU; fewer where there are fewer tiles than CUs and no
   // workspace to split them
   const int64_t most = p.ws != nullptr ? INT32_MAX : cols * (LAYOUT == 2 ? p.G * ((p.N + m - 1) / m)
                                            : p.R / m + std::min<int64_t>(p.G, p.R));
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, compute_units()));
-  ragged_tile_kernel<T, O, LAYOUT, FA, GATHER><<<dim3(grid), dim3(256), 0, st>>>(p);
+  ragged_tile_kernel<T, O, LAYOUT, FA, GATHER, EPI><<<dim3(grid), dim3(256), 0, st>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.ws == nullptr) return e;
   // half the tiles of a round at most are split, 8 FA strips each
   const unsigned strips = std::max(1u, grid / 2) * 8 * FA;
-  ragged_join_kernel<T, O, LAYOUT, FA><<<dim3(std::min(strips, 1024u)), dim3(256), 0, st>>>(p, grid);
+  ragged_join_kernel<T, O, LAYOUT, FA, EPI><<<dim3(std::min(strips, 1024u)), dim3(256), 0, st>>>(p, grid);
   return hipGetLastError();
 }
 
-template <typename T, typename O, int LAYOUT, int FA>
+template <typename T, typename O, int LAYOUT, int FA, int EPI = kPlain>
 hipError_t launch_tile_gather(const RaggedArgs& p, hipStream_t st) {
-  return p.row_index != nullptr ? launch_tile<T, O, LAYOUT, FA, true>(p, st)
-                                : launch_tile<T, O, LAYOUT, FA, false>(p, st);
+  return p.row_index != nullptr ? launch_tile<T, O, LAYOUT, FA, true, EPI>(p, st)
+                                : launch_tile<T, O, LAYOUT, FA, false, EPI>(p, st);
 }
 
 // Rows of a forward tile.  Experts of few rows want low tiles: what the copies
@@ -44,12 +44,12 @@ hipError_t launch_tile_gather(const RaggedArgs& p, hipStream_t st) {
 // and 249 at 96; 371, 310 and 261 at 192.  The bounds lie lower than the tile
 // heights because experts differ from the mean, which is over all of them, those without
 // rows too: only the device knows the splits.
-template <typename T, typename O>
+template <typename T, typename O, int EPI = kPlain>
 hipError_t launch_tile_rows(const RaggedArgs& p, hipStream_t st) {
   const int64_t mean = p.R / std::min<int64_t>(p.G, p.R);
-  if (mean <= 32) return launch_tile_gather<T, O, 0, 1>(p, st);
-  if (mean <= 96) return launch_tile_gather<T, O, 0, 2>(p, st);
-  return launch_tile_gather<T, O, 0, 4>(p, st);
+  if (mean <= 32) return launch_tile_gather<T, O, 0, 1, EPI>(p, st);
+  if (mean <= 96) return launch_tile_gather<T, O, 0, 2, EPI>(p, st);
+  return launch_tile_gather<T, O, 0, 4, EPI>(p, st);
 }
 
 }  // namespace mx

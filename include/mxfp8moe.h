@@ -660,6 +660,51 @@ mxfp8_status mxfp8_ragged_gemm_swiglu_bwd(int32_t type, const void* dy, int64_t 
  * first, N of the second.  0 where none is used, and for sizes that are refused. */
 size_t mxfp8_ragged_gemm_swiglu_workspace_bytes(int32_t backward, int64_t R, int64_t F, int64_t C, int32_t G);
 
+/*
+ * mxfp8_quantize_fp8 -- a tensor's rows in 8-bit floating point (E4M3, as above) with an fp32
+ * scale for each block of 128 values:
+ *   scale[t, b] = max|x[t, 128 b ..]| / 448 in fp32 (nearest); q[t, k] = the E4M3 value
+ *   nearest to x[t, k] / scale[t, k / 128], ties to even, at most 448 in size.
+ * A block of zeros: scale 0, codes 0.  A block with an infinity or NaN: scale NaN, codes 0, so
+ * that products with it are NaN.
+ *   x [T, K] bf16 / fp16 (type), row stride ldx;  q u8 [T, K];  scale fp32 [T, ceil(K / 128)]
+ * Errors: EINVAL for NULL, K < 1, T < 0, ldx < K; ENOTSUP for other types.
+ */
+mxfp8_status mxfp8_quantize_fp8(const void* x, int32_t type, int64_t T, int64_t K, int64_t ldx, uint8_t* q,
+                                float* scale, void* stream);
+
+/*
+ * mxfp8_quantize_fp8_weight -- the same for the weights of G experts, w [G, N, K], with a
+ * scale for each block of 128 x 128 of an expert's matrix: q u8 [G, N, K], scale fp32
+ * [G, ceil(N / 128), ceil(K / 128)].
+ * Errors: EINVAL for NULL (G > 0), N < 1, K < 1, G < 0, over 2^31 - 1 blocks; ENOTSUP for
+ * other types.
+ */
+mxfp8_status mxfp8_quantize_fp8_weight(const void* w, int32_t type, int64_t G, int64_t N, int64_t K,
+                                       uint8_t* q, float* scale, void* stream);
+
+/*
+ * mxfp8_ragged_gemm_fp8 -- the forward product of ragged experts on such data:
+ *   C[r, n] = sum_b scale[i(r), b] w_scale[g, n / 128, b] sum_{k in block b} q[i(r), k] w[g, n, k]
+ * The two scales are multiplied first (one fp32 rounding), blocks are added in fp32, the result
+ * is rounded once to its type.  fp32 results: a block's sum is fp32 too.  bf16 and fp16
+ * results: it may be formed by matrix instructions that keep 13 bits below a block's largest
+ * partial sum (an error of about 1.5e-5 of the sum on normal values; at most 2^-9 of the
+ * sum of the largest 8 consecutive products' sizes).
+ *   q [S, K], row stride ldq;  scale [S, ceil(K / 128)];  w [G, N, K];
+ *   w_scale [G, ceil(N / 128), ceil(K / 128)];  c [R, N], row stride ldc, c_type any
+ *   mxfp8_type;  the rest as mxfp8_ragged_gemm (NT).  Rows of zeros have scale 0.  For the
+ *   input's gradient, w holds the transposed weights [G, K, N], w_scale the transposed scales.
+ * mxfp8_ragged_gemm_fp8_workspace_bytes: 0 where none is used, and for sizes that are refused.
+ * Errors: as mxfp8_ragged_gemm.
+ */
+mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
+                                   const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
+                                   int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
+                                   const int32_t* row_index, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+size_t mxfp8_ragged_gemm_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,7 +14,8 @@ from .binding import (  # noqa: F401
     group_quantize_requant_noalloc, grouped_dbias, grouped_gemm, grouped_gemm_swiglu_quantize,
     grouped_gemm_wgrad_accumulate,
     grouped_scaled_bias_grad, gemm_workspace_bytes, moe_combine, moe_combine_bwd, moe_route,
-    moe_route_bwd, moe_route_workspace_bytes, quantize_int8, ragged_gemm, ragged_gemm_int8,
+    moe_route_bwd, moe_route_workspace_bytes, quantize_fp8, quantize_fp8_weight, quantize_int8, ragged_gemm, ragged_gemm_fp8,
+    ragged_gemm_fp8_workspace_bytes, ragged_gemm_int8,
     ragged_gemm_swiglu, ragged_gemm_swiglu_bwd, ragged_gemm_swiglu_workspace_bytes,
     ragged_gemm_workspace_bytes,
     requant_colwise, swiglu_bwd,

@@ -68,6 +68,11 @@ SIGNATURES = {
     "mxfp8_quantize_int8": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "mxfp8_ragged_gemm_int8": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64,
                                        c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
+    "mxfp8_quantize_fp8": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "mxfp8_quantize_fp8_weight": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "mxfp8_ragged_gemm_fp8": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64, c_i64, c_i64,
+                                      c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
+    "mxfp8_ragged_gemm_fp8_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i32]),
     "mxfp8_moe_route_workspace_bytes": (c_size, [c_i64, c_i32]),
     "mxfp8_moe_route": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp,
                                 c_vp, c_vp, c_vp, c_size, c_vp]),

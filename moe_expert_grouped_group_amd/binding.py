@@ -819,6 +819,105 @@ def ragged_gemm_int8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=t
     return out
 
 
+FP8 = torch.float8_e4m3fn
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def quantize_fp8(x, out=None, stream=None):
+    """Rows of a bf16 / fp16 matrix in 8-bit floating point with a scale for each block of
+    128 values: (q float8_e4m3fn [T, K], scale fp32 [T, ceil(K / 128)]) with x ~ q * scale,
+    scale = max|block| / 448.  x may have a row stride.  out: optional (q, scale) buffers."""
+    lib = _lib()
+    t, k = _matrix(x, "x")
+    ty = _type_of(x, "x")
+    ldx = _rows_of(x, x.dtype, (t, k), "x")
+    _on_current(x, "x")
+    q, scale = (None, None) if out is None else out
+    q = _empty((t, k), FP8, x.device, stream) if q is None else q
+    scale = _empty((t, _blocks(k)), torch.float32, x.device, stream) if scale is None else scale
+    _need(q, FP8, (t, k), "q")
+    _need(scale, torch.float32, (t, _blocks(k)), "scale")
+    _same_device(x, q=q, scale=scale)
+    st = lib.mxfp8_quantize_fp8(_ptr(x), ty, t, k, ldx, _ptr(q), _ptr(scale), _stream(stream))
+    _native.check(st, "mxfp8_quantize_fp8")
+    return q, scale
+
+
+def quantize_fp8_weight(w, out=None, stream=None):
+    """Weights [G, N, K] in 8-bit floating point with a scale for each block of 128 x 128:
+    (q float8_e4m3fn [G, N, K], scale fp32 [G, ceil(N / 128), ceil(K / 128)]).  For the
+    input's gradient, lay out the transposed weights the same way: their blocks and scales
+    are the transposed ones."""
+    lib = _lib()
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [G, N, K]")
+    g, n, k = w.shape
+    ty = _type_of(w, "w")
+    _need(w, w.dtype, (g, n, k), "w")
+    _on_current(w, "w")
+    q, scale = (None, None) if out is None else out
+    shape = (g, _blocks(n), _blocks(k))
+    q = _empty((g, n, k), FP8, w.device, stream) if q is None else q
+    scale = _empty(shape, torch.float32, w.device, stream) if scale is None else scale
+    _need(q, FP8, (g, n, k), "q")
+    _need(scale, torch.float32, shape, "scale")
+    _same_device(w, q=q, scale=scale)
+    st = lib.mxfp8_quantize_fp8_weight(_ptr(w), ty, g, n, k, _ptr(q), _ptr(scale), _stream(stream))
+    _native.check(st, "mxfp8_quantize_fp8_weight")
+    return q, scale
+
+
+@functools.lru_cache(maxsize=4096)
+def ragged_gemm_fp8_workspace_bytes(rows, x_rows, n, k, groups):
+    """Workspace of ragged_gemm_fp8 for these sizes; 0 where none is used."""
+    return int(_lib().mxfp8_ragged_gemm_fp8_workspace_bytes(rows, x_rows, n, k, groups))
+
+
+def ragged_gemm_fp8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=torch.bfloat16,
+                    out=None, stream=None, workspace=None):
+    """Forward product in 8-bit floating point: q [S, K] with scale [S, ceil(K / 128)] (as
+    quantize_fp8 gives them), w [G, N, K] with w_scale [G, ceil(N / 128), ceil(K / 128)] (as
+    quantize_fp8_weight) -> [R, N], the sum over blocks of (sum of q w) * scale * w_scale.
+    row_index and m_splits as ragged_gemm, the workspace of ragged_gemm_fp8_workspace_bytes.
+    q and out may have a row stride.  fp32 results are fp32 sums throughout; those of bf16 and fp16
+    may be formed by faster instructions that keep fewer bits (mxfp8_ragged_gemm_fp8)."""
+    lib = _lib()
+    ms = _splits(m_splits)
+    g = ms.numel()
+    s, k = _matrix(q, "q")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [G, N, K]")
+    n = w.shape[1]
+    index = _row_index(row_index, q)
+    r = s if index is None else index.numel()
+    ldq = _rows_of(q, FP8, (s, k), "q")
+    _need(scale, torch.float32, (s, _blocks(k)), "scale")
+    _need(w, FP8, (g, n, k), "w")
+    _need(w_scale, torch.float32, (g, _blocks(n), _blocks(k)), "w_scale")
+    _on_current(q, "q")
+    if out_dtype not in _TYPE:
+        raise NotImplementedError(f"output dtype {out_dtype} is not supported")
+    if out is None:
+        out = _empty((r, n), out_dtype, q.device, stream)
+    ldc = _rows_of(out, out_dtype, (r, n), "out")
+    need = ragged_gemm_fp8_workspace_bytes(r, s, n, k, g)
+    size = need
+    if workspace is not None:
+        size = _sized(workspace, need)
+    elif need:
+        workspace = _scratch(need, q.device, stream)
+    _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out,
+                 workspace=workspace)
+    st = lib.mxfp8_ragged_gemm_fp8(_ptr(q), ldq, _ptr(scale), _ptr(w), _ptr(w_scale), _ptr(out), ldc,
+                                   _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
+                                   _ptr(workspace), size, _stream(stream))
+    _native.check(st, "mxfp8_ragged_gemm_fp8")
+    return out
+
+
 @dataclass
 class Route:
     """Where the tokens go (moe_route): ids, weights and row_pos [T, top_k],

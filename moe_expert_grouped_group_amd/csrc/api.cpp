@@ -690,6 +690,87 @@ mxfp8_status mxfp8_ragged_gemm_int8(const int8_t* q, int64_t ldq, const float* s
                     fn);
 }
 
+mxfp8_status mxfp8_quantize_fp8(const void* x, int32_t type, int64_t T, int64_t K, int64_t ldx, uint8_t* q,
+                                float* scale, void* stream) {
+  const char* fn = "mxfp8_quantize_fp8";
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: type %d is not supported", fn, (int)type);
+  REQUIRE(T >= 0 && T <= kI32Max && K >= 1 && K <= kI32Max,
+          "%s: T = %lld must be 0 to 2^31 - 1, K = %lld 1 to 2^31 - 1", fn, (long long)T,
+          (long long)K);
+  REQUIRE(ldx >= K, "%s: ldx = %lld is shorter than a row", fn, (long long)ldx);
+  if (T == 0) return ok();
+  REQUIRE(x && q && scale, "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(x, 2) && aligned_to(scale, 4), "%s: a pointer is not aligned to its element",
+          fn);
+  return hip_status(
+      mx::launch_quantize_fp8(x, type == MXFP8_TYPE_F16, T, K, ldx, q, scale, as_stream(stream)), fn);
+}
+
+mxfp8_status mxfp8_quantize_fp8_weight(const void* w, int32_t type, int64_t G, int64_t N, int64_t K,
+                                       uint8_t* q, float* scale, void* stream) {
+  const char* fn = "mxfp8_quantize_fp8_weight";
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: type %d is not supported", fn, (int)type);
+  REQUIRE(G >= 0 && G <= kI32Max && N >= 1 && N <= kI32Max && K >= 1 && K <= kI32Max,
+          "%s: G = %lld must be 0 to 2^31 - 1, N = %lld and K = %lld 1 to 2^31 - 1", fn, (long long)G,
+          (long long)N, (long long)K);
+  const int64_t each = ((N + 127) / 128) * ((K + 127) / 128);
+  REQUIRE(each <= kI32Max && G * each <= kI32Max, "%s: over 2^31 - 1 blocks", fn);
+  if (G == 0) return ok();
+  REQUIRE(w && q && scale, "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(w, 2) && aligned_to(scale, 4), "%s: a pointer is not aligned to its element",
+          fn);
+  return hip_status(
+      mx::launch_quantize_fp8_weight(w, type == MXFP8_TYPE_F16, G, N, K, q, scale, as_stream(stream)), fn);
+}
+
+size_t mxfp8_ragged_gemm_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G) {
+  if (R < 0 || S < 0 || N < 1 || K < 1 || G < 1 || G > mx::kRaggedMaxGroups || R > kI32Max || S > kI32Max ||
+      N > kI32Max || K > kI32Max)
+    return 0;
+  return mx::ragged_fp8_workspace_bytes(R, S, N, K, G);
+}
+
+mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
+                                   const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
+                                   int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
+                                   const int32_t* row_index, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  const char* fn = "mxfp8_ragged_gemm_fp8";
+  if (c_type != MXFP8_TYPE_F32 && c_type != MXFP8_TYPE_BF16 && c_type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: output type %d is not supported", fn, (int)c_type);
+  mxfp8_status st = check_ragged(fn, MXFP8_LAYOUT_NT, R, S, N, K, m_splits, G, row_index);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(ldq >= K, "%s: ldq = %lld is shorter than a row", fn, (long long)ldq);
+  REQUIRE(ldc >= N, "%s: ldc = %lld is shorter than a row", fn, (long long)ldc);
+  if (R == 0) return ok();
+  REQUIRE(c && w && w_scale && (S == 0 || (q && scale)), "%s: NULL pointer", fn);
+  REQUIRE(aligned_to(scale, 4) && aligned_to(w_scale, 4) && aligned_to(c, c_type == 0 ? 4 : 2) &&
+              aligned_to(row_index, 4) && aligned_to(m_splits, 8),
+          "%s: a pointer is not aligned to its element", fn);
+  mx::RaggedArgs p{};
+  p.a = q;
+  p.b = w;
+  p.c = c;
+  p.lda = ldq;
+  p.ldb = K;
+  p.ldc = ldc;
+  p.R = R;
+  p.S = S;
+  p.N = N;
+  p.K = K;
+  p.m_splits = m_splits;
+  p.row_index = row_index;
+  p.sa = scale;
+  p.sb = w_scale;
+  p.G = G;
+  p.ws = usable_workspace(workspace);
+  return hip_status(mx::launch_ragged_gemm_fp8(
+                        c_type, p, p.ws != nullptr ? workspace_bytes : 0, as_stream(stream)),
+                    fn);
+}
+
 namespace {
 
 constexpr int32_t kRouteMaxExperts = 1024;

@@ -481,6 +481,8 @@ hipError_t with_tiles(int layout, int osize, RaggedArgs p, size_t ws_bytes, hipS
 
 }  // namespace
 
+bool ragged_few_rows(const RaggedArgs& p, int esize) { return few_rows(p, esize); }
+
 // Workspace that a product of these sizes uses (0: none), operands contiguous.
 size_t ragged_workspace_bytes(int layout, int esize, int64_t R, int64_t S, int64_t N, int64_t K, int32_t G) {
   if (R == 0) return 0;

@@ -48,6 +48,7 @@ struct RaggedArgs {
   const int32_t* row_index;   // NULL: row r of the product is row r of X
   const float* sa;      // int8: scale of each row of X [S]
   const float* sb;      // int8: scale of each output channel [G, N]
+                        // fp8: scales of blocks of 128, sa [S, K / 128], sb [G, N / 128, K / 128] (rounded up)
   int32_t G;
   // for the large tiles
   int64_t con;          // NT, NN: contraction with its zero padding
@@ -78,6 +79,9 @@ hipError_t launch_ragged_few_gated(bool f16, const RaggedArgs& p, hipStream_t st
 hipError_t launch_ragged_tile_gated(bool f16, const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_gated_f16(const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_gated_bwd(bool f16, const RaggedArgs& p, hipStream_t st);
+// 8-bit floating point (ragged_fp8.hip has the formula, ragged_fp8_tile.hip the large tiles).
+hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st);
+bool ragged_few_rows(const RaggedArgs& p, int esize);   // few_rows of ragged.hip
 size_t ragged_split_bytes();   // a partial 256 x 256 tile for each CU
 
 // Longest range of a bounded operand (32-bit offsets, less what marks a lane that
@@ -166,6 +170,22 @@ template <typename O>
 __device__ __forceinline__ float scaled(int sum, float row, float channel) {
   float v = (float)sum * row * channel;
   if (std::is_same<O, OutF16>::value) asm("" : "+v"(v));
+  return v;
+}
+
+// 16 bytes at p, of which the contraction holds n (n <= 0: none): zeros behind.
+template <typename E>
+__device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
+  u32x4_t v = {0, 0, 0, 0};
+  if (n >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (n > 0) {
+    E e[16 / sizeof(E)];
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(E)); ++i)
+      e[i] = (int64_t)(i * sizeof(E)) < n ? ((const E*)p)[i] : (E)0;
+    __builtin_memcpy(&v, e, 16);
+  }
   return v;
 }
 

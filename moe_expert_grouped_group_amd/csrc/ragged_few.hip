@@ -16,22 +16,6 @@
 
 namespace mx {
 
-// 16 bytes at p, of which the contraction holds n (n <= 0: none): zeros behind.
-template <typename E>
-__device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
-  u32x4_t v = {0, 0, 0, 0};
-  if (n >= 16) {
-    __builtin_memcpy(&v, p, 16);
-  } else if (n > 0) {
-    E e[16 / sizeof(E)];
-#pragma unroll
-    for (int i = 0; i < (int)(16 / sizeof(E)); ++i)
-      e[i] = (int64_t)(i * sizeof(E)) < n ? ((const E*)p)[i] : (E)0;
-    __builtin_memcpy(&v, e, 16);
-  }
-  return v;
-}
-
 // GATED: 16 gate columns and their 16 up columns, the activation of both (and the
 // projections, where p.h is given).
 template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false>

@@ -114,10 +114,11 @@ struct RaggedTable {
   int32_t tiles[kRaggedMaxGroups + 1];
   int32_t rows[kRaggedMaxGroups + 1];
 };
+template <int THREADS = 256>
 __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int G, int64_t R,
                                                    int tile, RaggedTable* t, int32_t* scan) {
   const int tid = threadIdx.x;
-  constexpr int per = kRaggedMaxGroups / 256;
+  constexpr int per = kRaggedMaxGroups / THREADS;
   int64_t rows[per], rs = 0;
   int32_t ts = 0;
 #pragma unroll
@@ -131,7 +132,7 @@ __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int 
   int64_t* s64 = (int64_t*)scan;
   s64[tid] = rs;
   __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
+  for (int d = 1; d < THREADS; d <<= 1) {
     const int64_t u = tid >= d ? s64[tid - d] : 0;
     __syncthreads();
     s64[tid] += u;
@@ -149,7 +150,7 @@ __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int 
   }
   scan[tid] = ts;
   __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
+  for (int d = 1; d < THREADS; d <<= 1) {
     const int32_t u = tid >= d ? scan[tid - d] : 0;
     __syncthreads();
     scan[tid] += u;
@@ -162,7 +163,7 @@ __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int 
     t->rows[tid * per + i] = off[i];
     t0 += (off[i + 1] - off[i] + tile - 1) / tile;
   }
-  if (tid == 255) {
+  if (tid == THREADS - 1) {
     t->tiles[kRaggedMaxGroups] = t0;
     t->rows[kRaggedMaxGroups] = off[per];
   }

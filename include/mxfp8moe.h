@@ -705,6 +705,57 @@ mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* s
                                    void* stream);
 size_t mxfp8_ragged_gemm_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
 
+/*
+ * mxfp8_residual_norm -- what follows a block whose output is f (for an expert layer, the
+ * join's): f normalized, gated and added to the scaled residual stream, and the sum
+ * normalized for the next block, in one pass.  For each row t, n(v) = v / sqrt(mean(v^2) + eps):
+ *   b[t] = n(f[t]) post_weight     f[t] where post_weight is NULL
+ *   r[t] = residual_scale x[t] + gate[t] b[t]     gate 1 where it is NULL
+ *   y[t] = n(r[t]) pre_weight
+ * n(r) is of r as it is stored (rounded to x's type), which is what the backward pass and
+ * every later reader see.  Statistics are fp32: the squares' sum must not pass 2^127.
+ *   x, r   [T, H], x_type: MXFP8_TYPE_F32 or `type`.  r may be x itself
+ *   f, y   [T, H], type: MXFP8_TYPE_BF16 or MXFP8_TYPE_F16
+ *   gate   fp32 [T] or NULL;  post_weight, pre_weight [H] or NULL, w_type: MXFP8_TYPE_F32 or `type`
+ *   f NULL: the norm before the first block, y[t] = n(x[t]) pre_weight; r, gate and
+ *          post_weight must be NULL, residual_scale is not used.
+ *   pre_weight NULL: y is not wanted and must be NULL (with f given).
+ *   H      1 to 16384
+ * Errors: EINVAL for NULL, sizes out of range, neither output, a negative or non-finite eps;
+ * ENOTSUP for other types.
+ */
+mxfp8_status mxfp8_residual_norm(const void* x, int32_t x_type, const void* f, int32_t type, int64_t T,
+                                 int64_t H, float residual_scale, const float* gate,
+                                 const void* post_weight, const void* pre_weight, int32_t w_type, float eps,
+                                 void* r, void* y, void* stream);
+
+/*
+ * mxfp8_residual_norm_bwd -- its gradients.  dy is that of y, dr the one that reaches r past
+ * this norm (from the blocks after it):
+ *   total  = dr + gradient of r through y
+ *   dx     = residual_scale total                  [T, H], x_type
+ *   df     = gradient of f for gate total          [T, H], type
+ *   dgate  [t] = <total[t], b[t]>                  fp32 [T]
+ *   dpost_weight, dpre_weight                      fp32 [H], sums over the rows in a fixed order
+ * Every output may be NULL (not wanted), not all of them.
+ *   dy  [T, H] type, NULL without pre_weight;  dr [T, H] x_type, or NULL (zeros); not both NULL
+ *   r   [T, H] x_type, as mxfp8_residual_norm stored it (x where f is NULL);  f as given there
+ *   the rest as there; dx may be dr, df may be dy or f.  f NULL: dx = total, df, dgate and
+ *   dpost_weight must be NULL.
+ *   workspace of mxfp8_residual_norm_bwd_workspace_bytes(T, H) bytes, 4-byte aligned, for the two
+ *   weights' gradients (NULL without both); needs no initialisation.
+ * T = 0 writes zeros to the weights' gradients.
+ * Errors: as mxfp8_residual_norm, and EINVAL for an output without what it is the gradient of,
+ * a small workspace.
+ */
+size_t mxfp8_residual_norm_bwd_workspace_bytes(int64_t T, int64_t H);
+mxfp8_status mxfp8_residual_norm_bwd(const void* dy, const void* dr, const void* r, int32_t x_type,
+                                     const void* f, int32_t type, int64_t T, int64_t H,
+                                     float residual_scale, const float* gate, const void* post_weight,
+                                     const void* pre_weight, int32_t w_type, float eps, void* dx, void* df,
+                                     float* dgate, float* dpost_weight, float* dpre_weight,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

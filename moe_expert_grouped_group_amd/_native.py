@@ -16,6 +16,7 @@ c_u8p = ctypes.c_void_p
 c_i64 = ctypes.c_int64
 c_i32 = ctypes.c_int32
 c_u32 = ctypes.c_uint32
+c_f32 = ctypes.c_float
 c_size = ctypes.c_size_t
 c_vp = ctypes.c_void_p
 
@@ -73,6 +74,12 @@ SIGNATURES = {
     "mxfp8_ragged_gemm_fp8": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64, c_i64, c_i64,
                                       c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
     "mxfp8_ragged_gemm_fp8_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i32]),
+    "mxfp8_residual_norm": (c_i32, [c_vp, c_i32, c_vp, c_i32, c_i64, c_i64, c_f32, c_vp, c_vp, c_vp, c_i32,
+                                    c_f32, c_vp, c_vp, c_vp]),
+    "mxfp8_residual_norm_bwd_workspace_bytes": (c_size, [c_i64, c_i64]),
+    "mxfp8_residual_norm_bwd": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_vp, c_i32, c_i64, c_i64, c_f32, c_vp,
+                                        c_vp, c_vp, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
+                                        c_vp]),
     "mxfp8_moe_route_workspace_bytes": (c_size, [c_i64, c_i32]),
     "mxfp8_moe_route": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp,
                                 c_vp, c_vp, c_vp, c_size, c_vp]),
@@ -84,7 +91,7 @@ SIGNATURES = {
                                       c_vp, c_vp, c_vp]),
 }
 
-ABI_VERSION = 4
+ABI_VERSION = 5
 
 MXFP8_OK, MXFP8_EINVAL, MXFP8_ENOTSUP, MXFP8_EHIP = 0, 1, 2, 3
 

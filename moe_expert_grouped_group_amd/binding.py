@@ -1055,3 +1055,138 @@ def moe_combine_bwd(dout, y, row_pos, weights=None, want_dy=True, want_dweights=
                                    _ptr(weights), _ptr(dy), _ptr(dw), _stream(stream))
     _native.check(st, "mxfp8_moe_combine_bwd")
     return dy, dw
+
+
+# ----------------------------------------------------------------------------
+# the norms around a block
+# ----------------------------------------------------------------------------
+
+@dataclass
+class ResidualNormGrad:
+    """Gradients of residual_norm: x and f [T, H], gate fp32 [T], the weights' fp32 [H]; None
+    for what the call did not have."""
+    x: Optional[torch.Tensor] = None
+    f: Optional[torch.Tensor] = None
+    gate: Optional[torch.Tensor] = None
+    post_weight: Optional[torch.Tensor] = None
+    pre_weight: Optional[torch.Tensor] = None
+
+
+def _norm_operands(x, name, f, out_dtype, gate, post_weight, pre_weight):
+    """Checks of what both directions take; (T, H, type of x, type, its torch type, type of the weights)."""
+    t, h = _matrix(x, name)
+    if f is None and (gate is not None or post_weight is not None):
+        raise ValueError("gate and post_weight need f")
+    dtype = f.dtype if f is not None else out_dtype
+    if dtype is None:
+        dtype = x.dtype if x.dtype != torch.float32 else torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise NotImplementedError(f"f of {dtype} is not supported")
+    if out_dtype not in (None, dtype):
+        raise NotImplementedError(f"output dtype {out_dtype} is not supported")
+    if x.dtype not in (dtype, torch.float32):
+        raise NotImplementedError(f"{name} of {x.dtype} beside {dtype} is not supported")
+    _need(x, x.dtype, (t, h), name)
+    _on_current(x, name)
+    if f is not None:
+        _need(f, dtype, (t, h), "f")
+    if gate is not None:
+        _need(gate, torch.float32, (t,), "gate")
+    weights = [w for w in (post_weight, pre_weight) if w is not None]
+    w_dtype = weights[0].dtype if weights else torch.float32
+    if w_dtype not in (dtype, torch.float32):
+        raise NotImplementedError(f"weights of {w_dtype} beside {dtype} are not supported")
+    for n, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if w is not None:
+            _need(w, w_dtype, (h,), n)
+    return t, h, _TYPE[x.dtype], _TYPE[dtype], dtype, _TYPE[w_dtype]
+
+
+def residual_norm(x, f=None, residual_scale=1.0, gate=None, post_weight=None, pre_weight=None, eps=1e-6,
+                  out_dtype=None, r=None, y=None, stream=None):
+    """What follows a block with output f, in one pass; n(v) = v / sqrt(mean(v^2) + eps) by row:
+
+        r = residual_scale * x + gate[:, None] * n(f) * post_weight     (f itself without post_weight)
+        y = n(r) * pre_weight                                           the next block's input
+
+    x [T, H] fp32 or of f's type, f [T, H] bf16 / fp16, gate fp32 [T], the weights [H] fp32
+    or of f's type (both alike); H up to 16384.  Returns (r, y): r of x's type, y of f's, None
+    without pre_weight.  n(r) is of r as it is stored.  Without f the norm before the first
+    block: (x, n(x) * pre_weight), y of out_dtype (x's, bf16 for fp32).  r may be x."""
+    lib = _lib()
+    t, h, x_ty, ty, dtype, w_ty = _norm_operands(x, "x", f, out_dtype, gate, post_weight, pre_weight)
+    if f is None and pre_weight is None:
+        raise ValueError("neither f nor pre_weight: nothing to compute")
+    if f is None:
+        if r is not None:
+            raise ValueError("r goes with f")
+    else:
+        r = _empty((t, h), x.dtype, x.device, stream) if r is None else r
+        _need(r, x.dtype, (t, h), "r")
+    if pre_weight is None:
+        if y is not None:
+            raise ValueError("y goes with pre_weight")
+    else:
+        y = _empty((t, h), dtype, x.device, stream) if y is None else y
+        _need(y, dtype, (t, h), "y")
+    _same_device(x, f=f, gate=gate, post_weight=post_weight, pre_weight=pre_weight, r=r, y=y)
+    st = lib.mxfp8_residual_norm(_ptr(x), x_ty, _ptr(f), ty, t, h, residual_scale, _ptr(gate),
+                                 _ptr(post_weight), _ptr(pre_weight), w_ty, eps, _ptr(r), _ptr(y),
+                                 _stream(stream))
+    _native.check(st, "mxfp8_residual_norm")
+    return (x if f is None else r), y
+
+
+@functools.lru_cache(maxsize=1024)
+def residual_norm_bwd_workspace_bytes(tokens, hidden):
+    return int(_lib().mxfp8_residual_norm_bwd_workspace_bytes(tokens, hidden))
+
+
+def residual_norm_bwd(dy, dr, r, f=None, residual_scale=1.0, gate=None, post_weight=None, pre_weight=None,
+                      eps=1e-6, out=None, workspace=None, stream=None):
+    """Gradients of residual_norm: dy [T, H] that of y (None without pre_weight), dr [T, H]
+    what reaches r past this norm (None: nothing), r as residual_norm gave it (x itself
+    without f), the rest as there.  Returns a ResidualNormGrad; out: optional one
+    with buffers to write into (x may be dr, f may be dy or f).  workspace: optional device
+    buffer of residual_norm_bwd_workspace_bytes(T, H), for the weights' gradients."""
+    lib = _lib()
+    t, h, x_ty, ty, dtype, w_ty = _norm_operands(r, "r", f, None if dy is None else dy.dtype, gate,
+                                                 post_weight, pre_weight)
+    if dy is None and dr is None:
+        raise ValueError("neither dy nor dr")
+    if (dy is None) != (pre_weight is None):
+        raise ValueError("dy goes with pre_weight")
+    if dy is not None:
+        _need(dy, dtype, (t, h), "dy")
+    if dr is not None:
+        _need(dr, r.dtype, (t, h), "dr")
+    got = ResidualNormGrad() if out is None else out
+    for name, wanted, shape, kind in (
+            ("x", True, (t, h), r.dtype), ("f", f is not None, (t, h), dtype),
+            ("gate", gate is not None, (t,), torch.float32),
+            ("post_weight", post_weight is not None, (h,), torch.float32),
+            ("pre_weight", pre_weight is not None, (h,), torch.float32)):
+        buf = getattr(got, name)
+        if not wanted:
+            if buf is not None:
+                raise ValueError(f"out.{name} is the gradient of what was not given")
+            continue
+        if buf is None:
+            buf = _empty(shape, kind, r.device, stream)
+            setattr(got, name, buf)
+        _need(buf, kind, shape, f"out.{name}")
+    need = residual_norm_bwd_workspace_bytes(t, h) if got.post_weight is not None or got.pre_weight is not None else 0
+    size = need
+    if workspace is not None:
+        size = _sized(workspace, need)
+    elif need:
+        workspace = _scratch(need, r.device, stream)
+    _same_device(r, dy=dy, dr=dr, f=f, gate=gate, post_weight=post_weight, pre_weight=pre_weight,
+                 out_x=got.x, out_f=got.f, out_gate=got.gate, out_post_weight=got.post_weight,
+                 out_pre_weight=got.pre_weight, workspace=workspace)
+    st = lib.mxfp8_residual_norm_bwd(
+        _ptr(dy), _ptr(dr), _ptr(r), x_ty, _ptr(f), ty, t, h, residual_scale, _ptr(gate), _ptr(post_weight),
+        _ptr(pre_weight), w_ty, eps, _ptr(got.x), _ptr(got.f), _ptr(got.gate), _ptr(got.post_weight),
+        _ptr(got.pre_weight), _ptr(workspace), size, _stream(stream))
+    _native.check(st, "mxfp8_residual_norm_bwd")
+    return got

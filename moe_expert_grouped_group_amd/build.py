@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp8moe.so")
 SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "ragged.hip", "ragged_few.hip", "ragged_tile_nt.hip",
            "ragged_tile_nn.hip", "ragged_tile_tn.hip", "ragged_tile_int8.hip", "ragged_tile_gated.hip",
-           "ragged_tile_gated_f16.hip", "ragged_tile_gated_bwd.hip", "ragged_fp8.hip", "ragged_fp8_tile.hip", "fp8.hip", "routing.hip"]
+           "ragged_tile_gated_f16.hip", "ragged_tile_gated_bwd.hip", "ragged_fp8.hip", "ragged_fp8_tile.hip", "fp8.hip", "norm.hip",
+           "routing.hip"]
 ARCH = "gfx950"
 
 

@@ -68,7 +68,7 @@ extern "C" {
 
 const char* mxfp8_last_error(void) { return g_err; }
 
-int32_t mxfp8_abi_version(void) { return 4; }
+int32_t mxfp8_abi_version(void) { return 5; }
 
 size_t mxfp8_dbias_workspace_bytes(int64_t T, int64_t N) {
   if (T <= 0 || N <= 0) return 0;
@@ -877,6 +877,91 @@ mxfp8_status mxfp8_moe_combine_bwd(const void* dout, const void* y, int32_t type
   return hip_status(mx::launch_join_bwd(dout, y, type == MXFP8_TYPE_F16, T, R, H, top_k, row_pos,
                                         weights, dy, dweights, as_stream(stream)),
                     fn);
+}
+
+namespace {
+
+mxfp8_status check_norm(const char* fn, int32_t x_type, int32_t type, int32_t w_type, int64_t T, int64_t H,
+                        float eps, const void* f, const float* gate, const void* post, const void* pre) {
+  if (type != MXFP8_TYPE_BF16 && type != MXFP8_TYPE_F16)
+    return fail(MXFP8_ENOTSUP, "%s: type %d is not supported", fn, (int)type);
+  if (x_type != MXFP8_TYPE_F32 && x_type != type)
+    return fail(MXFP8_ENOTSUP, "%s: residual type %d is not supported", fn, (int)x_type);
+  if (w_type != MXFP8_TYPE_F32 && w_type != type)
+    return fail(MXFP8_ENOTSUP, "%s: weight type %d is not supported", fn, (int)w_type);
+  REQUIRE(T >= 0 && T <= kI32Max, "%s: T = %lld must be 0 to 2^31 - 1", fn, (long long)T);
+  REQUIRE(H >= 1 && H <= mx::norm_max_hidden(), "%s: H = %lld must be 1 to %lld", fn, (long long)H,
+          (long long)mx::norm_max_hidden());
+  REQUIRE(eps >= 0.f && eps <= 3.4028235e38f, "%s: eps must be a finite number from 0 up", fn);
+  REQUIRE(f != nullptr || T == 0 || (gate == nullptr && post == nullptr), "%s: gate and post_weight need f", fn);
+  const size_t w = w_type == MXFP8_TYPE_F32 ? 4 : 2;
+  REQUIRE(aligned_to(f, 2) && aligned_to(gate, 4) && aligned_to(post, w) && aligned_to(pre, w),
+          "%s: a pointer is not aligned to its element", fn);
+  return MXFP8_OK;
+}
+
+}  // namespace
+
+mxfp8_status mxfp8_residual_norm(const void* x, int32_t x_type, const void* f, int32_t type, int64_t T,
+                                 int64_t H, float residual_scale, const float* gate,
+                                 const void* post_weight, const void* pre_weight, int32_t w_type, float eps,
+                                 void* r, void* y, void* stream) {
+  const char* fn = "mxfp8_residual_norm";
+  mxfp8_status st = check_norm(fn, x_type, type, w_type, T, H, eps, f, gate, post_weight, pre_weight);
+  if (st != MXFP8_OK) return st;
+  if (T == 0) return ok();
+  REQUIRE(x != nullptr, "%s: x is NULL", fn);
+  REQUIRE((f != nullptr) == (r != nullptr), "%s: r goes with f", fn);
+  REQUIRE((pre_weight != nullptr) == (y != nullptr), "%s: y goes with pre_weight", fn);
+  REQUIRE(r != nullptr || y != nullptr, "%s: no output asked for", fn);
+  const size_t xs = x_type == MXFP8_TYPE_F32 ? 4 : 2;
+  REQUIRE(aligned_to(x, xs) && aligned_to(r, xs) && aligned_to(y, 2),
+          "%s: a pointer is not aligned to its element", fn);
+  return hip_status(mx::launch_residual_norm(x, x_type == MXFP8_TYPE_F32, f, type == MXFP8_TYPE_F16, T, H,
+                                             residual_scale, gate, post_weight, pre_weight,
+                                             w_type == MXFP8_TYPE_F32, eps, r, y, as_stream(stream)),
+                    fn);
+}
+
+size_t mxfp8_residual_norm_bwd_workspace_bytes(int64_t T, int64_t H) {
+  if (T < 0 || T > kI32Max || H < 1 || H > mx::norm_max_hidden()) return 0;
+  return mx::norm_bwd_workspace_bytes(T, H);
+}
+
+mxfp8_status mxfp8_residual_norm_bwd(const void* dy, const void* dr, const void* r, int32_t x_type,
+                                     const void* f, int32_t type, int64_t T, int64_t H,
+                                     float residual_scale, const float* gate, const void* post_weight,
+                                     const void* pre_weight, int32_t w_type, float eps, void* dx, void* df,
+                                     float* dgate, float* dpost_weight, float* dpre_weight,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "mxfp8_residual_norm_bwd";
+  mxfp8_status st = check_norm(fn, x_type, type, w_type, T, H, eps, f, gate, post_weight, pre_weight);
+  if (st != MXFP8_OK) return st;
+  REQUIRE(T == 0 || dx || df || dgate || dpost_weight || dpre_weight, "%s: no output asked for", fn);
+  REQUIRE(dpost_weight == nullptr || post_weight != nullptr, "%s: dpost_weight needs post_weight", fn);
+  REQUIRE(dpre_weight == nullptr || pre_weight != nullptr, "%s: dpre_weight needs pre_weight", fn);
+  REQUIRE(dgate == nullptr || gate != nullptr, "%s: dgate needs gate", fn);
+  const size_t need = dpost_weight != nullptr || dpre_weight != nullptr ? mx::norm_bwd_workspace_bytes(T, H) : 0;
+  REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need && aligned_to(workspace, 4)),
+          "%s: needs a workspace of %zu bytes", fn, need);
+  if (T > 0) {
+    REQUIRE(dy != nullptr || dr != nullptr, "%s: neither dy nor dr", fn);
+    REQUIRE(dy == nullptr || pre_weight != nullptr, "%s: dy goes with pre_weight", fn);
+    REQUIRE(dpre_weight == nullptr || dy != nullptr, "%s: dpre_weight needs dy", fn);
+    REQUIRE(dy == nullptr || r != nullptr, "%s: r is NULL", fn);
+    REQUIRE(f != nullptr || df == nullptr, "%s: df needs f", fn);
+  }
+  const size_t xs = x_type == MXFP8_TYPE_F32 ? 4 : 2;
+  REQUIRE(aligned_to(dy, 2) && aligned_to(dr, xs) && aligned_to(r, xs) && aligned_to(dx, xs) &&
+              aligned_to(df, 2) && aligned_to(dgate, 4) && aligned_to(dpost_weight, 4) &&
+              aligned_to(dpre_weight, 4),
+          "%s: a pointer is not aligned to its element", fn);
+  return hip_status(
+      mx::launch_residual_norm_bwd(dy, dr, r, x_type == MXFP8_TYPE_F32, f, type == MXFP8_TYPE_F16, T, H,
+                                   f != nullptr ? residual_scale : 1.f, gate, post_weight, pre_weight,
+                                   w_type == MXFP8_TYPE_F32, eps, dx, df, dgate, dpost_weight, dpre_weight,
+                                   workspace, as_stream(stream)),
+      fn);
 }
 
 }  // extern "C"

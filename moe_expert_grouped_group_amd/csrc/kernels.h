@@ -81,6 +81,16 @@ hipError_t launch_quantize_fp8_weight(const void* w, bool f16, int64_t G, int64_
                                       float* scale, hipStream_t st);
 hipError_t launch_ragged_gemm_fp8(int out, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
 size_t ragged_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
+// The norms around a block (norm.hip).
+int64_t norm_max_hidden();
+size_t norm_bwd_workspace_bytes(int64_t T, int64_t H);
+hipError_t launch_residual_norm(const void* x, bool x_f32, const void* f, bool f16, int64_t T, int64_t H,
+                                float scale, const float* gate, const void* post, const void* pre, bool w_f32,
+                                float eps, void* r, void* y, hipStream_t st);
+hipError_t launch_residual_norm_bwd(const void* dy, const void* dr, const void* r, bool x_f32, const void* f,
+                                    bool f16, int64_t T, int64_t H, float scale, const float* gate,
+                                    const void* post, const void* pre, bool w_f32, float eps, void* dx, void* df,
+                                    float* dgate, float* dpost, float* dpre, void* ws, hipStream_t st);
 // Routing (routing.hip); type: 0 fp32, 1 bf16, 2 fp16.
 size_t route_workspace_bytes(int64_t T, int32_t E);
 hipError_t launch_route(const void* logits, int type, int64_t T, int32_t E, int32_t k, bool renorm,

@@ -1,0 +1,418 @@
+// What follows a block: its output normalized, gated and added to the scaled residual, and the sum
+// normalized for the next block; and the gradients of that.
+//
+//   n(v) = v / sqrt(mean(v^2) + eps) over a row
+//   b = n(f) post (or f),  r = residual_scale x + gate b,  y = n(r) pre     r as it is stored
+//
+//   total = dr + d n(r) for (dy pre),  d n(v) for u: rs u - rs^3 mean(u v) v,  rs = 1 / sqrt(mean(v^2) + eps)
+//   dx = residual_scale total,  db = gate total,  df = d n(f) for (db post) (or db),  dgate = <total, b>
+//   dpre = sum over rows of dy n(r),  dpost = sum over rows of db n(f)
+//
+// Bound by memory: every tensor passes once.  A row lies in the registers of a wave, of 4, 8 or 16
+// waves (8 values a lane and chunk), so the second norm and the gradients need no second read.  The
+// statistics are fp32.  Column sums stay in registers over the rows that a workgroup takes, one after
+// the other, and are joined by a second launch in a fixed order.
+#include <algorithm>
+
+#include "ragged_common.h"
+
+namespace mx {
+
+struct NormArgs {
+  const void *x, *f;            // forward; backward: x is r
+  const void *dy, *dr;          // backward
+  const float* gate;
+  const void *post, *pre;
+  bool w_f32;                   // type of the weights: fp32, else that of f
+  float scale, eps;
+  int64_t T;
+  int32_t H;
+  void *r, *y;                  // forward
+  void *dx, *df;                // backward
+  float* dgate;
+  float *dpre, *dpost;          // partial sums [slots, H], or NULL
+};
+
+// 8 values of a row as they lie in memory; the type is an output type.
+template <typename X>
+struct Eight {
+  static constexpr int kRegs = sizeof(typename X::elem) / 2;
+  u32x4_t v[kRegs];
+  // n: values that the row has from here on (zeros behind)
+  __device__ __forceinline__ void load(const void* base, int64_t at, int n) {
+    const uint8_t* p = (const uint8_t*)base + at * (int64_t)sizeof(typename X::elem);
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i)
+      v[i] = chunk_end<typename X::elem>(p + 16 * i, (int64_t)n * (int64_t)sizeof(typename X::elem) - 16 * i);
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at, int n) const {
+    uint8_t* p = (uint8_t*)base + at * (int64_t)sizeof(typename X::elem);
+    if (n >= 8) {
+      __builtin_memcpy(p, v, sizeof(v));
+    } else {
+      typename X::elem e[8];
+      __builtin_memcpy(e, v, sizeof(v));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) ((typename X::elem*)p)[i] = e[i];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (std::is_same<X, OutF32>::value) return __uint_as_float(v[i / 4][i % 4]);
+    else if constexpr (std::is_same<X, OutF16>::value) return widen<TypeF16>((uint16_t)(v[0][i / 2] >> (16 * (i & 1))));
+    else return widen<TypeBf16>((uint16_t)(v[0][i / 2] >> (16 * (i & 1))));
+  }
+  __device__ __forceinline__ void set(const float (&e)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (std::is_same<X, OutF32>::value) v[i / 4][i % 4] = __float_as_uint(e[i]);
+      else if (i % 2 == 0) v[0][i / 2] = (uint32_t)X::cvt(e[i]) | ((uint32_t)X::cvt(e[i + 1]) << 16);
+    }
+  }
+};
+
+// 8 weights; 1 where there are none.
+template <typename F>
+__device__ __forceinline__ void weights8(const void* w, bool f32, int at, int n, float (&out)[8]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = 1.f;
+  } else if (f32) {
+    Eight<OutF32> e;
+    e.load(w, at, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = e.get(i);
+  } else {
+    Eight<F> e;
+    e.load(w, at, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = e.get(i);
+  }
+}
+
+// Sums over the W threads of a row, in all of them, in a fixed order.  `side` alternates from call
+// to call, so that one barrier does: between two uses of a side lies the other's barrier.
+template <int W, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[N], int& side) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v[i] += __shfl_xor(v[i], d, 64);
+  if constexpr (W > 64) {
+    constexpr int kWaves = W / 64;
+    float(*at)[N] = lds + side * kWaves;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[threadIdx.x >> 6][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = at[0][i];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v[i] += at[w][i];
+    }
+    side ^= 1;
+  }
+}
+
+// W threads a row, NC chunks of 8 values a thread; workgroups of max(W, 256) threads.
+template <typename F, typename X, int W, int NC>
+__global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_kernel(NormArgs p) {
+  constexpr int kPer = W < 256 ? 256 / W : 1;
+  __shared__ float lds[2 * (W / 64)][1];
+  const int t = threadIdx.x % W;
+  int side = 0;
+  const float each = 1.f / (float)p.H;
+  for (int64_t row = (int64_t)blockIdx.x * kPer + threadIdx.x / W; row < p.T; row += (int64_t)gridDim.x * kPer) {
+    Eight<X> x[NC];
+    Eight<F> f[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * W + t) * 8, n = p.H - at;
+      x[c].load(p.x, row * p.H + at, n);
+      if (p.f != nullptr) f[c].load(p.f, row * p.H + at, n);
+    }
+    if (p.f != nullptr) {
+      float rs = p.gate != nullptr ? p.gate[row] : 1.f;
+      if (p.post != nullptr) {
+        float sum[1] = {0.f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(f[c].get(i), f[c].get(i), sum[0]);
+        row_sums<W>(sum, lds, side);
+        rs *= __builtin_amdgcn_rsqf(sum[0] * each + p.eps);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int at = (c * W + t) * 8, n = p.H - at;
+        float w[8], e[8];
+        weights8<F>(p.post, p.w_f32, at, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(p.scale, x[c].get(i), f[c].get(i) * w[i] * rs);
+        x[c].set(e);
+        x[c].store(p.r, row * p.H + at, n);
+      }
+    }
+    if (p.pre != nullptr) {
+      float sum[1] = {0.f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(x[c].get(i), x[c].get(i), sum[0]);
+      row_sums<W>(sum, lds, side);
+      const float rs = __builtin_amdgcn_rsqf(sum[0] * each + p.eps);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int at = (c * W + t) * 8, n = p.H - at;
+        float w[8], e[8];
+        weights8<F>(p.pre, p.w_f32, at, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = x[c].get(i) * rs * w[i];
+        Eight<F> y;
+        y.set(e);
+        y.store(p.y, row * p.H + at, n);
+      }
+    }
+  }
+}
+
+template <typename F, typename X, int W, int NC>
+__global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(NormArgs p) {
+  constexpr int kPer = W < 256 ? 256 / W : 1;
+  __shared__ float lds3[2 * (W / 64)][3], lds1[2 * (W / 64)][1];
+  const int t = threadIdx.x % W;
+  const int64_t slot = (int64_t)blockIdx.x * kPer + threadIdx.x / W;
+  int side3 = 0, side1 = 0;
+  const float each = 1.f / (float)p.H;
+  float dpre[NC][8] = {}, dpost[NC][8] = {};
+  for (int64_t row = slot; row < p.T; row += (int64_t)gridDim.x * kPer) {
+    Eight<X> r[NC], dr[NC];
+    Eight<F> f[NC], dy[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * W + t) * 8, n = p.H - at;
+      if (p.dr != nullptr) dr[c].load(p.dr, row * p.H + at, n);
+      if (p.dy != nullptr) {
+        r[c].load(p.x, row * p.H + at, n);
+        dy[c].load(p.dy, row * p.H + at, n);
+      }
+      if (p.f != nullptr) f[c].load(p.f, row * p.H + at, n);
+    }
+    const float gate = p.gate != nullptr ? p.gate[row] : 1.f;
+    // r^2, dy pre r, f^2
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (p.dy != nullptr) {
+        float w[8];
+        weights8<F>(p.pre, p.w_f32, (c * W + t) * 8, p.H - (c * W + t) * 8, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[0] = __builtin_fmaf(r[c].get(i), r[c].get(i), sum[0]);
+          sum[1] = __builtin_fmaf(dy[c].get(i) * w[i], r[c].get(i), sum[1]);
+        }
+      }
+      if (p.post != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[2] = __builtin_fmaf(f[c].get(i), f[c].get(i), sum[2]);
+      }
+    }
+    row_sums<W>(sum, lds3, side3);
+    const float rs = __builtin_amdgcn_rsqf(sum[0] * each + p.eps);
+    const float pull = rs * rs * rs * (sum[1] * each);
+    const float rf = p.post != nullptr ? __builtin_amdgcn_rsqf(sum[2] * each + p.eps) : 1.f;
+    // total, in the place of r's registers as fp32
+    float total[NC][8];
+    float dot[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * W + t) * 8, n = p.H - at;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) total[c][i] = p.dr != nullptr ? dr[c].get(i) : 0.f;
+      if (p.dy != nullptr) {
+        float w[8];
+        weights8<F>(p.pre, p.w_f32, at, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          total[c][i] += dy[c].get(i) * w[i] * rs - pull * r[c].get(i);
+          dpre[c][i] = __builtin_fmaf(dy[c].get(i), r[c].get(i) * rs, dpre[c][i]);
+        }
+      }
+      if (p.dx != nullptr) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = p.scale * total[c][i];
+        Eight<X> o;
+        o.set(e);
+        o.store(p.dx, row * p.H + at, n);
+      }
+      if (p.post != nullptr || p.dgate != nullptr) {
+        float w[8];
+        weights8<F>(p.post, p.w_f32, at, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot[0] = __builtin_fmaf(total[c][i] * w[i], f[c].get(i), dot[0]);
+      }
+    }
+    if (p.f == nullptr) continue;
+    if (p.post != nullptr || p.dgate != nullptr) row_sums<W>(dot, lds1, side1);
+    if (p.dgate != nullptr && t == 0) p.dgate[row] = rf * dot[0];
+    const float back = p.post != nullptr ? rf * rf * rf * (gate * dot[0] * each) : 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * W + t) * 8, n = p.H - at;
+      float w[8], e[8];
+      weights8<F>(p.post, p.w_f32, at, n, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float db = gate * total[c][i];
+        dpost[c][i] = __builtin_fmaf(db, f[c].get(i) * rf, dpost[c][i]);
+        e[i] = db * w[i] * rf - back * f[c].get(i);
+      }
+      if (p.df != nullptr) {
+        Eight<F> o;
+        o.set(e);
+        o.store(p.df, row * p.H + at, n);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int at = (c * W + t) * 8, n = p.H - at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= n) continue;
+      if (p.dpre != nullptr) p.dpre[slot * p.H + at + i] = dpre[c][i];
+      if (p.dpost != nullptr) p.dpost[slot * p.H + at + i] = dpost[c][i];
+    }
+  }
+}
+
+// Sums of the slots' rows: 64 columns a workgroup, 16 waves take every 16th slot.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* pre, const float* post, int32_t slots,
+                                                            int32_t H, float* dpre, float* dpost) {
+  __shared__ float part[16][64];
+  const float* in = blockIdx.y == 0 ? pre : post;
+  float* out = blockIdx.y == 0 ? dpre : dpost;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float sum = 0.f;
+  if (out != nullptr && col < H)
+    for (int s = wave; s < slots; s += 16) sum += in[(int64_t)s * H + col];
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (wave != 0 || out == nullptr || col >= H) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) sum += part[w][lane];
+  out[col] = sum;
+}
+
+namespace {
+
+constexpr int kNormMaxH = 16384;
+
+// Threads of a row and chunks of a thread.
+template <typename G>
+hipError_t with_shape(int64_t H, G launch) {
+  using std::integral_constant;
+#define MX_SHAPE(w, c) return launch(integral_constant<int, w>{}, integral_constant<int, c>{})
+  if (H <= 512) MX_SHAPE(64, 1);
+  if (H <= 1024) MX_SHAPE(64, 2);
+  if (H <= 2048) MX_SHAPE(256, 1);
+  if (H <= 4096) MX_SHAPE(256, 2);
+  if (H <= 8192) MX_SHAPE(512, 2);
+  MX_SHAPE(1024, 2);
+#undef MX_SHAPE
+}
+
+int rows_at_once(int64_t H) { return H <= 1024 ? 4 : 1; }   // of a workgroup
+
+// Workgroups of the backward launch, each with a row of partial sums for each row at once.
+int64_t bwd_blocks(int64_t T, int64_t H) {
+  const int64_t per = rows_at_once(H), most = H <= 4096 ? 512 : 256;
+  return std::min((T + per - 1) / per, most);
+}
+
+template <typename G>
+hipError_t with_types(bool f16, bool x_f32, G go) {
+  if (f16) return x_f32 ? go(OutF16{}, OutF32{}) : go(OutF16{}, OutF16{});
+  return x_f32 ? go(OutBf16{}, OutF32{}) : go(OutBf16{}, OutBf16{});
+}
+
+}  // namespace
+
+int64_t norm_max_hidden() { return kNormMaxH; }
+
+size_t norm_bwd_workspace_bytes(int64_t T, int64_t H) {
+  return (size_t)bwd_blocks(T, H) * rows_at_once(H) * H * 2 * sizeof(float);
+}
+
+hipError_t launch_residual_norm(const void* x, bool x_f32, const void* f, bool f16, int64_t T, int64_t H,
+                                float scale, const float* gate, const void* post, const void* pre, bool w_f32,
+                                float eps, void* r, void* y, hipStream_t st) {
+  NormArgs p{};
+  p.x = x;
+  p.f = f;
+  p.T = T;
+  p.H = (int32_t)H;
+  p.scale = scale;
+  p.gate = gate;
+  p.post = post;
+  p.pre = pre;
+  p.w_f32 = w_f32;
+  p.eps = eps;
+  p.r = r;
+  p.y = y;
+  const int64_t per = rows_at_once(H), blocks = std::min<int64_t>((T + per - 1) / per, 1 << 20);
+  return with_types(f16, x_f32, [&](auto F, auto X) {
+    return with_shape(H, [&](auto W, auto C) {
+      constexpr int w = decltype(W)::value;
+      residual_norm_kernel<decltype(F), decltype(X), w, decltype(C)::value>
+          <<<dim3((uint32_t)blocks), dim3(w < 256 ? 256 : w), 0, st>>>(p);
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_residual_norm_bwd(const void* dy, const void* dr, const void* r, bool x_f32, const void* f,
+                                    bool f16, int64_t T, int64_t H, float scale, const float* gate,
+                                    const void* post, const void* pre, bool w_f32, float eps, void* dx, void* df,
+                                    float* dgate, float* dpost, float* dpre, void* ws, hipStream_t st) {
+  NormArgs p{};
+  p.x = r;
+  p.f = f;
+  p.dy = dy;
+  p.dr = dr;
+  p.T = T;
+  p.H = (int32_t)H;
+  p.scale = scale;
+  p.gate = gate;
+  p.post = post;
+  p.pre = pre;
+  p.w_f32 = w_f32;
+  p.eps = eps;
+  p.dx = dx;
+  p.df = df;
+  p.dgate = dgate;
+  const int64_t blocks = bwd_blocks(T, H), slots = blocks * rows_at_once(H);
+  if (dpre != nullptr) p.dpre = (float*)ws;
+  if (dpost != nullptr) p.dpost = (float*)ws + slots * H;
+  if (T > 0) {
+    const hipError_t e = with_types(f16, x_f32, [&](auto F, auto X) {
+      return with_shape(H, [&](auto W, auto C) {
+        constexpr int w = decltype(W)::value;
+        residual_norm_bwd_kernel<decltype(F), decltype(X), w, decltype(C)::value>
+            <<<dim3((uint32_t)blocks), dim3(w < 256 ? 256 : w), 0, st>>>(p);
+        return hipGetLastError();
+      });
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (dpre == nullptr && dpost == nullptr) return hipSuccess;
+  norm_columns_kernel<<<dim3((uint32_t)((H + 63) / 64), 2), dim3(1024), 0, st>>>(p.dpre, p.dpost, (int32_t)slots,
+                                                                               (int32_t)H, dpre, dpost);
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -209,9 +209,33 @@ __device__ __forceinline__ int64_t part_stages(int layout, const RaggedArgs& p, 
   return (con * esize + kStageK - 1) / kStageK;
 }
 
+// 4 consecutive columns of each of two blocks of 16 (words 0, 1 and 2, 3), in rows l % 16, to 8
+// consecutive columns a lane, and back: its own inverse.
+__device__ __forceinline__ u32x4_t swap_blocks(u32x4_t v) {
+  const auto s0 = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false);
+  const auto s1 = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
+  return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+}
+// Two such runs of 16 rows by 32 columns (a: columns 0.., b: columns 32..) to two of 8 rows by 64, and
+// back: whole 128-byte lines.  Lanes of rows 8.. trade their a for the b of the row 8 above.
+__device__ __forceinline__ void whole_lines(u32x4_t& a, u32x4_t& b) {
+  const bool low = (threadIdx.x & 8) == 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t give = low ? b[k] : a[k];
+    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);   // row_ror:8
+    a[k] = low ? a[k] : got;
+    b[k] = low ? got : b[k];
+  }
+}
+// Row (of 16) and column (of 64) where lane ln's 8 columns of a, after that, belong; b: 8 rows on.
+__device__ __forceinline__ int line_row(int ln) { return ln & 7; }
+__device__ __forceinline__ int line_col(int ln) {
+  return 32 * ((ln >> 3) & 1) + 16 * ((ln >> 4) & 1) + 8 * (ln >> 5);
+}
+
 // A wave's 32 FA rows by 64 gate columns (accumulators 0..3 of a row block) and their up
-// columns (4..7): the activation and, KEEP, both projections.  8 consecutive columns a lane as
-// in the plain stores below.
+// columns (4..7): the activation and, KEEP, both projections, in whole lines.
 template <typename O, int FA, bool KEEP, typename Acc>
 __device__ __forceinline__ void store_gated(const RaggedArgs& p, Acc (&acc)[2 * FA][8], int32_t m0, int32_t n0,
                                             int32_t rows, int wm, int wn, int ln) {
@@ -221,39 +245,39 @@ __device__ __forceinline__ void store_gated(const RaggedArgs& p, Acc (&acc)[2 * 
   const auto out = make_rsrc((uint16_t*)p.c + (int64_t)m0 * p.ldc + n0, (int64_t)(rows - 1) * ec + (F - n0) * 2);
   const auto gate = make_rsrc((uint16_t*)p.h + (int64_t)m0 * 2 * F + n0, (int64_t)(rows - 1) * eh + (F - n0) * 2);
   const auto up = make_rsrc((uint16_t*)p.h + (int64_t)m0 * 2 * F + F + n0, (int64_t)(rows - 1) * eh + (F - n0) * 2);
+  const int n = wn * 64 + line_col(ln);
 #pragma unroll
   for (int i = 0; i < 2 * FA; ++i) {
-    const int m = wm * 32 * FA + 16 * i + (ln & 15);
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]), "+a"(acc[i][j + 4]), "+a"(acc[i][j + 5]));
-      const int n = wn * 64 + 16 * (j + ((ln >> 4) & 1)) + 8 * (ln >> 5);
-      const bool in = (n < right) & (m < rows);
-      auto pack = [&](auto value) {
-        uint32_t w[4];
+    for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+    const int m = wm * 32 * FA + 16 * i + line_row(ln);
+    const bool in0 = (n < right) & (m < rows), in1 = (n < right) & (m + 8 < rows);
+    auto put = [&](__amdgpu_buffer_rsrc_t to, uint32_t pitch, auto value) {
+      u32x4_t w[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          w[k] = (uint32_t)O::cvt(value(j + (k >> 1), 2 * (k & 1))) |
-                 ((uint32_t)O::cvt(value(j + (k >> 1), 2 * (k & 1) + 1)) << 16);
-        const auto s0 = __builtin_amdgcn_permlane16_swap(w[0], w[2], false, false);
-        const auto s1 = __builtin_amdgcn_permlane16_swap(w[1], w[3], false, false);
-        return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
-      };
-      __builtin_amdgcn_raw_buffer_store_b128(
-          pack([&](int b, int e) { return gated(acc[i][b][e], acc[i][b + 4][e]); }), out,
-          in ? (uint32_t)m * ec + (uint32_t)n * 2u : kOut, 0, 0);
-      if constexpr (KEEP) {
-        const uint32_t at = in ? (uint32_t)m * eh + (uint32_t)n * 2u : kOut;
-        __builtin_amdgcn_raw_buffer_store_b128(pack([&](int b, int e) { return acc[i][b][e]; }), gate, at, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(pack([&](int b, int e) { return acc[i][b + 4][e]; }), up, at, 0, 0);
+          w[b][k] = (uint32_t)O::cvt(value(2 * b + (k >> 1), 2 * (k & 1))) |
+                    ((uint32_t)O::cvt(value(2 * b + (k >> 1), 2 * (k & 1) + 1)) << 16);
+        w[b] = swap_blocks(w[b]);
       }
+      whole_lines(w[0], w[1]);
+      const uint32_t at = (uint32_t)m * pitch + (uint32_t)n * 2u;
+      __builtin_amdgcn_raw_buffer_store_b128(w[0], to, in0 ? at : kOut, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(w[1], to, in1 ? at + 8 * pitch : kOut, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+    };
+    put(out, ec, [&](int b, int e) { return gated(acc[i][b][e], acc[i][b + 4][e]); });
+    if constexpr (KEEP) {
+      put(gate, eh, [&](int b, int e) { return acc[i][b][e]; });
+      put(up, eh, [&](int b, int e) { return acc[i][b + 4][e]; });
     }
   }
 }
 
 // A wave's 32 FA rows by 128 columns of da: both projections are read (16 rows ahead of their
-// use), their gradients and the activation written.
+// use), their gradients and the activation written, in whole lines.
 template <typename T, typename O, int FA, typename Acc>
 __device__ __forceinline__ void store_gated_bwd(const RaggedArgs& p, Acc (&acc)[2 * FA][8], int32_t m0,
                                                 int32_t n0, int32_t rows, int wm, int wn, int ln) {
@@ -265,23 +289,20 @@ __device__ __forceinline__ void store_gated_bwd(const RaggedArgs& p, Acc (&acc)[
   const auto dg = make_rsrc((uint16_t*)p.c + at0, room), du = make_rsrc((uint16_t*)p.c + at0 + F, room);
   const auto act = make_rsrc((uint16_t*)p.act + (int64_t)m0 * F + n0,
                              p.act == nullptr ? 0 : (int64_t)(rows - 1) * ea + (F - n0) * 2);
-  auto col = [&](int j) { return wn * 128 + 16 * (j + ((ln >> 4) & 1)) + 8 * (ln >> 5); };
-  auto row = [&](int i) { return wm * 32 * FA + 16 * i + (ln & 15); };
+  // columns 64 c + .., rows 16 i + 8 b + ..
+  auto col = [&](int c) { return wn * 128 + 64 * c + line_col(ln); };
+  auto row = [&](int i, int b) { return wm * 32 * FA + 16 * i + 8 * b + line_row(ln); };
+  auto place = [&](int i, int b, int c, uint32_t pitch) {
+    return ((col(c) < right) & (row(i, b) < rows)) ? (uint32_t)row(i, b) * pitch + (uint32_t)col(c) * 2u : kOut;
+  };
   u32x4_t g[2][4], u[2][4];
   auto load = [&](int i) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t at = ((col(2 * q) < right) & (row(i) < rows))
-                              ? (uint32_t)row(i) * eh + (uint32_t)col(2 * q) * 2u : kOut;
+      const uint32_t at = place(i, q & 1, q >> 1, eh);
       g[i & 1][q] = __builtin_amdgcn_raw_buffer_load_b128(hg, at, 0, 0);
       u[i & 1][q] = __builtin_amdgcn_raw_buffer_load_b128(hu, at, 0, 0);
     }
-  };
-  // 8 consecutive columns a lane, and back to 4 of each of two blocks: the exchange is its own inverse
-  auto swap = [](u32x4_t v) {
-    const auto s0 = __builtin_amdgcn_permlane16_swap(v[0], v[2], false, false);
-    const auto s1 = __builtin_amdgcn_permlane16_swap(v[1], v[3], false, false);
-    return u32x4_t{(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
   };
   load(0);
 #pragma unroll
@@ -289,28 +310,42 @@ __device__ __forceinline__ void store_gated_bwd(const RaggedArgs& p, Acc (&acc)[
     if (i + 1 < 2 * FA) load(i + 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int j = 2 * q;
-      asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
-      const u32x4_t vg = swap(g[i & 1][q]), vu = swap(u[i & 1][q]);
-      u32x4_t og, ou, oa;
+    for (int c = 0; c < 2; ++c) {
+      u32x4_t vg[2] = {g[i & 1][2 * c], g[i & 1][2 * c + 1]}, vu[2] = {u[i & 1][2 * c], u[i & 1][2 * c + 1]};
+      whole_lines(vg[0], vg[1]);
+      whole_lines(vu[0], vu[1]);
+      u32x4_t og[2], ou[2], oa[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        GatedGrad r[2];
+      for (int b = 0; b < 2; ++b) {
+        const int j = 4 * c + 2 * b;
+        asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+        vg[b] = swap_blocks(vg[b]);
+        vu[b] = swap_blocks(vu[b]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          r[e] = gated_grad(acc[i][j + (k >> 1)][2 * (k & 1) + e], widen<T>((uint16_t)(vg[k] >> (16 * e))),
-                            widen<T>((uint16_t)(vu[k] >> (16 * e))));
-        og[k] = (uint32_t)O::cvt(r[0].gate) | ((uint32_t)O::cvt(r[1].gate) << 16);
-        ou[k] = (uint32_t)O::cvt(r[0].up) | ((uint32_t)O::cvt(r[1].up) << 16);
-        oa[k] = (uint32_t)O::cvt(r[0].act) | ((uint32_t)O::cvt(r[1].act) << 16);
+        for (int k = 0; k < 4; ++k) {
+          GatedGrad r[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            r[e] = gated_grad(acc[i][j + (k >> 1)][2 * (k & 1) + e], widen<T>((uint16_t)(vg[b][k] >> (16 * e))),
+                              widen<T>((uint16_t)(vu[b][k] >> (16 * e))));
+          og[b][k] = (uint32_t)O::cvt(r[0].gate) | ((uint32_t)O::cvt(r[1].gate) << 16);
+          ou[b][k] = (uint32_t)O::cvt(r[0].up) | ((uint32_t)O::cvt(r[1].up) << 16);
+          oa[b][k] = (uint32_t)O::cvt(r[0].act) | ((uint32_t)O::cvt(r[1].act) << 16);
+        }
+        og[b] = swap_blocks(og[b]);
+        ou[b] = swap_blocks(ou[b]);
+        oa[b] = swap_blocks(oa[b]);
       }
-      const bool in = (col(j) < right) & (row(i) < rows);
-      const uint32_t at = in ? (uint32_t)row(i) * eh + (uint32_t)col(j) * 2u : kOut;
-      __builtin_amdgcn_raw_buffer_store_b128(swap(og), dg, at, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(swap(ou), du, at, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(swap(oa), act,
-                                             in ? (uint32_t)row(i) * ea + (uint32_t)col(j) * 2u : kOut, 0, 0);
+      whole_lines(og[0], og[1]);
+      whole_lines(ou[0], ou[1]);
+      whole_lines(oa[0], oa[1]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t at = place(i, b, c, eh);
+        __builtin_amdgcn_raw_buffer_store_b128(og[b], dg, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(ou[b], du, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(oa[b], act, place(i, b, c, ea), 0, 0);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   }

@@ -178,69 +178,134 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_kernel(NormAr
   }
 }
 
-template <typename F, typename X, int W, int NC>
+// ALL: every input and output but the gate's is there, as in a training step; then the next row is
+// read while one is worked on, and rows of up to 512 threads keep the weights in registers.  Rows of
+// 1024 threads keep their column sums in LDS, for want of registers.
+template <typename F, typename X, int W, int NC, bool ALL>
 __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(NormArgs p) {
   constexpr int kPer = W < 256 ? 256 / W : 1;
+  constexpr bool kAhead = ALL && W <= 512;
   __shared__ float lds3[2 * (W / 64)][3], lds1[2 * (W / 64)][1];
   const int t = threadIdx.x % W;
-  const int64_t slot = (int64_t)blockIdx.x * kPer + threadIdx.x / W;
+  const int64_t slot = (int64_t)blockIdx.x * kPer + threadIdx.x / W, step = (int64_t)gridDim.x * kPer;
   int side3 = 0, side1 = 0;
   const float each = 1.f / (float)p.H;
-  float dpre[NC][8] = {}, dpost[NC][8] = {};
-  for (int64_t row = slot; row < p.T; row += (int64_t)gridDim.x * kPer) {
+  const bool has_dr = ALL || p.dr != nullptr, has_dy = ALL || p.dy != nullptr, has_f = ALL || p.f != nullptr;
+  const bool has_post = ALL || p.post != nullptr;
+  constexpr bool kLdsSums = W > 512;
+  __shared__ f32x4 lds_sums[kLdsSums ? 2 * NC * 2 * W : 1];
+  float kept_sums[2][kLdsSums ? 1 : NC][8];   // of dpre, dpost
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (kLdsSums) {
+        lds_sums[(2 * (2 * c + k)) * W + t] = f32x4{0, 0, 0, 0};
+        lds_sums[(2 * (2 * c + k) + 1) * W + t] = f32x4{0, 0, 0, 0};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kept_sums[k][c][i] = 0.f;
+      }
+    }
+  // sums k of chunk c: passed to fn and kept
+  auto sums = [&](int k, int c, auto fn) {
+    if constexpr (kLdsSums) {
+      float v[8];
+      f32x4* at = lds_sums + (2 * (2 * c + k)) * W + t;
+      const f32x4 lo = at[0], hi = at[W];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+      fn(v);
+      at[0] = f32x4{v[0], v[1], v[2], v[3]};
+      at[W] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      fn(kept_sums[k][c]);
+    }
+  };
+  struct Row {
     Eight<X> r[NC], dr[NC];
     Eight<F> f[NC], dy[NC];
+  };
+  auto load = [&](Row& v, int64_t row) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * W + t) * 8, n = p.H - at;
-      if (p.dr != nullptr) dr[c].load(p.dr, row * p.H + at, n);
-      if (p.dy != nullptr) {
-        r[c].load(p.x, row * p.H + at, n);
-        dy[c].load(p.dy, row * p.H + at, n);
+      if (has_dr) v.dr[c].load(p.dr, row * p.H + at, n);
+      if (has_dy) {
+        v.r[c].load(p.x, row * p.H + at, n);
+        v.dy[c].load(p.dy, row * p.H + at, n);
       }
-      if (p.f != nullptr) f[c].load(p.f, row * p.H + at, n);
+      if (has_f) v.f[c].load(p.f, row * p.H + at, n);
+    }
+  };
+  float kept_pre[kAhead ? NC : 1][8], kept_post[kAhead ? NC : 1][8];
+  Row ahead;
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = (c * W + t) * 8;
+      weights8<F>(p.pre, p.w_f32, at, p.H - at, kept_pre[c]);
+      weights8<F>(p.post, p.w_f32, at, p.H - at, kept_post[c]);
+    }
+    if (slot < p.T) load(ahead, slot);
+  }
+  auto weights = [&](const void* w, const float (&kept)[8], int at, float (&out)[8]) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = kept[i];
+    } else {
+      weights8<F>(w, p.w_f32, at, p.H - at, out);
+    }
+  };
+  for (int64_t row = slot; row < p.T; row += step) {
+    Row v;
+    if constexpr (kAhead) {
+      v = ahead;
+      if (row + step < p.T) load(ahead, row + step);
+    } else {
+      load(v, row);
     }
     const float gate = p.gate != nullptr ? p.gate[row] : 1.f;
     // r^2, dy pre r, f^2
     float sum[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (p.dy != nullptr) {
+      if (has_dy) {
         float w[8];
-        weights8<F>(p.pre, p.w_f32, (c * W + t) * 8, p.H - (c * W + t) * 8, w);
+        weights(p.pre, kept_pre[kAhead ? c : 0], (c * W + t) * 8, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          sum[0] = __builtin_fmaf(r[c].get(i), r[c].get(i), sum[0]);
-          sum[1] = __builtin_fmaf(dy[c].get(i) * w[i], r[c].get(i), sum[1]);
+          sum[0] = __builtin_fmaf(v.r[c].get(i), v.r[c].get(i), sum[0]);
+          sum[1] = __builtin_fmaf(v.dy[c].get(i) * w[i], v.r[c].get(i), sum[1]);
         }
       }
-      if (p.post != nullptr) {
+      if (has_post) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[2] = __builtin_fmaf(f[c].get(i), f[c].get(i), sum[2]);
+        for (int i = 0; i < 8; ++i) sum[2] = __builtin_fmaf(v.f[c].get(i), v.f[c].get(i), sum[2]);
       }
     }
     row_sums<W>(sum, lds3, side3);
     const float rs = __builtin_amdgcn_rsqf(sum[0] * each + p.eps);
     const float pull = rs * rs * rs * (sum[1] * each);
-    const float rf = p.post != nullptr ? __builtin_amdgcn_rsqf(sum[2] * each + p.eps) : 1.f;
-    // total, in the place of r's registers as fp32
+    const float rf = has_post ? __builtin_amdgcn_rsqf(sum[2] * each + p.eps) : 1.f;
     float total[NC][8];
     float dot[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * W + t) * 8, n = p.H - at;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) total[c][i] = p.dr != nullptr ? dr[c].get(i) : 0.f;
-      if (p.dy != nullptr) {
+      for (int i = 0; i < 8; ++i) total[c][i] = has_dr ? v.dr[c].get(i) : 0.f;
+      if (has_dy) {
         float w[8];
-        weights8<F>(p.pre, p.w_f32, at, n, w);
+        weights(p.pre, kept_pre[kAhead ? c : 0], at, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          total[c][i] += dy[c].get(i) * w[i] * rs - pull * r[c].get(i);
-          dpre[c][i] = __builtin_fmaf(dy[c].get(i), r[c].get(i) * rs, dpre[c][i]);
-        }
+        for (int i = 0; i < 8; ++i) total[c][i] += v.dy[c].get(i) * w[i] * rs - pull * v.r[c].get(i);
+        sums(0, c, [&](float (&d)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = __builtin_fmaf(v.dy[c].get(i), v.r[c].get(i) * rs, d[i]);
+        });
       }
-      if (p.dx != nullptr) {
+      if (ALL || p.dx != nullptr) {
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = p.scale * total[c][i];
@@ -248,29 +313,30 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
         o.set(e);
         o.store(p.dx, row * p.H + at, n);
       }
-      if (p.post != nullptr || p.dgate != nullptr) {
+      if (has_post || p.dgate != nullptr) {
         float w[8];
-        weights8<F>(p.post, p.w_f32, at, n, w);
+        weights(p.post, kept_post[kAhead ? c : 0], at, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot[0] = __builtin_fmaf(total[c][i] * w[i], f[c].get(i), dot[0]);
+        for (int i = 0; i < 8; ++i) dot[0] = __builtin_fmaf(total[c][i] * w[i], v.f[c].get(i), dot[0]);
       }
     }
-    if (p.f == nullptr) continue;
-    if (p.post != nullptr || p.dgate != nullptr) row_sums<W>(dot, lds1, side1);
+    if (!has_f) continue;
+    if (has_post || p.dgate != nullptr) row_sums<W>(dot, lds1, side1);
     if (p.dgate != nullptr && t == 0) p.dgate[row] = rf * dot[0];
-    const float back = p.post != nullptr ? rf * rf * rf * (gate * dot[0] * each) : 0.f;
+    const float back = has_post ? rf * rf * rf * (gate * dot[0] * each) : 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * W + t) * 8, n = p.H - at;
       float w[8], e[8];
-      weights8<F>(p.post, p.w_f32, at, n, w);
+      weights(p.post, kept_post[kAhead ? c : 0], at, w);
+      if (has_post)
+        sums(1, c, [&](float (&d)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float db = gate * total[c][i];
-        dpost[c][i] = __builtin_fmaf(db, f[c].get(i) * rf, dpost[c][i]);
-        e[i] = db * w[i] * rf - back * f[c].get(i);
-      }
-      if (p.df != nullptr) {
+          for (int i = 0; i < 8; ++i) d[i] = __builtin_fmaf(gate * total[c][i], v.f[c].get(i) * rf, d[i]);
+        });
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = gate * total[c][i] * w[i] * rf - back * v.f[c].get(i);
+      if (ALL || p.df != nullptr) {
         Eight<F> o;
         o.set(e);
         o.store(p.df, row * p.H + at, n);
@@ -281,10 +347,12 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
   for (int c = 0; c < NC; ++c) {
     const int at = (c * W + t) * 8, n = p.H - at;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= n) continue;
-      if (p.dpre != nullptr) p.dpre[slot * p.H + at + i] = dpre[c][i];
-      if (p.dpost != nullptr) p.dpost[slot * p.H + at + i] = dpost[c][i];
+    for (int k = 0; k < 2; ++k) {
+      float* to = k == 0 ? p.dpre : p.dpost;
+      if (to == nullptr || n <= 0) continue;
+      Eight<OutF32> o;
+      sums(k, c, [&](float (&d)[8]) { o.set(d); });
+      o.store(to, slot * p.H + at, n);
     }
   }
 }
@@ -298,8 +366,17 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* pre, co
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = blockIdx.x * 64 + lane;
   float sum = 0.f;
-  if (out != nullptr && col < H)
-    for (int s = wave; s < slots; s += 16) sum += in[(int64_t)s * H + col];
+  if (out != nullptr && col < H) {
+    int s = wave;
+    for (; s + 16 * 7 < slots; s += 16 * 8) {   // 8 loads in flight
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = in[(int64_t)(s + 16 * i) * H + col];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+    }
+    for (; s < slots; s += 16) sum += in[(int64_t)s * H + col];
+  }
   part[wave][lane] = sum;
   __syncthreads();
   if (wave != 0 || out == nullptr || col >= H) return;
@@ -330,7 +407,8 @@ int rows_at_once(int64_t H) { return H <= 1024 ? 4 : 1; }   // of a workgroup
 
 // Workgroups of the backward launch, each with a row of partial sums for each row at once.
 int64_t bwd_blocks(int64_t T, int64_t H) {
-  const int64_t per = rows_at_once(H), most = H <= 4096 ? 512 : 256;
+  // as many as the registers leave room for on 256 CUs
+  const int64_t per = rows_at_once(H), most = H <= 512 || (H > 1024 && H <= 2048) ? 768 : H <= 4096 ? 512 : 256;
   return std::min((T + per - 1) / per, most);
 }
 
@@ -399,11 +477,13 @@ hipError_t launch_residual_norm_bwd(const void* dy, const void* dr, const void* 
   if (dpre != nullptr) p.dpre = (float*)ws;
   if (dpost != nullptr) p.dpost = (float*)ws + slots * H;
   if (T > 0) {
+    const bool all = dy && dr && f && post && dx && df && dpre && dpost;
     const hipError_t e = with_types(f16, x_f32, [&](auto F, auto X) {
       return with_shape(H, [&](auto W, auto C) {
-        constexpr int w = decltype(W)::value;
-        residual_norm_bwd_kernel<decltype(F), decltype(X), w, decltype(C)::value>
-            <<<dim3((uint32_t)blocks), dim3(w < 256 ? 256 : w), 0, st>>>(p);
+        constexpr int w = decltype(W)::value, c = decltype(C)::value;
+        const dim3 grid((uint32_t)blocks), threads(w < 256 ? 256 : w);
+        if (all) residual_norm_bwd_kernel<decltype(F), decltype(X), w, c, true><<<grid, threads, 0, st>>>(p);
+        else residual_norm_bwd_kernel<decltype(F), decltype(X), w, c, false><<<grid, threads, 0, st>>>(p);
         return hipGetLastError();
       });
     });

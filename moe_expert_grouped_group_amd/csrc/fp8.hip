@@ -24,16 +24,18 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return v;
 }
 
-// Largest size of 8 values, as bits of their type without the sign: bits order like sizes,
-// infinities and NaN above all.
-__device__ __forceinline__ uint32_t max_bits(u32x4_t v, uint32_t m) {
+// Largest sizes of 8 values by halves of words, as bits of their type without the sign: bits order
+// like sizes, infinities and NaN above all.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 max_bits(u32x4_t v, u16x2 m) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu));
   return m;
 }
+__device__ __forceinline__ uint32_t larger(u16x2 m) { return m[0] > m[1] ? m[0] : m[1]; }
 
 struct BlockScale {
-  float scale, inverse;
+  float scale, low, high;   // the inverse, less and more 2^-21 of it
   bool zero;    // codes are 0 (no values, or no number among them)
   bool small;   // scales near the smallest numbers: every code by the exact way
 };
@@ -41,10 +43,19 @@ template <typename T>
 __device__ __forceinline__ BlockScale block_scale(uint32_t bits) {
   constexpr uint32_t kInf = std::is_same<T, TypeF16>::value ? 0x7C00u : 0x7F80u;
   BlockScale b;
-  b.scale = bits < kInf ? widen<T>((uint16_t)bits) / kE4m3Max : __builtin_nanf("");
+  const float top = widen<T>((uint16_t)bits);
   b.zero = bits == 0 || bits >= kInf;
-  b.small = b.scale < 0x1p-100f;
-  b.inverse = b.zero ? 0.f : __builtin_amdgcn_rcpf(b.scale);
+  b.small = top < 0x1p-90f;
+  // top / 448: the product with the inverse and one correction are correctly rounded, but not
+  // where numbers lose bits
+  constexpr float kInverse = 1.f / kE4m3Max;
+  const float near = top * kInverse;
+  b.scale = __builtin_fmaf(__builtin_fmaf(-near, kE4m3Max, top), kInverse, near);
+  if (b.small) b.scale = top / kE4m3Max;
+  if (b.zero) b.scale = bits == 0 ? 0.f : __builtin_nanf("");
+  const float inverse = __builtin_amdgcn_rcpf(b.scale);
+  b.low = inverse * (1.f - 0x1p-21f);
+  b.high = inverse * (1.f + 0x1p-21f);
   return b;
 }
 
@@ -52,7 +63,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t bits) {
 // even (a border between two codes is) and not exact, one step towards the exact one, so that
 // it lies on the exact quotient's side of every border.
 __device__ __forceinline__ float exact_quotient(float x, float scale) {
-  if (scale < 0x1p-100f) x *= 0x1p100f, scale *= 0x1p100f;   // the remainder below stays a number
+  if (scale < 0x1p-60f) x *= 0x1p100f, scale *= 0x1p100f;   // the remainder below keeps its bits
   const float v = x / scale;
   const float rest = __builtin_fmaf(-v, scale, x);
   uint32_t bits = __float_as_uint(v);
@@ -60,33 +71,37 @@ __device__ __forceinline__ float exact_quotient(float x, float scale) {
   return __uint_as_float(bits);
 }
 
-// 8 values to codes.  x * (1 / scale) is within 2 steps of fp32 of the quotient.  Codes of 2^-6
-// and more have 3 bits behind the leading one: where the other 20 are not within 4 steps of a
-// half, the product rounds as the quotient does.  The rest, and what is smaller, goes the exact
-// way (8 in 2^20 of the values, and those 28672 times smaller than their block's largest).
-template <typename T>
-__device__ __forceinline__ uint2 codes_of(u32x4_t v, const BlockScale& b) {
-  if (b.zero) return make_uint2(0u, 0u);
-  float x[8], y[8];
-  bool near = b.small;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = widen<T>((uint16_t)(v[i / 2] >> (16 * (i & 1))));
-    y[i] = x[i] * b.inverse;
-    const uint32_t bits = __float_as_uint(y[i]) & 0x7FFFFFFFu;
-    near |= (((bits + 4u - 0x80000u) & 0xFFFFFu) <= 8u) | (bits - 1u < 0x3C800000u - 1u);
-  }
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = exact_quotient(x[i], b.scale);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(y[i], -kE4m3Max, kE4m3Max);
+__device__ __forceinline__ uint2 convert(const float (&y)[8]) {
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
   int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
   return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// 8 values to codes.  The quotient lies between the products with the two inverses (the hardware's
+// is off by 2^-23 of it, each product by 2^-24): where both give the same code, it is the quotient's.
+// The rest goes the exact way, one wave in 20 on normal values.
+template <typename T>
+__device__ __forceinline__ uint2 codes_of(u32x4_t v, const BlockScale& b) {
+  float x[8], y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = widen<T>((uint16_t)(v[i / 2] >> (16 * (i & 1))));
+    y[i] = x[i] * b.low;
+  }
+  const uint2 one = convert(y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[i] * b.high;
+  uint2 codes = convert(y);
+  const bool differ = (one.x != codes.x) | (one.y != codes.y) | b.small;
+  if (differ & !b.zero) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] = __builtin_amdgcn_fmed3f(exact_quotient(x[i], b.scale), -kE4m3Max, kE4m3Max);
+    codes = convert(y);
+  }
+  return b.zero ? make_uint2(0u, 0u) : codes;
 }
 
 // 8 codes at any alignment, the first n of them.
@@ -100,37 +115,66 @@ __device__ __forceinline__ void store_codes(uint8_t* q, uint2 c, int64_t n) {
   }
 }
 
-// Tokens: 16 lanes a block, four blocks of a lane's in flight.
+// n / d for n below 2^31: (n + the high half of n magic) >> shift.
+struct Divide {
+  uint32_t magic, shift;
+  static Divide by(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return Divide{(uint32_t)(((((1ull << l) - d) << 32) / d) + 1), l};
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, magic) + n) >> shift; }
+};
+
+// 8 values of a row from `left` before its end; WHOLE: all or none.
+template <bool WHOLE>
+__device__ __forceinline__ u32x4_t load_values(const uint16_t* p, int64_t left) {
+  if constexpr (WHOLE) {
+    u32x4_t v = {0, 0, 0, 0};
+    if (left > 0) __builtin_memcpy(&v, p, 16);
+    return v;
+  } else {
+    return chunk_end<uint16_t>((const uint8_t*)p, left * 2);
+  }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store_values(uint8_t* q, uint2 c, int64_t left) {
+  if constexpr (!WHOLE) store_codes(q, c, left);
+  else if (left > 0) __builtin_memcpy(q, &c, 8);
+}
+
+// Tokens: 16 lanes a block, four blocks of a lane's in flight.  WHOLE: K is a multiple of 8.  LONG:
+// block numbers past 31 bits.
 constexpr int kFp8Unroll = 4;
-template <typename T, typename I>
-__global__ __launch_bounds__(256) void quantize_fp8_kernel(const uint16_t* x, int64_t ldx, int64_t K, I nb,
-                                                           I blocks, uint8_t* q, float* scale) {
+template <typename T, bool WHOLE, bool LONG>
+__global__ __launch_bounds__(256) void quantize_fp8_kernel(const uint16_t* x, int64_t ldx, int64_t K, int64_t nb,
+                                                           Divide by_nb, int64_t blocks, uint8_t* q, float* scale) {
   const int sub = threadIdx.x & 15;
-  const I step = (I)gridDim.x * 16;
-  for (I first = (I)blockIdx.x * 16 + (threadIdx.x >> 4); first < blocks;
-       first = blocks - first > step * kFp8Unroll ? first + step * kFp8Unroll : blocks) {
+  const int64_t step = (int64_t)gridDim.x * 16;
+  for (int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); first < blocks; first += step * kFp8Unroll) {
     u32x4_t v[kFp8Unroll];
     int64_t row[kFp8Unroll], at[kFp8Unroll];
 #pragma unroll
     for (int u = 0; u < kFp8Unroll; ++u) {
-      const I b = first + step * u;
-      const bool in = u == 0 || blocks - first > step * u;
-      row[u] = in ? (int64_t)(b / nb) : -1;
-      at[u] = in ? (int64_t)(b % nb) * 128 + sub * 8 : K;
-      v[u] = chunk_end<uint16_t>((const uint8_t*)(x + (in ? row[u] : 0) * ldx + at[u]), (K - at[u]) * 2);
+      const int64_t b = first + step * u;
+      if constexpr (LONG) row[u] = b / nb;
+      else row[u] = by_nb((uint32_t)b);
+      at[u] = b < blocks ? (b - row[u] * nb) * 128 + sub * 8 : K;
+      if (b >= blocks) row[u] = 0;
+      v[u] = load_values<WHOLE>(x + row[u] * ldx + at[u], K - at[u]);
     }
 #pragma unroll
     for (int u = 0; u < kFp8Unroll; ++u) {
-      if (row[u] < 0) break;   // the same for the 16 lanes of a block
-      const BlockScale b = block_scale<T>(row_max(max_bits(v[u], 0)));
-      store_codes(q + row[u] * K + at[u], codes_of<T>(v[u], b), K - at[u]);
-      if (sub == 0) scale[row[u] * (int64_t)nb + at[u] / 128] = b.scale;
+      if (first + step * u >= blocks) break;   // the same for the 16 lanes of a block
+      const BlockScale b = block_scale<T>(row_max(larger(max_bits(v[u], u16x2{0, 0}))));
+      store_values<WHOLE>(q + row[u] * K + at[u], codes_of<T>(v[u], b), K - at[u]);
+      if (sub == 0) scale[first + step * u] = b.scale;
     }
   }
 }
 
 // Weights: a workgroup a block, 16 rows at a time, the block in registers.
-template <typename T>
+template <typename T, bool WHOLE>
 __global__ __launch_bounds__(256) void quantize_fp8_weight_kernel(const uint16_t* w, int64_t N, int64_t K,
                                                                   uint32_t nb, uint32_t kb, uint8_t* q,
                                                                   float* scale, uint32_t first) {
@@ -140,15 +184,15 @@ __global__ __launch_bounds__(256) void quantize_fp8_weight_kernel(const uint16_t
   const int64_t k = (int64_t)k0 * 128 + (threadIdx.x & 15) * 8;
   const int64_t row0 = (int64_t)n0 * 128 + (threadIdx.x >> 4);
   u32x4_t v[8];
-  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t n = row0 + 16 * i;
-    v[i] = chunk_end<uint16_t>((const uint8_t*)(w + ((int64_t)g * N + n) * K + k), n < N ? (K - k) * 2 : 0);
+    v[i] = load_values<WHOLE>(w + ((int64_t)g * N + n) * K + k, n < N ? K - k : 0);
   }
+  u16x2 halves = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_bits(v[i], m);
-  m = row_max(m);
+  for (int i = 0; i < 8; ++i) halves = max_bits(v[i], halves);
+  uint32_t m = row_max(larger(halves));
   m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
   m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
   if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
@@ -157,7 +201,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_weight_kernel(const uint16_t
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t n = row0 + 16 * i;
-    if (n < N) store_codes(q + ((int64_t)g * N + n) * K + k, codes_of<T>(v[i], b), K - k);
+    if (n < N) store_values<WHOLE>(q + ((int64_t)g * N + n) * K + k, codes_of<T>(v[i], b), K - k);
   }
   if (threadIdx.x == 0) scale[((int64_t)g * nb + n0) * kb + k0] = b.scale;
 }
@@ -166,17 +210,21 @@ hipError_t launch_quantize_fp8(const void* x, bool f16, int64_t T, int64_t K, in
                                float* scale, hipStream_t st) {
   const int64_t nb = (K + 127) / 128, blocks = T * nb;
   const dim3 grid((uint32_t)std::min<int64_t>((blocks + 16 * kFp8Unroll - 1) / (16 * kFp8Unroll), 8192));
-  const uint16_t* in = (const uint16_t*)x;
-  // block numbers in 32 bits where they fit: the division by nb is three times shorter
-  if (blocks < (1ll << 31)) {
-    const uint32_t n = (uint32_t)nb, all = (uint32_t)blocks;
-    if (f16) quantize_fp8_kernel<TypeF16, uint32_t><<<grid, dim3(256), 0, st>>>(in, ldx, K, n, all, q, scale);
-    else quantize_fp8_kernel<TypeBf16, uint32_t><<<grid, dim3(256), 0, st>>>(in, ldx, K, n, all, q, scale);
+  const bool whole = K % 8 == 0, is_long = blocks + 4 * 16 * 8192ll * kFp8Unroll >= (1ll << 31);
+  const Divide by = is_long ? Divide{} : Divide::by((uint32_t)nb);
+#define MX_QUANTIZE(T, WHOLE, LONG) \
+  quantize_fp8_kernel<T, WHOLE, LONG><<<grid, dim3(256), 0, st>>>((const uint16_t*)x, ldx, K, nb, by, blocks, q, scale)
+  if (is_long) {
+    if (f16) MX_QUANTIZE(TypeF16, false, true);
+    else MX_QUANTIZE(TypeBf16, false, true);
+  } else if (whole) {
+    if (f16) MX_QUANTIZE(TypeF16, true, false);
+    else MX_QUANTIZE(TypeBf16, true, false);
   } else {
-    const uint64_t n = (uint64_t)nb, all = (uint64_t)blocks;
-    if (f16) quantize_fp8_kernel<TypeF16, uint64_t><<<grid, dim3(256), 0, st>>>(in, ldx, K, n, all, q, scale);
-    else quantize_fp8_kernel<TypeBf16, uint64_t><<<grid, dim3(256), 0, st>>>(in, ldx, K, n, all, q, scale);
+    if (f16) MX_QUANTIZE(TypeF16, false, false);
+    else MX_QUANTIZE(TypeBf16, false, false);
   }
+#undef MX_QUANTIZE
   return hipGetLastError();
 }
 
@@ -184,10 +232,12 @@ hipError_t launch_quantize_fp8_weight(const void* w, bool f16, int64_t G, int64_
                                       float* scale, hipStream_t st) {
   const uint32_t nb = (uint32_t)((N + 127) / 128), kb = (uint32_t)((K + 127) / 128);
   return launch_in_parts(G * nb * (int64_t)kb, 256, [&](uint32_t first, uint32_t n) {
-    if (f16)
-      quantize_fp8_weight_kernel<TypeF16><<<dim3(n), dim3(256), 0, st>>>((const uint16_t*)w, N, K, nb, kb, q, scale, first);
-    else
-      quantize_fp8_weight_kernel<TypeBf16><<<dim3(n), dim3(256), 0, st>>>((const uint16_t*)w, N, K, nb, kb, q, scale, first);
+    const uint16_t* in = (const uint16_t*)w;
+    const bool whole = K % 8 == 0;
+    if (f16 && whole) quantize_fp8_weight_kernel<TypeF16, true><<<dim3(n), dim3(256), 0, st>>>(in, N, K, nb, kb, q, scale, first);
+    else if (f16) quantize_fp8_weight_kernel<TypeF16, false><<<dim3(n), dim3(256), 0, st>>>(in, N, K, nb, kb, q, scale, first);
+    else if (whole) quantize_fp8_weight_kernel<TypeBf16, true><<<dim3(n), dim3(256), 0, st>>>(in, N, K, nb, kb, q, scale, first);
+    else quantize_fp8_weight_kernel<TypeBf16, false><<<dim3(n), dim3(256), 0, st>>>(in, N, K, nb, kb, q, scale, first);
   });
 }
 

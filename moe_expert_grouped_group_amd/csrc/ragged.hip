@@ -16,7 +16,8 @@ namespace mx {
 // ---------------------------------------------------------------------------
 // Any size, stride and alignment.
 //
-// 128 x 128 output tile, 4 waves of 64 x 64, contraction in steps of 64 bytes.
+// 128 x 128 output tile, 4 waves of 64 x 64, contraction in steps of 64 bytes (gated products: 128, which
+// halves the waits for memory; 1777 rows, 1034 x 1031 fp16: 51 us with steps of 64).
 // Chunks go through registers: a 16-byte load at element alignment where the
 // whole chunk lies inside the operand, single elements at its edge, zeros
 // outside.  Both operands lie in LDS with the contraction contiguous; an operand whose
@@ -25,8 +26,8 @@ namespace mx {
 // ---------------------------------------------------------------------------
 constexpr int kAnyT = 128;         // tile edge
 constexpr int kAnyBytes = 64;      // contraction bytes per step
-constexpr int kAnyPitch = 80;      // LDS row: 64 bytes + 16, so that 16-byte reads of
-                                   // consecutive rows start in different banks
+constexpr int kAnyPad = 16;        // an LDS row is that much longer than a step, so that 16-byte
+                                   // reads of consecutive rows start in different banks
 
 // Up to 16 bytes from p, the first n elements of them valid (n <= 0: none).
 template <typename E>
@@ -125,7 +126,11 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   constexpr bool kIsGated = EPI == kGated;
   constexpr int kCols = kIsGated ? kAnyT / 2 : kAnyT;
   constexpr int kPer = 16 / sizeof(E);             // elements of a chunk
-  constexpr int kStep = kAnyBytes / sizeof(E);     // contraction elements per step
+  constexpr int kBytes = EPI == kPlain ? kAnyBytes : 2 * kAnyBytes;
+  constexpr int kAnyPitch = kBytes + kAnyPad;
+  constexpr int kStep = kBytes / sizeof(E);        // contraction elements per step
+  constexpr int kRow = kBytes / 16;                // chunks of a row, contraction contiguous
+  constexpr int kParts = kAnyT * kRow / 256;       // chunks of a thread
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kAnyT * kAnyPitch];
   __shared__ int64_t scan[2 * 256 + 3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -152,19 +157,19 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
     expert_rows(p.m_splits, g, p.R, &lo, &con, scan);
   }
 
-  // this thread's chunks: two of each operand.  Contraction contiguous: row
-  // (tid >> 2) + 64 i, chunk tid & 3.  Contraction over rows: contraction
+  // this thread's chunks of each operand.  Contraction contiguous: row
+  // tid / kRow + 256 / kRow i, chunk tid % kRow.  Contraction over rows: contraction
   // row (tid >> 4) + 16 i, 8 columns from 8 (tid & 15).
   const E* a = (const E*)p.a;
   const E* b = (const E*)p.b;
   if (LAYOUT != 2) b += (int64_t)g * p.N * p.K;
-  u32x4_t ra[2], rb[2];
+  u32x4_t ra[kParts], rb[kParts];
   auto fetch = [&](int64_t k0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       if (LAYOUT != 2) {
-        const int r = (tid >> 2) + 64 * i;
-        const int64_t k = k0 + (tid & 3) * kPer;
+        const int r = tid / kRow + 256 / kRow * i;
+        const int64_t k = k0 + (tid % kRow) * kPer;
         int64_t n = r < rows ? con - k : 0;
         int64_t row = m0 + r;
         if (LAYOUT == 0 && p.row_index != nullptr) {
@@ -178,10 +183,10 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
         ra[i] = load_chunk<E>(a + (lo + k) * p.lda + m0 + c, k < con ? p.N - m0 - c : 0);
       }
       if (LAYOUT == 0) {
-        int64_t r = n0 + (tid >> 2) + 64 * i;
-        const int64_t k = k0 + (tid & 3) * kPer;
+        int64_t r = n0 + tid / kRow + 256 / kRow * i;
+        const int64_t k = k0 + (tid % kRow) * kPer;
         if constexpr (kIsGated) {
-          const int c = (tid >> 2) + 64 * i, f = 32 * (c >> 6) + (c & 31);
+          const int c = tid / kRow + 256 / kRow * i, f = 32 * (c >> 6) + (c & 31);
           r = n0 + f < cols ? n0 + f + ((c >> 5) & 1) * cols : p.N;
         }
         rb[i] = load_chunk<E>(b + r * p.K + k, r < p.N ? con - k : 0);
@@ -202,7 +207,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   uint8_t* lb = smem + kAnyT * kAnyPitch;
   auto put = [&](uint8_t* at, u32x4_t v, int i, bool over_rows) {
     if (!over_rows) {
-      *(u32x4_t*)(at + ((tid >> 2) + 64 * i) * kAnyPitch + (tid & 3) * 16) = v;
+      *(u32x4_t*)(at + (tid / kRow + 256 / kRow * i) * kAnyPitch + (tid % kRow) * 16) = v;
     } else {
       E e[kPer];
       __builtin_memcpy(e, &v, 16);
@@ -224,14 +229,14 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   if (con > 0) fetch(0);
   for (int64_t k0 = 0; k0 < con; k0 += kStep) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       put(la, ra[i], i, LAYOUT == 2);
       put(lb, rb[i], i, LAYOUT != 0);
     }
     __syncthreads();
     if (k0 + kStep < con) fetch(k0 + kStep);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kBytes / 32; ++s) {
       u32x4_t va[2], vb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -480,8 +485,6 @@ hipError_t with_tiles(int layout, int osize, RaggedArgs p, size_t ws_bytes, hipS
 }
 
 }  // namespace
-
-bool ragged_few_rows(const RaggedArgs& p, int esize) { return few_rows(p, esize); }
 
 // Workspace that a product of these sizes uses (0: none), operands contiguous.
 size_t ragged_workspace_bytes(int layout, int esize, int64_t R, int64_t S, int64_t N, int64_t K, int32_t G) {

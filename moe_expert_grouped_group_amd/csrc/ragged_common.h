@@ -81,7 +81,6 @@ hipError_t launch_ragged_tile_gated_f16(const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_gated_bwd(bool f16, const RaggedArgs& p, hipStream_t st);
 // 8-bit floating point (ragged_fp8.hip has the formula, ragged_fp8_tile.hip the large tiles).
 hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st);
-bool ragged_few_rows(const RaggedArgs& p, int esize);   // few_rows of ragged.hip
 size_t ragged_split_bytes();   // a partial 256 x 256 tile for each CU
 
 // Longest range of a bounded operand (32-bit offsets, less what marks a lane that
@@ -187,6 +186,18 @@ __device__ __forceinline__ u32x4_t chunk_end(const uint8_t* p, int64_t n) {
     __builtin_memcpy(&v, e, 16);
   }
   return v;
+}
+
+// 16 bytes at any address, from the dwords that hold them (each holds one of the bytes, so it may be
+// read): a load that is not on 4 bytes takes two to three times as long as one that is.
+__device__ __forceinline__ u32x4_t load16_odd(const uint8_t* p) {
+  const uint32_t off = (uint32_t)(uintptr_t)p & 3u;
+  const uint32_t* w = (const uint32_t*)(p - off);
+  u32x4_t v;
+  __builtin_memcpy(&v, __builtin_assume_aligned(w, 4), 16);
+  const uint32_t last = w[off != 0 ? 4 : 3];
+  return u32x4_t{__builtin_amdgcn_alignbyte(v[1], v[0], off), __builtin_amdgcn_alignbyte(v[2], v[1], off),
+                 __builtin_amdgcn_alignbyte(v[3], v[2], off), __builtin_amdgcn_alignbyte(last, v[3], off)};
 }
 
 // silu(g) = g sigmoid(g) with the hardware's exponential and reciprocal, 1 ulp each, ahead

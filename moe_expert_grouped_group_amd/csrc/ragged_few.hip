@@ -17,8 +17,8 @@
 namespace mx {
 
 // GATED: 16 gate columns and their 16 up columns, the activation of both (and the
-// projections, where p.h is given).
-template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false>
+// projections, where p.h is given).  ODD: rows that do not start on 4 bytes.
+template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false, bool ODD = false>
 __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, uint32_t first) {
   typedef typename T::elem E;
   typedef typename T::acc16 Acc;
@@ -69,9 +69,15 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
     for (int i = 0; i < 2 * U; ++i) {
       const int64_t at = run * (128 * U) + i * 64;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) __builtin_memcpy(&wv[i][b], w[b] + at, 16);
+      for (int b = 0; b < NB; ++b) {
+        if constexpr (ODD) wv[i][b] = load16_odd(w[b] + at);
+        else __builtin_memcpy(&wv[i][b], w[b] + at, 16);
+      }
 #pragma unroll
-      for (int m = 0; m < MR; ++m) __builtin_memcpy(&xv[i][m], x[m] + at, 16);
+      for (int m = 0; m < MR; ++m) {
+        if constexpr (ODD) xv[i][m] = load16_odd(x[m] + at);
+        else __builtin_memcpy(&xv[i][m], x[m] + at, 16);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2 * U; ++i)
@@ -162,12 +168,12 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_few_kernel(RaggedArgs p, ui
 
 namespace {
 
-template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false>
+template <typename T, typename O, int MR, int U, int WAVES, bool GATED = false, bool ODD = false>
 hipError_t launch_few(const RaggedArgs& p, hipStream_t st) {
   const int64_t rt = p.R / (16 * MR) + std::min<int64_t>(p.G, p.R);
   const int64_t blocks = rt * (((GATED ? p.N / 2 : p.N) + 15) / 16);
   return launch_in_parts(blocks, 64 * WAVES, [&](uint32_t first, uint32_t n) {
-    ragged_few_kernel<T, O, MR, U, WAVES, GATED><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
+    ragged_few_kernel<T, O, MR, U, WAVES, GATED, ODD><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
   });
 }
 
@@ -189,25 +195,31 @@ hipError_t launch_rows(const RaggedArgs& p, hipStream_t st) {
   return many ? launch_few<T, O, 4, 2, 4>(p, st) : launch_few<T, O, 4, 2, 8>(p, st);
 }
 
-// Gated: a workgroup has twice the loads in flight for a row of tokens.
-template <typename T, typename O>
+// Gated: twice the loads in flight for a row of tokens.  Measured (us, 2 to 8 lines by 4 or 8 waves):
+//   8 x 28672 x 4096, 16 rows    2 x 4: 285   4 x 4: 294   8 x 4: 295   2 x 8: 276   3 x 8: 278   4 x 8: 285
+//   64 x 2048 x 2048, 64 rows          99          108           98           118          109            96
+// Four runs and more for a wave, or all of its share at once, read fastest; two runs wait for each other.
+template <typename T, typename O, bool ODD>
 hipError_t launch_rows_gated(const RaggedArgs& p, hipStream_t st) {
   const int64_t groups = std::min<int64_t>(p.G, p.R);
   const int64_t mean = (p.R + groups - 1) / groups;
   const bool many = groups * ((p.N / 2 + 15) / 16) >= 1024;
-  const bool longk = p.K * (int64_t)sizeof(typename T::elem) >= 4 * 4 * 128;
+  const int64_t lines = p.K * (int64_t)sizeof(typename T::elem) / 128;
   if (mean <= 16) {
-    if (!many) return launch_few<T, O, 1, 2, 8, true>(p, st);
-    return longk ? launch_few<T, O, 1, 4, 4, true>(p, st) : launch_few<T, O, 1, 2, 4, true>(p, st);
+    if (!many || lines >= 4 * 2 * 8) return launch_few<T, O, 1, 2, 8, true, ODD>(p, st);
+    return lines >= 4 * 8 ? launch_few<T, O, 1, 4, 8, true, ODD>(p, st) : launch_few<T, O, 1, 2, 4, true, ODD>(p, st);
   }
-  if (mean <= 32) return many ? launch_few<T, O, 2, 2, 4, true>(p, st) : launch_few<T, O, 2, 2, 8, true>(p, st);
-  return many ? launch_few<T, O, 4, 1, 4, true>(p, st) : launch_few<T, O, 4, 1, 8, true>(p, st);
+  if (mean <= 32) return many ? launch_few<T, O, 2, 2, 4, true, ODD>(p, st) : launch_few<T, O, 2, 2, 8, true, ODD>(p, st);
+  return many ? launch_few<T, O, 4, 1, 4, true, ODD>(p, st) : launch_few<T, O, 4, 1, 8, true, ODD>(p, st);
 }
 
 }  // namespace
 
+// Rows off 4 bytes: 8 x 8192 x 4097, 16 rows, took 220 us with plain loads, where 4098 took 124.
 hipError_t launch_ragged_few_gated(bool f16, const RaggedArgs& p, hipStream_t st) {
-  return f16 ? launch_rows_gated<TypeF16, OutF16>(p, st) : launch_rows_gated<TypeBf16, OutBf16>(p, st);
+  const bool odd = (((uintptr_t)p.a | (uintptr_t)p.b) & 3) != 0 || p.K % 2 != 0 || p.lda % 2 != 0;
+  if (f16) return odd ? launch_rows_gated<TypeF16, OutF16, true>(p, st) : launch_rows_gated<TypeF16, OutF16, false>(p, st);
+  return odd ? launch_rows_gated<TypeBf16, OutBf16, true>(p, st) : launch_rows_gated<TypeBf16, OutBf16, false>(p, st);
 }
 
 hipError_t launch_ragged_few(bool f16, int out, const RaggedArgs& p, hipStream_t st) {

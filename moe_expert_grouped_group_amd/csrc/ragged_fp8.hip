@@ -33,16 +33,16 @@ __device__ __forceinline__ Wide widen_codes(u32x4_t c) {
 }
 
 // ---------------------------------------------------------------------------
-// Any size, stride and alignment: 128 x 128 output tile, 4 waves of 64 x 64, half a block (64 codes) of
-// the contraction at a time through registers to LDS, as ragged_any_kernel.
+// Any size, stride and alignment: 128 x 128 output tile, 4 waves of 64 x 64, a block of the contraction at
+// a time through registers to LDS, the next one's loads in flight meanwhile.
 // ---------------------------------------------------------------------------
 constexpr int kF8Tile = 128;
-constexpr int kF8Pitch = 80;   // LDS row: 64 codes + 16 bytes, so that consecutive rows start in other banks
+constexpr int kF8Pitch = 144;   // LDS row: 128 codes + 16 bytes, so that consecutive rows start in other banks
 
 template <typename O>
 __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, uint32_t first) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kF8Tile * kF8Pitch];
-  __shared__ float srow[2][kF8Tile];
+  __shared__ float srow[kF8Tile];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t nt = (p.N + kF8Tile - 1) / kF8Tile, kb = (p.K + 127) / 128;
   const int64_t at = first + blockIdx.x, ct = at % nt;
@@ -52,24 +52,24 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
   const int g = t.g, rows = t.rows;
   const int64_t m0 = t.row0;
 
-  // this thread's rows of both operands: (tid >> 2) + 64 i, 16 codes from 16 (tid & 3) on
-  const uint8_t *a[2], *b[2];
-  int64_t left_a[2], left_b[2];   // codes of the row, 0 for a row of zeros
+  // this thread's rows of both operands: (tid >> 3) + 32 i, 16 codes from 16 (tid & 7) on
+  const int64_t k0 = (tid & 7) * 16;
+  const uint8_t* a[4];
+  uint32_t there_a = 0, there_b = 0;   // bit i: row i is there; the others are rows of zeros
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (tid >> 2) + 64 * i;
-    int64_t row = m0 + r, n = n0 + r;
+  for (int i = 0; i < 4; ++i) {
+    const int r = (tid >> 3) + 32 * i;
+    int64_t row = m0 + r;
     bool ok = r < rows;
     if (p.row_index != nullptr && ok) {
       row = p.row_index[row];
       ok = row >= 0 && row < p.S;
     }
-    a[i] = (const uint8_t*)p.a + (ok ? row : 0) * p.lda + (tid & 3) * 16;
-    left_a[i] = ok ? p.K - (tid & 3) * 16 : 0;
-    ok = n < p.N;
-    b[i] = (const uint8_t*)p.b + ((int64_t)g * p.N + (ok ? n : 0)) * p.K + (tid & 3) * 16;
-    left_b[i] = ok ? p.K - (tid & 3) * 16 : 0;
+    a[i] = (const uint8_t*)p.a + (ok ? row : 0) * p.lda + k0;
+    there_a |= ok ? 1u << i : 0u;
+    there_b |= n0 + r < p.N ? 1u << i : 0u;
   }
+  const uint8_t* b = (const uint8_t*)p.b + ((int64_t)g * p.N + n0 + (tid >> 3)) * p.K + k0;
   // scales: thread r < 128 that of row r; the weights' is the tile's
   const float* sa = nullptr;
   if (tid < rows) {
@@ -78,43 +78,41 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
   }
   const float* sb = p.sb + ((int64_t)g * nt + ct) * kb;
 
-  u32x4_t ra[2], rb[2];
-  float next_sa = 0.f, next_sb = 0.f;
-  auto fetch = [&](int64_t k) {
+  u32x4_t ra[4], rb[4];
+  float next = 0.f;
+  auto fetch = [&](int64_t block) {
+    const int64_t k = block * 128, left = p.K - k0 - k;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ra[i] = chunk_end<uint8_t>(a[i] + k, left_a[i] - k);
-      rb[i] = chunk_end<uint8_t>(b[i] + k, left_b[i] - k);
+    for (int i = 0; i < 4; ++i) {
+      ra[i] = chunk_end<uint8_t>(a[i] + k, (there_a >> i) & 1 ? left : 0);
+      rb[i] = chunk_end<uint8_t>(b + 32 * i * p.K + k, (there_b >> i) & 1 ? left : 0);
     }
-    if (k % 128 == 0) {
-      next_sa = sa != nullptr ? sa[k / 128] : 0.f;
-      next_sb = sb[k / 128];
-    }
+    next = (sa != nullptr ? sa[block] : 0.f) * sb[block];
   };
   uint8_t* la = smem;
   uint8_t* lb = smem + kF8Tile * kF8Pitch;
   typedef TypeBf16::acc Acc;
-  Acc acc[2][2], part[2][2];
+  Acc acc[2][2];
   const Acc zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = part[i >> 1][i & 1] = zero;
+  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = zero;
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
   const uint8_t* fa = la + (wm + (lane & 31)) * kF8Pitch + (lane >> 5) * 16;
   const uint8_t* fb = lb + (wn + (lane & 31)) * kF8Pitch + (lane >> 5) * 16;
 
   fetch(0);
-  for (int64_t k = 0; k < kb * 128; k += 64) {
-    const int side = (int)((k / 128) & 1);
+  for (int64_t block = 0; block < kb; ++block) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      *(u32x4_t*)(la + ((tid >> 2) + 64 * i) * kF8Pitch + (tid & 3) * 16) = ra[i];
-      *(u32x4_t*)(lb + ((tid >> 2) + 64 * i) * kF8Pitch + (tid & 3) * 16) = rb[i];
+    for (int i = 0; i < 4; ++i) {
+      *(u32x4_t*)(la + ((tid >> 3) + 32 * i) * kF8Pitch + k0) = ra[i];
+      *(u32x4_t*)(lb + ((tid >> 3) + 32 * i) * kF8Pitch + k0) = rb[i];
     }
-    if (k % 128 == 0 && tid < kF8Tile) srow[side][tid] = next_sa * next_sb;
+    if (tid < kF8Tile) srow[tid] = next;
     __syncthreads();
-    if (k + 64 < kb * 128) fetch(k + 64);
+    if (block + 1 < kb) fetch(block + 1);
+    Acc part[2][2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       Wide va[2], vb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -126,21 +124,17 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          part[i][j] = TypeBf16::mma(vb[j].lo, va[i].lo, part[i][j]);
+          part[i][j] = TypeBf16::mma(vb[j].lo, va[i].lo, s == 0 ? zero : part[i][j]);
           part[i][j] = TypeBf16::mma(vb[j].hi, va[i].hi, part[i][j]);
         }
     }
-    if (k % 128 != 0) {   // the block is complete
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float s = srow[side][wm + 32 * i + (lane & 31)];
+    for (int i = 0; i < 2; ++i) {
+      const float s = srow[wm + 32 * i + (lane & 31)];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[i][j][r], s, acc[i][j][r]);
-          part[i][j] = zero;
-        }
-      }
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[i][j][r], s, acc[i][j][r]);
     }
     __syncthreads();
   }
@@ -166,7 +160,8 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
 // takes up to 16 MR rows of an expert and 16 output columns; its waves split the blocks of the
 // contraction in runs of U, weights go straight to the matrix instructions' registers.
 // ---------------------------------------------------------------------------
-template <typename O, int MR, int U, int WAVES>
+// ODD: rows that do not start on 4 bytes.
+template <typename O, int MR, int U, int WAVES, bool ODD>
 __global__ __launch_bounds__(64 * WAVES) void ragged_fp8_few_kernel(RaggedArgs p, uint32_t first) {
   typedef f32x4 Acc;
   __shared__ Acc sums[WAVES][MR][64];
@@ -215,6 +210,12 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_fp8_few_kernel(RaggedArgs p
       for (int e = 0; e < 4; ++e) acc[m][e] = __builtin_fmaf(part[e], s, acc[m][e]);
     }
   };
+  auto load = [](const uint8_t* at) {
+    if constexpr (ODD) return load16_odd(at);
+    u32x4_t v;
+    __builtin_memcpy(&v, at, 16);
+    return v;
+  };
   const int64_t whole = p.K / 128, runs = whole / U;
   for (int64_t run = wave; run < runs; run += WAVES) {
     u32x4_t wv[U][2], xv[U][MR][2];
@@ -223,11 +224,11 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_fp8_few_kernel(RaggedArgs p
     for (int i = 0; i < U; ++i) {
       const int64_t b = run * U + i;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) __builtin_memcpy(&wv[i][h], w + b * 128 + h * 64, 16);
+      for (int h = 0; h < 2; ++h) wv[i][h] = load(w + b * 128 + h * 64);
 #pragma unroll
       for (int m = 0; m < MR; ++m) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) __builtin_memcpy(&xv[i][m][h], x[m] + b * 128 + h * 64, 16);
+        for (int h = 0; h < 2; ++h) xv[i][m][h] = load(x[m] + b * 128 + h * 64);
         va[i][m] = sa[m][b];
       }
       vb[i] = sb[b];
@@ -284,19 +285,25 @@ hipError_t launch_fp8_any(const RaggedArgs& p, hipStream_t st) {
 template <typename O, int MR, int U, int WAVES>
 hipError_t launch_fp8_few(const RaggedArgs& p, hipStream_t st) {
   const int64_t blocks = (p.R / (16 * MR) + std::min<int64_t>(p.G, p.R)) * ((p.N + 15) / 16);
+  // (8 x 4096 x 4098, 16 rows, took 66 us with plain loads, where 4100 took 27)
+  const bool odd = (((uintptr_t)p.a | (uintptr_t)p.b) & 3) != 0 || p.K % 4 != 0 || p.lda % 4 != 0;
   return launch_in_parts(blocks, 64 * WAVES, [&](uint32_t first, uint32_t n) {
-    ragged_fp8_few_kernel<O, MR, U, WAVES><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
+    if (odd) ragged_fp8_few_kernel<O, MR, U, WAVES, true><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
+    else ragged_fp8_few_kernel<O, MR, U, WAVES, false><<<dim3(n), dim3(64 * WAVES), 0, st>>>(p, first);
   });
 }
 
+// Measured (us) by blocks of a run and waves: 8 x 14336 x 4096, 16 rows  1 x 4: 95   2 x 2: 90   2 x 4: 95
+// 3 x 4: 95   4 x 4: 99   8 x 4: 113;  128 x 2048 x 7168, 64 rows  123, 123, 121, 126, 133, 161;  4 x 4096 x
+// 4096, 4 rows  16, 14, 18, 20, -, -.  Of two waves more fit on a CU.  Where weights are few, 8 waves share them.
 template <typename O>
 hipError_t launch_fp8_rows(const RaggedArgs& p, hipStream_t st) {
   const int64_t groups = std::min<int64_t>(p.G, p.R);
   const int64_t mean = (p.R + groups - 1) / groups;
   const bool many = groups * ((p.N + 15) / 16) >= 1024;
-  if (mean <= 16) return many ? launch_fp8_few<O, 1, 4, 4>(p, st) : launch_fp8_few<O, 1, 2, 8>(p, st);
-  if (mean <= 32) return many ? launch_fp8_few<O, 2, 2, 4>(p, st) : launch_fp8_few<O, 2, 2, 8>(p, st);
-  return many ? launch_fp8_few<O, 4, 1, 4>(p, st) : launch_fp8_few<O, 4, 1, 8>(p, st);
+  if (mean <= 16) return many ? launch_fp8_few<O, 1, 2, 2>(p, st) : launch_fp8_few<O, 1, 2, 8>(p, st);
+  if (mean <= 32) return many ? launch_fp8_few<O, 2, 2, 2>(p, st) : launch_fp8_few<O, 2, 2, 8>(p, st);
+  return many ? launch_fp8_few<O, 4, 1, 2>(p, st) : launch_fp8_few<O, 4, 1, 8>(p, st);
 }
 
 bool fp8_tiles(int out, const RaggedArgs& p) {
@@ -308,16 +315,40 @@ bool fp8_tiles(int out, const RaggedArgs& p) {
   return 256 * p.K <= span && 256 * p.ldc * osize <= span && rows * p.lda <= span && rows * kb4 <= span && p.S > 0;
 }
 
+// Whether the few-rows form takes a product: bound by reading the weights, then by making bf16 of codes
+// anew for every 16 columns, about 8 + W (0.08 + 0.0115 m) us for W MB of weights and m rows an expert.
+// Measured (here, in the large tiles):
+//    17 (1 x 4096 x 4096)     m 32:  12,  30   96:  27,  38   192:  44,  57
+//    34 (8 x 2048 x 2048)     m 32:  19,  28   64:  33,  31    96:  52,  33
+//    67 (4 x 4096 x 4096)     m 24:  29,  41   32:  31,  42    64:  66,  47
+//   117 (4 x 7168 x 4096)     m 16:  33,  45   24:  45,  45    32:  50,  46
+//   134 (64 x 2048 x 1024)    m 12:  35,  39   16:  40,  39    24:  74,  40
+//   470 (8 x 14336 x 4096)    m  8: 105, 121   12: 119, 123    16: 130, 123
+// The any-size form takes about 1.7 us a block for each round of two workgroups a CU; here, there:
+//    12 (3 x 4099 x 1000)     m 48:  17,  21   96:  30,  24
+//    17 (1 x 4096 x 4096)     m 96:  26,  54  256:  56,  56
+//    67 (4 x 4096 x 4096)     m 48:  48,  60   64:  55,  61    96: 108,  62
+//   235 (8 x 4096 x 7168)     m  8:  47, 100   32: 105, 102    48: 169, 103
+bool fp8_few(const RaggedArgs& p, bool tiles) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R);
+  const double mean = (double)p.R / (double)groups, mb = 1e-6 * (double)groups * (double)p.N * (double)p.K;
+  if (p.R >= (1 << 20) || mean > 256) return false;
+  if (tiles) return mean <= 8 || (mean - 8) * mb <= (mb < 100 ? 1800 : 1200);
+  const double blocks = (double)((p.N + kF8Tile - 1) / kF8Tile) * (double)(p.R / kF8Tile + groups);
+  return mean <= 8 || 8 + mb * (0.08 + 0.0115 * mean) <= 4 + 1.7 * (double)((p.K + 127) / 128) * std::max(1.0, blocks / 512);
+}
+
 }  // namespace
 
 size_t ragged_fp8_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int32_t) { return 0; }
 
 hipError_t launch_ragged_gemm_fp8(int out, const RaggedArgs& p, size_t, hipStream_t st) {
-  if (ragged_few_rows(p, 1)) {
+  const bool tiles = fp8_tiles(out, p);
+  if (fp8_few(p, tiles)) {
     if (out == 0) return launch_fp8_rows<OutF32>(p, st);
     return out == 1 ? launch_fp8_rows<OutBf16>(p, st) : launch_fp8_rows<OutF16>(p, st);
   }
-  if (fp8_tiles(out, p)) return launch_ragged_fp8_tile(out, p, st);
+  if (tiles) return launch_ragged_fp8_tile(out, p, st);
   if (out == 0) return launch_fp8_any<OutF32>(p, st);
   return out == 1 ? launch_fp8_any<OutBf16>(p, st) : launch_fp8_any<OutF16>(p, st);
 }

@@ -665,10 +665,13 @@ def ragged_gemm(layout, a, b, m_splits, row_index=None, out_dtype=None, out=None
     return out
 
 
-def _on_current(t, name):
-    """Kernels run on the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _on_current(t, name, stream):
+    """Kernels run on the current device: a tensor or a stream of another one is refused."""
+    at = torch.cuda.current_device() if t.is_cuda else t.get_device()
+    if t.get_device() != at:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{at}")
+    if stream is not None and stream.device_index != at:
+        raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -709,7 +712,7 @@ def ragged_gemm_swiglu(x, w, m_splits, row_index=None, want_h=True, h=None, out=
     r = s if index is None else index.numel()
     ldx = _rows_of(x, x.dtype, (s, k), "x")
     _need(w, x.dtype, (g, 2 * f, k), "w")
-    _on_current(x, "x")
+    _on_current(x, "x", stream)
     if out is None:
         out = _empty((r, f), x.dtype, x.device, stream)
     lda = _rows_of(out, x.dtype, (r, f), "out")
@@ -749,7 +752,7 @@ def ragged_gemm_swiglu_bwd(dy, w, h, m_splits, want_a=True, dh=None, out=None, s
     lddy = _rows_of(dy, dy.dtype, (r, n), "dy")
     _need(w, dy.dtype, (g, n, f), "w")
     _need(h, dy.dtype, (r, 2 * f), "h")
-    _on_current(dy, "dy")
+    _on_current(dy, "dy", stream)
     if dh is None:
         dh = _empty((r, 2 * f), dy.dtype, dy.device, stream)
     _need(dh, dy.dtype, (r, 2 * f), "dh")
@@ -834,7 +837,7 @@ def quantize_fp8(x, out=None, stream=None):
     t, k = _matrix(x, "x")
     ty = _type_of(x, "x")
     ldx = _rows_of(x, x.dtype, (t, k), "x")
-    _on_current(x, "x")
+    _on_current(x, "x", stream)
     q, scale = (None, None) if out is None else out
     q = _empty((t, k), FP8, x.device, stream) if q is None else q
     scale = _empty((t, _blocks(k)), torch.float32, x.device, stream) if scale is None else scale
@@ -857,7 +860,7 @@ def quantize_fp8_weight(w, out=None, stream=None):
     g, n, k = w.shape
     ty = _type_of(w, "w")
     _need(w, w.dtype, (g, n, k), "w")
-    _on_current(w, "w")
+    _on_current(w, "w", stream)
     q, scale = (None, None) if out is None else out
     shape = (g, _blocks(n), _blocks(k))
     q = _empty((g, n, k), FP8, w.device, stream) if q is None else q
@@ -897,7 +900,7 @@ def ragged_gemm_fp8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=to
     _need(scale, torch.float32, (s, _blocks(k)), "scale")
     _need(w, FP8, (g, n, k), "w")
     _need(w_scale, torch.float32, (g, _blocks(n), _blocks(k)), "w_scale")
-    _on_current(q, "q")
+    _on_current(q, "q", stream)
     if out_dtype not in _TYPE:
         raise NotImplementedError(f"output dtype {out_dtype} is not supported")
     if out is None:
@@ -1072,7 +1075,7 @@ class ResidualNormGrad:
     pre_weight: Optional[torch.Tensor] = None
 
 
-def _norm_operands(x, name, f, out_dtype, gate, post_weight, pre_weight):
+def _norm_operands(x, name, f, out_dtype, gate, post_weight, pre_weight, stream):
     """Checks of what both directions take; (T, H, type of x, type, its torch type, type of the weights)."""
     t, h = _matrix(x, name)
     if f is None and (gate is not None or post_weight is not None):
@@ -1087,7 +1090,7 @@ def _norm_operands(x, name, f, out_dtype, gate, post_weight, pre_weight):
     if x.dtype not in (dtype, torch.float32):
         raise NotImplementedError(f"{name} of {x.dtype} beside {dtype} is not supported")
     _need(x, x.dtype, (t, h), name)
-    _on_current(x, name)
+    _on_current(x, name, stream)
     if f is not None:
         _need(f, dtype, (t, h), "f")
     if gate is not None:
@@ -1114,7 +1117,8 @@ def residual_norm(x, f=None, residual_scale=1.0, gate=None, post_weight=None, pr
     without pre_weight.  n(r) is of r as it is stored.  Without f the norm before the first
     block: (x, n(x) * pre_weight), y of out_dtype (x's, bf16 for fp32).  r may be x."""
     lib = _lib()
-    t, h, x_ty, ty, dtype, w_ty = _norm_operands(x, "x", f, out_dtype, gate, post_weight, pre_weight)
+    t, h, x_ty, ty, dtype, w_ty = _norm_operands(x, "x", f, out_dtype, gate, post_weight, pre_weight,
+                                                  stream)
     if f is None and pre_weight is None:
         raise ValueError("neither f nor pre_weight: nothing to compute")
     if f is None:
@@ -1151,7 +1155,7 @@ def residual_norm_bwd(dy, dr, r, f=None, residual_scale=1.0, gate=None, post_wei
     buffer of residual_norm_bwd_workspace_bytes(T, H), for the weights' gradients."""
     lib = _lib()
     t, h, x_ty, ty, dtype, w_ty = _norm_operands(r, "r", f, None if dy is None else dy.dtype, gate,
-                                                 post_weight, pre_weight)
+                                                 post_weight, pre_weight, stream)
     if dy is None and dr is None:
         raise ValueError("neither dy nor dr")
     if (dy is None) != (pre_weight is None):

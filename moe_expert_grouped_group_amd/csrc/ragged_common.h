@@ -81,6 +81,7 @@ hipError_t launch_ragged_tile_gated_f16(const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_gated_bwd(bool f16, const RaggedArgs& p, hipStream_t st);
 // 8-bit floating point (ragged_fp8.hip has the formula, ragged_fp8_tile.hip the large tiles).
 hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st);
+bool ragged_fp8_splits(const RaggedArgs& p);
 size_t ragged_split_bytes();   // a partial 256 x 256 tile for each CU
 
 // Longest range of a bounded operand (32-bit offsets, less what marks a lane that

@@ -340,15 +340,30 @@ bool fp8_few(const RaggedArgs& p, bool tiles) {
 
 }  // namespace
 
-size_t ragged_fp8_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int32_t) { return 0; }
+// For results of 16 bits and operands that are contiguous and on 16 bytes.
+size_t ragged_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G) {
+  RaggedArgs p{};
+  p.R = R;
+  p.S = S;
+  p.N = N;
+  p.K = K;
+  p.G = G;
+  p.lda = K;
+  p.ldc = N;
+  return R > 0 && fp8_tiles(1, p) && !fp8_few(p, true) && ragged_fp8_splits(p) ? ragged_split_bytes() : 0;
+}
 
-hipError_t launch_ragged_gemm_fp8(int out, const RaggedArgs& p, size_t, hipStream_t st) {
+hipError_t launch_ragged_gemm_fp8(int out, const RaggedArgs& p, size_t ws_bytes, hipStream_t st) {
   const bool tiles = fp8_tiles(out, p);
   if (fp8_few(p, tiles)) {
     if (out == 0) return launch_fp8_rows<OutF32>(p, st);
     return out == 1 ? launch_fp8_rows<OutBf16>(p, st) : launch_fp8_rows<OutF16>(p, st);
   }
-  if (tiles) return launch_ragged_fp8_tile(out, p, st);
+  if (tiles) {
+    RaggedArgs q = p;
+    if (ws_bytes < ragged_split_bytes() || !ragged_fp8_splits(p)) q.ws = nullptr;
+    return launch_ragged_fp8_tile(out, q, st);
+  }
   if (out == 0) return launch_fp8_any<OutF32>(p, st);
   return out == 1 ? launch_fp8_any<OutBf16>(p, st) : launch_fp8_any<OutF16>(p, st);
 }

@@ -46,14 +46,14 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
   __shared__ RaggedTable table;
   __shared__ RaggedArgs args;   // what only the start and end of a tile need: scalar registers are few
   __shared__ struct {
-    uint32_t rtiles, ctiles, full;
+    uint32_t rtiles, ctiles, full, rem, parts;
   } plan;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem, scale0 = (uint32_t)(uintptr_t)scales;
-  uint32_t ntiles;
+  uint32_t nunits;
   int kb;
   bool gather;
   {
@@ -61,28 +61,45 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
     build_ragged_table<kF8Threads>(p.m_splits, p.G, p.R, kTileM, &table, (int32_t*)smem);
     const uint32_t ctiles = (uint32_t)((p.N + kTileN - 1) / kTileN);
     const uint32_t rtiles = (uint32_t)__builtin_amdgcn_readfirstlane(table.tiles[kRaggedMaxGroups]);
-    ntiles = rtiles * ctiles;
     kb = (int)((p.K + 127) / 128);
+    const Units u = units_of(rtiles * ctiles, gridDim.x, kb, p.ws != nullptr);
+    nunits = (uint32_t)__builtin_amdgcn_readfirstlane((int)(u.full + u.rem * u.parts));
     gather = p.row_index != nullptr;
     if (tid == 0) {
       args = p;
       plan.rtiles = rtiles;
       plan.ctiles = ctiles;
-      plan.full = ntiles / gridDim.x * gridDim.x;
+      plan.full = u.full;
+      plan.rem = u.rem;
+      plan.parts = u.parts;
     }
   }
   uint32_t tile = blockIdx.x;
-  if (tile >= ntiles) return;
+  if (tile >= nunits) return;
   __syncthreads();
 
+  // A unit: a tile, or a part of one's stages (Units in ragged_tile.h; split: its number among the
+  // parts, or -1).
   struct Tile {
-    int32_t g, row0, rows, n0;
+    int32_t g, row0, rows, n0, first, end, split;
   };
   auto describe = [&](uint32_t i) {
     // of each full round of the grid an XCD takes consecutive tiles (as ragged_tile.h)
     const uint32_t n = gridDim.x;
-    if (n % 8 == 0 && i < plan.full) i = i - i % n + (i % n & 7) * (n / 8) + (i % n >> 3);
     Tile t;
+    t.first = 0;
+    t.end = kb;
+    t.split = -1;
+    if (i < plan.full) {
+      if (n % 8 == 0) i = i - i % n + (i % n & 7) * (n / 8) + (i % n >> 3);
+    } else if (plan.parts > 1) {
+      const uint32_t v = i - plan.full, which = v / plan.rem;
+      const int32_t each = kb / (int32_t)plan.parts, more = kb % (int32_t)plan.parts;
+      t.first = __builtin_amdgcn_readfirstlane((int32_t)which * each + min((int32_t)which, more));
+      t.end = __builtin_amdgcn_readfirstlane(t.first + each + ((int32_t)which < more ? 1 : 0));
+      t.split = __builtin_amdgcn_readfirstlane((int32_t)v);
+      i = plan.full + v % plan.rem;
+    }
     int32_t mt, nt;
     tile_order(i, plan.rtiles, plan.ctiles, &mt, &nt);
     int lo = 0, hi = args.G;   // tiles[lo] <= mt < tiles[hi]
@@ -149,23 +166,27 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
   constexpr int kCopies = kCopiesA + 4;
   uint32_t ctile = tile;
   int cst = 0, cslot = 0, cside = 0, cring = 0;   // stage, its slot, the place of its scales, of its rows
+  uint32_t scales_off = 0;
   Tile ct, after;
   uint32_t to_stage = 0, to_scales = 0, soff = 0, past[2] = {0, 0};
   bool with_scales = false;
   auto next_stage = [&]() {
-    if (cst == kb) {
-      cst = 0;
+    if (cst == ct.end) {
       ctile += gridDim.x;
-      if (ctile < ntiles) {
+      if (ctile < nunits) {
         cring ^= 1;
         ct = after;
         operands(ct, cring);
-        if (ctile + gridDim.x < ntiles) {
+        if (ctile + gridDim.x < nunits) {
           after = describe(ctile + gridDim.x);
           copy_rows(after, cring ^ 1);
         }
+        cst = ct.first;
       } else {
-        ctile = ntiles;
+        ctile = nunits;
+        cst = 0;
+        ct.first = 0;
+        ct.end = kb;
         sa[2] = sb[0][2] = sb[1][2] = ss[2] = 0;
       }
     }
@@ -173,17 +194,20 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
 #pragma unroll
     for (int h = 0; h < 2; ++h) past[h] = chunk(h) >= left ? kOut : 0u;
     to_stage = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(cslot * kStage));
-    soff = ctile < ntiles ? (uint32_t)cst * kStageK : 0u;
-    with_scales = (cst & 3) == 0 && 64 * wave <= kTileM;
+    soff = ctile < nunits ? (uint32_t)cst * kStageK : 0u;
+    // the scales of a group of four blocks with the first of them that the unit has
+    const bool opens = (cst & 3) == 0 || cst == ct.first;
+    with_scales = opens && 64 * wave <= kTileM;
+    scales_off = ctile < nunits ? (uint32_t)(cst & ~3) * 4u : 0u;
     to_scales = __builtin_amdgcn_readfirstlane(scale0 + (uint32_t)(cside * (int)sizeof(scales[0]) + wave * 1024));
-    if ((cst & 3) == 0) cside ^= 1;
+    if (opens) cside ^= 1;
     ++cst;
     cslot ^= 1;
   };
-  auto copy = [&](auto C) {   // copy c of that stage; the first with the scales of blocks cst .. cst + 3
+  auto copy = [&](auto C) {   // copy c of that stage; the first with the scales
     constexpr int c = decltype(C)::value;
     // (what lies past a row's last block is not used)
-    if (c == 0 && with_scales) copy16(ss, vs, soff / 32u, to_scales);
+    if (c == 0 && with_scales) copy16(ss, vs, scales_off, to_scales);
     if constexpr (c < kCopiesA)
       copy16(sa, va[c] | past[(kCopiesA * wave + c) & 1], soff, to_stage + (uint32_t)((kCopiesA * wave + c) * 1024));
     else
@@ -194,13 +218,14 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
   Tile t = describe(tile);
   ct = after = t;
   copy_rows(t, 0);
-  if (tile + gridDim.x < ntiles) {
+  if (tile + gridDim.x < nunits) {
     after = describe(tile + gridDim.x);
     copy_rows(after, 1);
   }
   __builtin_amdgcn_s_waitcnt(vm_wait(0));
   __syncthreads();
   operands(t, 0);
+  cst = t.first;
   __syncthreads();   // with one stage a tile, the second copies go on to the third tile's rows
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -233,8 +258,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
 #pragma unroll
   for (int j = 0; j < 4; ++j) fb[j] = fragment(base_b + lane_at, j * 2048);
   fa[0] = fragment(base_a + lane_at, 0);
-  float row = *(lds_f32_t*)row_scale;
-  float col = *(lds_f32_t*)col_scale;
+  float row = *(lds_f32_t*)(row_scale + (uint32_t)((t.first & 3) * 4));
+  float col = *(lds_f32_t*)(col_scale + (uint32_t)((t.first & 3) * 4));
   // the sums of block n - kLag of a stage (or of the stage before)
   auto add = [&](auto N) {
     constexpr int n = (decltype(N)::value + kBlocks - kLag) % kBlocks, i = n / 4, j = n % 4;
@@ -254,7 +279,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) part[j] = f32x4{0, 0, 0, 0};
-    for (int st = 0; st < kb; ++st) {
+    const int end = t.end;
+    for (int st = t.first; st < end; ++st) {
       const uint32_t at_a = hide(lane_at + (base_a + (uint32_t)(slot * kStage)));
       const uint32_t at_row = hide(row_scale + (uint32_t)(side * (int)sizeof(scales[0])) + (uint32_t)((st & 3) * 4));
       uint32_t at_b = 0;
@@ -270,10 +296,13 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
           __builtin_amdgcn_s_waitcnt(kLgkmWait0);
           __syncthreads();
           next_stage();
+          // (the unit that follows starts inside its tile only if it has four stages and more, so that it is
+          // the one copied now)
+          const int next_first = kb > 1 ? ct.first : 0;
           slot ^= 1;
-          if ((st & 3) == 3 || st == kb - 1) side ^= 1;
+          if ((st & 3) == 3 || st == end - 1) side ^= 1;
           const uint32_t to = (uint32_t)(side * (int)sizeof(scales[0])) +
-                              (st == kb - 1 ? 0u : (uint32_t)(((st + 1) & 3) * 4));
+                              (uint32_t)(((st == end - 1 ? next_first : st + 1) & 3) * 4);
           row = *(lds_f32_t*)hide(row_scale + to);
           col = *(lds_f32_t*)hide(col_scale + to);
           at_b = hide(lane_at + (base_b + (uint32_t)(slot * kStage)));
@@ -300,6 +329,18 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
     before = mine;
     unroll<kLag>([&](auto N) { add(N); });
     mine = 0.f;
+
+    if (t.split >= 0) {
+      // a part (the last unit of its workgroup): the sums as they lie
+      const auto ws = make_rsrc((const uint8_t*)args.ws + (int64_t)t.split * (kTileM * kTileN * 4), kTileM * kTileN * 4);
+#pragma unroll
+      for (int i = 0; i < RF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[i][j]), ws,
+                                                 (uint32_t)(((wave * RF + i) * 4 + j) * 1024 + lane * 16), 0, 0);
+      return;
+    }
 
     // Stores, whole lines of 64 columns, bounded, as in ragged_tile.h.  Sum e of block (i, j) in lane l:
     // row 16 i + l % 16, column 16 j + 4 (l / 16) + e.
@@ -331,30 +372,81 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (next >= ntiles) return;
+    if (next >= nunits) return;
     tile = next;
     t = kb > 1 ? ct : describe(tile);
   }
 }
 
+// Sums of the parts of split tiles, in order.  Workgroup b takes strips b, b + grid, ... (a wave's 16 rows).
+template <typename O, int RF>
+__global__ __launch_bounds__(256) void ragged_fp8_join_kernel(RaggedArgs p, uint32_t tile_grid) {
+  constexpr int kTileM = 32 * RF, kStrips = 8 * RF;
+  const int lane = threadIdx.x & 63, j = threadIdx.x >> 6;
+  const uint32_t ctiles = (uint32_t)((p.N + kTileN - 1) / kTileN);
+  const uint32_t rtiles = (uint32_t)wave_row_tile(p.m_splits, p.G, p.R, kTileM, -1, true).total;
+  const Units u = units_of(rtiles * ctiles, tile_grid, (p.K + 127) / 128, true);
+  if (u.parts < 2) return;
+  for (uint32_t b = blockIdx.x; b < u.rem * kStrips; b += gridDim.x) {
+    const uint32_t v = b / kStrips, strip = b % kStrips;
+    const int wave = (int)strip / RF, i = (int)strip % RF;
+    int32_t mt, nt;
+    tile_order(u.full + v, rtiles, ctiles, &mt, &nt);
+    const RowSpan t = wave_row_tile(p.m_splits, p.G, p.R, kTileM, mt, false);
+    const int m = (wave >> 2) * 16 * RF + 16 * i + (lane & 15);
+    const int64_t n = (int64_t)nt * kTileN + (wave & 3) * 64 + 16 * j + 4 * (lane >> 4);
+    if (m >= t.rows || n >= p.N) continue;   // columns come in eights
+    f32x4 sum = {0, 0, 0, 0};
+    for (uint32_t part = 0; part < u.parts; ++part)
+      sum += *(const f32x4*)((const uint8_t*)p.ws + (int64_t)(part * u.rem + v) * (kTileM * kTileN * 4) +
+                             ((wave * RF + i) * 4 + j) * 1024 + lane * 16);
+    typename O::elem o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = O::cvt(sum[e]);
+    __builtin_memcpy(__builtin_assume_aligned((typename O::elem*)p.c + (t.row0 + m) * p.ldc + n, sizeof(o)), o, sizeof(o));
+  }
+}
+
 namespace {
+
+int64_t fp8_tile_rows(const RaggedArgs& p) {
+  const int64_t mean = p.R / std::min<int64_t>(p.G, p.R);
+  return mean <= 32 ? 64 : mean <= 96 ? 128 : 256;
+}
 
 template <typename O, int RF>
 hipError_t launch_fp8_tile(const RaggedArgs& p, hipStream_t st) {
   const int64_t m = 32 * RF, tiles = ((p.N + kTileN - 1) / kTileN) * (p.R / m + std::min<int64_t>(p.G, p.R));
-  const unsigned grid = (unsigned)std::min<int64_t>(tiles, compute_units());
+  const unsigned grid = (unsigned)(p.ws != nullptr ? compute_units() : std::min<int64_t>(tiles, compute_units()));
   ragged_fp8_tile_kernel<O, RF><<<dim3(grid), dim3(kF8Threads), 0, st>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ws == nullptr) return e;
+  // half the tiles of a round at most are split
+  const unsigned strips = std::max(1u, grid / 2) * 8 * RF;
+  ragged_fp8_join_kernel<O, RF><<<dim3(std::min(strips, 1024u)), dim3(256), 0, st>>>(p, grid);
   return hipGetLastError();
 }
 
 template <typename O>
 hipError_t launch_fp8_tile_rows(const RaggedArgs& p, hipStream_t st) {
-  const int64_t mean = p.R / std::min<int64_t>(p.G, p.R);
-  if (mean <= 32) return launch_fp8_tile<O, 2>(p, st);
-  return mean <= 96 ? launch_fp8_tile<O, 4>(p, st) : launch_fp8_tile<O, 8>(p, st);
+  const int64_t rows = fp8_tile_rows(p);
+  if (rows == 64) return launch_fp8_tile<O, 2>(p, st);
+  return rows == 128 ? launch_fp8_tile<O, 4>(p, st) : launch_fp8_tile<O, 8>(p, st);
 }
 
 }  // namespace
+
+// Whether tiles are split where the experts' rows are even (the table of the launch, which has the real
+// ones, decides again): the stages saved, as units_of counts them, have to pay the second launch and the
+// workspace, about 8 us or six stages.  Measured (us, whole, split): 1 x 4096 x 14336, 257 rows 168, 76;
+// 8 x 4096 x 14336, 768 rows 191, 142, 2048 rows 229, 178; 8 x 2048 x 7168, 1024 rows 93, 77; 1 x 4096 x
+// 4096, 200 rows 56, 44; and with nothing to split 8 x 2048 x 2048, 2048 rows 42, 50.
+bool ragged_fp8_splits(const RaggedArgs& p) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R), m = fp8_tile_rows(p), stages = (p.K + 127) / 128;
+  const int64_t tiles = groups * ((p.R / groups + m - 1) / m) * ((p.N + kTileN - 1) / kTileN);
+  const Units u = units_of((uint32_t)std::min<int64_t>(tiles, 1 << 30), (uint32_t)compute_units(), stages, true);
+  return u.parts > 1 && stages - stages / u.parts - u.parts * u.rem / 7 > 6;
+}
 
 hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st) {
   return out == 1 ? launch_fp8_tile_rows<OutBf16>(p, st) : launch_fp8_tile_rows<OutF16>(p, st);

@@ -178,7 +178,7 @@ constexpr int kMinPart = 4;   // stages of a part
 struct Units {
   uint32_t full, rem, parts;
 };
-__device__ __forceinline__ Units units_of(uint32_t ntiles, uint32_t grid, int64_t stages, bool ws) {
+__host__ __device__ __forceinline__ Units units_of(uint32_t ntiles, uint32_t grid, int64_t stages, bool ws) {
   Units u;
   u.full = ntiles / grid * grid;
   u.rem = ntiles - u.full;
@@ -189,7 +189,9 @@ __device__ __forceinline__ Units units_of(uint32_t ntiles, uint32_t grid, int64_
     // stages / p + p rem / 7.
     const uint32_t most = (uint32_t)(stages / kMinPart < 1 ? 1 : stages / kMinPart);
     const uint32_t best = (uint32_t)sqrtf(7.f * (float)stages / (float)u.rem);
-    u.parts = max(1u, min(min(grid / u.rem, most), best));
+    const uint32_t fit = grid / u.rem, p = fit < most ? fit : most;
+    u.parts = p < best ? p : best;
+    if (u.parts < 1) u.parts = 1;
   }
   return u;
 }

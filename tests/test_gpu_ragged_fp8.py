@@ -362,3 +362,19 @@ def test_captured_and_replayed():
         want = mx.ragged_gemm_fp8(*mx.quantize_fp8(x), w, w_scale, ms)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+# few tiles of a long contraction: split among the CUs, each part four blocks and more, and joined.  Parts
+# that begin inside a group of four blocks, a ragged last block, rows and columns past the tile's
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("splits,k,n", [
+    ([200], 4096, 264), ([300], 4112, 4096), ([40, 300, 0, 260], 7184, 520), ([96, 95], 10128, 1032),
+    ([32, 31, 33], 28688, 1032), ([257, 1300], 4112, 9000)])   # tiles of 128 and 64 rows; a round and a part of one
+def test_few_tiles_of_long_sums(splits, k, n, dtype):
+    rows = sum(splits)
+    index = torch.randint(0, rows, (rows,), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    q, scale, w, w_scale = _case(rows, splits, k, n)
+    for i in (None, index):
+        got = mx.ragged_gemm_fp8(q, scale, w, w_scale, _ms(splits), row_index=i, out_dtype=dtype)
+        _check(q, scale, w, w_scale, splits, i, got)
+        assert torch.equal(got, mx.ragged_gemm_fp8(q, scale, w, w_scale, _ms(splits), row_index=i, out_dtype=dtype))

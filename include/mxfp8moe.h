@@ -695,7 +695,8 @@ mxfp8_status mxfp8_quantize_fp8_weight(const void* w, int32_t type, int64_t G, i
  *   w_scale [G, ceil(N / 128), ceil(K / 128)];  c [R, N], row stride ldc, c_type any
  *   mxfp8_type;  the rest as mxfp8_ragged_gemm (NT).  Rows of zeros have scale 0.  For the
  *   input's gradient, w holds the transposed weights [G, K, N], w_scale the transposed scales.
- * mxfp8_ragged_gemm_fp8_workspace_bytes: 0 where none is used, and for sizes that are refused.
+ * mxfp8_ragged_gemm_fp8_workspace_bytes: for results of 16 bits; 0 where none is used, and for
+ * sizes that are refused.  fp32 results use none.
  * Errors: as mxfp8_ragged_gemm.
  */
 mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
@@ -713,7 +714,8 @@ size_t mxfp8_ragged_gemm_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, in
  *   r[t] = residual_scale x[t] + gate[t] b[t]     gate 1 where it is NULL
  *   y[t] = n(r[t]) pre_weight
  * n(r) is of r as it is stored (rounded to x's type), which is what the backward pass and
- * every later reader see.  Statistics are fp32: the squares' sum must not pass 2^127.
+ * every later reader see.  Statistics are fp32: the squares' sum must not pass 2^127, nor
+ * mean(v^2) + eps fall under 2^-126 (a row of zeros with eps 0 is NaN, as the formula says).
  *   x, r   [T, H], x_type: MXFP8_TYPE_F32 or `type`.  r may be x itself
  *   f, y   [T, H], type: MXFP8_TYPE_BF16 or MXFP8_TYPE_F16
  *   gate   fp32 [T] or NULL;  post_weight, pre_weight [H] or NULL, w_type: MXFP8_TYPE_F32 or `type`

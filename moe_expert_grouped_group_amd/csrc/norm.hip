@@ -4,7 +4,8 @@
 //   n(v) = v / sqrt(mean(v^2) + eps) over a row
 //   b = n(f) post (or f),  r = residual_scale x + gate b,  y = n(r) pre     r as it is stored
 //
-//   total = dr + d n(r) for (dy pre),  d n(v) for u: rs u - rs^3 mean(u v) v,  rs = 1 / sqrt(mean(v^2) + eps)
+//   total = dr + d n(r) for (dy pre),  d n(v) for u: rs (u - (rs mean(u v)) n(v)),  rs = 1 / sqrt(mean(v^2) + eps)
+//     (rs^3 itself would leave the fp32 range for rows of 2^43 and of 2^-43)
 //   dx = residual_scale total,  db = gate total,  df = d n(f) for (db post) (or db),  dgate = <total, b>
 //   dpre = sum over rows of dy n(r),  dpost = sum over rows of db n(f)
 //
@@ -286,7 +287,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
     }
     row_sums<W>(sum, lds3, side3);
     const float rs = __builtin_amdgcn_rsqf(sum[0] * each + p.eps);
-    const float pull = rs * rs * rs * (sum[1] * each);
+    const float pull = rs * (rs * (sum[1] * each));
     const float rf = has_post ? __builtin_amdgcn_rsqf(sum[2] * each + p.eps) : 1.f;
     float total[NC][8];
     float dot[1] = {0.f};
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
         float w[8];
         weights(p.pre, kept_pre[kAhead ? c : 0], at, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) total[c][i] += v.dy[c].get(i) * w[i] * rs - pull * v.r[c].get(i);
+        for (int i = 0; i < 8; ++i) total[c][i] += v.dy[c].get(i) * w[i] * rs - pull * (v.r[c].get(i) * rs);
         sums(0, c, [&](float (&d)[8]) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] = __builtin_fmaf(v.dy[c].get(i), v.r[c].get(i) * rs, d[i]);
@@ -323,7 +324,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
     if (!has_f) continue;
     if (has_post || p.dgate != nullptr) row_sums<W>(dot, lds1, side1);
     if (p.dgate != nullptr && t == 0) p.dgate[row] = rf * dot[0];
-    const float back = has_post ? rf * rf * rf * (gate * dot[0] * each) : 0.f;
+    const float back = has_post ? rf * (rf * (gate * dot[0] * each)) : 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int at = (c * W + t) * 8, n = p.H - at;
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
           for (int i = 0; i < 8; ++i) d[i] = __builtin_fmaf(gate * total[c][i], v.f[c].get(i) * rf, d[i]);
         });
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = gate * total[c][i] * w[i] * rf - back * v.f[c].get(i);
+      for (int i = 0; i < 8; ++i) e[i] = gate * total[c][i] * w[i] * rf - back * (v.f[c].get(i) * rf);
       if (ALL || p.df != nullptr) {
         Eight<F> o;
         o.set(e);

@@ -161,6 +161,22 @@ def test_before_the_first_block(t, h, dtype, x_dtype):
         _check(case, 1.0, 1e-6, r, y, dy, dr, grad)
 
 
+@pytest.mark.parametrize("x_dtype", [BF, F32])
+@pytest.mark.parametrize("power", [55, -60])
+@pytest.mark.parametrize("t,h", [(5, 96), (300, 1031), (4, 4096)])
+def test_loud_and_quiet_rows(t, h, power, x_dtype):
+    """Rows whose squares are fp32 numbers and whose inverse norms' cubes are not."""
+    s = 2.0 ** power
+    case = _case(t, h, BF, x_dtype, True, True, True)
+    case["x"], case["f"] = case["x"] * s, case["f"] * s
+    case["gate"] = case["gate"] * s
+    kw = {k: v for k, v in case.items() if k not in ("x", "f")}
+    r, y = mx.residual_norm(case["x"], case["f"], residual_scale=0.5, eps=0.0, **kw)
+    dy, dr = _draw((t, h), 20, BF), _draw((t, h), 21, x_dtype) / s
+    grad = mx.residual_norm_bwd(dy, dr, r, case["f"], residual_scale=0.5, eps=0.0, **kw)
+    _check(case, 0.5, 0.0, r, y, dy, dr, grad)
+
+
 @pytest.mark.parametrize("t,h", [(5000, 64), (3000, 1000), (700, 2048), (600, 4096), (300, 8192)])
 def test_many_rows(t, h):
     """More rows than one to each workgroup: column sums over several."""

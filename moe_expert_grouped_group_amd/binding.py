@@ -875,7 +875,7 @@ def quantize_fp8_weight(w, out=None, stream=None):
 
 @functools.lru_cache(maxsize=4096)
 def ragged_gemm_fp8_workspace_bytes(rows, x_rows, n, k, groups):
-    """Workspace of ragged_gemm_fp8 for these sizes; 0 where none is used."""
+    """Workspace of ragged_gemm_fp8 for these sizes and results of 16 bits; 0 where none is used."""
     return int(_lib().mxfp8_ragged_gemm_fp8_workspace_bytes(rows, x_rows, n, k, groups))
 
 
@@ -906,7 +906,7 @@ def ragged_gemm_fp8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=to
     if out is None:
         out = _empty((r, n), out_dtype, q.device, stream)
     ldc = _rows_of(out, out_dtype, (r, n), "out")
-    need = ragged_gemm_fp8_workspace_bytes(r, s, n, k, g)
+    need = 0 if out_dtype == torch.float32 else ragged_gemm_fp8_workspace_bytes(r, s, n, k, g)
     size = need
     if workspace is not None:
         size = _sized(workspace, need)

@@ -436,16 +436,24 @@ hipError_t launch_fp8_tile_rows(const RaggedArgs& p, hipStream_t st) {
 
 }  // namespace
 
-// Whether tiles are split where the experts' rows are even (the table of the launch, which has the real
-// ones, decides again): the stages saved, as units_of counts them, have to pay the second launch and the
-// workspace, about 8 us or six stages.  Measured (us, whole, split): 1 x 4096 x 14336, 257 rows 168, 76;
+// Whether a launch may split tiles (the table in the kernel, which has the experts' rows, decides on how
+// many parts): the stages saved, as units_of counts them, have to pay the second launch and the
+// workspace, about 8 us or six stages, where experts' rows are even or on average over the numbers of
+// tiles that uneven ones can make.  Measured (us, whole, split): 1 x 4096 x 14336, 257 rows 168, 76;
 // 8 x 4096 x 14336, 768 rows 191, 142, 2048 rows 229, 178; 8 x 2048 x 7168, 1024 rows 93, 77; 1 x 4096 x
 // 4096, 200 rows 56, 44; and with nothing to split 8 x 2048 x 2048, 2048 rows 42, 50.
 bool ragged_fp8_splits(const RaggedArgs& p) {
   const int64_t groups = std::min<int64_t>(p.G, p.R), m = fp8_tile_rows(p), stages = (p.K + 127) / 128;
-  const int64_t tiles = groups * ((p.R / groups + m - 1) / m) * ((p.N + kTileN - 1) / kTileN);
-  const Units u = units_of((uint32_t)std::min<int64_t>(tiles, 1 << 30), (uint32_t)compute_units(), stages, true);
-  return u.parts > 1 && stages - stages / u.parts - u.parts * u.rem / 7 > 6;
+  const int64_t ctiles = (p.N + kTileN - 1) / kTileN;
+  auto saved = [&](int64_t rtiles) -> int64_t {
+    const Units u = units_of((uint32_t)std::min<int64_t>(rtiles * ctiles, 1 << 30), (uint32_t)compute_units(), stages, true);
+    return u.parts > 1 ? stages - stages / u.parts - u.parts * u.rem / 7 : 0;
+  };
+  if (saved(groups * ((p.R / groups + m - 1) / m)) > 6) return true;
+  const int64_t least = (p.R + m - 1) / m, most = p.R / m + groups;
+  int64_t sum = 0;
+  for (int i = 0; i < 8; ++i) sum += saved(least + (most - least) * i / 7);
+  return sum > 6 * 8;
 }
 
 hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st) {

@@ -151,7 +151,12 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_kernel(NormAr
         float w[8], e[8];
         weights8<F>(p.post, p.w_f32, at, n, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(p.scale, x[c].get(i), f[c].get(i) * w[i] * rs);
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_fmaf(p.scale, x[c].get(i), f[c].get(i) * w[i] * rs);
+          // (an fp32 number before it is rounded to the stored type, in every type: the compiler would round
+          // once to fp16, another value next to a tie)
+          asm("" : "+v"(e[i]));
+        }
         x[c].set(e);
         x[c].store(p.r, row * p.H + at, n);
       }

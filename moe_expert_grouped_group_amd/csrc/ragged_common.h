@@ -59,6 +59,20 @@ struct RaggedArgs {
   void* act;            // kGatedBwd: the activation [R, F], contiguous, or NULL
 };
 
+// A copy, member by member: of an assignment the compiler makes private arrays that it then puts into LDS,
+// and for their addresses every wave reads the launch's packet in the host's memory, one XCD after the
+// other: up to 12 us before the last one's workgroups began.
+__device__ __forceinline__ void copy_args(RaggedArgs& to, const RaggedArgs& p) {
+  to.a = p.a, to.b = p.b, to.c = p.c;
+  to.lda = p.lda, to.ldb = p.ldb, to.ldc = p.ldc;
+  to.R = p.R, to.S = p.S, to.N = p.N, to.K = p.K;
+  to.m_splits = p.m_splits, to.row_index = p.row_index;
+  to.sa = p.sa, to.sb = p.sb;
+  to.G = p.G;
+  to.con = p.con, to.ccols = p.ccols;
+  to.ws = p.ws, to.h = p.h, to.act = p.act;
+}
+
 // What becomes of a product's sums.
 //  kGated (NT, W [G, 2F, K] gate rows then up rows): C[r, f] = silu(z[r, f]) z[r, F + f], z the
 //    sums; kGatedKeep writes h = z too.

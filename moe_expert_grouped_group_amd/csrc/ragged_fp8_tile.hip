@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
     nunits = (uint32_t)__builtin_amdgcn_readfirstlane((int)(u.full + u.rem * u.parts));
     gather = p.row_index != nullptr;
     if (tid == 0) {
-      args = p;
+      copy_args(args, p);
       plan.rtiles = rtiles;
       plan.ctiles = ctiles;
       plan.full = u.full;

@@ -114,58 +114,58 @@ struct RaggedTable {
   int32_t tiles[kRaggedMaxGroups + 1];
   int32_t rows[kRaggedMaxGroups + 1];
 };
+// Inclusive sums over the wave's lanes; MOST: none past `most` (below 2^31).
+template <bool MOST>
+__device__ __forceinline__ uint32_t wave_sums(uint32_t v, uint32_t most) {
+  auto add = [&](uint32_t u) { v = MOST ? min(v + u, most) : v + u; };
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));   // row_shr: 1, 2, 4, 8
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast: 15, 31
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
+  return v;
+}
 template <int THREADS = 256>
 __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int G, int64_t R,
                                                    int tile, RaggedTable* t, int32_t* scan) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, wave = tid >> 6;
   constexpr int per = kRaggedMaxGroups / THREADS;
-  int64_t rows[per], rs = 0;
-  int32_t ts = 0;
+  const uint32_t most = (uint32_t)R;
+  uint32_t rows[per], own = 0;
 #pragma unroll
   for (int i = 0; i < per; ++i) {
     const int g = tid * per + i;
-    rows[i] = g < G ? split_rows(m_splits, g, R) : 0;
-    rs += rows[i];
+    rows[i] = g < G ? (uint32_t)split_rows(m_splits, g, R) : 0;
+    own = min(own + rows[i], most);
   }
-  // rows before this thread's experts, cut at R (sums of up to 1024 splits of at
-  // most R each, in 64 bits)
-  int64_t* s64 = (int64_t*)scan;
-  s64[tid] = rs;
+  const uint32_t upto = wave_sums<true>(own, most);
+  if ((tid & 63) == 63) scan[wave] = (int32_t)upto;
   __syncthreads();
-  for (int d = 1; d < THREADS; d <<= 1) {
-    const int64_t u = tid >= d ? s64[tid - d] : 0;
-    __syncthreads();
-    s64[tid] += u;
-    __syncthreads();
-  }
-  int64_t r0 = s64[tid] - rs;
-  __syncthreads();
-  int32_t off[per + 1];
+  // the rows of the lanes before (wave_shr: 1) and of the waves before
+  uint32_t off[per + 1];
+  off[0] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)upto, 0x138, 0xF, 0xF, false);
+  for (int w = 0; w < wave; ++w) off[0] = min(off[0] + (uint32_t)scan[w], most);
+  uint32_t tiles = 0;
 #pragma unroll
   for (int i = 0; i < per; ++i) {
-    off[i] = (int32_t)(r0 < R ? r0 : R);
-    r0 += rows[i];
-    off[i + 1] = (int32_t)(r0 < R ? r0 : R);
-    ts += (off[i + 1] - off[i] + tile - 1) / tile;
+    off[i + 1] = min(off[i] + rows[i], most);
+    tiles += (off[i + 1] - off[i] + (uint32_t)tile - 1) / (uint32_t)tile;
   }
-  scan[tid] = ts;
+  const uint32_t tiles_upto = wave_sums<false>(tiles, 0);
+  if ((tid & 63) == 63) scan[THREADS / 64 + wave] = (int32_t)tiles_upto;
   __syncthreads();
-  for (int d = 1; d < THREADS; d <<= 1) {
-    const int32_t u = tid >= d ? scan[tid - d] : 0;
-    __syncthreads();
-    scan[tid] += u;
-    __syncthreads();
-  }
-  int32_t t0 = scan[tid] - ts;
+  uint32_t t0 = tiles_upto - tiles;
+  for (int w = 0; w < wave; ++w) t0 += (uint32_t)scan[THREADS / 64 + w];
 #pragma unroll
   for (int i = 0; i < per; ++i) {
-    t->tiles[tid * per + i] = t0;
-    t->rows[tid * per + i] = off[i];
-    t0 += (off[i + 1] - off[i] + tile - 1) / tile;
+    t->tiles[tid * per + i] = (int32_t)t0;
+    t->rows[tid * per + i] = (int32_t)off[i];
+    t0 += (off[i + 1] - off[i] + (uint32_t)tile - 1) / (uint32_t)tile;
   }
   if (tid == THREADS - 1) {
-    t->tiles[kRaggedMaxGroups] = t0;
-    t->rows[kRaggedMaxGroups] = off[per];
+    t->tiles[kRaggedMaxGroups] = (int32_t)t0;
+    t->rows[kRaggedMaxGroups] = (int32_t)off[per];
   }
   __syncthreads();
 }
@@ -417,7 +417,7 @@ __global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedArgs p) {
       plan.rtiles = rtiles;
       plan.ctiles = ctiles;
       plan.band = band;
-      args = p;
+      copy_args(args, p);
     }
   }
   __syncthreads();

@@ -560,6 +560,22 @@ bool gated_tiles(bool bwd, const RaggedArgs& p) {
     return false;
   return p.row_index == nullptr || (p.S > 0 && p.S * p.lda * 2 <= span);
 }
+
+// Whether the few-rows form takes a forward product, as few_rows.  Measured (us; here, in the large tiles), by
+// MB of both projections' weights (experts x 2 F x K) and m rows an expert:
+//    34 (1 x 4096 x 4096)     m 16:  15,  19   32:  19,  19    64:  28,  22
+//    67 (8 x 2048 x 2048)     m 16:  22,  29   48:  28,  33    64:  31,  34   96: 52, 34
+//   134 (4 x 4096 x 4096)     m 16:  27,  33   24:  31,  33    32:  34,  33
+//   235 (4 x 7168 x 4096)     m  8:  43,  43   12:  45,  44    24:  57,  45
+//   268 (64 x 2048 x 1024)    m  8:  47,  49   12:  53,  49    16:  60,  49
+//   940 (8 x 14336 x 4096)    m  8: 193, 175   16: 226, 177
+// With fewer blocks of 16 columns than CUs (the first line) it slows down sooner.
+bool gated_few(const RaggedArgs& p) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
+  const double mb = 2e-6 * (double)groups * (double)p.N * (double)p.K;
+  const double most = groups * ((p.N / 2 + 15) / 16) < 256 ? 1200.0 : mb < 150.0 ? 3200.0 : 1400.0;
+  return p.R < (1 << 20) && mean <= 256 && (mean <= 4 || (double)(mean - 4) * mb <= most);
+}
 }  // namespace
 
 size_t ragged_gated_workspace_bytes(bool bwd, int64_t R, int64_t N, int64_t K, int32_t G) {
@@ -570,12 +586,12 @@ size_t ragged_gated_workspace_bytes(bool bwd, int64_t R, int64_t N, int64_t K, i
   p.K = K;
   p.G = G;
   const int64_t F = bwd ? K : N / 2, con = bwd ? N : K;
-  if (con % 8 != 0 || F % 8 != 0 || (!bwd && few_rows(p, 2))) return 0;
+  if (con % 8 != 0 || F % 8 != 0 || (!bwd && gated_few(p))) return 0;
   return split_bytes();
 }
 
 hipError_t launch_ragged_gated(bool f16, const RaggedArgs& p, size_t ws_bytes, hipStream_t st) {
-  if (few_rows(p, 2)) return launch_ragged_few_gated(f16, p, st);
+  if (gated_few(p)) return launch_ragged_few_gated(f16, p, st);
   if (gated_tiles(false, p)) {
     RaggedArgs q = p;
     q.con = p.K;

@@ -318,12 +318,12 @@ bool fp8_tiles(int out, const RaggedArgs& p) {
 // Whether the few-rows form takes a product: bound by reading the weights, then by making bf16 of codes
 // anew for every 16 columns, about 8 + W (0.08 + 0.0115 m) us for W MB of weights and m rows an expert.
 // Measured (here, in the large tiles):
-//    17 (1 x 4096 x 4096)     m 32:  12,  30   96:  27,  38   192:  44,  57
-//    34 (8 x 2048 x 2048)     m 32:  19,  28   64:  33,  31    96:  52,  33
-//    67 (4 x 4096 x 4096)     m 24:  29,  41   32:  31,  42    64:  66,  47
-//   117 (4 x 7168 x 4096)     m 16:  33,  45   24:  45,  45    32:  50,  46
-//   134 (64 x 2048 x 1024)    m 12:  35,  39   16:  40,  39    24:  74,  40
-//   470 (8 x 14336 x 4096)    m  8: 105, 121   12: 119, 123    16: 130, 123
+//    17 (1 x 4096 x 4096)     m 32:  11,  20   64:  17,  24    96:  26,  24
+//    34 (8 x 2048 x 2048)     m 32:  16,  21   48:  26,  24    96:  58,  24
+//    67 (4 x 4096 x 4096)     m 24:  27,  35   32:  31,  35    48:  47,  40
+//   117 (4 x 7168 x 4096)     m 12:  29,  37   16:  32,  37    24:  48,  37
+//   134 (64 x 2048 x 1024)    m  8:  31,  28   12:  34,  28    16:  38,  28
+//   470 (8 x 14336 x 4096)    m  8: 108, 104   12: 119, 120    16: 130, 105
 // The any-size form takes about 1.7 us a block for each round of two workgroups a CU; here, there:
 //    12 (3 x 4099 x 1000)     m 48:  17,  21   96:  30,  24
 //    17 (1 x 4096 x 4096)     m 96:  26,  54  256:  56,  56
@@ -333,7 +333,7 @@ bool fp8_few(const RaggedArgs& p, bool tiles) {
   const int64_t groups = std::min<int64_t>(p.G, p.R);
   const double mean = (double)p.R / (double)groups, mb = 1e-6 * (double)groups * (double)p.N * (double)p.K;
   if (p.R >= (1 << 20) || mean > 256) return false;
-  if (tiles) return mean <= 8 || (mean - 8) * mb <= (mb < 100 ? 1800 : 1200);
+  if (tiles) return mean <= 8 || (mean - 8) * mb <= (mb < 125 ? 1250 : 300);
   const double blocks = (double)((p.N + kF8Tile - 1) / kF8Tile) * (double)(p.R / kF8Tile + groups);
   return mean <= 8 || 8 + mb * (0.08 + 0.0115 * mean) <= 4 + 1.7 * (double)((p.K + 127) / 128) * std::max(1.0, blocks / 512);
 }

@@ -45,61 +45,6 @@ __device__ __forceinline__ u32x4_t load_chunk(const E* p, int64_t n) {
   return v;
 }
 
-// The row tile `t` (of `tile` rows) among all experts: its expert, first row
-// and row count, from the splits, by the whole workgroup.  Returns false past
-// the last tile.  G <= 1024, 256 threads.
-struct RowTile {
-  int g;
-  int64_t row0;
-  int rows;
-};
-__device__ bool find_row_tile(const int64_t* m_splits, int G, int64_t R, int tile, int64_t t,
-                              RowTile* out, int64_t* lds /* 2 * 256 + 3 */) {
-  const int tid = threadIdx.x;
-  constexpr int per = kRaggedMaxGroups / 256;
-  int64_t rows[per], r_sum = 0, t_sum = 0;
-#pragma unroll
-  for (int i = 0; i < per; ++i) {
-    const int g = tid * per + i;
-    rows[i] = g < G ? split_rows(m_splits, g, R) : 0;
-    r_sum += rows[i];
-    t_sum += (rows[i] + tile - 1) / tile;
-  }
-  int64_t* sr = lds;
-  int64_t* st = lds + 256;
-  int64_t* found = lds + 512;
-  sr[tid] = r_sum;
-  st[tid] = t_sum;
-  if (tid == 0) found[0] = -1;
-  __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const int64_t r = tid >= d ? sr[tid - d] : 0, u = tid >= d ? st[tid - d] : 0;
-    __syncthreads();
-    sr[tid] += r;
-    st[tid] += u;
-    __syncthreads();
-  }
-  int64_t r0 = sr[tid] - r_sum, t0 = st[tid] - t_sum;
-#pragma unroll
-  for (int i = 0; i < per; ++i) {
-    const int64_t nt = (rows[i] + tile - 1) / tile;
-    if (t >= t0 && t < t0 + nt) {
-      const int64_t lo = r0 + (t - t0) * tile;
-      const int64_t hi = r0 + rows[i] < R ? r0 + rows[i] : R;   // never past the rows there are
-      found[0] = tid * per + i;
-      found[1] = lo;
-      found[2] = hi - lo < tile ? hi - lo : tile;
-    }
-    r0 += rows[i];
-    t0 += nt;
-  }
-  __syncthreads();
-  out->g = (int)found[0];
-  out->row0 = found[1];
-  out->rows = (int)found[2];
-  return found[0] >= 0 && found[2] > 0;
-}
-
 // Rows [lo, lo + len) of expert g (TN), clipped to the R rows there are.
 __device__ void expert_rows(const int64_t* m_splits, int g, int64_t R, int64_t* lo, int64_t* len,
                             int64_t* lds /* 256 */) {
@@ -143,8 +88,8 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   int g;
   int64_t m0, rows, con, lo = 0;   // con: contraction length; lo: its first row (TN)
   if (LAYOUT != 2) {
-    RowTile t;
-    if (!find_row_tile(p.m_splits, p.G, p.R, kAnyT, rt, &t, scan)) return;
+    const RowSpan t = wave_row_tile(p.m_splits, p.G, p.R, kAnyT, rt, false);
+    if (t.g < 0) return;
     g = t.g;
     m0 = t.row0;
     rows = t.rows;

@@ -241,6 +241,18 @@ __device__ __forceinline__ int64_t split_rows(const int64_t* m_splits, int g, in
   return m < 0 ? 0 : (m < R ? m : R);
 }
 
+// Inclusive sums over the wave's lanes, all of them active; MOST: none past `most` (below 2^31).
+template <bool MOST>
+__device__ __forceinline__ uint32_t wave_sums(uint32_t v, uint32_t most) {
+  auto add = [&](uint32_t u) { v = MOST ? min(v + u, most) : v + u; };
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));   // row_shr: 1, 2, 4, 8
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast: 15, 31
+  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
+  return v;
+}
 // The expert, first row and row count of row tile rt (tiles of `tile` rows), by one
 // wave; g = -1 past the last.  total: row tiles of all experts (only if asked for).
 struct RowSpan {
@@ -250,40 +262,33 @@ struct RowSpan {
 __device__ __forceinline__ RowSpan wave_row_tile(const int64_t* m_splits, int G, int64_t R, int tile,
                                                  int64_t rt, bool want_total) {
   const int lane = threadIdx.x & 63;
+  const uint32_t most = (uint32_t)R;
   RowSpan s;
   s.g = -1;
   s.rows = 0;
   s.row0 = 0;
-  int64_t before_r = 0, before_t = 0;
+  uint32_t before_r = 0;
+  int64_t before_t = 0;
   for (int base = 0; base < G; base += 64) {
     const int e = base + lane;
-    const int64_t m = e < G ? split_rows(m_splits, e, R) : 0;
-    // rows, then tiles, of the experts up to this one
-    int64_t r = m;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t u = __shfl_up(r, d, 64);
-      if (lane >= d) r += u;
-    }
-    const int64_t hi = min(before_r + r, R), lo = min(before_r + r - m, R);   // cut at R
-    const int64_t t = (hi - lo + tile - 1) / tile;
-    int64_t ts = t;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t u = __shfl_up(ts, d, 64);
-      if (lane >= d) ts += u;
-    }
+    // rows, then tiles, of the experts up to this one, cut at R
+    const uint32_t r = wave_sums<true>(e < G ? (uint32_t)split_rows(m_splits, e, R) : 0u, most);
+    const uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)r, 0x138, 0xF, 0xF, false);   // wave_shr: 1
+    const uint32_t hi = min(before_r + r, most), lo = min(before_r + before, most);
+    const uint32_t t = (hi - lo + (uint32_t)tile - 1) / (uint32_t)tile;
+    const uint32_t ts = wave_sums<false>(t, 0);
     const int64_t first = before_t + ts - t;
     const uint64_t who = __ballot(rt >= first && rt < first + t);
     if (who != 0) {
       const int src = __builtin_ctzll(who);
       s.g = base + src;
-      s.row0 = __shfl(lo + (rt - first) * tile, src, 64);
-      s.rows = (int)min((int64_t)tile, __shfl(hi, src, 64) - s.row0);
+      const int64_t tiles = __builtin_amdgcn_readlane((int)(uint32_t)(rt - first), src);
+      s.row0 = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)lo, src) + tiles * tile;
+      s.rows = (int)min((int64_t)tile, (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, src) - s.row0);
       if (!want_total) break;
     }
-    before_r += __shfl(r, 63, 64);
-    before_t += __shfl(ts, 63, 64);
+    before_r = min(before_r + (uint32_t)__builtin_amdgcn_readlane((int)r, 63), most);
+    before_t += (uint32_t)__builtin_amdgcn_readlane((int)ts, 63);
   }
   s.total = before_t;
   return s;

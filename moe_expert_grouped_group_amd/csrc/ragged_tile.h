@@ -114,18 +114,6 @@ struct RaggedTable {
   int32_t tiles[kRaggedMaxGroups + 1];
   int32_t rows[kRaggedMaxGroups + 1];
 };
-// Inclusive sums over the wave's lanes; MOST: none past `most` (below 2^31).
-template <bool MOST>
-__device__ __forceinline__ uint32_t wave_sums(uint32_t v, uint32_t most) {
-  auto add = [&](uint32_t u) { v = MOST ? min(v + u, most) : v + u; };
-  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));   // row_shr: 1, 2, 4, 8
-  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
-  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
-  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
-  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast: 15, 31
-  add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
-  return v;
-}
 template <int THREADS = 256>
 __device__ __forceinline__ void build_ragged_table(const int64_t* m_splits, int G, int64_t R,
                                                    int tile, RaggedTable* t, int32_t* scan) {

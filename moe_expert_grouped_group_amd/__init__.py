@@ -4,7 +4,8 @@ The computation lives in hand-written HIP kernels behind the C ABI of
 ``libmxfp8moe.so`` (include/mxfp8moe.h); this package is the thin Python
 binding over it (torch supplies device memory and streams) plus the seeded
 input generators.  Beside the MXFP8 path it holds the products of experts with
-any number of rows (bf16, fp16, 8-bit integers) and the routing around them.
+any number of rows (bf16, fp16, 8-bit integers and floating point), plain and
+gated, the routing around them and the norms around a block.
 """
 
 from .binding import (  # noqa: F401

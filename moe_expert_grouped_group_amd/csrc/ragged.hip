@@ -306,7 +306,8 @@ int64_t pad16(int64_t n, int64_t size) { return (n * size + 15) / 16 * 16 / size
 // 0.24 W (8-bit) where W is large.  Off by most with many experts of short rows (537,
 // 128 x 2048 x 1024: 116, 108 at m 4 already).  Up to 256 rows, though small weights
 // would stay ahead beyond (1 x 1024 x 1024 at 384: 14, 32), because 22 experts of 808 x 151
-// with 760 rows each took 130 us here.
+// with 760 rows each took 130 us here.  (The tiles start some 10 us earlier since, copy_args; the bounds
+// stay, so that calls sum in the order they did.)
 bool few_rows(const RaggedArgs& p, int esize) {
   const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
   const double mb = 1e-6 * (double)groups * (double)p.N * (double)p.K * esize;
@@ -349,7 +350,7 @@ Repack repack_of(int layout, int esize, int osize, const RaggedArgs& p) {
 //   NN  1777,  517 x 1031, 5:  40,  52   3000, 2011 x 1031, 3: 132,  85   9000, 777 x 2051, 8: 154, 101
 //   TN  1777,  517 x 1031, 5:  43,  49   600, 4099 x 1003, 1:   94,  55   9000, 777 x 2051, 8: 291, 111
 // There a step of 64 contraction bytes takes 1.1 us (NT), 2.1 (NN) and 4.0 (TN) for each
-// round of two workgroups a CU, of 256; here 48 us, 1350 TFLOP/s and every byte twice at 4.5 TB/s.
+// round of two workgroups a CU, of 256; here 48 us (the large tiles' start was 10 us later then), 1350 TFLOP/s and every byte twice at 4.5 TB/s.
 bool repack_pays(int layout, int esize, const RaggedArgs& p, size_t bytes) {
   const double us = layout == 0 ? 1.1 : layout == 1 ? 2.1 : 4.0;
   const double con = layout == 0 ? (double)p.K : layout == 1 ? (double)p.N : (double)p.R / p.G;

@@ -13,9 +13,9 @@
 // of a block's sum on normal values); between blocks the sums are fp32.  It runs at twice the rate of
 // the bf16 ones that an exact sum would take.
 //
-// 8 x 4096 x 14336, 16384 rows: 1056 us, 1.82 PFLOP/s, where the MXFP8 product of this package, whose
-// scales the matrix instruction applies itself, takes 929 (zeros: 920; matrix cores busy 45 % at 1.75
-// GHz).  Without its copies to LDS the kernel takes 870, with every copy hitting L2 1045, without the
+// 8 x 4096 x 14336, 16384 rows: 950 to 1060 us by the machine's clock, 1.8 to 2.0 PFLOP/s, where the MXFP8
+// product of this package, whose scales the matrix instruction applies itself, takes 929 (zeros: 920; matrix
+// cores busy 51 % at 1.86 GHz).  Without its copies to LDS the kernel takes 870, with every copy hitting L2 1045, without the
 // scaling 1081 beside 1157 at the time.  All of a wave's copies at once instead of one to a matrix
 // instruction cost 4 %, one to two or three 2 and 5 %; a second meeting half way, so that three
 // quarters of the copies go out half a stage earlier, 0 to 1 %; the two waves of a SIMD copying in
@@ -444,7 +444,8 @@ hipError_t launch_fp8_tile_rows(const RaggedArgs& p, hipStream_t st) {
 // Whether a launch may split tiles (the table in the kernel, which has the experts' rows, decides on how
 // many parts): the stages saved, as units_of counts them, have to pay the second launch and the
 // workspace, about 8 us or six stages, where experts' rows are even or on average over the numbers of
-// tiles that uneven ones can make.  Measured (us, whole, split): 1 x 4096 x 14336, 257 rows 168, 76;
+// tiles that uneven ones can make.  Measured (us, whole, split; on the same kernel with a
+// slower start, 10 us on both): 1 x 4096 x 14336, 257 rows 168, 76;
 // 8 x 4096 x 14336, 768 rows 191, 142, 2048 rows 229, 178; 8 x 2048 x 7168, 1024 rows 93, 77; 1 x 4096 x
 // 4096, 200 rows 56, 44; and with nothing to split 8 x 2048 x 2048, 2048 rows 42, 50.
 bool ragged_fp8_splits(const RaggedArgs& p) {

@@ -190,6 +190,21 @@ def test_splits_that_do_not_fill_the_rows(rows, splits, kf):
         assert (t[end:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("k,f", [(1032, 2056), (2056, 3000)])   # one round of tiles; one and a part that is split
+def test_high_tiles(k, f, dtype):
+    """Tiles of 256 rows, gathered and not, both projections kept and not; experts that end inside one."""
+    splits = [700, 5, 0, 1300, 257]
+    rows, g, tokens = sum(splits), len(splits), 900
+    index = torch.randint(-1, tokens + 1, (rows,), generator=torch.Generator().manual_seed(9)).int().cuda()
+    w = _normal((g, 2 * f, k), 2, dtype, k ** -0.5)
+    for x, at in ((_normal((rows, k), 1, dtype), None), (_normal((tokens, k), 3, dtype), index)):
+        h, a = mx.ragged_gemm_swiglu(x, w, _ms(splits), row_index=at)
+        _check_forward(x, w, splits, at, h, a, rows)
+        none, only = mx.ragged_gemm_swiglu(x, w, _ms(splits), row_index=at, want_h=False)
+        assert none is None and torch.equal(only, a)
+
+
 @pytest.mark.parametrize("k,f", [(64, 128), (264, 136)])
 @pytest.mark.parametrize("rows", [40, 600])
 def test_strides_and_alignment(rows, k, f):

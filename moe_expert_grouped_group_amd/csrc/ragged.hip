@@ -64,7 +64,8 @@ __device__ void expert_rows(const int64_t* m_splits, int g, int64_t R, int64_t* 
   __syncthreads();
 }
 
-template <typename T, typename O, int LAYOUT, int EPI = kPlain>
+// TM: rows of the tile, 128 or (NT, NN) 64.
+template <typename T, typename O, int LAYOUT, int EPI = kPlain, int TM = kAnyT>
 __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32_t first) {
   typedef typename T::elem E;
   // gated: a tile is 64 gate columns and their up columns, in blocks of 32 in turn
@@ -75,8 +76,11 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   constexpr int kAnyPitch = kBytes + kAnyPad;
   constexpr int kStep = kBytes / sizeof(E);        // contraction elements per step
   constexpr int kRow = kBytes / 16;                // chunks of a row, contraction contiguous
-  constexpr int kParts = kAnyT * kRow / 256;       // chunks of a thread
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kAnyT * kAnyPitch];
+  constexpr int kParts = kAnyT * kRow / 256;       // chunks of a thread, of B
+  constexpr int kPartsA = LAYOUT == 2 ? kParts : TM * kRow / 256;
+  constexpr int MI = TM / 64;                      // blocks of 32 rows of a wave
+  static_assert(TM == kAnyT || (TM == 64 && LAYOUT != 2), "");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[(TM + kAnyT) * kAnyPitch];
   __shared__ int64_t scan[2 * 256 + 3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   int g;
   int64_t m0, rows, con, lo = 0;   // con: contraction length; lo: its first row (TN)
   if (LAYOUT != 2) {
-    const RowSpan t = wave_row_tile(p.m_splits, p.G, p.R, kAnyT, rt, false);
+    const RowSpan t = wave_row_tile(p.m_splits, p.G, p.R, TM, rt, false);
     if (t.g < 0) return;
     g = t.g;
     m0 = t.row0;
@@ -108,11 +112,11 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   const E* a = (const E*)p.a;
   const E* b = (const E*)p.b;
   if (LAYOUT != 2) b += (int64_t)g * p.N * p.K;
-  int64_t rows_a[LAYOUT != 2 ? kParts : 1];   // contraction contiguous: this thread's rows of A
-  bool there[LAYOUT != 2 ? kParts : 1];       // (rows of zeros are not)
+  int64_t rows_a[LAYOUT != 2 ? kPartsA : 1];   // contraction contiguous: this thread's rows of A
+  bool there[LAYOUT != 2 ? kPartsA : 1];       // (rows of zeros are not)
   if constexpr (LAYOUT != 2) {
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) {
+    for (int i = 0; i < kPartsA; ++i) {
       const int r = tid / kRow + 256 / kRow * i;
       there[i] = r < rows;
       rows_a[i] = there[i] ? m0 + r : 0;
@@ -123,11 +127,12 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
       }
     }
   }
-  u32x4_t ra[kParts], rb[kParts];
+  u32x4_t ra[kPartsA], rb[kParts];
   auto fetch = [&](int64_t k0) {
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-      if (LAYOUT != 2) {
+      if (i >= kPartsA) {
+      } else if (LAYOUT != 2) {
         const int64_t k = k0 + (tid % kRow) * kPer;
         ra[i] = load_chunk<E>(a + rows_a[i] * p.lda + k, there[i] ? con - k : 0);
       } else {
@@ -157,7 +162,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
     }
   };
   uint8_t* la = smem;
-  uint8_t* lb = smem + kAnyT * kAnyPitch;
+  uint8_t* lb = smem + TM * kAnyPitch;
   auto put = [&](uint8_t* at, u32x4_t v, int i, bool over_rows) {
     if (!over_rows) {
       *(u32x4_t*)(at + (tid / kRow + 256 / kRow * i) * kAnyPitch + (tid % kRow) * 16) = v;
@@ -170,12 +175,12 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
     }
   };
 
-  typename T::acc acc[2][2];
+  typename T::acc acc[MI][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2 * MI; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i >> 1][i & 1][r] = 0;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const int wm = (wave >> 1) * 32 * MI, wn = (wave & 1) * 64;
   const uint8_t* fa = la + (wm + (lane & 31)) * kAnyPitch + (lane >> 5) * 16;
   const uint8_t* fb = lb + (wn + (lane & 31)) * kAnyPitch + (lane >> 5) * 16;
 
@@ -183,21 +188,21 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   for (int64_t k0 = 0; k0 < con; k0 += kStep) {
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-      put(la, ra[i], i, LAYOUT == 2);
+      if (i < kPartsA) put(la, ra[i], i, LAYOUT == 2);
       put(lb, rb[i], i, LAYOUT != 0);
     }
     __syncthreads();
     if (k0 + kStep < con) fetch(k0 + kStep);
 #pragma unroll
     for (int s = 0; s < kBytes / 32; ++s) {
-      u32x4_t va[2], vb[2];
+      u32x4_t va[MI], vb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        va[i] = *(const u32x4_t*)(fa + i * 32 * kAnyPitch + s * 32);
+        if (i < MI) va[i] = *(const u32x4_t*)(fa + i * 32 * kAnyPitch + s * 32);
         vb[i] = *(const u32x4_t*)(fb + i * 32 * kAnyPitch + s * 32);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = T::mma(va[i], vb[j], acc[i][j]);
     }
@@ -209,7 +214,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   typename O::elem* c = (typename O::elem*)p.c;
   if constexpr (EPI != kPlain) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < (kIsGated ? 1 : 2); ++j) {
         const int64_t n = n0 + (kIsGated ? wn / 2 : wn) + 32 * j + (lane & 31);
@@ -238,7 +243,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   const int64_t ldc = LAYOUT == 2 ? p.K : p.ldc;
   c += LAYOUT == 2 ? ((int64_t)g * p.N + m0) * p.K : m0 * ldc;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int64_t n = n0 + wn + 32 * j + (lane & 31);
@@ -270,14 +275,28 @@ int64_t ragged_any_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G
                              : R / kAnyT + std::min<int64_t>(G, R));
 }
 
+template <typename T, typename O, int LAYOUT, int EPI, int TM>
+hipError_t launch_any_rows(const RaggedArgs& p, int64_t blocks, hipStream_t st) {
+  return launch_in_parts(blocks, 256, [&](uint32_t first, uint32_t n) {
+    ragged_any_kernel<T, O, LAYOUT, EPI, TM><<<dim3(n), dim3(256), 0, st>>>(p, first);
+  });
+}
 template <typename T, typename O, int LAYOUT, int EPI = kPlain>
 hipError_t launch_any(const RaggedArgs& p, hipStream_t st) {
-  // gated: F columns in tiles of 64, as many as 2 (F rounded up to 64) in tiles of 128
-  const int64_t N = EPI == kGated ? (p.N / 2 + kAnyT / 2 - 1) / (kAnyT / 2) * kAnyT : p.N;
-  const int64_t blocks = ragged_any_blocks(LAYOUT, p.R, N, p.K, p.G);
-  return launch_in_parts(blocks, 256, [&](uint32_t first, uint32_t n) {
-    ragged_any_kernel<T, O, LAYOUT, EPI><<<dim3(n), dim3(256), 0, st>>>(p, first);
-  });
+  if constexpr (EPI != kPlain) {
+    // gated: F columns in tiles of 64
+    const int64_t cols = EPI == kGated ? (p.N / 2 + kAnyT / 2 - 1) / (kAnyT / 2) : (p.K + kAnyT - 1) / kAnyT;
+    const int64_t groups = std::min<int64_t>(p.G, p.R);
+    // Low tiles while most CUs have none yet (half of an expert's last tile empty on average).  Measured (us,
+    // 64 and 128 rows, by tiles of 128): gated 5 x 517 x 1031, 81: 25, 29, 198: 29, 32, 378: 44, 41; 8 x 777 x
+    // 2051, 208: 44, 50, 325: 85, 57; backward 5 x 517 x 1031, 110: 68, 86, 210: 93, 86; 4 x 4099 x 1000, 99: 60,
+    // 65, 165: 82, 69.
+    if (cols * (p.R / kAnyT + groups / 2) <= (EPI == kGated ? 215 : 130))
+      return launch_any_rows<T, O, LAYOUT, EPI, 64>(p, cols * (p.R / 64 + groups), st);
+    return launch_any_rows<T, O, LAYOUT, EPI, kAnyT>(p, cols * (p.R / kAnyT + groups), st);
+  } else {
+    return launch_any_rows<T, O, LAYOUT, EPI, kAnyT>(p, ragged_any_blocks(LAYOUT, p.R, p.N, p.K, p.G), st);
+  }
 }
 
 template <typename T, typename O>

@@ -33,32 +33,36 @@ __device__ __forceinline__ Wide widen_codes(u32x4_t c) {
 }
 
 // ---------------------------------------------------------------------------
-// Any size, stride and alignment: 128 x 128 output tile, 4 waves of 64 x 64, a block of the contraction at
+// Any size, stride and alignment: 128 x 128 output tile, 4 waves of 64 x 64 (64 and 32 rows where tiles are few), a block at
 // a time through registers to LDS, the next one's loads in flight meanwhile.
 // ---------------------------------------------------------------------------
 constexpr int kF8Tile = 128;
 constexpr int kF8Pitch = 144;   // LDS row: 128 codes + 16 bytes, so that consecutive rows start in other banks
 
-template <typename O>
+// TM: rows of a tile, 128 or 64.
+template <typename O, int TM>
 __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, uint32_t first) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kF8Tile * kF8Pitch];
-  __shared__ float srow[kF8Tile];
+  constexpr int MI = TM / 64, PA = TM / 32;   // blocks of 32 rows of a wave, rows of a thread
+  __shared__ __attribute__((aligned(16))) uint8_t smem[(TM + kF8Tile) * kF8Pitch];
+  __shared__ float srow[TM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t nt = (p.N + kF8Tile - 1) / kF8Tile, kb = (p.K + 127) / 128;
   const int64_t at = first + blockIdx.x, ct = at % nt;
   const int64_t n0 = ct * kF8Tile;
-  const RowSpan t = wave_row_tile(p.m_splits, p.G, p.R, kF8Tile, at / nt, false);
+  const RowSpan t = wave_row_tile(p.m_splits, p.G, p.R, TM, at / nt, false);
   if (t.g < 0) return;
   const int g = t.g, rows = t.rows;
   const int64_t m0 = t.row0;
 
   // this thread's rows of both operands: (tid >> 3) + 32 i, 16 codes from 16 (tid & 7) on
   const int64_t k0 = (tid & 7) * 16;
-  const uint8_t* a[4];
+  const uint8_t* a[PA];
   uint32_t there_a = 0, there_b = 0;   // bit i: row i is there; the others are rows of zeros
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = (tid >> 3) + 32 * i;
+    there_b |= n0 + r < p.N ? 1u << i : 0u;
+    if (i >= PA) continue;
     int64_t row = m0 + r;
     bool ok = r < rows;
     if (p.row_index != nullptr && ok) {
@@ -67,7 +71,6 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
     }
     a[i] = (const uint8_t*)p.a + (ok ? row : 0) * p.lda + k0;
     there_a |= ok ? 1u << i : 0u;
-    there_b |= n0 + r < p.N ? 1u << i : 0u;
   }
   const uint8_t* b = (const uint8_t*)p.b + ((int64_t)g * p.N + n0 + (tid >> 3)) * p.K + k0;
   // scales: thread r < 128 that of row r; the weights' is the tile's
@@ -78,25 +81,25 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
   }
   const float* sb = p.sb + ((int64_t)g * nt + ct) * kb;
 
-  u32x4_t ra[4], rb[4];
+  u32x4_t ra[PA], rb[4];
   float next = 0.f;
   auto fetch = [&](int64_t block) {
     const int64_t k = block * 128, left = p.K - k0 - k;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      ra[i] = chunk_end<uint8_t>(a[i] + k, (there_a >> i) & 1 ? left : 0);
+      if (i < PA) ra[i] = chunk_end<uint8_t>(a[i] + k, (there_a >> i) & 1 ? left : 0);
       rb[i] = chunk_end<uint8_t>(b + 32 * i * p.K + k, (there_b >> i) & 1 ? left : 0);
     }
     next = (sa != nullptr ? sa[block] : 0.f) * sb[block];
   };
   uint8_t* la = smem;
-  uint8_t* lb = smem + kF8Tile * kF8Pitch;
+  uint8_t* lb = smem + TM * kF8Pitch;
   typedef TypeBf16::acc Acc;
-  Acc acc[2][2];
+  Acc acc[MI][2];
   const Acc zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = zero;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  for (int i = 0; i < 2 * MI; ++i) acc[i >> 1][i & 1] = zero;
+  const int wm = (wave >> 1) * 32 * MI, wn = (wave & 1) * 64;
   const uint8_t* fa = la + (wm + (lane & 31)) * kF8Pitch + (lane >> 5) * 16;
   const uint8_t* fb = lb + (wn + (lane & 31)) * kF8Pitch + (lane >> 5) * 16;
 
@@ -104,24 +107,24 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
   for (int64_t block = 0; block < kb; ++block) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      *(u32x4_t*)(la + ((tid >> 3) + 32 * i) * kF8Pitch + k0) = ra[i];
+      if (i < PA) *(u32x4_t*)(la + ((tid >> 3) + 32 * i) * kF8Pitch + k0) = ra[i];
       *(u32x4_t*)(lb + ((tid >> 3) + 32 * i) * kF8Pitch + k0) = rb[i];
     }
-    if (tid < kF8Tile) srow[tid] = next;
+    if (tid < TM) srow[tid] = next;
     __syncthreads();
     if (block + 1 < kb) fetch(block + 1);
-    Acc part[2][2];
+    Acc part[MI][2];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      Wide va[2], vb[2];
+      Wide va[MI], vb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        va[i] = widen_codes(*(const u32x4_t*)(fa + i * 32 * kF8Pitch + s * 32));
+        if (i < MI) va[i] = widen_codes(*(const u32x4_t*)(fa + i * 32 * kF8Pitch + s * 32));
         vb[i] = widen_codes(*(const u32x4_t*)(fb + i * 32 * kF8Pitch + s * 32));
       }
       // the weights first: a lane holds columns of one row
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           part[i][j] = TypeBf16::mma(vb[j].lo, va[i].lo, s == 0 ? zero : part[i][j]);
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < MI; ++i) {
       const float s = srow[wm + 32 * i + (lane & 31)];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(256, 2) void ragged_fp8_any_kernel(RaggedArgs p, ui
   // accumulator r of a 32 x 32 block in lane l: row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4
   typename O::elem* c = (typename O::elem*)p.c + m0 * p.ldc;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < MI; ++i) {
     const int m = wm + 32 * i + (lane & 31);
     if (m >= rows) continue;
 #pragma unroll
@@ -273,13 +276,21 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_fp8_few_kernel(RaggedArgs p
 
 namespace {
 
+template <typename O, int TM>
+hipError_t launch_fp8_any_rows(const RaggedArgs& p, hipStream_t st) {
+  const int64_t blocks = ((p.N + kF8Tile - 1) / kF8Tile) * (p.R / TM + std::min<int64_t>(p.G, p.R));
+  return launch_in_parts(blocks, 256, [&](uint32_t first, uint32_t n) {
+    ragged_fp8_any_kernel<O, TM><<<dim3(n), dim3(256), 0, st>>>(p, first);
+  });
+}
 template <typename O>
 hipError_t launch_fp8_any(const RaggedArgs& p, hipStream_t st) {
-  const int64_t blocks =
-      ((p.N + kF8Tile - 1) / kF8Tile) * (p.R / kF8Tile + std::min<int64_t>(p.G, p.R));
-  return launch_in_parts(blocks, 256, [&](uint32_t first, uint32_t n) {
-    ragged_fp8_any_kernel<O><<<dim3(n), dim3(256), 0, st>>>(p, first);
-  });
+  // Low tiles while they add few to what a CU does (half of an expert's last tile empty on average).
+  // Measured (us, 64 and 128 rows, by tiles of 128): 3 x 4099 x 1000, 99: 20, 24, 231: 30, 32, 429: 53, 46;
+  // 8 x 2048 x 2048, 128: 27, 33, 320: 39, 47, 576: 68, 69; 8 x 4096 x 7168, 160: 76, 100, 384: 109, 124,
+  // 640: 210, 161.
+  const int64_t tiles = ((p.N + kF8Tile - 1) / kF8Tile) * (p.R / kF8Tile + std::min<int64_t>(p.G, p.R) / 2);
+  return tiles <= 400 ? launch_fp8_any_rows<O, 64>(p, st) : launch_fp8_any_rows<O, 128>(p, st);
 }
 
 template <typename O, int MR, int U, int WAVES>
@@ -324,18 +335,19 @@ bool fp8_tiles(int out, const RaggedArgs& p) {
 //   117 (4 x 7168 x 4096)     m 12:  29,  37   16:  32,  37    24:  48,  37
 //   134 (64 x 2048 x 1024)    m  8:  31,  28   12:  34,  28    16:  38,  28
 //   470 (8 x 14336 x 4096)    m  8: 108, 104   12: 119, 120    16: 130, 105
-// The any-size form takes about 1.7 us a block for each round of two workgroups a CU; here, there:
-//    12 (3 x 4099 x 1000)     m 48:  17,  21   96:  30,  24
-//    17 (1 x 4096 x 4096)     m 96:  26,  54  256:  56,  56
-//    67 (4 x 4096 x 4096)     m 48:  48,  60   64:  55,  61    96: 108,  62
-//   235 (8 x 4096 x 7168)     m  8:  47, 100   32: 105, 102    48: 169, 103
+// The any-size form takes about 1.15 us a block while its tiles have a CU each, and more in proportion;
+// here, there:
+//    12 (3 x 4099 x 1000)     m 48:  16,  17   64:  17,  18    96:  28,  20
+//    17 (1 x 4096 x 4096)     m 96:  25,  38  128:  30,  39   192:  42,  39
+//    34 (8 x 2048 x 2048)     m 32:  16,  25   48:  25,  26    64:  30,  27
+//   235 (8 x 4096 x 7168)     m 16:  55,  76   32:  85,  77    64: 176,  80
 bool fp8_few(const RaggedArgs& p, bool tiles) {
   const int64_t groups = std::min<int64_t>(p.G, p.R);
   const double mean = (double)p.R / (double)groups, mb = 1e-6 * (double)groups * (double)p.N * (double)p.K;
   if (p.R >= (1 << 20) || mean > 256) return false;
   if (tiles) return mean <= 8 || (mean - 8) * mb <= (mb < 125 ? 1250 : 300);
   const double blocks = (double)((p.N + kF8Tile - 1) / kF8Tile) * (double)(p.R / kF8Tile + groups);
-  return mean <= 8 || 8 + mb * (0.08 + 0.0115 * mean) <= 4 + 1.7 * (double)((p.K + 127) / 128) * std::max(1.0, blocks / 512);
+  return mean <= 8 || 8 + mb * (0.08 + 0.0115 * mean) <= 6 + 1.15 * (double)((p.K + 127) / 128) * std::max(1.0, blocks / 320);
 }
 
 }  // namespace

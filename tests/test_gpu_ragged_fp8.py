@@ -378,3 +378,13 @@ def test_few_tiles_of_long_sums(splits, k, n, dtype):
         got = mx.ragged_gemm_fp8(q, scale, w, w_scale, _ms(splits), row_index=i, out_dtype=dtype)
         _check(q, scale, w, w_scale, splits, i, got)
         assert torch.equal(got, mx.ragged_gemm_fp8(q, scale, w, w_scale, _ms(splits), row_index=i, out_dtype=dtype))
+
+
+@pytest.mark.parametrize("splits,k,n", [([300, 0, 65, 128], 1031, 517), ([1300, 0, 1665, 1128], 257, 1801)])
+def test_any_size_tiles(splits, k, n):
+    """The any-size form with tiles of 64 and of 128 rows."""
+    rows = sum(splits)
+    index = torch.randint(-1, rows + 1, (rows,), generator=torch.Generator().manual_seed(4)).int().cuda()
+    case = _case(rows, splits, k, n)
+    for out in (F32, HF):
+        _check(*case, splits, index, mx.ragged_gemm_fp8(*case, _ms(splits), row_index=index, out_dtype=out))

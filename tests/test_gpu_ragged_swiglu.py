@@ -341,3 +341,15 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for one, other in zip(got, (h, a, dh, again)):
             assert torch.equal(one, other)
+
+
+@pytest.mark.parametrize("splits,k,f", [([300, 0, 65, 128], 1031, 517), ([1300, 0, 1665, 1128], 257, 1031)])
+def test_any_size_tiles(splits, k, f):
+    """The any-size form with tiles of 64 and of 128 rows, both directions."""
+    rows, g = sum(splits), len(splits)
+    x, w = _normal((rows, k), 1, BF), _normal((g, 2 * f, k), 2, BF, k ** -0.5)
+    index = torch.randint(-1, rows + 1, (rows,), generator=torch.Generator().manual_seed(4)).int().cuda()
+    h, a = mx.ragged_gemm_swiglu(x, w, _ms(splits), row_index=index)
+    _check_forward(x, w, splits, index, h, a, rows)
+    dy, w2 = _normal((rows, k), 3, BF), _normal((g, k, f), 4, BF, k ** -0.5)
+    _check_backward(dy, w2, h, splits, *mx.ragged_gemm_swiglu_bwd(dy, w2, h, _ms(splits)))

@@ -127,6 +127,9 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
       }
     }
   }
+  // Over rows: chunks of a wave go along the columns, which memory likes, or (backward of gated products) along
+  // the contraction, which LDS does: single values land in 8 banks side by side, not in 2.
+  const int over_k = EPI == kGatedBwd ? tid & 15 : tid >> 4, over_c = EPI == kGatedBwd ? tid >> 4 : tid & 15;
   u32x4_t ra[kPartsA], rb[kParts];
   auto fetch = [&](int64_t k0) {
 #pragma unroll
@@ -136,8 +139,8 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
         const int64_t k = k0 + (tid % kRow) * kPer;
         ra[i] = load_chunk<E>(a + rows_a[i] * p.lda + k, there[i] ? con - k : 0);
       } else {
-        const int64_t k = k0 + (tid >> 4) + 16 * i;
-        const int64_t c = (tid & 15) * 8;
+        const int64_t k = k0 + over_k + 16 * i;
+        const int64_t c = over_c * 8;
         ra[i] = load_chunk<E>(a + (lo + k) * p.lda + m0 + c, k < con ? p.N - m0 - c : 0);
       }
       if (LAYOUT == 0) {
@@ -149,8 +152,8 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
         }
         rb[i] = load_chunk<E>(b + r * p.K + k, r < p.N ? con - k : 0);
       } else {
-        const int64_t k = k0 + (tid >> 4) + 16 * i;
-        const int64_t c = n0 + (tid & 15) * 8;
+        const int64_t k = k0 + over_k + 16 * i;
+        const int64_t c = n0 + over_c * 8;
         int64_t n = k < con ? p.K - c : 0;
         int64_t row = lo + k;
         if (LAYOUT == 2 && p.row_index != nullptr) {
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
       __builtin_memcpy(e, &v, 16);
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        *(E*)(at + ((tid & 15) * 8 + j) * kAnyPitch + ((tid >> 4) + 16 * i) * sizeof(E)) = e[j];
+        *(E*)(at + (over_c * 8 + j) * kAnyPitch + (over_k + 16 * i) * sizeof(E)) = e[j];
     }
   };
 

@@ -16,8 +16,8 @@ namespace mx {
 // ---------------------------------------------------------------------------
 // Any size, stride and alignment.
 //
-// 128 x 128 output tile, 4 waves of 64 x 64, contraction in steps of 64 bytes (gated products: 128; 1777
-// rows, 1034 x 1031 fp16: 32.7 us, with steps of 64 34.2; 16384 rows, 14334 x 4091: 3254 and 3838).
+// 128 x 128 output tile, 4 waves of 64 x 64, contraction in steps of 64 bytes (gated products: 128, 16384
+// rows, 14334 x 4091 fp16: 3254 us, with steps of 64 3838; and 64 rows where tiles are few).
 // Chunks go through registers: a 16-byte load at element alignment where the
 // whole chunk lies inside the operand, single elements at its edge, zeros
 // outside.  Both operands lie in LDS with the contraction contiguous; an operand whose
@@ -128,7 +128,8 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
     }
   }
   // Over rows: chunks of a wave go along the columns, which memory likes, or (backward of gated products) along
-  // the contraction, which LDS does: single values land in 8 banks side by side, not in 2.
+  // the contraction, which LDS does: single values land in 8 banks side by side, not in 2 (3 x 1031 x 2011, 3000
+  // rows: 98 us, so 148).
   const int over_k = EPI == kGatedBwd ? tid & 15 : tid >> 4, over_c = EPI == kGatedBwd ? tid >> 4 : tid & 15;
   u32x4_t ra[kPartsA], rb[kParts];
   auto fetch = [&](int64_t k0) {
@@ -292,9 +293,9 @@ hipError_t launch_any(const RaggedArgs& p, hipStream_t st) {
     const int64_t groups = std::min<int64_t>(p.G, p.R);
     // Low tiles while most CUs have none yet (half of an expert's last tile empty on average).  Measured (us,
     // 64 and 128 rows, by tiles of 128): gated 5 x 517 x 1031, 81: 25, 29, 198: 29, 32, 378: 44, 41; 8 x 777 x
-    // 2051, 208: 44, 50, 325: 85, 57; backward 5 x 517 x 1031, 110: 68, 86, 210: 93, 86; 4 x 4099 x 1000, 99: 60,
-    // 65, 165: 82, 69.
-    if (cols * (p.R / kAnyT + groups / 2) <= (EPI == kGated ? 215 : 130))
+    // 2051, 208: 44, 50, 325: 85, 57; backward 5 x 517 x 1031, 110: 41, 59, 210: 57, 58; 8 x 777 x 2051, 112: 76,
+    // 92, 175: 104, 91; 8 x 3001 x 4091, 144: 144, 162, 240: 204, 171.
+    if (cols * (p.R / kAnyT + groups / 2) <= (EPI == kGated ? 215 : 150))
       return launch_any_rows<T, O, LAYOUT, EPI, 64>(p, cols * (p.R / 64 + groups), st);
     return launch_any_rows<T, O, LAYOUT, EPI, kAnyT>(p, cols * (p.R / kAnyT + groups), st);
   } else {

@@ -839,10 +839,14 @@ def quantize_fp8(x, out=None, stream=None):
     ldx = _rows_of(x, x.dtype, (t, k), "x")
     _on_current(x, "x", stream)
     q, scale = (None, None) if out is None else out
-    q = _empty((t, k), FP8, x.device, stream) if q is None else q
-    scale = _empty((t, _blocks(k)), torch.float32, x.device, stream) if scale is None else scale
-    _need(q, FP8, (t, k), "q")
-    _need(scale, torch.float32, (t, _blocks(k)), "scale")
+    if q is None:
+        q = _empty((t, k), FP8, x.device, stream)
+    else:
+        _need(q, FP8, (t, k), "q")
+    if scale is None:
+        scale = _empty((t, _blocks(k)), torch.float32, x.device, stream)
+    else:
+        _need(scale, torch.float32, (t, _blocks(k)), "scale")
     _same_device(x, q=q, scale=scale)
     st = lib.mxfp8_quantize_fp8(_ptr(x), ty, t, k, ldx, _ptr(q), _ptr(scale), _stream(stream))
     _native.check(st, "mxfp8_quantize_fp8")
@@ -1124,14 +1128,16 @@ def residual_norm(x, f=None, residual_scale=1.0, gate=None, post_weight=None, pr
     if f is None:
         if r is not None:
             raise ValueError("r goes with f")
+    elif r is None:
+        r = _empty((t, h), x.dtype, x.device, stream)
     else:
-        r = _empty((t, h), x.dtype, x.device, stream) if r is None else r
         _need(r, x.dtype, (t, h), "r")
     if pre_weight is None:
         if y is not None:
             raise ValueError("y goes with pre_weight")
+    elif y is None:
+        y = _empty((t, h), dtype, x.device, stream)
     else:
-        y = _empty((t, h), dtype, x.device, stream) if y is None else y
         _need(y, dtype, (t, h), "y")
     _same_device(x, f=f, gate=gate, post_weight=post_weight, pre_weight=pre_weight, r=r, y=y)
     st = lib.mxfp8_residual_norm(_ptr(x), x_ty, _ptr(f), ty, t, h, residual_scale, _ptr(gate),
@@ -1176,9 +1182,9 @@ def residual_norm_bwd(dy, dr, r, f=None, residual_scale=1.0, gate=None, post_wei
                 raise ValueError(f"out.{name} is the gradient of what was not given")
             continue
         if buf is None:
-            buf = _empty(shape, kind, r.device, stream)
-            setattr(got, name, buf)
-        _need(buf, kind, shape, f"out.{name}")
+            setattr(got, name, _empty(shape, kind, r.device, stream))
+        else:
+            _need(buf, kind, shape, f"out.{name}")
     need = residual_norm_bwd_workspace_bytes(t, h) if got.post_weight is not None or got.pre_weight is not None else 0
     size = need
     if workspace is not None:

@@ -331,3 +331,12 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(got, (r2, y2, *(getattr(want, n) for n in names))):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("t,h", [(1, 16), (37, 127), (1000, 128), (50, 130), (333, 256), (9, 257)])
+def test_short_rows(t, h):
+    """Rows of 16 and 32 lanes, several to a wave; the last wave's rows not all there."""
+    case = _case(t, h, HF, F32, True, True, True)
+    kw = {k: v for k, v in case.items() if k not in ("x", "f")}
+    r, y = mx.residual_norm(case["x"], case["f"], residual_scale=0.75, **kw)
+    _check(case, 0.75, 1e-6, r, y)

@@ -8,6 +8,7 @@
 // Bound by memory: x is read once, held in registers between the maximum and the codes.
 #include <algorithm>
 
+#include "fp8_quotient.h"
 #include "ragged_common.h"
 
 namespace mx {
@@ -57,18 +58,6 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t bits) {
   b.low = inverse * (1.f - 0x1p-21f);
   b.high = inverse * (1.f + 0x1p-21f);
   return b;
-}
-
-// x / scale for the conversion, decided exactly: the quotient rounded to fp32 and, where it is
-// even (a border between two codes is) and not exact, one step towards the exact one, so that
-// it lies on the exact quotient's side of every border.
-__device__ __forceinline__ float exact_quotient(float x, float scale) {
-  if (scale < 0x1p-60f) x *= 0x1p100f, scale *= 0x1p100f;   // the remainder below keeps its bits
-  const float v = x / scale;
-  const float rest = __builtin_fmaf(-v, scale, x);
-  uint32_t bits = __float_as_uint(v);
-  if (rest != 0.f && (bits & 1) == 0) bits += (rest > 0.f) == (v > 0.f) ? 1u : ~0u;
-  return __uint_as_float(bits);
 }
 
 __device__ __forceinline__ uint2 convert(const float (&y)[8]) {

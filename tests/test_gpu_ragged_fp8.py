@@ -129,6 +129,24 @@ def test_ties_and_borders():
         _check_codes(x, q, scale)
 
 
+@pytest.mark.parametrize("exponent", [-80, 0, 40, 100, 110])
+@pytest.mark.parametrize("k", [128, 131, 264])
+def test_tiny_values_beside_borders(k, exponent):
+    """A value on a border between two codes sends its neighbours of the same eight the exact way: those far
+    below the scale are zeros of their sign, down to quotients that no number holds."""
+    line = torch.zeros(k, dtype=torch.float64)
+    tiny = [2.0 ** e for e in (-133, -126, -120, -110, -60, -30) if e < exponent - 12]
+    for lane in range(0, min(k, 128) - 8, 8):
+        line[lane] = 1.0625 * 2.0 ** exponent
+        for i in range(7):
+            line[lane + 1 + i] = (-1) ** (i + lane // 8) * tiny[(i + lane // 8) % len(tiny)]
+    line[126], line[127] = -1.1875 * 2.0 ** exponent, 448.0 * 2.0 ** exponent
+    x = torch.stack([line, -line, line.flip(0)]).to(BF).cuda()
+    _check_codes(x, *mx.quantize_fp8(x))
+    w = torch.stack([line, -line]).expand(3, 2, k).to(BF).contiguous().cuda()
+    _check_codes(w, *mx.quantize_fp8_weight(w))
+
+
 def test_special_rows():
     """Zeros, infinities and NaN: scale 0 or NaN with codes 0, the other blocks as they are."""
     x = _normal((6, 300), 1, BF)

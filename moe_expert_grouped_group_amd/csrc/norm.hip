@@ -198,6 +198,8 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
   const float each = 1.f / (float)p.H;
   const bool has_dr = ALL || p.dr != nullptr, has_dy = ALL || p.dy != nullptr, has_f = ALL || p.f != nullptr;
   const bool has_post = ALL || p.post != nullptr;
+  // without its norm, f itself is in the gate's gradient only
+  const bool uses_f = has_post || p.dgate != nullptr;
   constexpr bool kLdsSums = W > 512;
   __shared__ f32x4 lds_sums[kLdsSums ? 2 * NC * 2 * W : 1];
   float kept_sums[2][kLdsSums ? 1 : NC][8];   // of dpre, dpost
@@ -241,7 +243,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
         v.r[c].load(p.x, row * p.H + at, n);
         v.dy[c].load(p.dy, row * p.H + at, n);
       }
-      if (has_f) v.f[c].load(p.f, row * p.H + at, n);
+      if (uses_f) v.f[c].load(p.f, row * p.H + at, n);
     }
   };
   float kept_pre[kAhead ? NC : 1][8], kept_post[kAhead ? NC : 1][8];
@@ -319,7 +321,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
         o.set(e);
         o.store(p.dx, row * p.H + at, n);
       }
-      if (has_post || p.dgate != nullptr) {
+      if (uses_f) {
         float w[8];
         weights(p.post, kept_post[kAhead ? c : 0], at, w);
 #pragma unroll
@@ -327,7 +329,7 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
       }
     }
     if (!has_f) continue;
-    if (has_post || p.dgate != nullptr) row_sums<W>(dot, lds1, side1);
+    if (uses_f) row_sums<W>(dot, lds1, side1);
     if (p.dgate != nullptr && t == 0) p.dgate[row] = rf * dot[0];
     const float back = has_post ? rf * (rf * (gate * dot[0] * each)) : 0.f;
 #pragma unroll
@@ -341,7 +343,10 @@ __global__ __launch_bounds__(W < 256 ? 256 : W) void residual_norm_bwd_kernel(No
           for (int i = 0; i < 8; ++i) d[i] = __builtin_fmaf(gate * total[c][i], v.f[c].get(i) * rf, d[i]);
         });
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = gate * total[c][i] * w[i] * rf - back * (v.f[c].get(i) * rf);
+      for (int i = 0; i < 8; ++i) {
+        e[i] = gate * total[c][i] * w[i] * rf;
+        if (has_post) e[i] -= back * (v.f[c].get(i) * rf);
+      }
       if (ALL || p.df != nullptr) {
         Eight<F> o;
         o.set(e);

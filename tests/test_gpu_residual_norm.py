@@ -207,6 +207,25 @@ def test_rows_of_zeros_and_no_numbers():
     assert torch.isfinite(grad.x[[0, 1, 4]].float()).all() and torch.isnan(grad.x[2]).any()
 
 
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("h", [8, 300, 1031, 4096, 9000])
+@pytest.mark.parametrize("dtype,x_dtype", [(BF, BF), (BF, F32), (HF, HF)])
+def test_no_numbers_in_an_output_without_its_norm(dtype, x_dtype, h, gate):
+    """f without a norm of its own reaches no gradient but the gate's: df = gate dr, whatever f holds."""
+    t = 7
+    case = _case(t, h, dtype, x_dtype, False, gate, False)
+    f, gates = case["f"], case["gate"]
+    f[1, h - 1], f[2], f[3, 0] = math.inf, math.nan, -math.inf
+    dr = _draw((t, h), 21, x_dtype)
+    r, _ = mx.residual_norm(case["x"], f, residual_scale=0.5, gate=gates)
+    grad = mx.residual_norm_bwd(None, dr, r, f, residual_scale=0.5, gate=gates)
+    g = 1.0 if gates is None else gates[:, None]
+    assert torch.equal(grad.f, (g * dr.float()).to(dtype))
+    assert torch.equal(grad.x, (0.5 * dr.float()).to(x_dtype))
+    if gate:
+        assert torch.isfinite(grad.gate[[0, 4, 5, 6]]).all() and not torch.isfinite(grad.gate[1:4]).any()
+
+
 def test_in_place_and_buffers():
     """r may be x; dx may be dr, df may be dy or f."""
     t, h = 40, 520

@@ -4,13 +4,7 @@
 
 #include <cstdint>
 
-#ifdef __HIP__
-#include <hip/hip_runtime.h>
-
-#define MX_BOTH_SIDES __host__ __device__ __forceinline__
-#else
-#define MX_BOTH_SIDES inline
-#endif
+#include "both_sides.h"
 
 namespace mx {
 

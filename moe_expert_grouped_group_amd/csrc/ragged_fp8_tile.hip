@@ -22,6 +22,7 @@
 // turn 6 %.
 #include <type_traits>
 
+#include "fp8_tile_ranges.h"
 #include "ragged_tile_launch.h"
 
 namespace mx {
@@ -134,10 +135,10 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
       return x >= 0 && x < p.S ? x : (int32_t)-1;
     };
     const int64_t first = gather ? 0 : t.row0, count = (gather ? p.S : p.R) - first;
-    sa = bounded((const uint8_t*)p.a + first * p.lda, (count - 1) * p.lda + p.K);
+    sa = bounded((const uint8_t*)p.a + first * p.lda, rows_range(count, p.lda, p.K));
     const uint8_t* w = (const uint8_t*)p.b + ((int64_t)t.g * p.N + t.n0) * p.K;
-    sb[0] = bounded(w, (p.N - t.n0) * p.K);
-    sb[1] = bounded(w + 16 * p.K, (p.N - t.n0 - 16) * p.K);
+    sb[0] = bounded(w, rows_range(p.N - t.n0, p.K, p.K));
+    sb[1] = bounded(w + 16 * p.K, rows_range(p.N - t.n0 - 16, p.K, p.K));
 #pragma unroll
     for (int j = 0; j < kCopiesA; ++j) {
       const int32_t r = row(8 * (kCopiesA * wave + j) + (lane >> 3));
@@ -146,11 +147,11 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
     // waves of rows copy their scales; the next one those of the two halves of the columns
     if (64 * wave < kTileM) {
       const int32_t r = row(64 * wave + lane);
-      ss = bounded(p.sa + first * kb, count * kb * 4);
+      ss = bounded(p.sa + first * kb, rows_range(count, kb * 4, kb * 4));
       vs = r < 0 ? kOut : (uint32_t)r * (uint32_t)kb * 4u;
     } else {
       const int64_t nb = (p.N + 127) / 128, b0 = t.n0 / 128;
-      ss = bounded(p.sb + ((int64_t)t.g * nb + b0) * kb, (nb - b0) * kb * 4);
+      ss = bounded(p.sb + ((int64_t)t.g * nb + b0) * kb, rows_range(nb - b0, kb * 4, kb * 4));
       vs = lane < 2 ? (uint32_t)lane * (uint32_t)kb * 4u : kOut;
     }
   };
@@ -211,7 +212,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
     if constexpr (c < kCopiesA)
       copy16(sa, va[c] | past[(kCopiesA * wave + c) & 1], soff, to_stage + (uint32_t)((kCopiesA * wave + c) * 1024));
     else
-      copy16(sb[(c - kCopiesA) >> 1], vb[(c - kCopiesA) & 1] | past[(c - kCopiesA) & 1], soff,
+      copy16(sb[(c - kCopiesA) >> 1], vb[(c - kCopiesA) & 1] | past[(c - kCopiesA) & 1],
+             c - kCopiesA < 2 ? soff : row_offset((uint32_t)sb[1][2], soff),
              to_stage + kOffB + (uint32_t)((4 * wave + c - kCopiesA) * 1024));
   };
 

@@ -686,11 +686,8 @@ mxfp8_status mxfp8_quantize_fp8_weight(const void* w, int32_t type, int64_t G, i
 /*
  * mxfp8_ragged_gemm_fp8 -- the forward product of ragged experts on such data:
  *   C[r, n] = sum_b scale[i(r), b] w_scale[g, n / 128, b] sum_{k in block b} q[i(r), k] w[g, n, k]
- * The two scales are multiplied first (one fp32 rounding), blocks are added in fp32, the result
- * is rounded once to its type.  fp32 results: a block's sum is fp32 too.  bf16 and fp16
- * results: it may be formed by matrix instructions that keep 13 bits below a block's largest
- * partial sum (an error of about 1.5e-5 of the sum on normal values; at most 2^-9 of the
- * sum of the largest 8 consecutive products' sizes).
+ * The two scales are multiplied first (one fp32 rounding), blocks are formed and added in fp32,
+ * the result is rounded once to its type.
  *   q [S, K], row stride ldq;  scale [S, ceil(K / 128)];  w [G, N, K];
  *   w_scale [G, ceil(N / 128), ceil(K / 128)];  c [R, N], row stride ldc, c_type any
  *   mxfp8_type;  the rest as mxfp8_ragged_gemm (NT).  Rows of zeros have scale 0.  For the
@@ -705,6 +702,20 @@ mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* s
                                    const int32_t* row_index, void* workspace, size_t workspace_bytes,
                                    void* stream);
 size_t mxfp8_ragged_gemm_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
+
+/*
+ * mxfp8_ragged_gemm_fp8_fast -- the same with fewer bits in the sums, where speed counts for more: a
+ * block's sum may be formed by 8-bit matrix instructions, which keep 13 bits below the largest
+ * of 8 consecutive products (an error of about 1.5e-5 of the sum on normal values; at most 2^-9
+ * of the sum of the largest 8 consecutive products' sizes).  Sizes and alignment decide whether it is, so
+ * that a row's result may differ with the rows beside it.  Arguments and workspace as there.
+ * Errors: as there, and ENOTSUP for fp32 results.
+ */
+mxfp8_status mxfp8_ragged_gemm_fp8_fast(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
+                                        const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
+                                        int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
+                                        const int32_t* row_index, void* workspace, size_t workspace_bytes,
+                                        void* stream);
 
 /*
  * mxfp8_residual_norm -- what follows a block whose output is f (for an expert layer, the

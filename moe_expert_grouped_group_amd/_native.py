@@ -73,6 +73,8 @@ SIGNATURES = {
     "mxfp8_quantize_fp8_weight": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "mxfp8_ragged_gemm_fp8": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64, c_i64, c_i64,
                                       c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
+    "mxfp8_ragged_gemm_fp8_fast": (c_i32, [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i64, c_i64, c_i64,
+                                           c_i64, c_vp, c_i32, c_vp, c_vp, c_size, c_vp]),
     "mxfp8_ragged_gemm_fp8_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i32]),
     "mxfp8_residual_norm": (c_i32, [c_vp, c_i32, c_vp, c_i32, c_i64, c_i64, c_f32, c_vp, c_vp, c_vp, c_i32,
                                     c_f32, c_vp, c_vp, c_vp]),
@@ -91,7 +93,7 @@ SIGNATURES = {
                                       c_vp, c_vp, c_vp]),
 }
 
-ABI_VERSION = 5
+ABI_VERSION = 6
 
 MXFP8_OK, MXFP8_EINVAL, MXFP8_ENOTSUP, MXFP8_EHIP = 0, 1, 2, 3
 

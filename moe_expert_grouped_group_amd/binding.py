@@ -884,13 +884,14 @@ def ragged_gemm_fp8_workspace_bytes(rows, x_rows, n, k, groups):
 
 
 def ragged_gemm_fp8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=torch.bfloat16,
-                    out=None, stream=None, workspace=None):
+                    out=None, stream=None, workspace=None, fast_sums=False):
     """Forward product in 8-bit floating point: q [S, K] with scale [S, ceil(K / 128)] (as
     quantize_fp8 gives them), w [G, N, K] with w_scale [G, ceil(N / 128), ceil(K / 128)] (as
     quantize_fp8_weight) -> [R, N], the sum over blocks of (sum of q w) * scale * w_scale.
     row_index and m_splits as ragged_gemm, the workspace of ragged_gemm_fp8_workspace_bytes.
-    q and out may have a row stride.  fp32 results are fp32 sums throughout; those of bf16 and fp16
-    may be formed by faster instructions that keep fewer bits (mxfp8_ragged_gemm_fp8)."""
+    q and out may have a row stride.  Sums are fp32 throughout.  fast_sums=True (results of 16
+    bits): a block's sum may be formed by faster instructions that keep fewer bits
+    (mxfp8_ragged_gemm_fp8_fast)."""
     lib = _lib()
     ms = _splits(m_splits)
     g = ms.numel()
@@ -907,6 +908,8 @@ def ragged_gemm_fp8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=to
     _on_current(q, "q", stream)
     if out_dtype not in _TYPE:
         raise NotImplementedError(f"output dtype {out_dtype} is not supported")
+    if fast_sums and out_dtype == torch.float32:
+        raise NotImplementedError("fast_sums of fp32 results is not supported")
     if out is None:
         out = _empty((r, n), out_dtype, q.device, stream)
     ldc = _rows_of(out, out_dtype, (r, n), "out")
@@ -918,10 +921,10 @@ def ragged_gemm_fp8(q, scale, w, w_scale, m_splits, row_index=None, out_dtype=to
         workspace = _scratch(need, q.device, stream)
     _same_device(q, scale=scale, w=w, w_scale=w_scale, m_splits=ms, row_index=index, out=out,
                  workspace=workspace)
-    st = lib.mxfp8_ragged_gemm_fp8(_ptr(q), ldq, _ptr(scale), _ptr(w), _ptr(w_scale), _ptr(out), ldc,
-                                   _TYPE[out_dtype], r, s, n, k, _ptr(ms), g, _ptr(index),
-                                   _ptr(workspace), size, _stream(stream))
-    _native.check(st, "mxfp8_ragged_gemm_fp8")
+    fn = "mxfp8_ragged_gemm_fp8_fast" if fast_sums else "mxfp8_ragged_gemm_fp8"
+    st = getattr(lib, fn)(_ptr(q), ldq, _ptr(scale), _ptr(w), _ptr(w_scale), _ptr(out), ldc, _TYPE[out_dtype], r,
+                          s, n, k, _ptr(ms), g, _ptr(index), _ptr(workspace), size, _stream(stream))
+    _native.check(st, fn)
     return out
 
 

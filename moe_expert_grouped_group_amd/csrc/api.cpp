@@ -68,7 +68,7 @@ extern "C" {
 
 const char* mxfp8_last_error(void) { return g_err; }
 
-int32_t mxfp8_abi_version(void) { return 5; }
+int32_t mxfp8_abi_version(void) { return 6; }
 
 size_t mxfp8_dbias_workspace_bytes(int64_t T, int64_t N) {
   if (T <= 0 || N <= 0) return 0;
@@ -732,12 +732,12 @@ size_t mxfp8_ragged_gemm_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, in
   return mx::ragged_fp8_workspace_bytes(R, S, N, K, G);
 }
 
-mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
-                                   const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
-                                   int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
-                                   const int32_t* row_index, void* workspace, size_t workspace_bytes,
-                                   void* stream) {
-  const char* fn = "mxfp8_ragged_gemm_fp8";
+namespace {
+
+mxfp8_status ragged_gemm_fp8(const char* fn, bool fast, const uint8_t* q, int64_t ldq, const float* scale,
+                             const uint8_t* w, const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
+                             int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
+                             const int32_t* row_index, void* workspace, size_t workspace_bytes, void* stream) {
   if (c_type != MXFP8_TYPE_F32 && c_type != MXFP8_TYPE_BF16 && c_type != MXFP8_TYPE_F16)
     return fail(MXFP8_ENOTSUP, "%s: output type %d is not supported", fn, (int)c_type);
   mxfp8_status st = check_ragged(fn, MXFP8_LAYOUT_NT, R, S, N, K, m_splits, G, row_index);
@@ -767,8 +767,30 @@ mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* s
   p.G = G;
   p.ws = usable_workspace(workspace);
   return hip_status(mx::launch_ragged_gemm_fp8(
-                        c_type, p, p.ws != nullptr ? workspace_bytes : 0, as_stream(stream)),
+                        c_type, fast, p, p.ws != nullptr ? workspace_bytes : 0, as_stream(stream)),
                     fn);
+}
+
+}  // namespace
+
+mxfp8_status mxfp8_ragged_gemm_fp8(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
+                                   const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
+                                   int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
+                                   const int32_t* row_index, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  return ragged_gemm_fp8("mxfp8_ragged_gemm_fp8", false, q, ldq, scale, w, w_scale, c, ldc, c_type, R, S, N, K,
+                         m_splits, G, row_index, workspace, workspace_bytes, stream);
+}
+
+mxfp8_status mxfp8_ragged_gemm_fp8_fast(const uint8_t* q, int64_t ldq, const float* scale, const uint8_t* w,
+                                        const float* w_scale, void* c, int64_t ldc, int32_t c_type, int64_t R,
+                                        int64_t S, int64_t N, int64_t K, const int64_t* m_splits, int32_t G,
+                                        const int32_t* row_index, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  const char* fn = "mxfp8_ragged_gemm_fp8_fast";
+  if (c_type == MXFP8_TYPE_F32) return fail(MXFP8_ENOTSUP, "%s: fp32 results need fp32 sums", fn);
+  return ragged_gemm_fp8(fn, true, q, ldq, scale, w, w_scale, c, ldc, c_type, R, S, N, K, m_splits, G, row_index,
+                         workspace, workspace_bytes, stream);
 }
 
 namespace {

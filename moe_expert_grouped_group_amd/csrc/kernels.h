@@ -74,12 +74,12 @@ int64_t ragged_blocks(int layout, int64_t R, int64_t N, int64_t K, int32_t G);
 hipError_t launch_quantize_int8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx,
                                 int8_t* q, float* scale, hipStream_t st);
 // 8-bit floating point with a scale for each block of 128 (fp8.hip, ragged_fp8.hip); out: 0 fp32,
-// 1 bf16, 2 fp16.
+// 1 bf16, 2 fp16; fast: sums of 16-bit results may be formed by the 8-bit matrix instructions.
 hipError_t launch_quantize_fp8(const void* x, bool f16, int64_t T, int64_t K, int64_t ldx, uint8_t* q,
                                float* scale, hipStream_t st);
 hipError_t launch_quantize_fp8_weight(const void* w, bool f16, int64_t G, int64_t N, int64_t K, uint8_t* q,
                                       float* scale, hipStream_t st);
-hipError_t launch_ragged_gemm_fp8(int out, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
+hipError_t launch_ragged_gemm_fp8(int out, bool fast, const RaggedArgs& p, size_t ws_bytes, hipStream_t st);
 size_t ragged_fp8_workspace_bytes(int64_t R, int64_t S, int64_t N, int64_t K, int32_t G);
 // The norms around a block (norm.hip).
 int64_t norm_max_hidden();

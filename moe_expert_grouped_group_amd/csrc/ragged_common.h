@@ -94,8 +94,14 @@ hipError_t launch_ragged_tile_gated(bool f16, const RaggedArgs& p, hipStream_t s
 hipError_t launch_ragged_tile_gated_f16(const RaggedArgs& p, hipStream_t st);
 hipError_t launch_ragged_tile_gated_bwd(bool f16, const RaggedArgs& p, hipStream_t st);
 // 8-bit floating point (ragged_fp8.hip has the formula, ragged_fp8_tile.hip the large tiles).
-hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st);
-bool ragged_fp8_splits(const RaggedArgs& p);
+hipError_t launch_ragged_fp8_tile(int out, bool fast, const RaggedArgs& p, hipStream_t st);
+// Rows of a tile, whether tiles may be split, about how long it takes (us; fp32 sums only).
+struct Fp8Plan {
+  int rows;
+  bool split;
+  double us;
+};
+Fp8Plan ragged_fp8_plan(bool fast, bool can_split, const RaggedArgs& p);
 size_t ragged_split_bytes();   // a partial 256 x 256 tile for each CU
 
 // Longest range of a bounded operand (32-bit offsets, less what marks a lane that
@@ -156,6 +162,15 @@ template <typename T>
 __device__ __forceinline__ float widen(uint16_t v) {
   if constexpr (std::is_same<T, TypeF16>::value) return (float)__builtin_bit_cast(_Float16, v);
   else return __uint_as_float((uint32_t)v << 16);
+}
+
+// 8 codes of 8-bit floating point (e4m3) as bf16 values: exact, e4m3 has 3 bits behind the leading one.
+__device__ __forceinline__ u32x4_t widen_codes8(uint32_t lo, uint32_t hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return u32x4_t{__builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
+                 __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
+                 __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
+                 __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true))};
 }
 
 // Output conversion: one rounding (nearest even) of the fp32 value.

@@ -3,23 +3,29 @@
 //
 // One workgroup per CU walks output tiles of 32 RF x 256; 8 waves, 2 x 4, each 16 RF x 64.  Operands go
 // from memory to LDS without passing registers, in stages of 128 contraction bytes: one block of scales
-// (two slots, rows and chunks laid out as in ragged_tile.h).  A stage is one 16 x 16 x 128 matrix
-// instruction for each 16 x 16 block of the result, which starts from zero; its sums times the two scales
-// are added to the fp32 sums by vector instructions, which run beside the next matrix instructions
-// (16 cycles to 32).  They cannot reach the accumulation registers: eight waves of 128 sums each in
-// ordinary registers, not four of 256.
+// (two slots, rows and chunks laid out as in ragged_tile.h).  A stage's sums start from zero for each
+// 16 x 16 block of the result; times the two scales they are added to the fp32 sums by vector
+// instructions, which run beside the next matrix instructions.  Those cannot reach the accumulation
+// registers: eight waves of 128 sums each in ordinary registers, not four of 256.
 //
-// The 8-bit matrix instruction keeps 13 bits below the largest partial sum of its 128 products (1.5e-5
-// of a block's sum on normal values); between blocks the sums are fp32.  It runs at twice the rate of
-// the bf16 ones that an exact sum would take.
-//
-// 8 x 4096 x 14336, 16384 rows: 950 to 1060 us by the machine's clock, 1.8 to 2.0 PFLOP/s, where the MXFP8
-// product of this package, whose scales the matrix instruction applies itself, takes 929 (zeros: 920; matrix
-// cores busy 51 % at 1.86 GHz).  Without its copies to LDS the kernel takes 870, with every copy hitting L2 1045, without the
-// scaling 1081 beside 1157 at the time.  All of a wave's copies at once instead of one to a matrix
-// instruction cost 4 %, one to two or three 2 and 5 %; a second meeting half way, so that three
-// quarters of the copies go out half a stage earlier, 0 to 1 %; the two waves of a SIMD copying in
-// turn 6 %.
+// The sums of a stage (FAST chooses):
+//  * fp32: four 16 x 16 x 32 bf16 matrix instructions on widened codes.  A wave widens what it has read
+//    from LDS, in registers: 12 conversions for 8 matrix instructions (16 cycles each), the rows of the
+//    next group beside the last block of this one, the columns of the next stage beside the last block of
+//    this one and the first three of the next.  Widened once into LDS instead, the tile would be read at
+//    twice the bytes: 3072 of the 4096 cycles that a stage's matrix instructions take, and the widening's
+//    reads and writes come on top.
+//    8 x 4096 x 14336, 16384 rows: 1500 us, 1.28 PFLOP/s, the power that bf16 matrix instructions draw (the
+//    bf16 product of ragged_tile.h 1.2).
+//  * 8-bit (the caller asked for them): one 16 x 16 x 128 instruction, which keeps 13 bits below the
+//    largest of 8 consecutive products (1.5e-5 of a block's sum on normal values, where bf16 has 9e-9; the 16 x 16 x
+//    32 one for 8-bit operands the same).  It runs at twice the rate: 950 to 1060 us by the machine's clock, 1.8
+//    to 2.0 PFLOP/s, where the MXFP8 product of this package, whose scales the matrix instruction applies
+//    itself, takes 929 (zeros: 920; matrix cores busy 51 % at 1.86 GHz).  Without its copies to LDS the kernel
+//    takes 870, with every copy hitting L2 1045, without the scaling 1081 beside 1157 at the time.  All of
+//    a wave's copies at once instead of one to a block cost 4 %, one to two or three 2 and 5 %; a second
+//    meeting half way, so that three quarters of the copies go out half a stage earlier, 0 to 1 %; the two
+//    waves of a SIMD copying in turn 6 %.
 #include <type_traits>
 
 #include "fp8_tile_ranges.h"
@@ -31,14 +37,14 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kF8Threads = 512;
 
-template <typename O, int RF>
+template <typename O, int RF, bool FAST>
 __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedArgs kernel_args) {
   constexpr int kTileM = 32 * RF;
   constexpr int kOffB = kTileM * kStageK, kStage = kOffB + kTileN * kStageK;
   constexpr int kCopiesA = RF / 2;                 // of a wave for a stage: 8 rows each; 4 of B
   constexpr int kGroup = 4;                        // blocks whose scales are copied together
   constexpr int kBlocks = 4 * RF;                  // matrix instructions of a wave for a stage
-  constexpr int kLag = 3;                          // of them between one and the use of its sums
+  constexpr int kLag = FAST ? 3 : 1;               // blocks between one and the use of its sums
   static_assert(RF == 8 || RF == 4 || RF == 2, "");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
   // scales of four blocks: [row][4], then [half of the columns][4], twice
@@ -248,27 +254,42 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
   const uint32_t row_scale = scale0 + (uint32_t)((wm * 16 * RF + (lane & 15)) * kGroup * 4);
   const uint32_t col_scale = scale0 + (uint32_t)((kTileM + (wn >> 1)) * kGroup * 4);
 
-  // A stage: RF groups of 16 rows, 4 matrix instructions each, from zero.  Each one's sums are scaled and
-  // added kLag instructions later, beside those that run then; the next group's fragments are read
+  // A stage: RF groups of 16 rows, 4 blocks each, from zero.  Each one's sums are scaled and
+  // added kLag blocks later, beside the instructions that run then; the next group's fragments are read
   // meanwhile.  Ahead of the last group every fragment of the stage is in registers: there the waves
   // meet (the next stage has landed, this one's slot is free), and the last group's instructions cover
-  // the first reads of the next stage.
-  f32x4 acc[RF][4], part[4];
-  i32x8 fa[2], fb[4];
+  // the first reads of the next stage.  (!FAST: registers are few.  fb holds codes of two blocks of B on their
+  // way to wb: 1 and 2 at a stage's start, with block 0 widened before it.)
+  constexpr int kKept = kLag + 1;   // blocks whose sums are not added yet
+  f32x4 acc[RF][4], part[kKept];
   float before = 0.f, mine = 0.f;   // scales of the group before and of this one
   int slot = 0, side = 0;           // of the stage computed
-#pragma unroll
-  for (int j = 0; j < 4; ++j) fb[j] = fragment(base_b + lane_at, j * 2048);
+  i32x8 fa[FAST ? 2 : 1], fb[FAST ? 4 : 2];
+  u32x4_t wa[4], wb[4][4];   // !FAST: runs of 32 of the contraction, in bf16
+  auto widened = [](const i32x8& c, int s) { return widen_codes8((uint32_t)c[2 * s], (uint32_t)c[2 * s + 1]); };
   fa[0] = fragment(base_a + lane_at, 0);
+  if constexpr (FAST) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fb[j] = fragment(base_b + lane_at, j * 2048);
+  } else {
+    fb[0] = fragment(base_b + lane_at, 0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      wa[s] = widened(fa[0], s);
+      wb[0][s] = widened(fb[0], s);
+    }
+    fb[1] = fragment(base_b + lane_at, 2048);
+    fb[0] = fragment(base_b + lane_at, 2 * 2048);
+  }
   float row = *(lds_f32_t*)(row_scale + (uint32_t)((t.first & 3) * 4));
   float col = *(lds_f32_t*)(col_scale + (uint32_t)((t.first & 3) * 4));
   // the sums of block n - kLag of a stage (or of the stage before)
-  auto add = [&](auto N) {
+  auto add = [&](auto N, int from, int to) {
     constexpr int n = (decltype(N)::value + kBlocks - kLag) % kBlocks, i = n / 4, j = n % 4;
     constexpr bool same = decltype(N)::value / 4 == i;
     const float s = same ? mine : before;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[n % 4][e], s, acc[i][j][e]);
+    for (int e = from; e < to; ++e) acc[i][j][e] = __builtin_fmaf(part[n % kKept][e], s, acc[i][j][e]);
     // (held in place: the compiler would move all of a stage's sums behind its branches)
     asm volatile("" : "+v"(acc[i][j]));
   };
@@ -280,7 +301,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part[j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < kKept; ++j) part[j] = f32x4{0, 0, 0, 0};
     const int end = t.end;
     for (int st = t.first; st < end; ++st) {
       const uint32_t at_a = hide(lane_at + (base_a + (uint32_t)(slot * kStage)));
@@ -291,7 +312,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
         before = mine;
         mine = row * col;
         if constexpr (i + 1 < RF) {
-          fa[(i + 1) & 1] = fragment(at_a, (i + 1) * 2048);
+          fa[FAST ? (i + 1) & 1 : 0] = fragment(at_a, (i + 1) * 2048);
           row = *(lds_f32_t*)(at_row + (uint32_t)((i + 1) * 16 * kGroup * 4));
         } else {
           __builtin_amdgcn_s_waitcnt(vm_wait(0));
@@ -308,28 +329,50 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
           row = *(lds_f32_t*)hide(row_scale + to);
           col = *(lds_f32_t*)hide(col_scale + to);
           at_b = hide(lane_at + (base_b + (uint32_t)(slot * kStage)));
+          if constexpr (!FAST) fa[0] = fragment(hide(lane_at + (base_a + (uint32_t)(slot * kStage))), 0);
         }
         __builtin_amdgcn_sched_barrier(0);
         unroll<4>([&](auto J) {
           constexpr int j = decltype(J)::value;
           using N = std::integral_constant<int, 4 * i + j>;
-          part[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], f32x4{0, 0, 0, 0}, 0, 0, 0, 127,
-                                                                     0, 127);
-          asm volatile("" : "+v"(part[j]));
-          __builtin_amdgcn_sched_barrier(0);
-          add(N{});
-          if constexpr (i == RF - 1) fb[j] = fragment(at_b, j * 2048);
+          f32x4& sum = part[N::value % kKept];
+          if constexpr (FAST) {
+            sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], f32x4{0, 0, 0, 0}, 0, 0, 0, 127, 0,
+                                                                   127);
+            asm volatile("" : "+v"(sum));
+            __builtin_amdgcn_sched_barrier(0);
+            add(N{}, 0, 4);
+            if constexpr (i == RF - 1) fb[j] = fragment(at_b, j * 2048);
+          } else {
+            unroll<4>([&](auto S) {
+              constexpr int s = decltype(S)::value;
+              sum = TypeBf16::mma16(wb[j][s], wa[s], s == 0 ? f32x4{0, 0, 0, 0} : sum);
+              asm volatile("" : "+v"(sum));
+              __builtin_amdgcn_sched_barrier(0);
+              if constexpr (s == 1) add(N{}, 0, 2);
+              if constexpr (s == 2) add(N{}, 2, 4);
+              if constexpr (j == 3) wa[s] = widened(fa[0], s);
+              if constexpr (i == 0 && j < 3) wb[j + 1][s] = widened(fb[(j + 1) & 1], s);
+              if constexpr (i == RF - 1 && j == 2) wb[0][s] = widened(fb[0], s);
+              __builtin_amdgcn_sched_barrier(0);
+            });
+            // the codes of B: the next stage's first two once a block of this one's is done
+            if constexpr (i == RF - 1 && j == 0) fb[0] = fragment(at_b, 0), fb[1] = fragment(at_b, 2048);
+            if constexpr (i == RF - 1 && j == 2) fb[0] = fragment(at_b, 2 * 2048);
+            if constexpr (i == 0 && j == 0)
+              fb[1] = fragment(hide(lane_at + (base_b + (uint32_t)(slot * kStage))), 3 * 2048);
+          }
           // the copies of the stage two ahead go out one to a matrix instruction, from the last group on
           constexpr int at = ((i + 1) % RF) * 4 + j;
           if constexpr (at < kCopies) copy(std::integral_constant<int, at>{});
           __builtin_amdgcn_sched_barrier(0);
         });
-        if constexpr (i == RF - 1) fa[0] = fragment(hide(lane_at + (base_a + (uint32_t)(slot * kStage))), 0);
+        if constexpr (FAST && i == RF - 1) fa[0] = fragment(hide(lane_at + (base_a + (uint32_t)(slot * kStage))), 0);
       });
     }
     // the last kLag blocks
     before = mine;
-    unroll<kLag>([&](auto N) { add(N); });
+    unroll<kLag>([&](auto N) { add(N, 0, 4); });
     mine = 0.f;
 
     if (t.split >= 0) {
@@ -411,21 +454,11 @@ __global__ __launch_bounds__(256) void ragged_fp8_join_kernel(RaggedArgs p, uint
 
 namespace {
 
-// Rows of a tile: low ones for experts of few rows and where high ones would leave CUs idle (half of an
-// expert's last tile empty on average).  Measured (us, 64, 128 and 256 rows): 8 x 14336 x 4096, 32 rows an
-// expert 106, 112, 126, 96 rows 179, 125, 134; 8 x 2048 x 2048, 128 rows 24, 25, 32, 512 rows 39 to 55, 29 to
-// 46 (uneven), 36; 4 x 7168 x 4096, 192 rows 69, 52, 56, 256 rows 76, 52 to 79, 57.
-int64_t fp8_tile_rows(const RaggedArgs& p) {
-  const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
-  if (mean <= 32) return 64;
-  return mean <= 96 || (p.R / 128 + groups / 2) * ((p.N + kTileN - 1) / kTileN) <= compute_units() ? 128 : 256;
-}
-
-template <typename O, int RF>
+template <typename O, int RF, bool FAST>
 hipError_t launch_fp8_tile(const RaggedArgs& p, hipStream_t st) {
   const int64_t m = 32 * RF, tiles = ((p.N + kTileN - 1) / kTileN) * (p.R / m + std::min<int64_t>(p.G, p.R));
   const unsigned grid = (unsigned)(p.ws != nullptr ? compute_units() : std::min<int64_t>(tiles, compute_units()));
-  ragged_fp8_tile_kernel<O, RF><<<dim3(grid), dim3(kF8Threads), 0, st>>>(p);
+  ragged_fp8_tile_kernel<O, RF, FAST><<<dim3(grid), dim3(kF8Threads), 0, st>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.ws == nullptr) return e;
   // half the tiles of a round at most are split
@@ -434,24 +467,31 @@ hipError_t launch_fp8_tile(const RaggedArgs& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename O>
-hipError_t launch_fp8_tile_rows(const RaggedArgs& p, hipStream_t st) {
-  const int64_t rows = fp8_tile_rows(p);
-  if (rows == 64) return launch_fp8_tile<O, 2>(p, st);
-  return rows == 128 ? launch_fp8_tile<O, 4>(p, st) : launch_fp8_tile<O, 8>(p, st);
+template <typename O, bool FAST>
+hipError_t launch_fp8_tile_rows(int rows, const RaggedArgs& p, hipStream_t st) {
+  if (rows == 64) return launch_fp8_tile<O, 2, FAST>(p, st);
+  return rows == 128 ? launch_fp8_tile<O, 4, FAST>(p, st) : launch_fp8_tile<O, 8, FAST>(p, st);
 }
 
-}  // namespace
+// 8-bit sums.  Rows of a tile: low ones for experts of few rows and where high ones would leave CUs idle (half
+// of an expert's last tile empty on average).  Measured (us, 64, 128 and 256 rows): 8 x 14336 x 4096, 32 rows an
+// expert 106, 112, 126, 96 rows 179, 125, 134; 8 x 2048 x 2048, 128 rows 24, 25, 32, 512 rows 39 to 55, 29 to
+// 46 (uneven), 36; 4 x 7168 x 4096, 192 rows 69, 52, 56, 256 rows 76, 52 to 79, 57.
+int fast_rows(const RaggedArgs& p) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R), mean = p.R / groups;
+  if (mean <= 32) return 64;
+  return mean <= 96 || (p.R / 128 + groups / 2) * ((p.N + kTileN - 1) / kTileN) <= compute_units() ? 128 : 256;
+}
 
-// Whether a launch may split tiles (the table in the kernel, which has the experts' rows, decides on how
-// many parts): the stages saved, as units_of counts them, have to pay the second launch and the
+// 8-bit sums.  Whether a launch may split tiles (the table in the kernel, which has the experts' rows, decides on
+// how many parts): the stages saved, as units_of counts them, have to pay the second launch and the
 // workspace, about 8 us or six stages, where experts' rows are even or on average over the numbers of
 // tiles that uneven ones can make.  Measured (us, whole, split; on the same kernel with a
 // slower start, 10 us on both): 1 x 4096 x 14336, 257 rows 168, 76;
 // 8 x 4096 x 14336, 768 rows 191, 142, 2048 rows 229, 178; 8 x 2048 x 7168, 1024 rows 93, 77; 1 x 4096 x
 // 4096, 200 rows 56, 44; and with nothing to split 8 x 2048 x 2048, 2048 rows 42, 50.
-bool ragged_fp8_splits(const RaggedArgs& p) {
-  const int64_t groups = std::min<int64_t>(p.G, p.R), m = fp8_tile_rows(p), stages = (p.K + 127) / 128;
+bool fast_splits(const RaggedArgs& p, int64_t m) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R), stages = (p.K + 127) / 128;
   const int64_t ctiles = (p.N + kTileN - 1) / kTileN;
   auto saved = [&](int64_t rtiles) -> int64_t {
     const Units u = units_of((uint32_t)std::min<int64_t>(rtiles * ctiles, 1 << 30), (uint32_t)compute_units(), stages, true);
@@ -464,8 +504,59 @@ bool ragged_fp8_splits(const RaggedArgs& p) {
   return sum > 6 * 8;
 }
 
-hipError_t launch_ragged_fp8_tile(int out, const RaggedArgs& p, hipStream_t st) {
-  return out == 1 ? launch_fp8_tile_rows<OutBf16>(p, st) : launch_fp8_tile_rows<OutF16>(p, st);
+// fp32 sums.  About what a launch takes, in us, by the rows of its tiles: a stage while each CU has a tile, what
+// comes once, a second launch where tiles may be split (half of it also if none is).  Half by the number of tiles
+// of even experts, half by the mean over the numbers that uneven ones can make.  Measured, even experts and ones
+// of 0.2 to 1.8 times the mean (64, 128 and 256 rows; s: may be split):
+//   1 x 4096 x 4096    128 rows each  47  58  95, s  32  32  47    256:  47  59  96, s  50  40  49
+//                              1024:  50  64  97, s  52  65  99
+//   8 x 2048 x 2048    128 rows each  29  35  53, s  31  37  56    256:  29  36  54, s  32  39  57; uneven 50  37  55
+//   4 x 4096 x 4096    192 rows each  52  61  96, s  54  65  99    512:  91  66  98; uneven 130 116 100, s 116  97 102
+//   8 x 4096 x 7168     96 rows each  89 102 162                   256: 168 109 163; uneven 223 197 168, s 203 164 171
+//   64 x 2048 x 1024    64 rows each  36  42  64; uneven  47  58  65;   128:  59  46  66; uneven  71  77  92
+//   8 x 14336 x 4096    64 rows each 126 145 216; uneven 170 144 204;   128: 221 151 215; uneven 260 207 204
+//                                                                       512: 705 466 416; uneven 709 506 493
+Fp8Plan fp32_sums_plan(const RaggedArgs& p, bool can_split) {
+  const int64_t groups = std::min<int64_t>(p.G, p.R), stages = (p.K + 127) / 128;
+  const int64_t ctiles = (p.N + kTileN - 1) / kTileN, cus = compute_units();
+  const struct { int rows; double stage, once; } kinds[] = {{64, 1.25, 7.0}, {128, 1.6, 8.0}, {256, 2.66, 10.5}};
+  Fp8Plan best{0, false, 0.0};
+  for (const auto& kind : kinds)
+    for (int split = 0; split <= (can_split ? 1 : 0); ++split) {
+      auto us = [&](int64_t rtiles) {
+        const Units u = units_of((uint32_t)std::min<int64_t>(rtiles * ctiles, 1 << 30), (uint32_t)cus, stages, split != 0);
+        const double last = u.rem == 0 ? 0.0 : u.parts > 1 ? (double)((stages + u.parts - 1) / u.parts) + 3.0 / kind.stage
+                                                           : (double)stages;
+        return kind.once + 3.0 * split + kind.stage * ((double)stages * (double)(u.full / cus) + last);
+      };
+      const int64_t least = (p.R + kind.rows - 1) / kind.rows, most = p.R / kind.rows + groups;
+      double uneven = 0.0;
+      for (int i = 0; i < 8; ++i) uneven += us(least + (most - least) * i / 7) / 8;
+      const double both = 0.5 * (us(groups * ((p.R / groups + kind.rows - 1) / kind.rows)) + uneven);
+      if (best.rows == 0 || both < best.us) best = Fp8Plan{kind.rows, split != 0, both};
+    }
+  // (reading the weights takes its time, however few the rows)
+  best.us = std::max(best.us, 7.0 + 1e-6 * (double)groups * (double)p.N * (double)p.K / 4.7);
+  return best;
+}
+
+}  // namespace
+
+Fp8Plan ragged_fp8_plan(bool fast, bool can_split, const RaggedArgs& p) {
+  if (!fast) return fp32_sums_plan(p, can_split);
+  const int rows = fast_rows(p);
+  return Fp8Plan{rows, can_split && fast_splits(p, rows), 0.0};
+}
+
+hipError_t launch_ragged_fp8_tile(int out, bool fast, const RaggedArgs& p, hipStream_t st) {
+  const Fp8Plan plan = ragged_fp8_plan(fast, p.ws != nullptr, p);
+  RaggedArgs q = p;
+  if (!plan.split) q.ws = nullptr;
+  if (fast)
+    return out == 1 ? launch_fp8_tile_rows<OutBf16, true>(plan.rows, q, st)
+                    : launch_fp8_tile_rows<OutF16, true>(plan.rows, q, st);
+  return out == 1 ? launch_fp8_tile_rows<OutBf16, false>(plan.rows, q, st)
+                  : launch_fp8_tile_rows<OutF16, false>(plan.rows, q, st);
 }
 
 }  // namespace mx

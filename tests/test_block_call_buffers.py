@@ -146,3 +146,10 @@ def test_refused_before_the_library(pools, monkeypatch, name):  # noqa: F811
         m.setattr(binding, "_lib", Untouched)
         with pytest.raises(error):
             call()
+
+
+def test_fast_sums_of_fp32_results(pools):  # noqa: F811
+    with pytest.raises(NotImplementedError):
+        _fp8(out_dtype=F32, fast_sums=True)
+    assert not pools
+    _fp8(fast_sums=True)

@@ -85,3 +85,15 @@ def test_binding_refuses(lib):
     with pytest.raises(ValueError):
         mx.ragged_gemm_fp8(x.to(torch.float8_e4m3fn), torch.zeros((4, 1)), x[None].to(torch.float8_e4m3fn),
                            torch.zeros((1, 1, 1)), torch.tensor([4]))   # host splits
+
+
+def test_fast_gemm_refuses(lib):
+    """As the other one, and fp32 results."""
+    def call(ct=BF16, R=8, q=FAKE, ldq=64, S=8):
+        return lib.mxfp8_ragged_gemm_fp8_fast(q, ldq, FAKE, FAKE, FAKE, FAKE, 64, ct, R, S, 64, 64, FAKE, 2, None, None, 0,
+                                              None)
+    for ct in (F32, 3, -1):
+        assert call(ct=ct) == 2
+    assert "mxfp8_ragged_gemm_fp8_fast" in lib.mxfp8_last_error().decode()
+    for kw in ({"R": -1}, {"q": None}, {"ldq": 63}, {"S": 9}):
+        assert call(**kw) == 1, kw

@@ -1159,8 +1159,8 @@ def residual_norm_bwd(dy, dr, r, f=None, residual_scale=1.0, gate=None, post_wei
                       eps=1e-6, out=None, workspace=None, stream=None):
     """Gradients of residual_norm: dy [T, H] that of y (None without pre_weight), dr [T, H]
     what reaches r past this norm (None: nothing), r as residual_norm gave it (x itself
-    without f), the rest as there.  Returns a ResidualNormGrad; out: optional one
-    with buffers to write into (x may be dr, f may be dy or f).  workspace: optional device
+    without f), the rest as there.  Returns a ResidualNormGrad of its own; out: optional one
+    with buffers to write into (x may be dr, f may be dy or f), which is not changed.  workspace: optional device
     buffer of residual_norm_bwd_workspace_bytes(T, H), for the weights' gradients."""
     lib = _lib()
     t, h, x_ty, ty, dtype, w_ty = _norm_operands(r, "r", f, None if dy is None else dy.dtype, gate,
@@ -1173,21 +1173,23 @@ def residual_norm_bwd(dy, dr, r, f=None, residual_scale=1.0, gate=None, post_wei
         _need(dy, dtype, (t, h), "dy")
     if dr is not None:
         _need(dr, r.dtype, (t, h), "dr")
-    got = ResidualNormGrad() if out is None else out
+    given = ResidualNormGrad() if out is None else out
+    got = ResidualNormGrad()   # the caller's stays as it is: what it lacks is made anew by each call
     for name, wanted, shape, kind in (
             ("x", True, (t, h), r.dtype), ("f", f is not None, (t, h), dtype),
             ("gate", gate is not None, (t,), torch.float32),
             ("post_weight", post_weight is not None, (h,), torch.float32),
             ("pre_weight", pre_weight is not None, (h,), torch.float32)):
-        buf = getattr(got, name)
+        buf = getattr(given, name)
         if not wanted:
             if buf is not None:
                 raise ValueError(f"out.{name} is the gradient of what was not given")
             continue
         if buf is None:
-            setattr(got, name, _empty(shape, kind, r.device, stream))
+            buf = _empty(shape, kind, r.device, stream)
         else:
             _need(buf, kind, shape, f"out.{name}")
+        setattr(got, name, buf)
     need = residual_norm_bwd_workspace_bytes(t, h) if got.post_weight is not None or got.pre_weight is not None else 0
     size = need
     if workspace is not None:

@@ -153,3 +153,14 @@ def test_fast_sums_of_fp32_results(pools):  # noqa: F811
         _fp8(out_dtype=F32, fast_sums=True)
     assert not pools
     _fp8(fast_sums=True)
+
+
+def test_norm_backward_leaves_the_given_out_as_it_is(pools):  # noqa: F811
+    """Buffers that it lacks are each call's own: a second call writes none of the first one's."""
+    x = T(6, 8)
+    out = mx.ResidualNormGrad(x=x)
+    first, second = _norm_bwd(out=out), _norm_bwd(out=out)
+    assert out == mx.ResidualNormGrad(x=x)
+    assert first.x is x and second.x is x
+    for name in ("f", "gate", "post_weight", "pre_weight"):
+        assert getattr(first, name) is not getattr(second, name), name

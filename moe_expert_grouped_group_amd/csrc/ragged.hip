@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256, 2) void ragged_any_kernel(RaggedArgs p, uint32
   constexpr int MI = TM / 64;                      // blocks of 32 rows of a wave
   static_assert(TM == kAnyT || (TM == 64 && LAYOUT != 2), "");
   __shared__ __attribute__((aligned(16))) uint8_t smem[(TM + kAnyT) * kAnyPitch];
-  __shared__ int64_t scan[2 * 256 + 3];
+  __shared__ int64_t scan[LAYOUT == 2 ? 256 : 1];   // of expert_rows
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 
   // the tile: rows [m0, m0 + rows) of A's output dimension, columns from n0

@@ -80,6 +80,19 @@ def test_a_row_beside_few_and_many_rows(k, n):
             assert (got == k // 8).all(), (rows, out, got[0, :4])
 
 
+@pytest.mark.parametrize("fast", [False, True])
+@pytest.mark.parametrize("k", [16, 128, 256, 400])
+def test_many_tiles_of_few_stages(k, fast):
+    """One, two and four blocks of the contraction: the copies run up to two tiles ahead of the sums."""
+    splits, n = [3000, 0, 901], 5128
+    rows = sum(splits)
+    index = torch.randint(-1, rows + 1, (rows,), generator=torch.Generator().manual_seed(4)).int().cuda()
+    case = _case(rows, splits, k, n)
+    for at in (None, index):
+        got = mx.ragged_gemm_fp8(*case, _ms(splits), row_index=at, fast_sums=fast)
+        (_check if fast else _check_fp32_sums)(*case, splits, at, got)
+
+
 @pytest.mark.parametrize("splits,k,n", SIZES)
 def test_fast_sums(splits, k, n):
     """Within what 8-bit sums may lose, and the same from call to call."""

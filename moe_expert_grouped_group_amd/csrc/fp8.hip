@@ -104,7 +104,8 @@ __device__ __forceinline__ void store_codes(uint8_t* q, uint2 c, int64_t n) {
   }
 }
 
-// n / d for n below 2^31: (n + the high half of n magic) >> shift.
+// n / d for n below 2^31, by the division by invariant integers of Granlund and Montgomery (1994):
+// (n + the high half of n magic) >> shift.
 struct Divide {
   uint32_t magic, shift;
   static Divide by(uint32_t d) {

@@ -15,8 +15,9 @@
 //    this one and the first three of the next.  Widened once into LDS instead, the tile would be read at
 //    twice the bytes: 3072 of the 4096 cycles that a stage's matrix instructions take, and the widening's
 //    reads and writes come on top.
-//    8 x 4096 x 14336, 16384 rows: 1500 us, 1.28 PFLOP/s, the power that bf16 matrix instructions draw (the
-//    bf16 product of ragged_tile.h 1.2).
+//    8 x 4096 x 14336, 16384 rows: 1500 to 1660 us by the machine's clock, 1.16 to 1.28 PFLOP/s (matrix cores
+//    busy 57 % at 1.64 GHz; the bf16 product of ragged_tile.h 1594 to 1624: the power is spent alike).  128 x 128
+//    tiles through registers (ragged_fp8.hip) take 2440.
 //  * 8-bit (the caller asked for them): one 16 x 16 x 128 instruction, which keeps 13 bits below the
 //    largest of 8 consecutive products (1.5e-5 of a block's sum on normal values, where bf16 has 9e-9; the 16 x 16 x
 //    32 one for 8-bit operands the same).  It runs at twice the rate: 950 to 1060 us by the machine's clock, 1.8

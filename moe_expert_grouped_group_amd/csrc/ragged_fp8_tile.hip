@@ -11,10 +11,10 @@
 // The sums of a stage (FAST chooses):
 //  * fp32: four 16 x 16 x 32 bf16 matrix instructions on widened codes.  A wave widens what it has read
 //    from LDS, in registers: 12 conversions for 8 matrix instructions (16 cycles each), the rows of the
-//    next group beside the last block of this one, the columns of the next stage beside the last block of
-//    this one and the first three of the next.  Widened once into LDS instead, the tile would be read at
-//    twice the bytes: 3072 of the 4096 cycles that a stage's matrix instructions take, and the widening's
-//    reads and writes come on top.
+//    next group beside the last block of this one, the columns of a stage beside a block of the last group
+//    before it and the first three of its own.  Widened once into LDS instead, the tile would be read at
+//    twice the bytes: LDS busy for three quarters of the time that a stage's matrix instructions take, with the
+//    widening's reads and writes on top.
 //    8 x 4096 x 14336, 16384 rows: 1500 to 1660 us by the machine's clock, 1.16 to 1.28 PFLOP/s (matrix cores
 //    busy 57 % at 1.64 GHz; the bf16 product of ragged_tile.h 1594 to 1624: the power is spent alike).  128 x 128
 //    tiles through registers (ragged_fp8.hip) take 2440.
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void ragged_fp8_tile_kernel(RaggedAr
   constexpr int kOffB = kTileM * kStageK, kStage = kOffB + kTileN * kStageK;
   constexpr int kCopiesA = RF / 2;                 // of a wave for a stage: 8 rows each; 4 of B
   constexpr int kGroup = 4;                        // blocks whose scales are copied together
-  constexpr int kBlocks = 4 * RF;                  // matrix instructions of a wave for a stage
+  constexpr int kBlocks = 4 * RF;                  // blocks of a wave, each with its sums of a stage
   constexpr int kLag = FAST ? 3 : 1;               // blocks between one and the use of its sums
   static_assert(RF == 8 || RF == 4 || RF == 2, "");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
